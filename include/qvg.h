@@ -436,6 +436,158 @@ qvg_status qvg_get_status(void *stream);
  */
 qvg_status qvg_debug_set_wait(uint64_t limit_ns, int32_t inject);
 
+/* ======================================================================
+ * Token-wise operators: rotary positions and a paged cache that is written
+ * one token at a time.
+ *
+ * A chunk is compressed (above) once it is complete.  The tokens of the
+ * chunk being generated, and any history whose tokens arrive one by one or
+ * as a drafted tree, live in a paged cache instead: fp8 or fp4 codes with
+ * power-of-two scales, which need nothing but the token's own row.  The
+ * pages have no counterpart for this part; its formulas stand here.
+ * ====================================================================== */
+
+/* qvg_rope_plan.layout */
+#define QVG_ROPE_HALF 0        /* pair i = channels i and i + dims / 2           */
+#define QVG_ROPE_INTERLEAVED 1 /* pair i = channels 2 i and 2 i + 1              */
+/* `scaling` of qvg_rope_plan_init, for contexts longer than the trained one. */
+#define QVG_ROPE_PLAIN 0
+#define QVG_ROPE_LINEAR 1 /* positions divided by `factor`                       */
+#define QVG_ROPE_NTK 2    /* base * factor^(n / (n - 2)), n = the axis' channels */
+#define QVG_ROPE_PARTS 3  /* fast pairs kept, slow pairs divided (see below)     */
+
+#define QVG_ROPE_MAX_PAIRS 64
+#define QVG_ROPE_MAX_AXES 4
+
+/*
+ * Rotary positions of one model: a host structure that qvg_rope_plan_init
+ * fills and every call takes by pointer (its contents travel with the
+ * launch; nothing is allocated, and the structure may be copied, saved, or
+ * changed after the call).
+ *   step   what one position adds to pair i's angle, in units of 2^-64 turns.
+ *          A position times a step, modulo 2^64, is the angle's fraction of
+ *          a turn to 2^-64 with no rounding, at any int32 position.
+ *   axis   the position axis that pair i follows.
+ */
+typedef struct {
+    int32_t dims;  /* rotated channels: the first `dims` of each head */
+    int32_t axes;  /* positions per token                             */
+    int32_t layout;
+    float mscale;  /* factor on the rotated channels                  */
+    uint64_t step[QVG_ROPE_MAX_PAIRS];
+    uint8_t axis[QVG_ROPE_MAX_PAIRS];
+} qvg_rope_plan;
+
+/*
+ * Fill a plan.  Axis a owns axis_dims[a] channels, i.e. axis_dims[a] / 2
+ * consecutive pairs; the axes follow one another, and dims is their sum (one
+ * axis: text; frame, row and column: video).  Pair i of an axis with n
+ * channels turns by f_i = base^(-2 i / n) radians per position, and
+ *   QVG_ROPE_LINEAR: f_i / factor;
+ *   QVG_ROPE_NTK:    f_i with base * factor^(n / (n - 2)) (n = 2: base);
+ *   QVG_ROPE_PARTS:  f_i (k + (1 - k) / factor), with r = original f_i / 2 pi
+ *                    the turns of the pair over the trained context of
+ *                    `original` positions and k = (r - slow) / (fast - slow)
+ *                    clamped to [0, 1];
+ * scaled_axes: bit a set = axis a is scaled (others stay plain).
+ * Errors: QVG_ERR_INVALID_ARG for axes outside 1 .. QVG_ROPE_MAX_AXES, an
+ * odd, zero or negative axis_dims, more than QVG_ROPE_MAX_PAIRS pairs, an
+ * unknown layout or scaling, a base or factor that is not finite or below 1,
+ * a non-finite mscale; with QVG_ROPE_PARTS original <= 0 or fast <= slow.
+ */
+qvg_status qvg_rope_plan_init(qvg_rope_plan *plan, int32_t axes, const int32_t *axis_dims, int32_t layout,
+                              double base, int32_t scaling, double factor, double original, double fast,
+                              double slow, uint32_t scaled_axes, float mscale);
+
+/*
+ * Rotate n tokens' heads: pair (a, b) at angle t becomes
+ *   mscale (a cos t - b sin t, b cos t + a sin t);
+ * channels from `dims` on are copied.  In fp32, rounded once to the type.
+ *   x          [n][H][d] of `dtype` (QVG_OUT_F32 or QVG_OUT_BF16), d = 64 or
+ *              128; token t starts at element t * x_stride (>= H d).
+ *   positions  int32 [n][axes] device.
+ *   transpose  1: the angles' signs turned -- the gradient of this call with
+ *              respect to x (and, where mscale is 1, its inverse).
+ *   out        as x, with out_stride.  out may be x itself when the strides
+ *              are equal; otherwise they must not overlap.
+ * Errors: QVG_ERR_INVALID_ARG for a bad plan (dims over d, an axis out of
+ * range), n < 0, H < 1, a stride below H d, an unknown dtype, x, out or
+ * positions missing or not aligned to their elements; QVG_ERR_UNSUPPORTED
+ * for another d.  n = 0 does nothing.
+ */
+qvg_status qvg_rope(const qvg_rope_plan *plan, const void *x, int32_t dtype, int32_t n, int32_t H, int32_t d,
+                    int64_t x_stride, const int32_t *positions, int32_t transpose, void *out, int64_t out_stride,
+                    void *stream);
+
+/*
+ * A paged token cache (K and V of one layer): num_pages pages of page_size
+ * token slots; slot s is token s % page_size of page s / page_size.  Which
+ * page holds what is the caller's business (a block table, below).
+ *   bits 8: codes are fp8 numbers (e4m3: 4 exponent bits, 3 mantissa bits,
+ *           largest 448), one scale per token and head;
+ *   bits 4: codes are fp4 numbers (e2m1: 0 0.5 1 1.5 2 3 4 6 and their
+ *           negatives), channel 2 i in the low half of byte i, one scale per
+ *           token, head and 32 consecutive channels.
+ *   k_codes, v_codes    uint8 [num_pages][H][page_size][d * bits / 8]
+ *   k_scales, v_scales  uint8 [num_pages][H][page_size][G], G = 1 (8 bits) or
+ *                       d / 32: a scale of 2^(byte - 127), the smallest with
+ *                       which no value of the group exceeds the largest code
+ *                       (at least byte 1); 255 marks a row that held an
+ *                       infinity or a NaN, whose codes are 0 and whose values
+ *                       read as NaN (8 bits: the row; 4 bits: the group).
+ * A power-of-two scale makes each step exact but the rounding to the code
+ * (nearest, ties to even): a value is off by at most 2^-4 of itself (8 bits)
+ * or a quarter of it (4 bits), or half the smallest step, and reading it back
+ * into bf16 adds nothing.  (A value within the last step below 2^128 takes the
+ * code below it, so that every finite value stays finite.)
+ * All four buffers are caller-allocated, 16-byte aligned device memory of the
+ * size that qvg_paged_bytes reports.  H >= 1, d = 64 or 128, page_size 16,
+ * 32, 64, 128 or 256.
+ */
+typedef struct {
+    int32_t H;
+    int32_t d;
+    int32_t page_size;
+    int32_t num_pages;
+    int32_t bits;
+    uint8_t *k_codes;
+    uint8_t *k_scales;
+    uint8_t *v_codes;
+    uint8_t *v_scales;
+} qvg_paged;
+
+/* Bytes of a codes buffer and of a scales buffer (K's and V's are alike). */
+qvg_status qvg_paged_bytes(int32_t H, int32_t d, int32_t page_size, int32_t num_pages, int32_t bits,
+                           size_t *codes, size_t *scales);
+
+/*
+ * Quantise n tokens into their slots.
+ *   k, v       bf16 [n][H][d], 16-byte aligned; token t starts at element
+ *              t * k_stride (t * v_stride), a multiple of 8 and >= H d.
+ *   slots      int64 [n] device.  A negative slot skips its token; the
+ *              others must differ from one another (a slot given twice ends
+ *              up with parts of both tokens).
+ *   plan       NULL, or rotary positions that K gets on the way: the rotated
+ *              row is rounded to bf16 and then quantised, as if qvg_rope had
+ *              written it.  positions int32 [n][axes] device.
+ * A slot at or beyond num_pages * page_size is skipped and latches
+ * QVG_ERR_INVALID_ARG in the device's status word (qvg_get_status).
+ * Nothing but the tokens' slots is written.
+ * Errors: QVG_ERR_INVALID_ARG for a bad cache or plan, n < 0, missing or
+ * misaligned pointers, bad strides; QVG_ERR_UNSUPPORTED for another d.
+ */
+qvg_status qvg_paged_append(const qvg_paged *cache, const void *k_bf16, const void *v_bf16, int32_t n,
+                            int64_t k_stride, int64_t v_stride, const int64_t *slots, const qvg_rope_plan *plan,
+                            const int32_t *positions, void *stream);
+
+/*
+ * Read n slots back: k_out, v_out [n][H][d] fp32 or bf16 (out_dtype), 16-byte
+ * aligned; either may be NULL.  Exact in both types.  A negative slot gives
+ * zeros; a slot beyond the cache gives zeros and latches QVG_ERR_INVALID_ARG.
+ */
+qvg_status qvg_paged_read(const qvg_paged *cache, const int64_t *slots, int32_t n, void *k_out, void *v_out,
+                          int32_t out_dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

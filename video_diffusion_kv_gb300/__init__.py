@@ -27,12 +27,16 @@ QVG_PSAC_RANK = 8
 QVG_CACHE_NBUF = 14
 QVG_OUT_F32, QVG_OUT_BF16 = 0, 1
 QVG_OP_COMPRESS, QVG_OP_ATTENTION, QVG_OP_PSAC_BASIS = 0, 1, 2
+QVG_ROPE_HALF, QVG_ROPE_INTERLEAVED = 0, 1
+QVG_ROPE_PLAIN, QVG_ROPE_LINEAR, QVG_ROPE_NTK, QVG_ROPE_PARTS = 0, 1, 2, 3
+QVG_ROPE_MAX_PAIRS, QVG_ROPE_MAX_AXES = 64, 4
 
 EXPORTED = (
     "qvg_status_string", "qvg_cache_bytes", "qvg_workspace_size", "qvg_compress_chunk",
     "qvg_decompress", "qvg_attention", "quantwm_query_stats", "quantwm_psac_basis",
     "qvg_get_status", "qvg_last_cuda_error", "qvg_compress_chunk_noalloc", "qvg_attention_ar",
-    "qvg_debug_set_wait",
+    "qvg_debug_set_wait", "qvg_rope_plan_init", "qvg_rope", "qvg_paged_bytes", "qvg_paged_append",
+    "qvg_paged_read",
 )
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -62,6 +66,17 @@ class _Cache(ct.Structure):
                 ("anchor", ct.c_void_p), ("chunk_anchor", ct.c_void_p)]
 
 
+class _RopePlan(ct.Structure):
+    _fields_ = [("dims", ct.c_int32), ("axes", ct.c_int32), ("layout", ct.c_int32), ("mscale", ct.c_float),
+                ("step", ct.c_uint64 * QVG_ROPE_MAX_PAIRS), ("axis", ct.c_uint8 * QVG_ROPE_MAX_PAIRS)]
+
+
+class _Paged(ct.Structure):
+    _fields_ = [("H", ct.c_int32), ("d", ct.c_int32), ("page_size", ct.c_int32), ("num_pages", ct.c_int32),
+                ("bits", ct.c_int32), ("k_codes", ct.c_void_p), ("k_scales", ct.c_void_p),
+                ("v_codes", ct.c_void_p), ("v_scales", ct.c_void_p)]
+
+
 _lib = None
 
 
@@ -86,6 +101,12 @@ def lib():
                                        sz, vp]
         L.quantwm_query_stats.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp]
         L.quantwm_psac_basis.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp]
+        i64, dbl = ct.c_int64, ct.c_double
+        L.qvg_rope_plan_init.argtypes = [vp, i32, vp, i32, dbl, i32, dbl, dbl, dbl, dbl, ct.c_uint32, ct.c_float]
+        L.qvg_rope.argtypes = [vp, vp, i32, i32, i32, i32, i64, vp, i32, vp, i64, vp]
+        L.qvg_paged_bytes.argtypes = [i32, i32, i32, i32, i32, vp, vp]
+        L.qvg_paged_append.argtypes = [vp, vp, vp, i32, i64, i64, vp, vp, vp, vp]
+        L.qvg_paged_read.argtypes = [vp, vp, i32, vp, vp, i32, vp]
         L.qvg_get_status.argtypes = [vp]
         L.qvg_debug_set_wait.argtypes = [ct.c_uint64, i32]
         L.qvg_last_cuda_error.restype = ct.c_char_p
@@ -318,6 +339,183 @@ def attention_ar(params: Params, q, kc: CompressedKV, vc: CompressedKV, k_cur, v
                                0 if workspace is None else workspace.numel(), _stream(stream))
     _check(s, "qvg_attention_ar")
     return out, lse, top1
+
+
+class RopePlan:
+    """Rotary positions of one model (qvg_rope_plan_init): `axis_dims` channels
+    per position axis, the first sum(axis_dims) of each head.  A host object;
+    it may be shared by streams and devices."""
+
+    def __init__(self, axis_dims, layout=QVG_ROPE_HALF, base=10000.0, scaling=QVG_ROPE_PLAIN, factor=1.0,
+                 original=0.0, fast=32.0, slow=1.0, scaled_axes=0xFFFFFFFF, mscale=1.0):
+        self._c = _RopePlan()
+        dims = (ct.c_int32 * max(1, len(axis_dims)))(*axis_dims)
+        _check(lib().qvg_rope_plan_init(ct.byref(self._c), len(axis_dims), dims, layout, base, scaling, factor,
+                                        original, fast, slow, scaled_axes, mscale), "qvg_rope_plan_init")
+        self._ref = ct.byref(self._c)
+        self.dims, self.axes, self.layout = self._c.dims, self._c.axes, layout
+
+
+def _heads(x, where):
+    """(tokens, heads, channels, token stride) of a [n, H, d] tensor whose
+    heads and channels are contiguous."""
+    if x.dim() != 3:
+        raise ValueError("%s: a [tokens, heads, channels] tensor is wanted" % where)
+    n, H, d = x.shape
+    s = x.stride()
+    if (s[2] != 1 and d > 1) or (s[1] != d and H > 1):
+        raise ValueError("%s: heads and channels must be contiguous" % where)
+    return n, H, d, (s[0] if n > 1 else H * d)
+
+
+def _on(dev, where, **tensors):
+    """Checks (dtype, contiguity, device) of the tensors handed to a call that
+    runs on `dev`."""
+    for name, (t, dtype) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise ValueError("%s: %s is %s, %s is wanted" % (where, name, t.dtype, dtype))
+        if t.device != dev:
+            raise ValueError("%s: %s is on %s, not on %s" % (where, name, t.device, dev))
+        if not t.is_contiguous():
+            raise ValueError("%s: %s must be contiguous" % (where, name))
+
+
+class _Device:
+    """Makes `dev` the current device of the calling thread, where it is not
+    already (the library works on the current device)."""
+    __slots__ = ("dev", "was")
+
+    def __init__(self, dev):
+        import torch
+        if dev.type != "cuda":
+            raise ValueError("CUDA tensors are wanted, got one on %s" % dev)
+        self.dev, self.was = dev.index, torch.cuda.current_device()
+
+    def __enter__(self):
+        if self.dev != self.was:
+            import torch
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.dev != self.was:
+            import torch
+            torch.cuda.set_device(self.was)
+
+
+def _empty(shape, dtype, dev, stream):
+    """An output or workspace for a kernel on `stream` (None: the current
+    stream), from that stream's own memory: memory that the current stream
+    has given back may still be in use there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _positions(plan, positions, n, where):
+    if positions is None:
+        raise ValueError("%s: a plan needs positions" % where)
+    if positions.numel() != n * plan.axes:
+        raise ValueError("%s: positions must be int32 [%d, %d]" % (where, n, plan.axes))
+
+
+def rope(plan: RopePlan, x, positions, transpose=False, out=None, stream=None):
+    """Rotate x (bf16 or fp32 [n, H, d]; tokens may be strided) at positions
+    (int32 [n, axes], or [n] with one axis).  transpose=True turns the angles'
+    signs: the gradient with respect to x.  out may be x itself."""
+    import torch
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("rope: bf16 or fp32 is wanted, got %s" % x.dtype)
+    n, H, d, xs = _heads(x, "rope")
+    if out is None:
+        out = _empty((n, H, d), x.dtype, x.device, stream)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+        raise ValueError("rope: out must match x")
+    _, _, _, os_ = _heads(out, "rope")
+    _positions(plan, positions, n, "rope")
+    _on(x.device, "rope", positions=(positions, torch.int32))
+    with _Device(x.device):
+        _check(lib().qvg_rope(plan._ref, x.data_ptr(), QVG_OUT_F32 if x.dtype == torch.float32 else QVG_OUT_BF16, n, H,
+                              d, xs, positions.data_ptr(), 1 if transpose else 0, out.data_ptr(), os_,
+                              _stream(stream)), "qvg_rope")
+    return out
+
+
+def paged_bytes(H, d, page_size, num_pages, bits):
+    """(codes, scales) bytes of one of a paged cache's two tensors."""
+    a, b = ct.c_size_t(0), ct.c_size_t(0)
+    _check(lib().qvg_paged_bytes(H, d, page_size, num_pages, bits, ct.byref(a), ct.byref(b)), "qvg_paged_bytes")
+    return int(a.value), int(b.value)
+
+
+class PagedKV:
+    """K and V of one layer in pages of fp8 (bits=8) or fp4 (bits=4) codes
+    with power-of-two scales (qvg_paged in include/qvg.h).  `buffers`: the four
+    uint8 tensors (k codes, k scales, v codes, v scales) where the caller
+    allocates them."""
+
+    def __init__(self, H, d, page_size, num_pages, bits=8, device="cuda", buffers=None):
+        import torch
+        sizes = paged_bytes(H, d, page_size, num_pages, bits)
+        self.H, self.d, self.page_size, self.num_pages, self.bits = H, d, page_size, num_pages, bits
+        rows = (num_pages, H, page_size)
+        shapes = [rows + (d * bits // 8,), rows + (1 if bits == 8 else d // 32,)] * 2
+        if buffers is None:
+            buffers = [torch.zeros(s, dtype=torch.uint8, device=device) for s in shapes]
+        for t, need in zip(buffers, sizes * 2):
+            if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != need or t.device != buffers[0].device:
+                raise ValueError("PagedKV: each buffer must be contiguous uint8 of the size paged_bytes reports")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = (t.view(s) for t, s in zip(buffers, shapes))
+        self.device = self.k_codes.device
+        self._c = _Paged(H, d, page_size, num_pages, bits, self.k_codes.data_ptr(), self.k_scales.data_ptr(),
+                         self.v_codes.data_ptr(), self.v_scales.data_ptr())
+        self._ref = ct.byref(self._c)
+
+    @property
+    def nbytes(self):
+        return sum(t.numel() for t in (self.k_codes, self.k_scales, self.v_codes, self.v_scales))
+
+
+def paged_append(cache: PagedKV, k, v, slots, plan=None, positions=None, stream=None):
+    """Quantise k and v (bf16 [n, H, d]; tokens may be strided) into the slots
+    (int64 [n]; negative: skip).  With a RopePlan, K is rotated at `positions`
+    on the way.  A slot beyond the cache is reported by get_status()."""
+    import torch
+    n, H, d, ks = _heads(k, "paged_append")
+    _, _, _, vs = _heads(v, "paged_append")
+    if k.shape != v.shape or (H, d) != (cache.H, cache.d) or slots.numel() != n:
+        raise ValueError("paged_append: k, v must be [n, %d, %d] and slots [n]" % (cache.H, cache.d))
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.device != cache.device or v.device != cache.device:
+        raise ValueError("paged_append: k and v must be bf16 on the cache's device")
+    _on(cache.device, "paged_append", slots=(slots, torch.int64), positions=(positions, torch.int32))
+    if plan is not None:
+        _positions(plan, positions, n, "paged_append")
+    with _Device(cache.device):
+        _check(lib().qvg_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), n, ks, vs, slots.data_ptr(),
+                                      None if plan is None else plan._ref,
+                                      None if plan is None else positions.data_ptr(), _stream(stream)),
+               "qvg_paged_append")
+
+
+def paged_read(cache: PagedKV, slots, out_dtype=QVG_OUT_BF16, k_out=None, v_out=None, stream=None):
+    """The rows that the slots (int64 [n]; negative: zeros) hold: (K, V), each
+    bf16 or fp32 [n, H, d]."""
+    import torch
+    n = slots.numel()
+    dt = torch.float32 if out_dtype == QVG_OUT_F32 else torch.bfloat16
+    shape = (n, cache.H, cache.d)
+    k_out = _empty(shape, dt, cache.device, stream) if k_out is None else k_out
+    v_out = _empty(shape, dt, cache.device, stream) if v_out is None else v_out
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError("paged_read: outputs must be [n, %d, %d]" % (cache.H, cache.d))
+    _on(cache.device, "paged_read", slots=(slots, torch.int64), k_out=(k_out, dt), v_out=(v_out, dt))
+    with _Device(cache.device):
+        _check(lib().qvg_paged_read(cache._ref, slots.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(), out_dtype,
+                                    _stream(stream)), "qvg_paged_read")
+    return k_out, v_out
 
 
 def query_stats(q, H, M=None, w=None, count=None, accumulate=False, stream=None):
