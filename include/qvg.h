@@ -437,8 +437,8 @@ qvg_status qvg_get_status(void *stream);
 qvg_status qvg_debug_set_wait(uint64_t limit_ns, int32_t inject);
 
 /* ======================================================================
- * Token-wise operators: rotary positions and a paged cache that is written
- * one token at a time.
+ * Token-wise operators: rotary positions, a paged cache that is written one
+ * token at a time, and attention of a few new tokens over it.
  *
  * A chunk is compressed (above) once it is complete.  The tokens of the
  * chunk being generated, and any history whose tokens arrive one by one or
@@ -532,9 +532,9 @@ qvg_status qvg_rope(const qvg_rope_plan *plan, const void *x, int32_t dtype, int
  *   k_scales, v_scales  uint8 [num_pages][H][page_size][G], G = 1 (8 bits) or
  *                       d / 32: a scale of 2^(byte - 127), the smallest with
  *                       which no value of the group exceeds the largest code
- *                       (at least byte 1); 255 marks a row that held an
- *                       infinity or a NaN, whose codes are 0 and whose values
- *                       read as NaN (8 bits: the row; 4 bits: the group).
+ *                       (at least byte 1); 255 marks a row (token and head)
+ *                       that held an infinity or a NaN: its codes are 0, its
+ *                       scales all 255, and its values read as NaN.
  * A power-of-two scale makes each step exact but the rounding to the code
  * (nearest, ties to even): a value is off by at most 2^-4 of itself (8 bits)
  * or a quarter of it (4 bits), or half the smallest step, and reading it back
@@ -587,6 +587,84 @@ qvg_status qvg_paged_append(const qvg_paged *cache, const void *k_bf16, const vo
  */
 qvg_status qvg_paged_read(const qvg_paged *cache, const int64_t *slots, int32_t n, void *k_out, void *v_out,
                           int32_t out_dtype, void *stream);
+
+/* mask_mode of qvg_paged_attention */
+#define QVG_MASK_NONE 0   /* every token of the sequence                          */
+#define QVG_MASK_CAUSAL 1 /* new token t sees the history and new tokens 0 .. t   */
+#define QVG_MASK_TREE 2   /* the history and the new tokens its mask row names    */
+
+/*
+ * Mask rows of drafted trees: row t of a sequence has the bits of t itself
+ * and of all its ancestors.
+ *   parents  int32 [total_q] device: the parent's number within the
+ *            sequence's new tokens, which is below the token's own, or -1
+ *            (the token follows the history).  Another value latches
+ *            QVG_ERR_INVALID_ARG and counts as -1.
+ *   cu_q     int32 [B + 1] device: sequence b's new tokens are rows
+ *            cu_q[b] .. cu_q[b + 1] - 1; NULL: max_q rows each.
+ *   mask     uint32 [total_q][words] device, words >= ceil(max_q / 32);
+ *            bit j % 32 of word j / 32 is new token j.  Every word of the
+ *            rows cu_q[0] .. cu_q[B] - 1 is written.
+ * Errors: QVG_ERR_INVALID_ARG for B < 0, max_q < 0, too few words, missing
+ * or misaligned pointers.
+ */
+qvg_status qvg_tree_mask(const int32_t *parents, const int32_t *cu_q, int32_t B, int32_t max_q, int32_t words,
+                         uint32_t *mask, void *stream);
+
+/*
+ * Scratch bytes of qvg_paged_attention on the current device (256-byte
+ * aligned; no initialisation needed, dead after the call).
+ */
+qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B, int32_t max_q, size_t *bytes);
+
+/*
+ * Attention of B sequences' new tokens over their pages: one token each
+ * (decoding), a drafted tree, or the tokens of a chunk.  The new tokens' K
+ * and V have been appended: they are the last tokens of the sequence.  With
+ * L = kv_len[b] tokens and T new ones, key j < L - T is history and key
+ * L - T + i is new token i; new token t sees what mask_mode says, and
+ *   O = softmax(scale * Q K^T) V   over the keys it sees.
+ *   q          bf16 [total_q][Hq][d], 16-byte aligned; token t starts at
+ *              element t * q_stride (a multiple of 8, >= Hq d).  Query head
+ *              hq reads KV head hq / (Hq / H).
+ *   cu_q       int32 [B + 1] device, ascending from 0: first row of each
+ *              sequence's new tokens; NULL: max_q rows each.  Rows from
+ *              cu_q[B] on are neither read nor written.
+ *   max_q      at least the largest T.  A longer sequence's tokens beyond it
+ *              are left out and latch QVG_ERR_INVALID_ARG.
+ *   table      int32 [B][table_stride] device: page of tokens
+ *              p * page_size .. of sequence b.  Entries past the sequence's
+ *              last page are not read.
+ *   kv_len     int32 [B] device, the new tokens included; 0: no keys.  A
+ *              sequence longer than its table row, and a page outside the
+ *              cache, latch QVG_ERR_INVALID_ARG and make the sequence's
+ *              output undefined.
+ *   mask       QVG_MASK_TREE: uint32 [total_q][mask_words] (qvg_tree_mask, or
+ *              any bits); mask_words >= ceil(max_q / 32).
+ *   scale      as in qvg_attention.
+ *   out        [total_q][Hq][d] fp32 or bf16, 16-byte aligned; a row that
+ *              sees no key is 0.
+ *   lse        fp32 [Hq][total_q] natural-log log-sum-exp of the scaled
+ *              logits (-inf for a row that sees no key), or NULL.
+ *   total_q    rows of q, out and lse.
+ *   workspace  at least qvg_paged_workspace_size(H, d, Hq, B, max_q) bytes.
+ * Keys that a token does not see, and slots past kv_len, have no influence
+ * on it, whatever they hold.  Q enters the product as the sum of two fp8
+ * numbers (exact for channels down to 2^-10 of the row's largest, off by at
+ * most 2^-19 of the largest below), K as its codes; the weights times V's
+ * scale are rounded to fp16 against V's codes; all sums are fp32.  (4 bits:
+ * groups below 2^-14, in V 2^-24, of their row's largest scale count as 0.)
+ * A row of q
+ * with an infinity or a NaN gives NaN.  The results do not depend on what
+ * else the GPU runs: the split of the work follows from the sizes alone.
+ * All sizes on the device are read when the kernels run: a captured call can
+ * be replayed with other lengths, tables and masks.
+ */
+qvg_status qvg_paged_attention(const qvg_paged *cache, const void *q_bf16, int64_t q_stride, int32_t total_q,
+                               int32_t Hq, int32_t B, int32_t max_q, const int32_t *cu_q, const int32_t *table,
+                               int32_t table_stride, const int32_t *kv_len, int32_t mask_mode,
+                               const uint32_t *mask, int32_t mask_words, float scale, void *out,
+                               int32_t out_dtype, float *lse, void *workspace, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

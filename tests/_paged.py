@@ -53,10 +53,10 @@ def rope(x, positions, f, axis, layout, mscale=1.0, transpose=False):
 
 def quantise(x, bits):
     """x [..., d] float64 -> (values of the codes, scale bytes), groups of d (8
-    bits) or 32 (4 bits).  A group with an infinity or a NaN: 0 and 255."""
+    bits) or 32 (4 bits).  A row with an infinity or a NaN: 0 and 255."""
     d = x.shape[-1]
     g = x.reshape(*x.shape[:-1], 1 if bits == 8 else d // 32, -1)
-    bad = ~np.isfinite(g).all(-1)
+    bad = np.broadcast_to(~np.isfinite(g).all(-1).all(-1, keepdims=True), g.shape[:-1])
     g = np.where(bad[..., None], 0.0, g)
     top = np.abs(g).max(-1)
     m, e = np.frexp(top / TOP[bits])  # top / TOP = m 2^e with m in [0.5, 1): the smallest power of two above is 2^e, or 2^(e-1) at m = 0.5

@@ -151,3 +151,63 @@ def test_python_refusals(lib):
         qvg.paged_read(c, slots, k_out=torch.zeros(4, 2, 32, dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         qvg.PagedKV(2, 64, 16, 4, buffers=[torch.zeros(8, dtype=torch.uint8)] * 4)
+
+
+def test_tree_mask_refusals(lib):
+    call = lambda par=P, cu=None, B=2, mq=40, w=2, m=P: lib.qvg_tree_mask(par, cu, B, mq, w, m, None)  # noqa: E731
+    for kw in (dict(B=-1), dict(mq=-1), dict(w=1), dict(par=None), dict(m=None), dict(m=ct.c_void_p(0x10002)),
+               dict(cu=ct.c_void_p(0x10001))):
+        assert call(**kw) == BAD, kw
+    assert call(mq=8193, w=300) == UNS
+    assert call(B=0, par=None, m=None) == qvg.QVG_OK
+
+
+def test_paged_workspace(lib):
+    size = ct.c_size_t(0)
+    for kw, code in ((dict(), 0), (dict(H=0), BAD), (dict(Hq=3), BAD), (dict(B=-1), BAD), (dict(mq=-1), BAD), (dict(d=80), UNS)):
+        a = {**dict(H=2, d=64, Hq=4, B=3, mq=5), **kw}
+        assert lib.qvg_paged_workspace_size(a["H"], a["d"], a["Hq"], a["B"], a["mq"], ct.byref(size)) == code, kw
+    assert lib.qvg_paged_workspace_size(2, 64, 4, 3, 5, None) == BAD
+    assert size.value > 0
+
+
+def test_paged_attention_refusals(lib):
+    need = ct.c_size_t(0)
+    assert lib.qvg_paged_workspace_size(2, 64, 4, 3, 40, ct.byref(need)) == qvg.QVG_OK
+
+    def call(c=None, q=P, qs=256, tq=120, Hq=4, B=3, mq=40, cu=None, table=P, ts=8, kv=P, mode=1, mask=None, words=0, scale=0.0,
+             out=P, dt=1, lse=None, ws=P, wb=need.value):
+        c = fake() if c is None else c
+        return lib.qvg_paged_attention(ct.byref(c), q, qs, tq, Hq, B, mq, cu, table, ts, kv, mode, mask, words, scale, out, dt, lse,
+                                       ws, wb, None)
+    for kw in BAD_CACHES:
+        assert call(fake(**kw)) == BAD, kw
+    assert call(fake(d=32)) == UNS
+    for kw in (dict(qs=255), dict(qs=260), dict(Hq=3), dict(Hq=0), dict(B=-1), dict(mq=-1), dict(tq=-1), dict(tq=119),
+               dict(ts=0), dict(mode=3), dict(mode=2), dict(mode=2, mask=P, words=1), dict(mode=2, mask=ct.c_void_p(0x10002), words=2),
+               dict(scale=math.nan), dict(scale=math.inf), dict(dt=2), dict(q=None), dict(out=None), dict(table=None), dict(kv=None),
+               dict(q=ct.c_void_p(0x10008)), dict(out=ct.c_void_p(0x10008)), dict(kv=ct.c_void_p(0x10002)),
+               dict(cu=ct.c_void_p(0x10002)), dict(lse=ct.c_void_p(0x10002))):
+        assert call(**kw) == BAD, kw
+    for kw in (dict(ws=None), dict(wb=need.value - 1), dict(ws=ct.c_void_p(0x10080))):
+        assert call(**kw) == WS, kw
+    for kw in (dict(B=0), dict(mq=0), dict(tq=0, B=0)):
+        assert call(**{**kw, **dict(q=None, out=None, table=None, kv=None, ws=None, wb=0)}) == qvg.QVG_OK, kw
+
+
+def test_python_attention_refusals(lib):
+    c = qvg.PagedKV(2, 64, 16, 4, device="cpu")
+    q = torch.zeros(4, 4, 64, dtype=torch.bfloat16)
+    table, kv = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for kw in (dict(q=q.float()), dict(q=q[..., :32]), dict(table=table[:1]), dict(table=table[0]), dict(kv=kv.long()),
+               dict(cu_q=kv), dict(mask_mode=2), dict(mask_mode=2, mask=torch.zeros(3, 1, dtype=torch.int32)),
+               dict(out=torch.zeros(4, 2, 64, dtype=torch.bfloat16)), dict(workspace=torch.zeros(9)), dict()):
+        a = {**dict(q=q, table=table, kv=kv), **kw}
+        q_, t_, k_ = a.pop("q"), a.pop("table"), a.pop("kv")
+        with pytest.raises(ValueError):
+            qvg.paged_attention(c, q_, t_, k_, 2, **a)
+    par = torch.zeros(4, dtype=torch.int32)
+    for args, kw in (((par, 3), {}), ((par, 0), {}), ((par, 2), dict(out=torch.zeros(3, 1, dtype=torch.int32))), ((par.long(), 2), {}),
+                     ((par, 2), {})):
+        with pytest.raises(ValueError):
+            qvg.tree_mask(*args, **kw)

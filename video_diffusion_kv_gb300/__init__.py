@@ -30,13 +30,14 @@ QVG_OP_COMPRESS, QVG_OP_ATTENTION, QVG_OP_PSAC_BASIS = 0, 1, 2
 QVG_ROPE_HALF, QVG_ROPE_INTERLEAVED = 0, 1
 QVG_ROPE_PLAIN, QVG_ROPE_LINEAR, QVG_ROPE_NTK, QVG_ROPE_PARTS = 0, 1, 2, 3
 QVG_ROPE_MAX_PAIRS, QVG_ROPE_MAX_AXES = 64, 4
+QVG_MASK_NONE, QVG_MASK_CAUSAL, QVG_MASK_TREE = 0, 1, 2
 
 EXPORTED = (
     "qvg_status_string", "qvg_cache_bytes", "qvg_workspace_size", "qvg_compress_chunk",
     "qvg_decompress", "qvg_attention", "quantwm_query_stats", "quantwm_psac_basis",
     "qvg_get_status", "qvg_last_cuda_error", "qvg_compress_chunk_noalloc", "qvg_attention_ar",
     "qvg_debug_set_wait", "qvg_rope_plan_init", "qvg_rope", "qvg_paged_bytes", "qvg_paged_append",
-    "qvg_paged_read",
+    "qvg_paged_read", "qvg_tree_mask", "qvg_paged_workspace_size", "qvg_paged_attention",
 )
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -107,6 +108,10 @@ def lib():
         L.qvg_paged_bytes.argtypes = [i32, i32, i32, i32, i32, vp, vp]
         L.qvg_paged_append.argtypes = [vp, vp, vp, i32, i64, i64, vp, vp, vp, vp]
         L.qvg_paged_read.argtypes = [vp, vp, i32, vp, vp, i32, vp]
+        L.qvg_tree_mask.argtypes = [vp, vp, i32, i32, i32, vp, vp]
+        L.qvg_paged_workspace_size.argtypes = [i32, i32, i32, i32, i32, vp]
+        L.qvg_paged_attention.argtypes = [vp, vp, i64, i32, i32, i32, i32, vp, vp, i32, vp, i32, vp, i32, ct.c_float,
+                                          vp, i32, vp, vp, sz, vp]
         L.qvg_get_status.argtypes = [vp]
         L.qvg_debug_set_wait.argtypes = [ct.c_uint64, i32]
         L.qvg_last_cuda_error.restype = ct.c_char_p
@@ -516,6 +521,71 @@ def paged_read(cache: PagedKV, slots, out_dtype=QVG_OUT_BF16, k_out=None, v_out=
         _check(lib().qvg_paged_read(cache._ref, slots.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(), out_dtype,
                                     _stream(stream)), "qvg_paged_read")
     return k_out, v_out
+
+
+def tree_mask(parents, max_q, cu_q=None, out=None, stream=None):
+    """Mask rows of drafted trees (int32 [total_q, ceil(max_q / 32)], read as
+    unsigned bits): a token sees itself and its ancestors.  parents: int32
+    [total_q], the parent's number within the sequence's new tokens or -1;
+    cu_q: int32 [B + 1], or None when every sequence has max_q tokens."""
+    import torch
+    total, words = parents.numel(), max(1, -(-max_q // 32))
+    if cu_q is None and (max_q < 1 or total % max_q != 0):
+        raise ValueError("tree_mask: without cu_q every sequence has max_q tokens")
+    if out is None:
+        out = _empty((total, words), torch.int32, parents.device, stream)
+    elif out.dim() != 2 or out.shape[0] != total or out.shape[1] < words:
+        raise ValueError("tree_mask: out must be [total_q, words] with at least %d words" % words)
+    B = total // max_q if cu_q is None else cu_q.numel() - 1
+    _on(parents.device, "tree_mask", parents=(parents, torch.int32), cu_q=(cu_q, torch.int32), out=(out, torch.int32))
+    with _Device(parents.device):
+        _check(lib().qvg_tree_mask(parents.data_ptr(), None if cu_q is None else cu_q.data_ptr(), B, max_q, out.shape[1],
+                                   out.data_ptr(), _stream(stream)), "qvg_tree_mask")
+    return out
+
+
+def paged_workspace_size(cache: PagedKV, Hq, B, max_q):
+    b = ct.c_size_t(0)
+    with _Device(cache.device):
+        _check(lib().qvg_paged_workspace_size(cache.H, cache.d, Hq, B, max_q, ct.byref(b)), "qvg_paged_workspace_size")
+    return int(b.value)
+
+
+def paged_attention(cache: PagedKV, q, block_table, kv_len, max_q, cu_q=None, mask_mode=QVG_MASK_CAUSAL, mask=None,
+                    scale=0.0, out_dtype=QVG_OUT_BF16, want_lse=False, out=None, workspace=None, stream=None):
+    """Attention of the new tokens q (bf16 [total_q, Hq, d]; tokens may be
+    strided), which are the last ones of their sequences, over the cache.
+    block_table: int32 [B, pages]; kv_len: int32 [B], new tokens included;
+    cu_q: int32 [B + 1] (None: max_q tokens each); mask: tree_mask's rows, with
+    mask_mode QVG_MASK_TREE.  Returns (out, lse or None).  Two calls that run
+    at once need a workspace each (None: one per call)."""
+    import torch
+    total, Hq, d, qs = _heads(q, "paged_attention")
+    B = kv_len.numel()
+    dt = torch.float32 if out_dtype == QVG_OUT_F32 else torch.bfloat16
+    if q.dtype != torch.bfloat16 or q.device != cache.device or d != cache.d:
+        raise ValueError("paged_attention: q must be bf16 [total_q, Hq, %d] on the cache's device" % cache.d)
+    if block_table.dim() != 2 or block_table.shape[0] != B or (cu_q is not None and cu_q.numel() != B + 1):
+        raise ValueError("paged_attention: block_table must be [B, pages], kv_len [B], cu_q [B + 1]")
+    if mask_mode == QVG_MASK_TREE and (mask is None or mask.dim() != 2 or mask.shape[0] < total):
+        raise ValueError("paged_attention: QVG_MASK_TREE needs mask rows [total_q, words]")
+    if out is None:
+        out = _empty((total, Hq, d), dt, q.device, stream)
+    elif out.shape != (total, Hq, d):
+        raise ValueError("paged_attention: out must be [total_q, Hq, d]")
+    _on(q.device, "paged_attention", block_table=(block_table, torch.int32), kv_len=(kv_len, torch.int32),
+        cu_q=(cu_q, torch.int32), mask=(mask, torch.int32), out=(out, dt), workspace=(workspace, torch.uint8))
+    lse = _empty((Hq, total), torch.float32, q.device, stream) if want_lse else None
+    if workspace is None:
+        workspace = _empty((paged_workspace_size(cache, Hq, B, max_q),), torch.uint8, q.device, stream)
+    with _Device(q.device):
+        _check(lib().qvg_paged_attention(
+            cache._ref, q.data_ptr(), qs, total, Hq, B, max_q, None if cu_q is None else cu_q.data_ptr(),
+            block_table.data_ptr(), block_table.shape[1], kv_len.data_ptr(), mask_mode,
+            None if mask is None else mask.data_ptr(), 0 if mask is None else mask.shape[1], scale, out.data_ptr(),
+            out_dtype, None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            _stream(stream)), "qvg_paged_attention")
+    return out, lse
 
 
 def query_stats(q, H, M=None, w=None, count=None, accumulate=False, stream=None):

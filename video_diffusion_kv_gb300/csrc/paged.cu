@@ -48,7 +48,8 @@ __device__ __forceinline__ size_t row_of(const PagedArgs &a, long long slot, int
 
 // 16 channels of one row (packed bf16 pairs) into their codes.  The lanes of
 // a row are neighbours (LANES of them).  8 bits: one scale for the row.
-// 4 bits: one for 32 channels, i.e. two lanes.
+// 4 bits: one for 32 channels, i.e. two lanes.  An infinity
+// or a NaN marks every group of the row.
 template <int BITS, int LANES>
 __device__ __forceinline__ void quantise16(const uint32_t (&x)[8], uint8_t *codes, uint8_t *scales, size_t row, int u,
                                            bool live) {
@@ -59,7 +60,10 @@ __device__ __forceinline__ void quantise16(const uint32_t (&x)[8], uint8_t *code
     constexpr int kSpan = BITS == 8 ? LANES : 2;
 #pragma unroll
     for (int o = 1; o < kSpan; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    const uint32_t sb = scale_byte<BITS>(amax);
+    uint32_t row_max = amax;
+#pragma unroll
+    for (int o = kSpan; o < LANES; o <<= 1) row_max = max(row_max, __shfl_xor_sync(0xFFFFFFFFu, row_max, o));
+    const uint32_t sb = row_max >= 0x7F80u ? 255u : scale_byte<BITS>(amax);
     const float inv = sb == 255u ? 0.0f : scale_inverse(sb);
     const uint32_t keep = sb == 255u ? 0u : 0xFFFFFFFFu;  // a row with an infinity or a NaN: codes 0
     // Under the largest scale a magnitude above 1.875 2^127 (1.75 2^127 at 4

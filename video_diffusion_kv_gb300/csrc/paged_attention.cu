@@ -1,0 +1,243 @@
+// paged_attention.cu -- attention over a paged cache: launch, the join of
+// units that several CTAs shared, the mask rows of drafted trees, and the
+// entry points.  The kernel is in paged_attention.cuh.
+#include <cudaTypedefs.h>
+
+#include <cmath>
+
+#include "paged_attention.cuh"
+
+namespace qvg {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // compress.cu
+
+namespace {
+
+// The unit that begins in CTA i and goes on to CTA `last` left one partial
+// sum per CTA: slot 1 of CTA i, slot 0 of the others.  With references m_z,
+// sums l_z and O_z: m = max m_z, l = sum l_z 2^(m_z - m), O likewise.  One
+// warp per query row; parts in CTA order, so the result is the same each time.
+template <int D, int NB>
+__global__ void __launch_bounds__(256) k_paged_merge(const __grid_constant__ pa::Args a) {
+    constexpr int E = D / 32;
+    pdl_wait();
+    const int4 u = a.desc[blockIdx.x];
+    if (u.x < 0) return;
+    const int n = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const pa::Seq s = pa::seq_of<NB>(a, u.x, false);
+    const long long gi = static_cast<long long>(u.z) * NB + n;
+    const int tq = static_cast<int>(gi / a.grp), j = static_cast<int>(gi - static_cast<long long>(tq) * a.grp);
+    if (tq >= s.nq) return;
+    const int first = blockIdx.x, last = u.w;
+    float m = -INFINITY;
+    for (int z = first; z <= last; ++z) {
+        const size_t at = static_cast<size_t>(2 * z + (z == first ? 1 : 0)) * NB + n;
+        if (a.pl[at] != 0.0f) m = fmaxf(m, a.pm[at]);
+    }
+    float acc[E], l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    for (int z = first; z <= last; ++z) {
+        const size_t at = static_cast<size_t>(2 * z + (z == first ? 1 : 0)) * NB + n;
+        const float lz = a.pl[at];
+        if (lz == 0.0f) continue;  // no key of this part is seen
+        const float w = exp2f(a.pm[at] - m);
+        l = fmaf(w, lz, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, a.po[at * D + lane * E + e], acc[e]);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const long long row = static_cast<long long>(s.q0 + tq) * a.Hq + u.y * a.grp + j;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (a.out32)
+            a.out32[row * D + lane * E + e] = acc[e] * inv;
+        else
+            a.out16[row * D + lane * E + e] = f32_to_bf16(acc[e] * inv);
+    }
+    if (lane == 0 && a.lse)
+        a.lse[(row % a.Hq) * a.total_q + row / a.Hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// One block per sequence: parents in shared memory, a thread walks up from
+// its token.  A parent is below its child, so a walk has at most T steps.
+__global__ void k_tree_mask(const int32_t *__restrict__ parents, const int32_t *__restrict__ cu_q, int max_q, int words,
+                            uint32_t *__restrict__ mask, int *err) {
+    extern __shared__ int32_t s_up[];
+    const int b = blockIdx.x;
+    const long long q0 = cu_q ? cu_q[b] : static_cast<long long>(b) * max_q;
+    const int n = cu_q ? min(cu_q[b + 1] - cu_q[b], max_q) : max_q;
+    if (cu_q && threadIdx.x == 0 && cu_q[b + 1] - cu_q[b] > max_q) raise_error(err, QVG_ERR_INVALID_ARG);
+    for (int t = threadIdx.x; t < n; t += blockDim.x) {
+        int p = parents[q0 + t];
+        if (p < -1 || p >= t) {
+            raise_error(err, QVG_ERR_INVALID_ARG);
+            p = -1;
+        }
+        s_up[t] = p;
+    }
+    __syncthreads();
+    // a thread makes one word of one row: bits [32 w, 32 w + 32)
+    for (long long i = threadIdx.x; i < static_cast<long long>(n) * words; i += blockDim.x) {
+        const int t = static_cast<int>(i / words), w = static_cast<int>(i % words);
+        uint32_t m = 0;
+        for (int j = t; j >= 32 * w; j = s_up[j])
+            if ((j >> 5) == w) m |= 1u << (j & 31);
+        mask[(q0 + t) * words + w] = m;
+    }
+}
+
+constexpr int kMaxTree = 8192;  // new tokens of one sequence whose parents fit 32 KB of shared memory
+
+// Query rows of a unit: the smallest block that holds a sequence's rows, at
+// most 64.
+int rows_of_block(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+struct Workspace {
+    size_t po, pm, pl, desc, bytes;  // offsets
+};
+Workspace carve(int ctas, int NB, int d) {
+    auto al = [](size_t b) { return (b + 255) & ~static_cast<size_t>(255); };
+    const size_t rows = static_cast<size_t>(ctas) * 2 * NB;
+    Workspace w{};
+    w.pm = al(rows * d * 4);
+    w.pl = w.pm + al(rows * 4);
+    w.desc = w.pl + al(rows * 4);
+    w.bytes = w.desc + al(static_cast<size_t>(ctas) * sizeof(int4));
+    return w;
+}
+
+// K's codes as [pages][H][page][d] bytes; a box is one page's rows of a head
+// (at most 128), swizzled as the tensor core reads them.
+bool k_tensor_map(CUtensorMap *m, const qvg_paged *c) {
+    const auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t d = static_cast<cuuint64_t>(c->d), pg = static_cast<cuuint64_t>(c->page_size);
+    const cuuint64_t dims[4] = {d, pg, static_cast<cuuint64_t>(c->H), static_cast<cuuint64_t>(c->num_pages)};
+    const cuuint64_t strides[3] = {d, d * pg, d * pg * static_cast<cuuint64_t>(c->H)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(c->d), static_cast<cuuint32_t>(std::min(c->page_size, 128)), 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(c->k_codes), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, c->d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int BITS, int NB>
+qvg_status launch(const CUtensorMap &map, const pa::Args &a, int ctas, cudaStream_t st) {
+    using C = pa::Cfg<D, BITS, NB>;
+    static std::atomic<uint64_t> done{0};
+    const qvg_status s = smem_limit_once(done, reinterpret_cast<const void *>(pa::k_paged_attention<D, BITS, NB>), C::kSmem);
+    if (s != QVG_OK) return s;
+    pa::k_paged_attention<D, BITS, NB><<<ctas, C::kWarps * 32, C::kSmem, st>>>(map, a);
+    QVG_LAUNCH_CHECK();
+    const cudaError_t e = launch_pdl(k_paged_merge<D, NB>, dim3(ctas, NB / 8), dim3(256), 0, st, a);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        note_cuda_error(e);
+        return QVG_ERR_CUDA;
+    }
+    return QVG_OK;
+}
+
+template <int D, int BITS>
+qvg_status launch_nb(int NB, const CUtensorMap &map, const pa::Args &a, int ctas, cudaStream_t st) {
+    if (NB == 16) return launch<D, BITS, 16>(map, a, ctas, st);
+    if (NB == 32) return launch<D, BITS, 32>(map, a, ctas, st);
+    return launch<D, BITS, 64>(map, a, ctas, st);
+}
+
+bool misaligned(const void *p, uintptr_t to) { return !p || reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+}  // namespace
+}  // namespace qvg
+
+using namespace qvg;
+
+extern "C" {
+
+qvg_status qvg_tree_mask(const int32_t *parents, const int32_t *cu_q, int32_t B, int32_t max_q, int32_t words,
+                         uint32_t *mask, void *stream) {
+    if (B < 0 || max_q < 0 || words < ceil_div(max_q, 32)) return QVG_ERR_INVALID_ARG;
+    if (max_q > kMaxTree) return QVG_ERR_UNSUPPORTED;
+    if (B == 0 || max_q == 0) return QVG_OK;
+    if (misaligned(parents, 4) || misaligned(mask, 4) || (cu_q && misaligned(cu_q, 4))) return QVG_ERR_INVALID_ARG;
+    const int threads = static_cast<int>(std::min<long long>(1024, (static_cast<long long>(max_q) * words + 31) / 32 * 32));
+    k_tree_mask<<<B, threads, static_cast<size_t>(max_q) * sizeof(int32_t), static_cast<cudaStream_t>(stream)>>>(
+        parents, cu_q, max_q, words, mask, device_error_word());
+    QVG_LAUNCH_CHECK();
+    return QVG_OK;
+}
+
+qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B, int32_t max_q, size_t *bytes) {
+    if (!bytes || H < 1 || Hq < 1 || Hq % H != 0 || B < 0 || max_q < 0) return QVG_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return QVG_ERR_UNSUPPORTED;
+    *bytes = carve(sm_count_current(), rows_of_block(static_cast<long long>(max_q) * (Hq / H)), d).bytes;
+    return QVG_OK;
+}
+
+qvg_status qvg_paged_attention(const qvg_paged *cache, const void *q_bf16, int64_t q_stride, int32_t total_q,
+                               int32_t Hq, int32_t B, int32_t max_q, const int32_t *cu_q, const int32_t *table,
+                               int32_t table_stride, const int32_t *kv_len, int32_t mask_mode,
+                               const uint32_t *mask, int32_t mask_words, float scale, void *out,
+                               int32_t out_dtype, float *lse, void *workspace, size_t ws_bytes, void *stream) {
+    qvg_status s = check_paged(cache, false);
+    if (s != QVG_OK) return s;
+    const int H = cache->H, d = cache->d;
+    if (Hq < 1 || Hq % H != 0 || B < 0 || max_q < 0 || total_q < 0 || table_stride < 1) return QVG_ERR_INVALID_ARG;
+    if (q_stride < static_cast<int64_t>(Hq) * d || q_stride % 8 != 0) return QVG_ERR_INVALID_ARG;
+    if (mask_mode != QVG_MASK_NONE && mask_mode != QVG_MASK_CAUSAL && mask_mode != QVG_MASK_TREE) return QVG_ERR_INVALID_ARG;
+    if (out_dtype != QVG_OUT_F32 && out_dtype != QVG_OUT_BF16) return QVG_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return QVG_ERR_INVALID_ARG;
+    if (!cu_q && static_cast<int64_t>(B) * max_q > total_q) return QVG_ERR_INVALID_ARG;
+    if (B == 0 || max_q == 0 || total_q == 0) return QVG_OK;
+    if (misaligned(q_bf16, 16) || misaligned(out, 16) || misaligned(table, 4) || misaligned(kv_len, 4) ||
+        (cu_q && misaligned(cu_q, 4)) || (lse && misaligned(lse, 4)))
+        return QVG_ERR_INVALID_ARG;
+    if (mask_mode == QVG_MASK_TREE && (misaligned(mask, 4) || mask_words < ceil_div(max_q, 32))) return QVG_ERR_INVALID_ARG;
+    const int ctas = sm_count_current();
+    const int NB = rows_of_block(static_cast<long long>(max_q) * (Hq / H));
+    const Workspace w = carve(ctas, NB, d);
+    if (!workspace || ws_bytes < w.bytes || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return QVG_ERR_WORKSPACE;
+    CUtensorMap map{};
+    if (cache->bits == 8 && !k_tensor_map(&map, cache)) return QVG_ERR_CUDA;
+    pa::Args a{};
+    a.q = static_cast<const uint16_t *>(q_bf16);
+    a.q_stride = q_stride;
+    a.total_q = total_q;
+    a.Hq = Hq;
+    a.H = H;
+    a.grp = Hq / H;
+    a.B = B;
+    a.max_q = max_q;
+    a.cu_q = cu_q;
+    a.table = table;
+    a.kv_len = kv_len;
+    a.table_stride = table_stride;
+    a.mode = mask_mode;
+    a.mask = mask;
+    a.words = mask_words;
+    a.scale_log2 = (scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(d))) * 1.4426950408889634f;
+    a.out32 = out_dtype == QVG_OUT_F32 ? static_cast<float *>(out) : nullptr;
+    a.out16 = out_dtype == QVG_OUT_BF16 ? static_cast<uint16_t *>(out) : nullptr;
+    a.lse = lse;
+    a.kc = cache->k_codes;
+    a.ks = cache->k_scales;
+    a.vc = cache->v_codes;
+    a.vs = cache->v_scales;
+    a.page_log2 = __builtin_ctz(static_cast<unsigned>(cache->page_size));
+    a.num_pages = cache->num_pages;
+    char *base = static_cast<char *>(workspace);
+    a.po = reinterpret_cast<float *>(base + w.po);
+    a.pm = reinterpret_cast<float *>(base + w.pm);
+    a.pl = reinterpret_cast<float *>(base + w.pl);
+    a.desc = reinterpret_cast<int4 *>(base + w.desc);
+    a.err = device_error_word();
+    a.wait_ns = wait_limit_ns();
+    a.inject = wait_inject();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (d == 64)
+        return cache->bits == 8 ? launch_nb<64, 8>(NB, map, a, ctas, st) : launch_nb<64, 4>(NB, map, a, ctas, st);
+    return cache->bits == 8 ? launch_nb<128, 8>(NB, map, a, ctas, st) : launch_nb<128, 4>(NB, map, a, ctas, st);
+}
+
+}  // extern "C"
