@@ -650,10 +650,11 @@ qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B,
  *   workspace  at least qvg_paged_workspace_size(H, d, Hq, B, max_q) bytes.
  * Keys that a token does not see, and slots past kv_len, have no influence
  * on it, whatever they hold.  Q enters the product as the sum of two fp8
- * numbers (exact for channels down to 2^-10 of the row's largest, off by at
- * most 2^-19 of the largest below), K as its codes; the weights times V's
- * scale are rounded to fp16 against V's codes; all sums are fp32.  (4 bits:
- * groups below 2^-14, in V 2^-24, of their row's largest scale count as 0.)
+ * numbers (exact for channels down to 2^-14 of the row's largest, off by at
+ * most 2^-21 of the largest below), K and V as their codes; the weights times
+ * V's scale enter as the sum of three fp8 numbers (off by at most 2^-9 of
+ * themselves, or 2^-26 of the largest); all sums are fp32.  (4 bits: groups
+ * whose scale is below 2^-14 of their row's largest count as 0.)
  * A row of q
  * with an infinity or a NaN gives NaN.  The results do not depend on what
  * else the GPU runs: the split of the work follows from the sizes alone.

@@ -107,9 +107,9 @@ Workspace carve(int ctas, int NB, int d) {
     return w;
 }
 
-// K's codes as [pages][H][page][d] bytes; a box is one page's rows of a head
-// (at most 128), swizzled as the tensor core reads them.
-bool k_tensor_map(CUtensorMap *m, const qvg_paged *c) {
+// A tensor's 8-bit codes as [pages][H][page][d] bytes; a box is one page's rows
+// of a head (at most 128), swizzled as the tensor core reads them.
+bool codes_map(CUtensorMap *m, const qvg_paged *c, const uint8_t *codes) {
     const auto fn = tensor_map_encoder();
     if (!fn) return false;
     const cuuint64_t d = static_cast<cuuint64_t>(c->d), pg = static_cast<cuuint64_t>(c->page_size);
@@ -117,18 +117,18 @@ bool k_tensor_map(CUtensorMap *m, const qvg_paged *c) {
     const cuuint64_t strides[3] = {d, d * pg, d * pg * static_cast<cuuint64_t>(c->H)};
     const cuuint32_t box[4] = {static_cast<cuuint32_t>(c->d), static_cast<cuuint32_t>(std::min(c->page_size, 128)), 1, 1};
     const cuuint32_t es[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(c->k_codes), dims, strides, box, es,
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(codes), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, c->d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, int BITS, int NB>
-qvg_status launch(const CUtensorMap &map, const pa::Args &a, int ctas, cudaStream_t st) {
+qvg_status launch(const CUtensorMap (&map)[2], const pa::Args &a, int ctas, cudaStream_t st) {
     using C = pa::Cfg<D, BITS, NB>;
     static std::atomic<uint64_t> done{0};
     const qvg_status s = smem_limit_once(done, reinterpret_cast<const void *>(pa::k_paged_attention<D, BITS, NB>), C::kSmem);
     if (s != QVG_OK) return s;
-    pa::k_paged_attention<D, BITS, NB><<<ctas, C::kWarps * 32, C::kSmem, st>>>(map, a);
+    pa::k_paged_attention<D, BITS, NB><<<ctas, C::kWarps * 32, C::kSmem, st>>>(map[0], map[1], a);
     QVG_LAUNCH_CHECK();
     const cudaError_t e = launch_pdl(k_paged_merge<D, NB>, dim3(ctas, NB / 8), dim3(256), 0, st, a);
     if (e != cudaSuccess) {
@@ -140,7 +140,7 @@ qvg_status launch(const CUtensorMap &map, const pa::Args &a, int ctas, cudaStrea
 }
 
 template <int D, int BITS>
-qvg_status launch_nb(int NB, const CUtensorMap &map, const pa::Args &a, int ctas, cudaStream_t st) {
+qvg_status launch_nb(int NB, const CUtensorMap (&map)[2], const pa::Args &a, int ctas, cudaStream_t st) {
     if (NB == 16) return launch<D, BITS, 16>(map, a, ctas, st);
     if (NB == 32) return launch<D, BITS, 32>(map, a, ctas, st);
     return launch<D, BITS, 64>(map, a, ctas, st);
@@ -198,8 +198,9 @@ qvg_status qvg_paged_attention(const qvg_paged *cache, const void *q_bf16, int64
     const int NB = rows_of_block(static_cast<long long>(max_q) * (Hq / H));
     const Workspace w = carve(ctas, NB, d);
     if (!workspace || ws_bytes < w.bytes || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return QVG_ERR_WORKSPACE;
-    CUtensorMap map{};
-    if (cache->bits == 8 && !k_tensor_map(&map, cache)) return QVG_ERR_CUDA;
+    CUtensorMap map[2] = {};
+    if (cache->bits == 8 && (!codes_map(&map[0], cache, cache->k_codes) || !codes_map(&map[1], cache, cache->v_codes)))
+        return QVG_ERR_CUDA;
     pa::Args a{};
     a.q = static_cast<const uint16_t *>(q_bf16);
     a.q_stride = q_stride;

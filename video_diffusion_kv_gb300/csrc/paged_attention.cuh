@@ -10,23 +10,31 @@
 // sequences fill the GPU alike.  A unit cut by a border leaves fp32 partial
 // sums that k_paged_merge joins.
 //
-// The product runs transposed, keys on the tensor core's 128 rows:
-//   S^T [keys x rows] = K Q^T        K's fp8 codes as they lie in the cache
-//   O^T [d x rows]   += V^T P^T      V's codes as fp16, P in fp16
-// so its cost follows the number of query rows (N), not a padded 128.
-//   - K needs no conversion: its codes are the A operand, and Q is the sum of
-//     two fp8 numbers hi + lo (a bf16 number has 8 significant bits, an e4m3
-//     number 4: exact while the channel is within 2^-10 of the row's largest),
-//     two products into one accumulator.
-//   - A key's scale is one number per row of S^T, i.e. per softmax thread.
-//   - V's scale goes into the weight: w = p sv.  V's codes become fp16 in
-//     shared memory (exact); w is rounded to fp16 (2^-11).
+// The product runs transposed, keys on the tensor core's 128 rows, and takes
+// the cache's fp8 codes as they lie there (4-bit codes become fp8 first):
+//   S^T [keys x rows] = K Q^T        A = K's codes
+//   O^T [d x rows]   += V^T P^T      A = V's codes, read across (MN-major)
+// so its cost follows the number of query rows (N), not a padded 128, and K
+// and V are touched once by the copy and once by the tensor core.  The other
+// operand is made of several fp8 numbers side by side along N, each with its
+// own accumulator columns; a product with N <= 64 takes the tensor core the
+// same 45 clocks whatever N is, so the extra columns are free there:
+//   - Q as two: hi + lo / 16 in e4m3 (4 significant bits each, a bf16 number
+//     has 8: exact while the channel is within 2^-14 of the row's largest);
+//   - P as three: h1 + h2 / 8 + h3 / 64 in e5m2, the first two cut off an
+//     fp16 number's upper byte (e5m2 is just that), the last rounded: at most
+//     2^-9 of the weight off, and fp16's range, which e4m3 lacks.
+// A key's scale is one number per row of S^T, i.e. per softmax thread; V's
+// scale goes into the weight: w = p sv.
 // Softmax: a thread owns one key and NC columns.  The weights of a column are
-// taken relative to a reference that is set from the unit's first tile (its
-// largest w becomes 2^kTarget) and raised when a w would pass 2^kTop, so the
-// sums l and O are rescaled rarely, and a tile needs one vote, no maximum
-// across threads.  A w 2^-29 below the reference's largest still counts in
-// fp16 (subnormals); l takes p in fp32.
+// taken relative to a reference that is set from the first tile (its largest
+// w becomes 2^kTarget) and raised when a w would pass 2^kTop, so the sums l
+// and O are rescaled rarely, and a tile needs one vote, no maximum across
+// threads.  A w of 2^-26 of the reference's largest still counts; l takes p in
+// fp32.
+// Up to 32 query rows, two softmax warpgroups take the tiles in turn, each
+// with its own reference and sums (two streams, joined at the unit's end);
+// with 64 rows they share every tile, 32 columns each.
 #pragma once
 
 #include <cuda.h>
@@ -38,7 +46,7 @@ namespace qvg {
 namespace pa {
 
 constexpr int kTile = 128;
-constexpr float kTarget = 4.0f, kTop = 15.0f;
+constexpr float kTarget = 4.0f, kTop = 14.0f;  // a w up to 2^14: its remainders times 8 stay in fp16
 constexpr uint64_t kDrainNs = 2000000000ull;
 
 struct Args {
@@ -170,17 +178,16 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Barrier over the 128 threads of softmax warpgroup `wg`; true if any of them
-// brought true.
-__device__ __forceinline__ bool wg_any(int wg, bool p) {
+// Barrier `id` over `count` threads; true if any of them brought true.
+__device__ __forceinline__ bool any_of(int id, int count, bool p) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred a, b;\n\t"
         "setp.ne.u32 a, %1, 0;\n\t"
-        "barrier.cta.red.or.pred b, %2, 128, a;\n\t"
+        "barrier.cta.red.or.pred b, %2, %3, a;\n\t"
         "selp.u32 %0, 1, 0, b;\n\t}"
         : "=r"(r)
-        : "r"(p ? 1u : 0u), "r"(wg + 1)
+        : "r"(p ? 1u : 0u), "r"(id), "r"(count)
         : "memory");
     return r != 0;
 }
@@ -217,13 +224,17 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *map, int c
         : "memory");
 }
 
-// Operand of one row of D bytes per key (or query row), K-major, swizzled:
-// 128-byte rows with the 128-byte swizzle, 64-byte rows with the 64-byte one
-// (16-byte piece c of row i at c ^ (i / 2 % 4)); eight rows are one atom.
+// Tiles of one row of D bytes per key (or query row), swizzled in 16-byte
+// pieces: 128-byte rows with the 128-byte swizzle (piece c of row i at
+// c ^ (i % 8)), 64-byte rows with the 64-byte one (c ^ (i / 2 % 4)).  Eight
+// rows are one atom.  The same bytes serve as a K-major operand (the product
+// runs along the row) and as an MN-major one (it runs down the rows; lbo: from
+// one D-wide block to the next).
 template <int D>
-__device__ __forceinline__ uint64_t desc_rows8(uint32_t addr) {
+__device__ __forceinline__ uint64_t desc_rows8(uint32_t addr, uint32_t lbo = 0) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
     d |= static_cast<uint64_t>((8 * D) >> 4) << 32;
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(D == 128 ? 2u : 4u) << 61;
@@ -233,9 +244,9 @@ template <int D>
 __device__ __forceinline__ uint32_t swizzle8(uint32_t off) {
     return D == 128 ? off ^ ((off >> 3) & 0x70u) : off ^ ((off >> 3) & 0x30u);
 }
-// kind::f8f6f4 with A and B e4m3, both K-major; D fp32.
-__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) {
-    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+// kind::f8f6f4, A e4m3, B e4m3 (b = 0) or e5m2 (b = 1), D fp32, K-major.
+__host__ __device__ constexpr uint32_t idesc_f8(uint32_t M, uint32_t N, uint32_t b) {
+    return (1u << 4) | (b << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -246,16 +257,65 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, 
         : "memory");
 }
 
-// Lane i receives 16 consecutive columns of TMEM lane (base + i).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+// Lane i receives 16 consecutive columns of TMEM lane (base + i), from each
+// of two places.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, uint32_t (&r)[16], uint32_t (&q)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(q[0]),
+          "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]), "=r"(q[9]),
+          "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15])
+        : "r"(t0), "r"(t1)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
+        : "r"(t)
         : "memory");
+}
+// Eight columns from each of three places `step` columns apart (the three
+// parts of O).
+__device__ __forceinline__ void tmem_ld8x3(uint32_t t, uint32_t step, uint32_t (&a)[8], uint32_t (&b)[8], uint32_t (&c)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%24];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%25];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%26];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(b[0]),
+          "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(c[0]), "=r"(c[1]),
+          "=r"(c[2]), "=r"(c[3]), "=r"(c[4]), "=r"(c[5]), "=r"(c[6]), "=r"(c[7])
+        : "r"(t), "r"(t + step), "r"(t + 2 * step)
+        : "memory");
+}
+
+// Four weights (two fp16 pairs) -> their three e5m2 parts, four bytes each.
+__device__ __forceinline__ void three_parts(uint32_t a, uint32_t b, uint32_t &h1, uint32_t &h2, uint32_t &h3) {
+    const __half2 eight = __half2half2(__ushort_as_half(0x4800));  // 8
+    auto rest = [&](uint32_t x) {  // 8 (x - its upper byte): exact
+        const uint32_t cut = x & 0xFF00FF00u;
+        const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&cut)), eight);
+        return *reinterpret_cast<const uint32_t *>(&d);
+    };
+    h1 = __byte_perm(a, b, 0x7531);
+    a = rest(a);
+    b = rest(b);
+    h2 = __byte_perm(a, b, 0x7531);
+    a = rest(a);
+    b = rest(b);
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(a));
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(hi) : "r"(b));
+    h3 = static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
 }
 
 // Sum or maximum over the warp's lanes of each of W columns held by every
@@ -287,29 +347,31 @@ __device__ __forceinline__ float across_lanes(float (&v)[W]) {
 
 template <int D, int BITS, int NB>
 struct Cfg {
-    static constexpr int NSW = NB >= 64 ? 2 : 1;  // softmax warpgroups
-    static constexpr int NC = NB / NSW;           // columns of a softmax thread
+    static constexpr int NSTR = NB <= 32 ? 2 : 1;   // streams (see above)
+    static constexpr int NC = NSTR == 2 ? NB : NB / 2;  // columns of a softmax thread
+    static constexpr int kParty = NSTR == 2 ? 4 : 8;    // softmax warps on one tile
     static constexpr int G = BITS == 8 ? 1 : D / 32;
     static constexpr int kRow = D * BITS / 8;         // bytes of a row of codes
     static constexpr int kRaw = kTile * kRow;         // a tile's codes (K or V)
     static constexpr int kStage = 2 * kRaw + 1024;    // K, V, their scales
-    static constexpr int kK8 = BITS == 4 ? kTile * D : 0;  // K as e4m3 (4 bits), two buffers
-    static constexpr int kVf = kTile * D * 2;         // V as fp16, two buffers
-    static constexpr int kP = 16384 * ((NB + 63) / 64);  // weights, two buffers
-    static constexpr int kQ = NB * D;                 // Q hi; lo follows
-    static constexpr int kFixed = 2 * kK8 + 2 * kVf + 2 * kP + 2 * kQ;
-    static constexpr int kMaxStages = (225 * 1024 - 4096 - kFixed) / kStage;
-    static constexpr int kStages = kMaxStages > 6 ? 6 : kMaxStages;
+    static constexpr int kOp = BITS == 4 ? kTile * D : 0;  // K or V as e4m3 (4 bits), two buffers each
+    static constexpr int kP = 16384 * ((3 * NB + 127) / 128);  // weights, two buffers
+    static constexpr int kQ = 2 * NB * D;             // Q: hi rows, lo rows
+    static constexpr int kFixed = 4 * kOp + 2 * kP + kQ;
+    static constexpr int kMaxStages = (225 * 1024 - 6144 - kFixed) / kStage;
+    static constexpr int kStages = kMaxStages > 8 ? 8 : kMaxStages;
     static constexpr int kSmem = kFixed + kStages * kStage + 1024;
-    static constexpr int kWarps = 8 + 4 * NSW;
-    static constexpr int kTmem = NB == 16 ? 64 : NB == 32 ? 128 : 256;
-    static_assert(kStages >= 2, "shared memory");
+    static constexpr int kConv = BITS == 4 ? 4 : 0;   // converter warps
+    static constexpr int kWarps = 12 + kConv;         // loads, S, PV, TMEM; softmax 4 - 11; converters
+    static constexpr int kTmemUsed = 2 * 2 * NB + NSTR * 3 * NB;
+    static constexpr int kTmem = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+    static_assert(kStages >= 3, "shared memory");
 };
 
 // e2m1 magnitudes times 2^(6 - k) as e4m3 bytes, for a group whose scale is
 // 2^-k of the row's largest (k <= 14; beyond, the values are under 2^-9 and
-// count as 0), eight bytes a row: the K operand of a 4-bit cache.
-__device__ __forceinline__ uint2 k_levels(int k) {
+// count as 0), eight bytes: the operands of a 4-bit cache.
+__device__ __forceinline__ uint2 levels_of(int k) {
     // magnitude 2^e m: byte (e + 7) << 3 | mantissa, subnormal below 2^-6
     uint32_t w[2] = {0, 0};
 #pragma unroll
@@ -323,17 +385,18 @@ __device__ __forceinline__ uint2 k_levels(int k) {
 
 template <int D, int BITS, int NB>
 __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
-    k_paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ Args a) {
+    k_paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const __grid_constant__ Args a) {
     using C = Cfg<D, BITS, NB>;
-    constexpr int S = C::kStages, NSW = C::NSW, NC = C::NC;
+    constexpr int S = C::kStages, NSTR = C::NSTR, NC = C::NC;
     extern __shared__ uint8_t dyn[];
     __shared__ uint64_t full[S], empty[S], s_full[2], s_free[2], p_full[2], v_full[2], k_full[2], k_done[2], pv_done[2],
         q_full, drain, never;
     __shared__ uint32_t tmem_base;
     __shared__ int fail, s_issued;
-    __shared__ __align__(16) float2 s_qs[NB / 2], s_nm[NB / 2];  // per column: Q's scale, minus the reference
-    __shared__ float s_red[4][NB], s_dl[NB];
-    __shared__ int s_tok[NB];       // new token of each row
+    __shared__ __align__(16) float s_qs[NB], s_nm[NSTR][NB];  // per column: Q's scale, minus the reference
+    __shared__ __align__(16) float s_red[2][4][NB], s_dl[2][NB], s_l[NSTR][NB], s_wt[NSTR][NB];
+    __shared__ int s_tok[NB];        // new token of each row
     __shared__ long long s_row[NB];  // out row, or -1
     __shared__ long long s_scan[C::kWarps], s_at[4];
 
@@ -394,35 +457,34 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
 
     uint8_t *base = dyn + ((1024u - (umma::smem_u32(dyn) & 1023u)) & 1023u);
     const uint32_t sm = umma::smem_u32(base);
-    const uint32_t vf0 = sm, p0 = vf0 + 2 * C::kVf, k80 = p0 + 2 * C::kP, qh = k80 + 2 * C::kK8, ql = qh + C::kQ,
-                   st0 = ql + C::kQ;
+    const uint32_t p0 = sm, k80 = p0 + 2 * C::kP, v80 = k80 + 2 * C::kOp, q0 = v80 + 2 * C::kOp, st0 = q0 + C::kQ;
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             umma::mbar_init(&full[i], 1);
-            umma::mbar_init(&empty[i], (BITS == 8 ? 1 : 0) + 4 + 4 * NSW);  // S done, V read, scales read
+            umma::mbar_init(&empty[i], (BITS == 8 ? 2 : 4) + C::kParty);  // products (or converters) done, scales read
         }
         for (int i = 0; i < 2; ++i) {
             umma::mbar_init(&s_full[i], 1);
-            umma::mbar_init(&s_free[i], 4 * NSW);
-            umma::mbar_init(&p_full[i], 4 * NSW);
+            umma::mbar_init(&s_free[i], C::kParty);
+            umma::mbar_init(&p_full[i], C::kParty);
             umma::mbar_init(&v_full[i], 4);
             umma::mbar_init(&k_full[i], 4);
             umma::mbar_init(&k_done[i], 1);
             umma::mbar_init(&pv_done[i], 1);
         }
-        umma::mbar_init(&q_full, 4 * NSW);
-        umma::mbar_init(&drain, 1);
+        umma::mbar_init(&q_full, 8);
+        umma::mbar_init(&drain, 2);
         umma::mbar_init(&never, 1);
         umma::fence_barrier_init();
     }
-    if (warp == 2) {
+    if (warp == 3) {
         umma::tmem_alloc(&tmem_base, C::kTmem);
         umma::tmem_relinquish();
     }
     __syncthreads();
     umma::tc_fence_after();
     const uint32_t tmem = tmem_base;
-    const uint32_t t_o = tmem + 2 * NB;
+    const uint32_t t_o = tmem + 4 * NB;  // S: two buffers of 2 NB columns; O: 3 NB per stream
     volatile int *vfail = &fail;
     const int n_tiles = static_cast<int>(pos1 - pos0);
 
@@ -453,11 +515,13 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                     const uint32_t dst = st0 + st * C::kStage;
                     const int off = tok & ((1 << a.page_log2) - 1);
                     const size_t at = ((static_cast<size_t>(page) * a.H + g.h) << a.page_log2) + off;  // first row
-                    if constexpr (BITS == 8)
+                    if constexpr (BITS == 8) {
                         tma_load_4d(dst + lane * pr * C::kRow, &kmap, off, g.h, page, &full[st]);
-                    else
+                        tma_load_4d(dst + C::kRaw + lane * pr * C::kRow, &vmap, off, g.h, page, &full[st]);
+                    } else {
                         bulk_copy(dst + lane * pr * C::kRow, a.kc + at * C::kRow, pr * C::kRow, &full[st]);
-                    bulk_copy(dst + C::kRaw + lane * pr * C::kRow, a.vc + at * C::kRow, pr * C::kRow, &full[st]);
+                        bulk_copy(dst + C::kRaw + lane * pr * C::kRow, a.vc + at * C::kRow, pr * C::kRow, &full[st]);
+                    }
                     bulk_copy(dst + 2 * C::kRaw + lane * pr * C::G, a.ks + at * C::G, pr * C::G, &full[st]);
                     bulk_copy(dst + 2 * C::kRaw + 512 + lane * pr * C::G, a.vs + at * C::G, pr * C::G, &full[st]);
                 }
@@ -466,189 +530,134 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
         }
         if (lane == 0) s_issued = it;
     } else if (warp == 1) {
-        // ---- products ------------------------------------------------------------------
+        // ---- S = K Q^T -------------------------------------------------------------------
         if (lane == 0) {
-            constexpr uint32_t id_s = idesc_e4m3(128, NB), id_o = umma::idesc_f16(128, NB, 0) | (1u << 15) | (1u << 16);
-            const uint64_t dqh = desc_rows8<D>(qh), dql = desc_rows8<D>(ql);
-            bool ok = true;
-            auto issue_s = [&](int it) {
-                const int st = it % S, bf = it & 1;
-                ok = ok && wait(&full[st], (it / S) & 1, vfail, a.wait_ns);
-                if (BITS == 4) ok = ok && wait(&k_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
-                if (it >= 2) ok = ok && wait(&s_free[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
-                if (!ok) return;
-                umma::tc_fence_after();
-                const uint64_t dk = desc_rows8<D>(BITS == 8 ? st0 + st * C::kStage : k80 + bf * C::kK8);
-#pragma unroll
-                for (int s = 0; s < D / 32; ++s) mma_f8(tmem + bf * NB, dk + 2 * s, dqh + 2 * s, id_s, s != 0);
-#pragma unroll
-                for (int s = 0; s < D / 32; ++s) mma_f8(tmem + bf * NB, dk + 2 * s, dql + 2 * s, id_s, 1);
-                umma::mma_commit(&s_full[bf]);
-                umma::mma_commit(BITS == 8 ? &empty[st] : &k_done[bf]);
-            };
-            auto issue_pv = [&](int it, bool fresh) {
-                const int bf = it & 1;
-                ok = ok && wait(&p_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
-                ok = ok && wait(&v_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
-                if (!ok) return;
-                umma::tc_fence_after();
-                // d = 64: the accumulator's upper 64 rows repeat the lower ones and are not read
-                const uint64_t dv = umma::desc_sw128_mn(vf0 + bf * C::kVf, D == 128 ? kTile * 128 : 0);
-                const uint64_t dp = umma::desc_sw128_mn(p0 + bf * C::kP, kTile * 128);
-#pragma unroll
-                for (int s = 0; s < kTile / 16; ++s)
-                    umma::mma_f16(t_o, dv + s * 128, dp + s * 128, id_o, !(fresh && s == 0));
-                umma::mma_commit(&pv_done[bf]);
-            };
+            constexpr uint32_t id = idesc_f8(128, 2 * NB, 0);
+            const uint64_t dq = desc_rows8<D>(q0);
             Walk<NB> walk(a, pos0, pos1, b_at, f_at);
             Segment g;
             int it = 0, n_seg = 0;
-            bool fresh = false;  // tile it - 1 opened its segment
+            bool ok = true;
             while (ok && walk.next(a, g)) {
+                ok = wait(&q_full, n_seg & 1, vfail, a.wait_ns);
+                ++n_seg;
                 for (int t = g.t0; ok && t < g.t1; ++t, ++it) {
-                    if (t == g.t0) {
-                        if (it > 0) issue_pv(it - 1, fresh);
-                        ok = ok && wait(&q_full, n_seg & 1, vfail, a.wait_ns);
-                        ++n_seg;
-                    }
-                    issue_s(it);
+                    const int st = it % S, bf = it & 1;
+                    ok = BITS == 8 ? wait(&full[st], (it / S) & 1, vfail, a.wait_ns)
+                                   : wait(&k_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                    if (it >= 2) ok = ok && wait(&s_free[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
+                    if (!ok) break;
+                    umma::tc_fence_after();
+                    const uint64_t dk = desc_rows8<D>(BITS == 8 ? st0 + st * C::kStage : k80 + bf * C::kOp);
+#pragma unroll
+                    for (int s = 0; s < D / 32; ++s) mma_f8(tmem + bf * 2 * NB, dk + 2 * s, dq + 2 * s, id, s != 0);
+                    umma::mma_commit(&s_full[bf]);
+                    umma::mma_commit(BITS == 8 ? &empty[st] : &k_done[bf]);
                     // test hook: with S in flight, wait for what never comes
-                    if (ok && it == 0 && a.inject) ok = wait(&never, 0, vfail, a.wait_ns);
-                    if (t > g.t0) issue_pv(it - 1, fresh);
-                    fresh = t == g.t0;
+                    if (it == 0 && a.inject) ok = wait(&never, 0, vfail, a.wait_ns);
                 }
             }
-            if (ok && it > 0) issue_pv(it - 1, fresh);
-            // all products issued complete before TMEM goes back
+            umma::mma_commit(&drain);
+        }
+    } else if (warp == 2) {
+        // ---- O += V^T P^T (its own warp: starting a batch of products takes longer than the batch) ----
+        if (lane == 0) {
+            constexpr uint32_t id = idesc_f8(128, 3 * NB, 1) | (1u << 15) | (1u << 16);  // both MN-major
+            Walk<NB> walk(a, pos0, pos1, b_at, f_at);
+            Segment g;
+            int it = 0;
+            bool ok = true;
+            while (ok && walk.next(a, g)) {
+                for (int t = g.t0; ok && t < g.t1; ++t, ++it) {
+                    const int st = it % S, bf = it & 1;
+                    // (4 bits: the stage itself may be in its next use by now)
+                    ok = BITS == 8 ? wait(&full[st], (it / S) & 1, vfail, a.wait_ns)
+                                   : wait(&v_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                    ok = ok && wait(&p_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                    if (!ok) break;
+                    umma::tc_fence_after();
+                    // d = 64: the accumulator's upper 64 rows repeat the lower ones and are not read
+                    const uint64_t dv = desc_rows8<D>(BITS == 8 ? st0 + st * C::kStage + C::kRaw : v80 + bf * C::kOp);
+                    const uint64_t dp = desc_rows8<128>(p0 + bf * C::kP, kTile * 128);
+                    const bool fresh = t - g.t0 < NSTR;  // the stream's first tile of the unit
+#pragma unroll
+                    for (int s = 0; s < kTile / 32; ++s)
+                        mma_f8(t_o + (NSTR == 2 ? bf * 3 * NB : 0), dv + s * (32 * D / 16), dp + s * 256, id, !(fresh && s == 0));
+                    umma::mma_commit(&pv_done[bf]);
+                    if (BITS == 8) umma::mma_commit(&empty[st]);
+                }
+            }
+            // all products issued, S's too, complete before TMEM goes back
             umma::mma_commit(&drain);
             umma::mbar_wait(&drain, 0, kDrainNs);
         }
-    } else if (warp >= 4 && warp < 8) {
-        // ---- V (and 4-bit K) into operands ------------------------------------------------
-        const int w = tid - 128;
+    } else if (warp >= 12) {
+        // ---- 4-bit codes into e4m3 operands: one (row, 32-channel group) a step, its scale relative to the row's largest
+        const int w = tid - 384;
+        constexpr int GR = D / 32;
         for (int it = 0; it < n_tiles; ++it) {
             const int st = it % S, bf = it & 1;
             const uint8_t *src = base + (st0 - sm) + st * C::kStage;
-            uint8_t *vdst = base + (vf0 - sm) + bf * C::kVf;
             bool ok = wait(&full[st], (it / S) & 1, vfail, a.wait_ns);
-            if (it >= 2) {
-                if (BITS == 4) ok = ok && wait(&k_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
-            }
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            if constexpr (BITS == 8) {
-                if (it >= 2) ok = wait(&pv_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
-                if (!__all_sync(0xFFFFFFFFu, ok)) break;
-                constexpr int PPR = D / 16;  // 16-code pieces a row
-#pragma unroll
-                for (int i = 0; i < kTile * PPR / 128; ++i) {
-                    const int idx = w + 128 * i, row = idx / PPR, c = idx % PPR;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(src + C::kRaw + idx * 16);
-                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t o[8];
-                    // a code that is no number (slots never written) becomes one: weights of 0 stay 0
-                    const __half2 floor2 = __half2half2(__ushort_as_half(0xDF00));  // -448
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t h = e4m3x2_to_f16x2(vw[j / 2] >> (16 * (j & 1)));
-                        const __half2 m = __hmax2(*reinterpret_cast<const __half2 *>(&h), floor2);
-                        o[j] = *reinterpret_cast<const uint32_t *>(&m);
-                    }
-                    // channels 16 c .. of the row: 64-channel half, then 16-byte pieces 2 (c % 4), + 1
-                    uint8_t *line = vdst + (c >> 2) * (kTile * 128) + row * 128;
-                    const int e0 = ((2 * (c & 3)) ^ (row & 7)) << 4, e1 = ((2 * (c & 3) + 1) ^ (row & 7)) << 4;
-                    const uint4 x = make_uint4(o[0], o[1], o[2], o[3]), y = make_uint4(o[4], o[5], o[6], o[7]);
-                    // the halves' lanes store their pieces in opposite order: no bank twice
-                    const bool swap = c >= 4;
-                    *reinterpret_cast<uint4 *>(line + (swap ? e1 : e0)) = swap ? y : x;
-                    *reinterpret_cast<uint4 *>(line + (swap ? e0 : e1)) = swap ? x : y;
-                }
-            } else {
-                // one (row, 32-channel group) per step; the group's scale relative to the row's largest
-                constexpr int GR = D / 32;
 #pragma unroll 1
-                for (int which = 0; which < 2; ++which) {
-                    if (which == 1) {
-                        if (it >= 2) ok = wait(&pv_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
-                        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-                    }
+            for (int which = 0; which < 2; ++which) {
+                if (it >= 2) ok = ok && wait(which ? &pv_done[bf] : &k_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                uint8_t *dst = base + ((which ? v80 : k80) - sm) + bf * C::kOp;
 #pragma unroll 2
-                    for (int i = 0; i < GR; ++i) {
-                        const int idx = w + 128 * i, row = idx / GR, gq = idx % GR;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(src + which * C::kRaw + idx * 16);
-                        const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-                        const uint8_t *sc = src + 2 * C::kRaw + which * 512 + row * GR;
-                        uint32_t top = 0;
+                for (int i = 0; i < GR; ++i) {
+                    const int idx = w + 128 * i, row = idx / GR, gq = idx % GR;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(src + which * C::kRaw + idx * 16);
+                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+                    const uint8_t *sc = src + 2 * C::kRaw + which * 512 + row * GR;
+                    uint32_t top = 0;
 #pragma unroll
-                        for (int j = 0; j < GR; ++j) top = max(top, static_cast<uint32_t>(sc[j]));
-                        const int down = static_cast<int>(top) - sc[gq];
-                        if (which == 0) {
-                            const uint2 lv = k_levels(down);
-                            uint32_t o[8];
+                    for (int j = 0; j < GR; ++j) top = max(top, static_cast<uint32_t>(sc[j]));
+                    const uint2 lv = levels_of(static_cast<int>(top) - sc[gq]);
+                    uint32_t o[8];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t mg = vw[j] & 0x77777777u, sg = vw[j] & 0x88888888u;
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t mg = vw[j] & 0x77777777u, sg = vw[j] & 0x88888888u;
 #pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const uint32_t m = __byte_perm(lv.x, lv.y, mg >> (16 * k));
-                                    // 0xFF where the sign is set, 0x80 elsewhere: its low bit is the sign
-                                    uint32_t s;
-                                    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(s) : "r"(0x80u), "r"(sg >> (16 * k)));
-                                    o[2 * j + k] = m | ((s << 7) & 0x80808080u);
-                                }
-                            }
-                            uint8_t *kd = base + (k80 - sm) + bf * C::kK8;
-                            *reinterpret_cast<uint4 *>(kd + swizzle8<D>(row * D + gq * 32)) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4 *>(kd + swizzle8<D>(row * D + gq * 32 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
-                        } else {
-                            // fp16 values of the codes times 2^-down (below 2^-24: 0)
-                            const __half2 f = __half2half2(down > 24 ? __ushort_as_half(0) : __float2half_rn(__uint_as_float((127u - down) << 23)));
-                            uint8_t *line = vdst + (gq >> 1) * (kTile * 128) + row * 128;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t o[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const uint32_t h = e2m1x2_to_f16x2((vw[j] >> (8 * k)) & 0xFFu);
-                                    const __half2 m = __hmul2(*reinterpret_cast<const __half2 *>(&h), f);
-                                    o[k] = *reinterpret_cast<const uint32_t *>(&m);
-                                }
-                                *reinterpret_cast<uint4 *>(line + (((4 * (gq & 1) + j) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                            }
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t m = __byte_perm(lv.x, lv.y, mg >> (16 * k));
+                            // 0xFF where the sign is set, 0x80 elsewhere: its low bit is the sign
+                            uint32_t s;
+                            asm("prmt.b32 %0, %1, 0, %2;" : "=r"(s) : "r"(0x80u), "r"(sg >> (16 * k)));
+                            o[2 * j + k] = m | ((s << 7) & 0x80808080u);
                         }
                     }
-                    if (which == 0) {
-                        umma::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) umma::mbar_arrive(&k_full[bf]);
-                    }
+                    *reinterpret_cast<uint4 *>(dst + swizzle8<D>(row * D + gq * 32)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(dst + swizzle8<D>(row * D + gq * 32 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
-                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                umma::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(which ? &v_full[bf] : &k_full[bf]);
             }
-            umma::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                umma::mbar_arrive(&v_full[bf]);
-                umma::mbar_arrive(&empty[st]);
-            }
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (lane == 0) umma::mbar_arrive(&empty[st]);
         }
-    } else if (warp >= 8) {
+    } else if (warp >= 4) {
         // ---- softmax: thread = key (S^T's row), columns [c0, c0 + NC) --------------------------
-        const int wg = (warp - 8) >> 2, quad = warp & 3, r = quad * 32 + lane, c0 = wg * NC;
+        const int wg = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane, c0 = NSTR == 2 ? 0 : wg * NC;
+        const int own = NSTR == 2 ? wg : 0;  // the stream
         const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t t_own = t_o + t_lane + own * 3 * NB;
         Walk<NB> walk(a, pos0, pos1, b_at, f_at);
         Segment g;
         int it = 0;
         bool dead = false;
         while (!dead && walk.next(a, g)) {
-            // Q rows of this warpgroup's columns: two fp8 numbers a channel
+            // Q rows: two fp8 numbers a channel
             {
-                constexpr int LR = D / 8, RP = 128 / LR;  // lanes a row, rows a pass
+                constexpr int LR = D / 8, RP = 256 / LR;  // lanes a row, rows a pass
+                const int me = wg * 128 + r;
 #pragma unroll 1
-                for (int n = c0 + r / LR; n < c0 + NC; n += RP) {
+                for (int n = me / LR; n < NB; n += RP) {
                     const long long gi = static_cast<long long>(g.r) * NB + n;
                     const int tq = static_cast<int>(gi / a.grp), j = static_cast<int>(gi - static_cast<long long>(tq) * a.grp);
                     const bool live = tq < g.s.nq;
-                    const int ch = (r % LR) * 8;
+                    const int ch = (me % LR) * 8;
                     uint4 v = make_uint4(0, 0, 0, 0);
                     if (live)
                         v = *reinterpret_cast<const uint4 *>(a.q + (g.s.q0 + tq) * a.q_stride +
@@ -669,22 +678,23 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                         hi[i] = e4m3x2(f0, f1);
                         const uint32_t hh = e4m3x2_to_f16x2(hi[i]);
                         const float2 b2 = __half22float2(*reinterpret_cast<const __half2 *>(&hh));
-                        lo[i] = e4m3x2(f0 - b2.x, f1 - b2.y);
+                        lo[i] = e4m3x2((f0 - b2.x) * 16.0f, (f1 - b2.y) * 16.0f);
                         if (sb == 255u) hi[i] = 0x7F7Fu, lo[i] = 0;  // an infinity or a NaN: the row is NaN
                     }
-                    const uint32_t off = swizzle8<D>(n * D + ch);
-                    *reinterpret_cast<uint2 *>(base + (qh - sm) + off) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-                    *reinterpret_cast<uint2 *>(base + (ql - sm) + off) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-                    if (r % LR == 0) {
-                        reinterpret_cast<float *>(s_qs)[n] = sb == 255u ? 1.0f : scale_of(sb);
-                        reinterpret_cast<float *>(s_nm)[n] = 0.0f;
+                    const uint32_t oh = swizzle8<D>(n * D + ch), ol = swizzle8<D>((NB + n) * D + ch);
+                    *reinterpret_cast<uint2 *>(base + (q0 - sm) + oh) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                    *reinterpret_cast<uint2 *>(base + (q0 - sm) + ol) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                    if (me % LR == 0) {
+                        s_qs[n] = sb == 255u ? 1.0f : scale_of(sb);
+#pragma unroll
+                        for (int z = 0; z < NSTR; ++z) s_nm[z][n] = 0.0f;
                         s_tok[n] = live ? tq : 0;
                         s_row[n] = live ? static_cast<long long>(g.s.q0 + tq) * a.Hq + g.h * a.grp + j : -1;
                     }
                 }
             }
             umma::fence_proxy_async_smem();
-            wg_any(wg, false);
+            any_of(3, 256, false);
             if (lane == 0) umma::mbar_arrive(&q_full);
 
             uint64_t l2[NC / 2];
@@ -692,13 +702,14 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
             for (int i = 0; i < NC / 2; ++i) l2[i] = 0;
             const int hist = g.s.kv - g.s.nq;  // keys before the new tokens
             const int clear = a.mode == QVG_MASK_NONE ? g.s.kv : min(g.s.kv, hist);
+            int last = -1;  // this warpgroup's latest tile of the segment
             for (int t = g.t0; t < g.t1; ++t, ++it) {
                 const int st = it % S, bf = it & 1;
-                const bool first = t == g.t0;
+                if (NSTR == 2 && bf != wg) continue;
+                const bool first = last < 0;
                 bool ok = wait(&s_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
                 if (it >= 2) ok = ok && wait(&pv_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
-                // (the scales landed with the tile whose S is here, but through the async proxy: wait on their own barrier)
-                ok = ok && wait(&full[st], (it / S) & 1, vfail, a.wait_ns);
+                ok = ok && wait(&full[st], (it / S) & 1, vfail, a.wait_ns);  // (the scales: written by the async proxy)
                 umma::tc_fence_after();
                 const uint8_t *sc = base + (st0 - sm) + st * C::kStage + 2 * C::kRaw;
                 uint32_t kb = 0, vb = 0;
@@ -714,24 +725,33 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                 }
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive(&empty[st]);
-                // 4 bits: K's operand is 2^6 times the values over the largest scale
+                // 4 bits: the operands are 2^6 times the values over the largest scale
                 const float ka = scale_of(kb) * (BITS == 8 ? a.scale_log2 : a.scale_log2 * 0x1p-6f);
-                const float sv = scale_of(vb), lsv = static_cast<float>(static_cast<int>(vb) - 127);
+                const float sv = scale_of(vb) * (BITS == 8 ? 1.0f : 0x1p-6f);
+                const float lsv = static_cast<float>(static_cast<int>(vb) - (BITS == 8 ? 127 : 133));
                 const int key = t * kTile + r;
                 const bool part = (t + 1) * kTile > clear;
-                const uint64_t ka2 = pk2(ka, ka);
+                const uint64_t ka2 = pk2(ka, ka), lo2 = pk2(0.0625f, 0.0625f);
                 float y[NC];
                 // logits (base 2) less the reference; -inf where the row does not see the key
                 auto logits = [&]() {
 #pragma unroll
                     for (int c = 0; c < NC; c += 16) {
-                        uint32_t v[16];
-                        tmem_ld16(tmem + t_lane + bf * NB + c0 + c, v);
+                        uint32_t v[16], u[16];
+                        tmem_ld16x2(tmem + t_lane + bf * 2 * NB + c0 + c, tmem + t_lane + bf * 2 * NB + NB + c0 + c, v, u);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 qs = s_qs[(c0 + c) / 2 + i], nm = s_nm[(c0 + c) / 2 + i];
-                            const uint64_t x = mul2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ka2);
-                            up2(fma2(x, pk2(qs.x, qs.y), pk2(nm.x, nm.y)), y[c + 2 * i], y[c + 2 * i + 1]);
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 qs = *reinterpret_cast<const float4 *>(&s_qs[c0 + c + 4 * i]);
+                            const float4 nm = *reinterpret_cast<const float4 *>(&s_nm[own][c0 + c + 4 * i]);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int k = 4 * i + 2 * h;
+                                const uint64_t x = mul2(fma2(pk2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])), lo2,
+                                                             pk2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]))),
+                                                        ka2);
+                                up2(fma2(x, h ? pk2(qs.z, qs.w) : pk2(qs.x, qs.y), h ? pk2(nm.z, nm.w) : pk2(nm.x, nm.y)),
+                                    y[c + k], y[c + k + 1]);
+                            }
                         }
                     }
                     if (part) {
@@ -753,120 +773,173 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                 float top = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) top = fmaxf(top, y[c]);
-                if (wg_any(wg, first || !ok || top + lsv > kTop)) {
+                if (any_of(wg + 1, 128, first || !ok || top + lsv > kTop)) {
                     // set or raise references: the column maxima of w over the tile
                     float v[NC];
                     const float lw = fmaxf(lsv, -64.0f);
 #pragma unroll
                     for (int c = 0; c < NC; ++c) v[c] = y[c] + lw;
                     const float m = across_lanes<NC, true>(v);
-                    if (lane < NC) s_red[quad][c0 + lane] = m;
-                    if (!first) ok = ok && wait(&pv_done[bf ^ 1], ((it - 1) >> 1) & 1, vfail, a.wait_ns);
-                    dead = wg_any(wg, !ok);
+                    if (lane < NC) s_red[wg][quad][c0 + lane] = m;
+                    // (two streams: the last product into these sums is the one whose weights were here before)
+                    if (!first && NSTR == 1) ok = ok && wait(&pv_done[bf ^ 1], ((it - 1) >> 1) & 1, vfail, a.wait_ns);
+                    dead = any_of(wg + 1, 128, !ok);
                     if (dead) break;
                     umma::tc_fence_after();
                     if (r < NC) {
                         const int n = c0 + r;
-                        const float mx = fmaxf(fmaxf(s_red[0][n], s_red[1][n]), fmaxf(s_red[2][n], s_red[3][n]));
+                        const float mx = fmaxf(fmaxf(s_red[wg][0][n], s_red[wg][1][n]), fmaxf(s_red[wg][2][n], s_red[wg][3][n]));
                         const bool move = first ? mx > -INFINITY : mx > kTop;
                         const float d = move ? mx - kTarget : 0.0f;
-                        reinterpret_cast<float *>(s_nm)[n] -= d;
-                        s_dl[n] = ex2(-d);
+                        s_nm[own][n] -= d;
+                        s_dl[wg][n] = ex2(-d);
                     }
-                    wg_any(wg, false);
+                    any_of(wg + 1, 128, false);
                     if (!first) {
+#pragma unroll 1
+                        for (int z = 0; z < 3; ++z)
+#pragma unroll 1
+                            for (int c = 0; c < NC; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(t_own + z * NB + c0 + c, o);
 #pragma unroll
-                        for (int c = 0; c < NC; c += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(t_o + t_lane + c0 + c, o);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * s_dl[c0 + c + i]);
-                            umma::tmem_st16(t_o + t_lane + c0 + c, o);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                l2[c / 2 + i] = mul2(l2[c / 2 + i], pk2(s_dl[c0 + c + 2 * i], s_dl[c0 + c + 2 * i + 1]));
-                        }
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * s_dl[wg][c0 + c + i]);
+                                umma::tmem_st16(t_own + z * NB + c0 + c, o);
+                            }
                         umma::tmem_st_wait();
+#pragma unroll
+                        for (int i = 0; i < NC / 2; ++i)
+                            l2[i] = mul2(l2[i], pk2(s_dl[wg][c0 + 2 * i], s_dl[wg][c0 + 2 * i + 1]));
                     }
                     logits();
                 }
+                last = it;
                 umma::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive(&s_free[bf]);
+                // 8 bits: V's rows meet weights of 0 where a row does not see them, but 0 times a code that is no
+                // number would be one more NaN: slots past the end become 0, and so does such a code in the rows of
+                // the new tokens, which are the ones that a mask can hide (a slot that was never written)
+                if (BITS == 8 && part && (NSTR == 2 || wg == 0) && key >= hist) {
+                    uint4 *vr = reinterpret_cast<uint4 *>(base + (st0 - sm) + st * C::kStage + C::kRaw + r * D);
+#pragma unroll 1
+                    for (int i = 0; i < D / 16; ++i) {
+                        uint4 v = vr[i];
+                        uint32_t *w = &v.x;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t no = ((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes 0x7F, 0xFF
+                            w[j] = key < g.s.kv ? w[j] & ~((no >> 7) * 0xFFu) : 0u;
+                        }
+                        vr[i] = v;
+                    }
+                }
                 uint8_t *prow = base + (p0 - sm) + bf * C::kP + r * 128;
 #pragma unroll
-                for (int c = 0; c < NC; c += 8) {
-                    uint32_t w[4];
+                for (int c = 0; c < NC; c += 16) {
+                    uint32_t h[3][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float pa = ex2(y[c + 2 * i]), pb = ex2(y[c + 2 * i + 1]);
-                        l2[c / 2 + i] = add2(l2[c / 2 + i], pk2(pa, pb));
-                        float wa = pa * sv, wb = pb * sv;
-                        if (part) {  // an unseen key has weight 0 whatever its scale is
-                            wa = y[c + 2 * i] == -INFINITY ? 0.0f : wa;
-                            wb = y[c + 2 * i + 1] == -INFINITY ? 0.0f : wb;
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t w[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int e = c + 4 * k + 2 * i;
+                            const float pa = ex2(y[e]), pb = ex2(y[e + 1]);
+                            l2[e / 2] = add2(l2[e / 2], pk2(pa, pb));
+                            float wa = pa * sv, wb = pb * sv;
+                            if (part) {  // an unseen key has weight 0 whatever its scale is
+                                wa = y[e] == -INFINITY ? 0.0f : wa;
+                                wb = y[e + 1] == -INFINITY ? 0.0f : wb;
+                            }
+                            w[i] = f16x2(wa, wb);
                         }
-                        w[i] = f16x2(wa, wb);
+                        three_parts(w[0], w[1], h[0][k], h[1][k], h[2][k]);
                     }
-                    const int n = c0 + c;
-                    *reinterpret_cast<uint4 *>(prow + (n >> 6) * (kTile * 128) + ((((n >> 3) & 7) ^ (r & 7)) << 4)) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                    for (int z = 0; z < 3; ++z) {
+                        const int n = z * NB + c0 + c;
+                        *reinterpret_cast<uint4 *>(prow + (n >> 7) * (kTile * 128) + ((((n >> 4) & 7) ^ (r & 7)) << 4)) =
+                            make_uint4(h[z][0], h[z][1], h[z][2], h[z][3]);
+                    }
                 }
                 umma::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive(&p_full[bf]);
             }
-            if (dead) break;
-            // ---- the segment's sums ---------------------------------------------------------
-            const int last = it - 1;
-            const bool ok = wait(&pv_done[last & 1], (last >> 1) & 1, vfail, a.wait_ns);
+            // ---- the segment's sums (both warpgroups come here, also after a failure) ------------
+            bool ok = !dead;
+            if (ok && last >= 0) ok = wait(&pv_done[last & 1], (last >> 1) & 1, vfail, a.wait_ns);
             {
                 float v[NC];
 #pragma unroll
                 for (int i = 0; i < NC / 2; ++i) up2(l2[i], v[2 * i], v[2 * i + 1]);
                 const float s = across_lanes<NC, false>(v);
-                if (lane < NC) s_red[quad][c0 + lane] = s;
+                if (lane < NC) s_red[wg][quad][c0 + lane] = s;
             }
-            dead = wg_any(wg, !ok);
+            dead = any_of(3, 256, !ok);
             if (dead) break;
             umma::tc_fence_after();
             const int slot = cta * 2 + (g.t0 > 0 ? 0 : 1);
-            if (r < NC) {
-                const int n = c0 + r;
-                const float l = (s_red[0][n] + s_red[1][n]) + (s_red[2][n] + s_red[3][n]);
-                const float m = -reinterpret_cast<float *>(s_nm)[n];
-                if (g.whole()) {
-                    s_dl[n] = l == 0.0f ? 0.0f : 1.0f / l;
-                    const long long row = s_row[n];
-                    if (a.lse && row >= 0)
-                        a.lse[(row % a.Hq) * a.total_q + row / a.Hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-                } else {
-                    a.pm[static_cast<long long>(slot) * NB + n] = m;
-                    a.pl[static_cast<long long>(slot) * NB + n] = l;
+            const bool whole = g.whole();
+            if (wg == 0 && r < NB) {
+                float l[NSTR], m = -INFINITY, sum = 0.0f;
+#pragma unroll
+                for (int z = 0; z < NSTR; ++z) {
+                    const int w = NSTR == 2 ? z : (r >= NC ? 1 : 0);
+                    l[z] = (s_red[w][0][r] + s_red[w][1][r]) + (s_red[w][2][r] + s_red[w][3][r]);
+                    if (l[z] != 0.0f) m = fmaxf(m, -s_nm[z][r]);
+                }
+                float wt[NSTR];
+#pragma unroll
+                for (int z = 0; z < NSTR; ++z) {
+                    wt[z] = l[z] != 0.0f ? (NSTR == 2 ? ex2(-s_nm[z][r] - m) : 1.0f) : 0.0f;
+                    if (wt[z] != 0.0f) sum = fmaf(l[z], wt[z], sum);
+                }
+                const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                for (int z = 0; z < NSTR; ++z) s_wt[z][r] = wt[z] * inv;
+                const long long row = s_row[r];
+                if (!whole) {
+                    a.pm[static_cast<long long>(slot) * NB + r] = m;
+                    a.pl[static_cast<long long>(slot) * NB + r] = sum;
+                } else if (a.lse && row >= 0) {
+                    a.lse[(row % a.Hq) * a.total_q + row / a.Hq] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
                 }
             }
-            wg_any(wg, false);
+            any_of(3, 256, false);
 #pragma unroll 1
-            for (int c = 0; c < NC; c += 16) {
-                uint32_t o[16];
-                tmem_ld16(t_o + t_lane + c0 + c, o);
+            for (int c = wg * (NB / 2); c < (wg + 1) * (NB / 2); c += 8) {
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+#pragma unroll
+                for (int z = 0; z < NSTR; ++z) {
+                    uint32_t x[3][8];
+                    tmem_ld8x3(t_o + t_lane + z * 3 * NB + c, NB, x[0], x[1], x[2]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float w = s_wt[z][c + i];
+                        const float f = fmaf(__uint_as_float(x[2][i]), 0x1p-6f, fmaf(__uint_as_float(x[1][i]), 0x1p-3f, __uint_as_float(x[0][i])));
+                        if (w != 0.0f) o[i] = fmaf(f, w, o[i]);  // (a stream without a tile holds anything)
+                    }
+                }
                 if (r < D) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int n = c0 + c + i;
+                    for (int i = 0; i < 8; ++i) {
+                        const int n = c + i;
                         const long long row = s_row[n];
                         if (row < 0) continue;
-                        if (!g.whole())
-                            a.po[(static_cast<long long>(slot) * NB + n) * D + r] = __uint_as_float(o[i]);
+                        if (!whole)
+                            a.po[(static_cast<long long>(slot) * NB + n) * D + r] = o[i];
                         else if (a.out32)
-                            a.out32[row * D + r] = __uint_as_float(o[i]) * s_dl[n];
+                            a.out32[row * D + r] = o[i];
                         else
-                            a.out16[row * D + r] = f32_to_bf16(__uint_as_float(o[i]) * s_dl[n]);
+                            a.out16[row * D + r] = f32_to_bf16(o[i]);
                     }
                 }
             }
             umma::tc_fence_before();
-            wg_any(wg, false);  // s_row, s_dl and s_red have been read
+            any_of(3, 256, false);  // everything of this segment has been read
         }
     }
     __syncwarp();
@@ -877,7 +950,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
         // the copies in flight land before the CTA ends
         for (int j = max(0, s_issued - S); j < s_issued; ++j) umma::mbar_wait(&full[j % S], (j / S) & 1, kDrainNs);
     }
-    if (warp == 2) {
+    if (warp == 3) {
         umma::tc_fence_after();
         umma::tmem_dealloc(tmem, C::kTmem);
     }
