@@ -653,7 +653,7 @@ qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B,
  * numbers (exact for channels down to 2^-14 of the row's largest, off by at
  * most 2^-21 of the largest below), K and V as their codes; the weights times
  * V's scale enter as the sum of three fp8 numbers (off by at most 2^-9 of
- * themselves, or 2^-26 of the largest); all sums are fp32.  (4 bits: groups
+ * themselves, or 2^-25 of the largest); all sums are fp32.  (4 bits: groups
  * whose scale is below 2^-14 of their row's largest count as 0.)
  * A row of q
  * with an infinity or a NaN gives NaN.  The results do not depend on what

@@ -73,8 +73,9 @@ class Batch:
         (Q's fp8 pair; fp32 sums of 2 d products; the base-2 form's roundings
         of the logit), so a weight by 2 D + 2^-20 (2^x) of itself; a weight
         times V's scale by 2^-11 (fp16) and 2^-9 (three e5m2 parts) more or,
-        far below the largest, by 2^-27 of the largest, against codes up to
-        twice the largest's own; sums over the keys: L 2^-24."""
+        far below the largest, by 2^-25 of the largest (half of e5m2's smallest
+        step, 2^-17, against 2^8), against codes up to twice the largest's
+        own; sums over the keys: L 2^-24."""
         k_all, v_all = (x.transpose(0, 2, 1, 3).reshape(-1, self.H, self.d) for x in ref.held(self.cache))
         got, q = out.double().cpu().numpy(), self.q.double().cpu().numpy()
         got_lse = None if lse is None else lse.double().cpu().numpy()
@@ -101,7 +102,7 @@ class Batch:
                 dd = (dd + 8 * 2.0 ** -24 * np.abs(s)).max(-1, keepdims=True)
                 rel = 2 * dd + 2.0 ** -20 + 2.0 ** -11 + 2.0 ** -9 + len(js) * 2.0 ** -24
                 mean = ((p / den)[..., None] * np.abs(vv)).sum(1)
-                lost = len(js) * 2.0 ** -26 * np.abs((p / den)[..., None] * np.abs(vv).max(-1, keepdims=True)).max(1)
+                lost = len(js) * 2.0 ** -24 * np.abs((p / den)[..., None] * np.abs(vv).max(-1, keepdims=True)).max(1)
                 bound = rel * mean + lost + half * np.abs(want) + 1e-37
                 err = np.abs(row - want)
                 assert (err <= bound).all(), (b, t, float((err / bound).max()))

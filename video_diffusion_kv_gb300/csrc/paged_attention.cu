@@ -16,7 +16,9 @@ namespace {
 // The unit that begins in CTA i and goes on to CTA `last` left one partial
 // sum per CTA: slot 1 of CTA i, slot 0 of the others.  With references m_z,
 // sums l_z and O_z: m = max m_z, l = sum l_z 2^(m_z - m), O likewise.  One
-// warp per query row; parts in CTA order, so the result is the same each time.
+// warp per query row; lane z weighs part z, then the lanes share the channels
+// and go through the parts in CTA order (32 at a time, the loads of eight in
+// flight), so the result is the same each time.
 template <int D, int NB>
 __global__ void __launch_bounds__(256) k_paged_merge(const __grid_constant__ pa::Args a) {
     constexpr int E = D / 32;
@@ -29,22 +31,33 @@ __global__ void __launch_bounds__(256) k_paged_merge(const __grid_constant__ pa:
     const int tq = static_cast<int>(gi / a.grp), j = static_cast<int>(gi - static_cast<long long>(tq) * a.grp);
     if (tq >= s.nq) return;
     const int first = blockIdx.x, last = u.w;
+    auto at = [&](int z) { return static_cast<size_t>(2 * z + (z == first ? 1 : 0)) * NB + n; };
     float m = -INFINITY;
-    for (int z = first; z <= last; ++z) {
-        const size_t at = static_cast<size_t>(2 * z + (z == first ? 1 : 0)) * NB + n;
-        if (a.pl[at] != 0.0f) m = fmaxf(m, a.pm[at]);
-    }
+    for (int z = first + lane; z <= last; z += 32)
+        if (a.pl[at(z)] != 0.0f) m = fmaxf(m, a.pm[at(z)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     float acc[E], l = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int z = first; z <= last; ++z) {
-        const size_t at = static_cast<size_t>(2 * z + (z == first ? 1 : 0)) * NB + n;
-        const float lz = a.pl[at];
-        if (lz == 0.0f) continue;  // no key of this part is seen
-        const float w = exp2f(a.pm[at] - m);
-        l = fmaf(w, lz, l);
+    for (int z0 = first; z0 <= last; z0 += 32) {
+        const int z = z0 + lane;
+        float lz = z <= last ? a.pl[at(z)] : 0.0f;
+        const float w = lz == 0.0f ? 0.0f : exp2f(a.pm[at(z)] - m);  // 0: no key of this part is seen
+        lz *= w;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, a.po[at * D + lane * E + e], acc[e]);
+        for (int o = 16; o > 0; o >>= 1) lz += __shfl_xor_sync(0xFFFFFFFFu, lz, o);
+        l += lz;
+        const int parts = min(32, last - z0 + 1);
+#pragma unroll 8
+        for (int k = 0; k < parts; ++k) {
+            const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+            const float *o = a.po + at(z0 + k) * D + lane * E;
+            if (wk != 0.0f) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, o[e], acc[e]);
+            }
+        }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const long long row = static_cast<long long>(s.q0 + tq) * a.Hq + u.y * a.grp + j;
@@ -189,6 +202,7 @@ qvg_status qvg_paged_attention(const qvg_paged *cache, const void *q_bf16, int64
     if (out_dtype != QVG_OUT_F32 && out_dtype != QVG_OUT_BF16) return QVG_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return QVG_ERR_INVALID_ARG;
     if (!cu_q && static_cast<int64_t>(B) * max_q > total_q) return QVG_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(max_q) * (Hq / H) > INT32_MAX - 64) return QVG_ERR_UNSUPPORTED;
     if (B == 0 || max_q == 0 || total_q == 0) return QVG_OK;
     if (misaligned(q_bf16, 16) || misaligned(out, 16) || misaligned(table, 4) || misaligned(kv_len, 4) ||
         (cu_q && misaligned(cu_q, 4)) || (lse && misaligned(lse, 4)))

@@ -21,19 +21,21 @@
 // same 45 clocks whatever N is, so the extra columns are free there:
 //   - Q as two: hi + lo / 16 in e4m3 (4 significant bits each, a bf16 number
 //     has 8: exact while the channel is within 2^-14 of the row's largest);
-//   - P as three: h1 + h2 / 8 + h3 / 64 in e5m2, the first two cut off an
-//     fp16 number's upper byte (e5m2 is just that), the last rounded: at most
-//     2^-9 of the weight off, and fp16's range, which e4m3 lacks.
+//   - P as three: h1 + h2 + h3 in e5m2, which is the upper byte of an fp16
+//     number: the first two cut off, the last rounded: at most 2^-9 of the
+//     weight off, and nearly fp16's range, which e4m3 lacks.
 // A key's scale is one number per row of S^T, i.e. per softmax thread; V's
 // scale goes into the weight: w = p sv.
-// Softmax: a thread owns one key and NC columns.  The weights of a column are
-// taken relative to a reference that is set from the first tile (its largest
-// w becomes 2^kTarget) and raised when a w would pass 2^kTop, so the sums l
-// and O are rescaled rarely, and a tile needs one vote, no maximum across
-// threads.  A w of 2^-26 of the reference's largest still counts; l takes p in
-// fp32.
+// Softmax: a thread owns one key and 16 or 32 columns.  The weights of a column
+// are taken relative to a reference that is set from the first tile (its
+// largest w becomes 2^kTarget) and raised when a w would pass 2^kTop, so the
+// sums l and O are rescaled rarely, and a tile needs one vote, no maximum
+// across threads.  A w of 2^-25 of the reference's largest still counts; l
+// takes p in fp32.  The loop's code is kept small (one instance of each part):
+// with copies for the rare cases it outgrew the instruction cache and took
+// 1.5 times as long.
 // Up to 32 query rows, two softmax warpgroups take the tiles in turn, each
-// with its own reference and sums (two streams, joined at the unit's end);
+// with its own references and sums (two streams, joined at the unit's end);
 // with 64 rows they share every tile, 32 columns each.
 #pragma once
 
@@ -46,7 +48,7 @@ namespace qvg {
 namespace pa {
 
 constexpr int kTile = 128;
-constexpr float kTarget = 4.0f, kTop = 14.0f;  // a w up to 2^14: its remainders times 8 stay in fp16
+constexpr float kTarget = 8.0f, kTop = 15.0f;
 constexpr uint64_t kDrainNs = 2000000000ull;
 
 struct Args {
@@ -98,49 +100,27 @@ __device__ __forceinline__ Seq seq_of(const Args &a, int b, bool report) {
     int kv = a.kv_len[b];
     bad = bad || kv < 0 || kv > most;
     kv = static_cast<int>(max(0ll, min(static_cast<long long>(kv), most)));
-    if (report && bad) raise_error(a.err, QVG_ERR_INVALID_ARG);
     s.q0 = q0;
     s.nq = nq;
     s.kv = kv;
     s.nt = max(1, static_cast<int>((static_cast<long long>(kv) + kTile - 1) / kTile));
     s.rb = static_cast<int>((static_cast<long long>(nq) * a.grp + NB - 1) / NB);
+    bad = bad || s.tiles(a.H) > 0xFFFFFFFFll;
+    if (report && bad) raise_error(a.err, QVG_ERR_INVALID_ARG);
     return s;
 }
 
-// A stretch of one unit's tiles inside a CTA's part.
-struct Segment {
-    int b, h, r, t0, t1;
-    Seq s;
-    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == s.nt; }
+// A stretch [t0, t1) of one unit's tiles inside a CTA's part.  One warp of the
+// CTA makes them and hands them to the others through a ring in shared memory
+// (each role working them out for itself cost code that the instruction cache
+// then missed, 75 clocks an instruction the first time).
+struct __align__(16) Segment {
+    int b, h, r, t0, t1;  // t1 = 0: no more
+    int q0, nq, kv, nt;
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
 };
-
-template <int NB>
-struct Walk {
-    long long pos, end, first;  // first: the position where sequence b begins
-    int b;
-    Seq s;
-
-    __device__ __forceinline__ Walk(const Args &a, long long pos_, long long end_, int b_, long long first_)
-        : pos(pos_), end(end_), first(first_), b(b_), s(seq_of<NB>(a, b_, false)) {}
-
-    __device__ __forceinline__ bool next(const Args &a, Segment &g) {
-        if (pos >= end) return false;
-        while (pos >= first + s.tiles(a.H)) {
-            first += s.tiles(a.H);
-            s = seq_of<NB>(a, ++b, false);
-        }
-        const long long rel = pos - first;
-        const long long u = rel / s.nt;
-        g.b = b;
-        g.s = s;
-        g.h = static_cast<int>(u / s.rb);
-        g.r = static_cast<int>(u % s.rb);
-        g.t0 = static_cast<int>(rel - u * s.nt);
-        g.t1 = static_cast<int>(min(static_cast<long long>(s.nt), g.t0 + (end - pos)));
-        pos += g.t1 - g.t0;
-        return true;
-    }
-};
+constexpr int kRing = 8;  // segments ahead; a copy can run that far ahead in one-tile units
+constexpr int kChunks = 256;
 
 // ---- small pieces ---------------------------------------------------------------
 
@@ -192,8 +172,10 @@ __device__ __forceinline__ bool any_of(int id, int count, bool p) {
     return r != 0;
 }
 
-// Bounded wait that also ends when another role has failed.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *fail, uint64_t limit_ns) {
+// Bounded wait that also ends when another role has failed.  (Out of line but
+// for the first try: a tile's loop has many waits, and its code has to stay
+// small.)
+__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *fail, uint64_t limit_ns) {
     for (int i = 0; i < 32; ++i)
         if (umma::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = umma::globaltimer_ns();
@@ -206,6 +188,9 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
             return false;
         }
     }
+}
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *fail, uint64_t limit_ns) {
+    return umma::mbar_try_wait(bar, parity) || wait_on(bar, parity, fail, limit_ns);
 }
 
 // Contiguous global -> shared copy (16-byte aligned, a multiple of 16 bytes),
@@ -257,9 +242,9 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, 
         : "memory");
 }
 
-// Lane i receives 16 consecutive columns of TMEM lane (base + i), from each
-// of two places.
-__device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, uint32_t (&r)[16], uint32_t (&q)[16]) {
+// Lane i receives 16 consecutive columns of TMEM lane (base + i) from t and
+// from t + step.
+__device__ __forceinline__ void tmem_ld_pair(uint32_t t, uint32_t step, uint32_t (&r)[16], uint32_t (&q)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
@@ -270,7 +255,7 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t t0, uint32_t t1, uint32_t (
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(q[0]),
           "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]), "=r"(q[9]),
           "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15])
-        : "r"(t0), "r"(t1)
+        : "r"(t), "r"(t + step)
         : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t (&r)[16]) {
@@ -298,81 +283,82 @@ __device__ __forceinline__ void tmem_ld8x3(uint32_t t, uint32_t step, uint32_t (
         : "memory");
 }
 
-// Four weights (two fp16 pairs) -> their three e5m2 parts, four bytes each.
+// Four weights (two fp16 pairs, not negative) -> their three e5m2 parts, four
+// bytes each.  x less its upper byte is exact; adding half a step to the bits
+// of the last rest rounds its upper byte.
 __device__ __forceinline__ void three_parts(uint32_t a, uint32_t b, uint32_t &h1, uint32_t &h2, uint32_t &h3) {
-    const __half2 eight = __half2half2(__ushort_as_half(0x4800));  // 8
-    auto rest = [&](uint32_t x) {  // 8 (x - its upper byte): exact
+    auto rest = [](uint32_t x) {
         const uint32_t cut = x & 0xFF00FF00u;
-        const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&cut)), eight);
+        const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&cut));
         return *reinterpret_cast<const uint32_t *>(&d);
     };
     h1 = __byte_perm(a, b, 0x7531);
     a = rest(a);
     b = rest(b);
     h2 = __byte_perm(a, b, 0x7531);
-    a = rest(a);
-    b = rest(b);
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(a));
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(hi) : "r"(b));
-    h3 = static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
+    a = rest(a) + 0x00800080u;
+    b = rest(b) + 0x00800080u;
+    h3 = __byte_perm(a, b, 0x7531);
 }
 
-// Sum or maximum over the warp's lanes of each of W columns held by every
-// lane; lane i ends up with column i % W's.  W = 16 or 32.
-template <int W, bool MAX>
-__device__ __forceinline__ float across_lanes(float (&v)[W]) {
-    const int lane = threadIdx.x & 31;
-    if constexpr (W == 16) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float o = __shfl_xor_sync(0xFFFFFFFFu, v[i], 16);
-            v[i] = MAX ? fmaxf(v[i], o) : v[i] + o;
+// Position in a ring of N buffers and the parity of its current use.
+template <int N>
+struct Ring {
+    int i = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            parity ^= 1u;
         }
     }
-#pragma unroll
-    for (int s = W / 2; s > 0; s >>= 1) {
-        const bool up = lane & s;
-#pragma unroll
-        for (int i = 0; i < s; ++i) {
-            const float give = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
-            const float o = __shfl_xor_sync(0xFFFFFFFFu, give, s);
-            v[i] = MAX ? fmaxf(keep, o) : keep + o;
-        }
+};
+
+// Sum or maximum of each of NC columns over the warpgroup's 128 rows, in part:
+// scratch [128][NC] has been filled; thread r takes column r % NC of every
+// (128 / NC)-th row from r / NC on, into red[r / NC][r % NC].
+template <int NC, bool MAX>
+__device__ __forceinline__ void reduce_columns(const float *scratch, float (*red)[NC], int r) {
+    float x = MAX ? -INFINITY : 0.0f;
+#pragma unroll 4
+    for (int i = r / NC; i < 128; i += 128 / NC) {
+        const float v = scratch[i * NC + r % NC];
+        x = MAX ? fmaxf(x, v) : x + v;
     }
-    return v[0];
+    red[r / NC][r % NC] = x;
 }
 
 // ---- shared memory ---------------------------------------------------------------
 
 template <int D, int BITS, int NB>
 struct Cfg {
-    static constexpr int NSTR = NB <= 32 ? 2 : 1;   // streams (see above)
-    static constexpr int NC = NSTR == 2 ? NB : NB / 2;  // columns of a softmax thread
-    static constexpr int kParty = NSTR == 2 ? 4 : 8;    // softmax warps on one tile
+    static constexpr int NSTR = NB <= 32 ? 2 : 1;  // streams (see above)
+    static constexpr int NC = NB <= 32 ? NB : 32;   // columns of a softmax thread
+    static constexpr int kSoft = 2;                 // softmax warpgroups
+    static constexpr int kParty = 8 / NSTR;         // softmax warps on one tile
     static constexpr int G = BITS == 8 ? 1 : D / 32;
-    static constexpr int kRow = D * BITS / 8;         // bytes of a row of codes
-    static constexpr int kRaw = kTile * kRow;         // a tile's codes (K or V)
-    static constexpr int kStage = 2 * kRaw + 1024;    // K, V, their scales
-    static constexpr int kOp = BITS == 4 ? kTile * D : 0;  // K or V as e4m3 (4 bits), two buffers each
+    static constexpr int kRow = D * BITS / 8;       // bytes of a row of codes
+    static constexpr int kRaw = kTile * kRow;       // a tile's codes (K or V)
+    static constexpr int kOp = BITS == 4 ? kTile * D : 0;   // K or V as e4m3 (4 bits), two buffers each
     static constexpr int kP = 16384 * ((3 * NB + 127) / 128);  // weights, two buffers
-    static constexpr int kQ = 2 * NB * D;             // Q: hi rows, lo rows
-    static constexpr int kFixed = 4 * kOp + 2 * kP + kQ;
-    static constexpr int kMaxStages = (225 * 1024 - 6144 - kFixed) / kStage;
-    static constexpr int kStages = kMaxStages > 8 ? 8 : kMaxStages;
-    static constexpr int kSmem = kFixed + kStages * kStage + 1024;
-    static constexpr int kConv = BITS == 4 ? 4 : 0;   // converter warps
-    static constexpr int kWarps = 12 + kConv;         // loads, S, PV, TMEM; softmax 4 - 11; converters
+    static constexpr int kQ = 2 * NB * D;           // Q: hi rows, lo rows; two buffers
+    static constexpr int kFixed = 4 * kOp + 2 * kP + 2 * kQ;
+    static constexpr int kVSlot = kRaw + 1024;      // V's codes, K's and V's scales
+    // K's and V's copies in flight: a K buffer is free once S is there, a V buffer once O has it
+    static constexpr int kSlots = (224 * 1024 - 8192 - kFixed - 8 * 1024) / kRaw;
+    static constexpr int kSK = kSlots / 2 > 6 ? 6 : kSlots / 2, kSV = kSlots - kSK > 8 ? 8 : kSlots - kSK;
+    static constexpr int kSmem = kFixed + kSK * kRaw + kSV * kVSlot + 1024;
+    static constexpr int kWarps = 16;  // K's loads, S, PV, segments (4 bits: and Q); softmax 4 - 11; 12 V's loads, 13 - 15 Q, or (4 bits) converters
+    static constexpr int kQWarps = BITS == 8 ? 3 : 1;
     static constexpr int kTmemUsed = 2 * 2 * NB + NSTR * 3 * NB;
     static constexpr int kTmem = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-    static_assert(kStages >= 3, "shared memory");
+    static_assert(kSK >= 3 && kSV >= 3, "shared memory");
 };
 
 // e2m1 magnitudes times 2^(6 - k) as e4m3 bytes, for a group whose scale is
 // 2^-k of the row's largest (k <= 14; beyond, the values are under 2^-9 and
 // count as 0), eight bytes: the operands of a 4-bit cache.
 __device__ __forceinline__ uint2 levels_of(int k) {
-    // magnitude 2^e m: byte (e + 7) << 3 | mantissa, subnormal below 2^-6
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
@@ -383,96 +369,234 @@ __device__ __forceinline__ uint2 levels_of(int k) {
     return make_uint2(w[0], w[1]);
 }
 
+// ---- what a softmax warp does rarely, out of its loop's code -----------------------
+
+// Logits of 16 columns, base 2, less the reference.
+__device__ __forceinline__ void logits16(uint32_t t_hi, uint32_t t_lo, const float *qs, const float *nm, float ka, float (&y)[16]) {
+    uint32_t v[16], u[16];
+    tmem_ld16(t_hi, v);
+    tmem_ld16(t_lo, u);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        y[i] = fmaf(fmaf(__uint_as_float(u[i]), 0.0625f, __uint_as_float(v[i])) * ka, qs[i], nm[i]);
+}
+
+// The rows (columns of S) that do not see this thread's key: their logits
+// become -inf in tensor memory.  Returns them as bits.
+//   t_s: S's column c0 (hi; lo is `lo` columns on); tok: the rows' new tokens;
+// mw: room for the tile's mask words; j: the key's number among the new
+// tokens; w0: the first mask word that the tile needs.
+template <int NC>
+__device__ __noinline__ uint32_t hide_keys(const Args &a, uint32_t t_s, uint32_t lo, const int *tok, uint32_t (*mw)[5], int wg,
+                                           int r, int q0, int key, int kv, int j, int w0) {
+    if (a.mode == QVG_MASK_TREE) {
+        for (int i = r; i < NC * 5; i += 128) {
+            const int c = i / 5, k = w0 + i % 5;
+            mw[c][i % 5] = k < a.words ? a.mask[static_cast<long long>(q0 + tok[c]) * a.words + k] : 0u;
+        }
+        any_of(wg + 1, 128, false);
+    }
+    uint32_t hidden = 0;
+#pragma unroll 1
+    for (int c = 0; c < NC; ++c) {
+        bool see = key < kv;
+        if (see && j >= 0) {
+            if (a.mode == QVG_MASK_CAUSAL) see = j <= tok[c];
+            if (a.mode == QVG_MASK_TREE) see = (mw[c][(j >> 5) - w0] >> (j & 31)) & 1u;
+        }
+        if (__any_sync(0xFFFFFFFFu, !see)) {
+            uint32_t v, u;
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%2];\n\t"
+                "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%3];\n\t"
+                "tcgen05.wait::ld.sync.aligned;"
+                : "=r"(v), "=r"(u)
+                : "r"(t_s + c), "r"(t_s + lo + c)
+                : "memory");
+            v = see ? v : 0xFF800000u;
+            u = see ? u : 0u;
+            asm volatile(
+                "tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%2};\n\t"
+                "tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%3};" ::"r"(t_s + c),
+                "r"(t_s + lo + c), "r"(v), "r"(u)
+                : "memory");
+        }
+        hidden |= (see ? 0u : 1u) << c;
+    }
+    umma::tmem_st_wait();
+    return hidden;
+}
+
+// V's rows meet weights of 0 where a row does not see them, but 0 times a code
+// that is no number would be one more NaN: slots past the end become 0, and so
+// does such a code in the rows of the new tokens, which are the ones that a
+// mask can hide (a slot that was never written).
+// Thread r of 128 takes every 128th 16 bytes from row `from` on; rows from
+// `past` on are past the end.
+template <int D>
+__device__ __noinline__ void clean_values(uint8_t *v, int from, int past, int r) {
+#pragma unroll 1
+    for (int i = from * (D / 16) + r; i < kTile * (D / 16); i += 128) {
+        uint4 x = reinterpret_cast<uint4 *>(v)[i];
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t no = ((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes 0x7F, 0xFF
+            w[j] = i >= past * (D / 16) ? 0u : w[j] & ~((no >> 7) * 0xFFu);
+        }
+        reinterpret_cast<uint4 *>(v)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Set (first) or raise the references of this warpgroup's columns after the
+// tile's logits: from the columns' largest w over the tile.  O's sums follow;
+// dl gets the factors for l.  False: some thread has given up.
+template <int NC, int NB>
+__device__ __noinline__ bool set_references(uint32_t t_s, uint32_t t_own, const float *qs, float *nm, float *scratch, float (*red)[NC],
+                                            float *dl, int wg, int r, float ka, float lsv, bool first, bool ok) {
+    const float lw = fmaxf(lsv, -64.0f);
+#pragma unroll 1
+    for (int c = 0; c < NC; c += 16) {
+        float y[16];
+        logits16(t_s + c, t_s + NB + c, qs + c, nm + c, ka, y);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4 *>(scratch + r * NC + c + i) = make_float4(y[i] + lw, y[i + 1] + lw, y[i + 2] + lw, y[i + 3] + lw);
+    }
+    if (any_of(wg + 1, 128, !ok)) return false;
+    reduce_columns<NC, true>(scratch, red, r);
+    any_of(wg + 1, 128, false);
+    umma::tc_fence_after();
+    if (r < NC) {
+        float mx = -INFINITY;
+        for (int i = 0; i < 128 / NC; ++i) mx = fmaxf(mx, red[i][r]);
+        const bool move = first ? mx > -INFINITY : mx > kTop;
+        const float d = move ? mx - kTarget : 0.0f;
+        nm[r] -= d;
+        dl[r] = ex2(-d);
+    }
+    any_of(wg + 1, 128, false);
+    if (!first) {
+#pragma unroll 1
+        for (int z = 0; z < 3 * (NC / 16); ++z) {
+            const int c = (z / 3) * 16;
+            uint32_t o[16];
+            tmem_ld16(t_own + (z % 3) * NB + c, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * dl[c + i]);
+            umma::tmem_st16(t_own + (z % 3) * NB + c, o);
+        }
+        umma::tmem_st_wait();
+    }
+    return true;
+}
+
+// Q rows n0, n0 + step, .. of a unit (step rows at a time are a warp's share)
+// as pairs of fp8 numbers into dst, with their scales, tokens and out rows.
+template <int D, int NB>
+__device__ __noinline__ void make_q(const Args &a, const Segment &g, uint8_t *dst, float *qs, int *tok, long long *rows, int n0, int step) {
+    constexpr int LR = D / 8;  // lanes a row; 32 / LR rows a pass
+    const int lane = threadIdx.x & 31, ch = (lane % LR) * 8;
+    auto fetch = [&](int n, int &tq, int &j) {
+        const uint32_t gi = static_cast<uint32_t>(g.r) * NB + n;  // (the call has made sure that it fits)
+        tq = static_cast<int>(gi / static_cast<uint32_t>(a.grp));
+        j = static_cast<int>(gi) - tq * a.grp;
+        if (n >= NB || tq >= g.nq) return make_uint4(0, 0, 0, 0);
+        return *reinterpret_cast<const uint4 *>(a.q + (g.q0 + tq) * a.q_stride + static_cast<long long>(g.h * a.grp + j) * D + ch);
+    };
+    int n = n0 + lane / LR, tq, j, tq1, j1, tq2, j2;
+    uint4 v = fetch(n, tq, j), v1 = fetch(n + step, tq1, j1), v2;
+#pragma unroll 1
+    for (; n < NB; n += step, v = v1, tq = tq1, j = j1, v1 = v2, tq1 = tq2, j1 = j2) {
+        v2 = fetch(n + 2 * step, tq2, j2);  // two passes ahead
+        const bool live = tq < g.nq;
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, x[i] & 0x7FFF7FFFu);
+        uint32_t amax = max(m2 & 0xFFFFu, m2 >> 16);
+#pragma unroll
+        for (int o = 1; o < LR; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        const uint32_t sb = scale_byte<8>(amax);
+        const float inv = sb == 255u ? 0.0f : scale_inverse(sb);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f0 = __uint_as_float(x[i] << 16) * inv, f1 = __uint_as_float(x[i] & 0xFFFF0000u) * inv;
+            hi[i] = e4m3x2(f0, f1);
+            const uint32_t hh = e4m3x2_to_f16x2(hi[i]);
+            const float2 b2 = __half22float2(*reinterpret_cast<const __half2 *>(&hh));
+            lo[i] = e4m3x2((f0 - b2.x) * 16.0f, (f1 - b2.y) * 16.0f);
+            if (sb == 255u) hi[i] = 0x7F7Fu, lo[i] = 0;  // an infinity or a NaN: the row is NaN
+        }
+        const uint32_t oh = swizzle8<D>(n * D + ch), ol = swizzle8<D>((NB + n) * D + ch);
+        *reinterpret_cast<uint2 *>(dst + oh) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+        *reinterpret_cast<uint2 *>(dst + ol) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        if (lane % LR == 0) {
+            qs[n] = sb == 255u ? 1.0f : scale_of(sb);
+            tok[n] = live ? tq : 0;
+            rows[n] = live ? static_cast<long long>(g.q0 + tq) * a.Hq + g.h * a.grp + j : -1;
+        }
+    }
+    umma::fence_proxy_async_smem();
+    __syncwarp();
+}
+
 template <int D, int BITS, int NB>
 __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
     k_paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ Args a) {
     using C = Cfg<D, BITS, NB>;
-    constexpr int S = C::kStages, NSTR = C::NSTR, NC = C::NC;
+    constexpr int SK = C::kSK, SV = C::kSV, NSTR = C::NSTR, NC = C::NC;
     extern __shared__ uint8_t dyn[];
-    __shared__ uint64_t full[S], empty[S], s_full[2], s_free[2], p_full[2], v_full[2], k_full[2], k_done[2], pv_done[2],
-        q_full, drain, never;
+    __shared__ uint64_t k_full[SK], k_empty[SK], v_full[SV], v_empty[SV];  // codes (and scales, with V's) as loaded
+    __shared__ uint64_t ko_full[2], ko_done[2], vo_full[2];                // 4 bits: operands made of them
+    __shared__ uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full[2], q_free[2], drain, never;
     __shared__ uint32_t tmem_base;
-    __shared__ int fail, s_issued;
-    __shared__ __align__(16) float s_qs[NB], s_nm[NSTR][NB];  // per column: Q's scale, minus the reference
-    __shared__ __align__(16) float s_red[2][4][NB], s_dl[2][NB], s_l[NSTR][NB], s_wt[NSTR][NB];
-    __shared__ int s_tok[NB];        // new token of each row
-    __shared__ long long s_row[NB];  // out row, or -1
-    __shared__ long long s_scan[C::kWarps], s_at[4];
+    __shared__ int fail, s_issued[2];
+    __shared__ __align__(16) float s_qs[2][NB], s_nm[NSTR][NB];  // per column: Q's scale, minus the reference
+    __shared__ __align__(16) float s_red[C::kSoft][128 / NC][NC], s_dl[C::kSoft][NC], s_wt[NSTR][NB];
+    __shared__ int s_tok[2][NB];        // new token of each row
+    __shared__ long long s_row[2][NB];  // out row, or -1
+    __shared__ uint32_t s_mw[C::kSoft][NC][5];  // the mask words of a tile's new tokens
+    __shared__ uint2 s_lv[BITS == 4 ? 16 : 1];
+    __shared__ Segment s_seg[kRing];
+    __shared__ uint64_t seg_full[kRing], seg_free[kRing];
+    __shared__ long long s_chunk[kChunks];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x;
 
-    // ---- this CTA's part of the line ------------------------------------------------
-    long long total = 0;
-    {
-        long long mine = 0;
-        for (int b = tid; b < a.B; b += C::kWarps * 32) mine += seq_of<NB>(a, b, cta == 0).tiles(a.H);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-        if (lane == 0) s_scan[warp] = mine;
-        if (tid == 0) fail = 0;
-        __syncthreads();
-        for (int w = 0; w < C::kWarps; ++w) total += s_scan[w];
-        __syncthreads();
-    }
-    const long long per = max(1ll, (total + gridDim.x - 1) / gridDim.x);
-    const long long pos0 = min(total, cta * per), pos1 = min(total, pos0 + per);
-    if (tid == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
-    if (pos0 >= pos1) return;
-    {
-        long long before = 0;  // tiles of the sequences before this round's
-        for (int b0 = 0; b0 < a.B; b0 += C::kWarps * 32) {
-            const int b = b0 + tid;
-            const long long w = b < a.B ? seq_of<NB>(a, b, false).tiles(a.H) : 0;
-            long long x = w;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-                if (lane >= o) x += y;
-            }
-            if (lane == 31) s_scan[warp] = x;
-            __syncthreads();
-            long long f = before + x - w;
-            for (int v = 0; v < C::kWarps; ++v) {
-                if (v < warp) f += s_scan[v];
-                before += s_scan[v];
-            }
-            if (w > 0 && pos0 >= f && pos0 < f + w) s_at[0] = b, s_at[1] = f;
-            if (w > 0 && pos1 - 1 >= f && pos1 - 1 < f + w) s_at[2] = b, s_at[3] = f;
-            __syncthreads();
-        }
-    }
-    const int b_at = static_cast<int>(s_at[0]);
-    const long long f_at = s_at[1];
-    if (tid == 0) {
-        // the unit at the part's end: if it begins here and goes on, the CTAs that share it
-        const int b = static_cast<int>(s_at[2]);
-        const Seq s = seq_of<NB>(a, b, false);
-        const long long u = (pos1 - 1 - s_at[3]) / s.nt;
-        const long long u0 = s_at[3] + u * s.nt, u1 = u0 + s.nt;
-        if (u0 >= pos0 && u1 > pos1)
-            a.desc[cta] = make_int4(b, static_cast<int>(u / s.rb), static_cast<int>(u % s.rb), static_cast<int>((u1 - 1) / per));
-    }
-
     uint8_t *base = dyn + ((1024u - (umma::smem_u32(dyn) & 1023u)) & 1023u);
     const uint32_t sm = umma::smem_u32(base);
-    const uint32_t p0 = sm, k80 = p0 + 2 * C::kP, v80 = k80 + 2 * C::kOp, q0 = v80 + 2 * C::kOp, st0 = q0 + C::kQ;
+    const uint32_t p0 = sm, k80 = p0 + 2 * C::kP, v80 = k80 + 2 * C::kOp, q0 = v80 + 2 * C::kOp, kr0 = q0 + 2 * C::kQ,
+                   vr0 = kr0 + SK * C::kRaw;
     if (tid == 0) {
-        for (int i = 0; i < S; ++i) {
-            umma::mbar_init(&full[i], 1);
-            umma::mbar_init(&empty[i], (BITS == 8 ? 2 : 4) + C::kParty);  // products (or converters) done, scales read
+        fail = 0;
+        s_issued[0] = s_issued[1] = 0;
+        for (int i = 0; i < kRing; ++i) {
+            umma::mbar_init(&seg_full[i], 1);
+            umma::mbar_init(&seg_free[i], 15);  // every other warp
+        }
+        for (int i = 0; i < SK; ++i) {
+            umma::mbar_init(&k_full[i], 1);
+            umma::mbar_init(&k_empty[i], BITS == 8 ? 1 : 2);  // S done, or the converters
+        }
+        for (int i = 0; i < SV; ++i) {
+            umma::mbar_init(&v_full[i], 33);  // the codes; each lane's part of the scales
+            umma::mbar_init(&v_empty[i], (BITS == 8 ? 1 : 4) + C::kParty);  // O done, or the converters; scales read
         }
         for (int i = 0; i < 2; ++i) {
+            umma::mbar_init(&ko_full[i], 2);
+            umma::mbar_init(&vo_full[i], 2);
+            umma::mbar_init(&ko_done[i], 1);
             umma::mbar_init(&s_full[i], 1);
             umma::mbar_init(&s_free[i], C::kParty);
             umma::mbar_init(&p_full[i], C::kParty);
-            umma::mbar_init(&v_full[i], 4);
-            umma::mbar_init(&k_full[i], 4);
-            umma::mbar_init(&k_done[i], 1);
             umma::mbar_init(&pv_done[i], 1);
+            umma::mbar_init(&q_full[i], C::kQWarps);
+            umma::mbar_init(&q_free[i], 1 + 4 * C::kSoft);  // S done, softmax warps done
         }
-        umma::mbar_init(&q_full, 8);
         umma::mbar_init(&drain, 2);
         umma::mbar_init(&never, 1);
         umma::fence_barrier_init();
@@ -481,237 +605,95 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
         umma::tmem_alloc(&tmem_base, C::kTmem);
         umma::tmem_relinquish();
     }
+    for (int i = tid; i < NSTR * NB; i += C::kWarps * 32) (&s_nm[0][0])[i] = 0.0f;
+    if (BITS == 4 && tid < 16) s_lv[tid] = levels_of(tid);
     __syncthreads();
     umma::tc_fence_after();
     const uint32_t tmem = tmem_base;
     const uint32_t t_o = tmem + 4 * NB;  // S: two buffers of 2 NB columns; O: 3 NB per stream
     volatile int *vfail = &fail;
-    const int n_tiles = static_cast<int>(pos1 - pos0);
-
-    if (warp == 0) {
-        // ---- loads: lane i fetches the tile's i-th piece (a page, or 128 tokens of one) ----
+    // The next segment for this warp (n of them so far); false: no more, or gave up.
+    auto next_segment = [&](Segment &g, int n) {
+        const int i = n & (kRing - 1);
+        const bool ok = wait(&seg_full[i], (n / kRing) & 1, vfail, a.wait_ns);
+        g = s_seg[i];
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&seg_free[i]);
+        return __all_sync(0xFFFFFFFFu, ok) && g.t1 > 0;
+    };
+    // One tile's K or V, by a whole warp: lane i fetches the tile's i-th piece (a page, or 128 tokens of one).
+    // Issuing a copy takes a warp about 90 clocks, so K and V have a warp each where they can, and the scales, 16
+    // bytes at a time, go by plain asynchronous copies of all lanes.  Waits for the buffer; false: gave up.
+    auto load_tile = [&](const Segment &g, int t, bool is_k, uint64_t *full, uint64_t *empty, uint32_t dst, uint32_t parity, bool used) {
         const int pr_log2 = min(a.page_log2, 7), pr = 1 << pr_log2;
-        const int pieces = kTile >> pr_log2;
-        Walk<NB> walk(a, pos0, pos1, b_at, f_at);
-        Segment g;
-        int it = 0;
-        bool ok = true;
-        while (ok && walk.next(a, g)) {
-            const int32_t *row = a.table + g.b * a.table_stride;
-            for (int t = g.t0; t < g.t1; ++t, ++it) {
-                const int tok = t * kTile + (lane << pr_log2);
-                const bool there = lane < pieces && tok < g.s.kv;
-                const int page = there ? row[tok >> a.page_log2] : 0;
-                const bool good = there && page >= 0 && page < a.num_pages;
-                if (there && !good) raise_error(a.err, QVG_ERR_INVALID_ARG);
-                const int st = it % S;
-                if (it >= S) ok = wait(&empty[st], ((it / S) - 1) & 1, vfail, a.wait_ns);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
-                if (lane == 0) umma::mbar_arrive_expect_tx(&full[st], n * 2u * (C::kRow + C::G) * pr);
-                __syncwarp();
-                if (good) {
-                    const uint32_t dst = st0 + st * C::kStage;
-                    const int off = tok & ((1 << a.page_log2) - 1);
-                    const size_t at = ((static_cast<size_t>(page) * a.H + g.h) << a.page_log2) + off;  // first row
-                    if constexpr (BITS == 8) {
-                        tma_load_4d(dst + lane * pr * C::kRow, &kmap, off, g.h, page, &full[st]);
-                        tma_load_4d(dst + C::kRaw + lane * pr * C::kRow, &vmap, off, g.h, page, &full[st]);
-                    } else {
-                        bulk_copy(dst + lane * pr * C::kRow, a.kc + at * C::kRow, pr * C::kRow, &full[st]);
-                        bulk_copy(dst + C::kRaw + lane * pr * C::kRow, a.vc + at * C::kRow, pr * C::kRow, &full[st]);
-                    }
-                    bulk_copy(dst + 2 * C::kRaw + lane * pr * C::G, a.ks + at * C::G, pr * C::G, &full[st]);
-                    bulk_copy(dst + 2 * C::kRaw + 512 + lane * pr * C::G, a.vs + at * C::G, pr * C::G, &full[st]);
-                }
-                __syncwarp();
-            }
+        const int tok = t * kTile + (lane << pr_log2);
+        const bool there = lane < (kTile >> pr_log2) && tok < g.kv;
+        const int page = there ? a.table[g.b * a.table_stride + (tok >> a.page_log2)] : 0;
+        const bool good = there && page >= 0 && page < a.num_pages;
+        if (there && !good) raise_error(a.err, QVG_ERR_INVALID_ARG);
+        const int off = tok & ((1 << a.page_log2) - 1);
+        const long long at = good ? ((static_cast<long long>(page) * a.H + g.h) << a.page_log2) + off : -1;  // first row
+        const bool ok = !used || wait(empty, parity ^ 1u, vfail, a.wait_ns);
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+        const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
+        if (lane == 0) umma::mbar_arrive_expect_tx(full, n * C::kRow * pr);
+        __syncwarp();
+        if (good) {
+            if constexpr (BITS == 8)
+                tma_load_4d(dst + lane * pr * C::kRow, is_k ? &kmap : &vmap, off, g.h, page, full);
+            else
+                bulk_copy(dst + lane * pr * C::kRow, (is_k ? a.kc : a.vc) + at * C::kRow, pr * C::kRow, full);
         }
-        if (lane == 0) s_issued = it;
-    } else if (warp == 1) {
-        // ---- S = K Q^T -------------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t id = idesc_f8(128, 2 * NB, 0);
-            const uint64_t dq = desc_rows8<D>(q0);
-            Walk<NB> walk(a, pos0, pos1, b_at, f_at);
-            Segment g;
-            int it = 0, n_seg = 0;
-            bool ok = true;
-            while (ok && walk.next(a, g)) {
-                ok = wait(&q_full, n_seg & 1, vfail, a.wait_ns);
-                ++n_seg;
-                for (int t = g.t0; ok && t < g.t1; ++t, ++it) {
-                    const int st = it % S, bf = it & 1;
-                    ok = BITS == 8 ? wait(&full[st], (it / S) & 1, vfail, a.wait_ns)
-                                   : wait(&k_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
-                    if (it >= 2) ok = ok && wait(&s_free[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
-                    if (!ok) break;
-                    umma::tc_fence_after();
-                    const uint64_t dk = desc_rows8<D>(BITS == 8 ? st0 + st * C::kStage : k80 + bf * C::kOp);
+        __syncwarp();
+        if (!is_k) {
+            // the scales: 128 G bytes each of K's and V's, in 16-byte parts
 #pragma unroll
-                    for (int s = 0; s < D / 32; ++s) mma_f8(tmem + bf * 2 * NB, dk + 2 * s, dq + 2 * s, id, s != 0);
-                    umma::mma_commit(&s_full[bf]);
-                    umma::mma_commit(BITS == 8 ? &empty[st] : &k_done[bf]);
-                    // test hook: with S in flight, wait for what never comes
-                    if (it == 0 && a.inject) ok = wait(&never, 0, vfail, a.wait_ns);
+            for (int i0 = 0; i0 < 16 * C::G; i0 += 32) {
+                const int i = i0 + lane;
+                const bool v = i >= 8 * C::G;
+                const int c = v ? i - 8 * C::G : i, first = c * (16 / C::G);  // part c begins with this key's
+                const long long piece_at = __shfl_sync(0xFFFFFFFFu, at, (first >> pr_log2) & 31);
+                if (i < 16 * C::G && piece_at >= 0) {
+                    const uint8_t *from = (v ? a.vs : a.ks) + (piece_at + (first & (pr - 1))) * C::G;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst + C::kRaw + (v ? 512 : 0) + c * 16), "l"(from)
+                                 : "memory");
                 }
             }
-            umma::mma_commit(&drain);
+            umma::cp_async_arrive_noinc(full);
         }
-    } else if (warp == 2) {
-        // ---- O += V^T P^T (its own warp: starting a batch of products takes longer than the batch) ----
-        if (lane == 0) {
-            constexpr uint32_t id = idesc_f8(128, 3 * NB, 1) | (1u << 15) | (1u << 16);  // both MN-major
-            Walk<NB> walk(a, pos0, pos1, b_at, f_at);
-            Segment g;
-            int it = 0;
-            bool ok = true;
-            while (ok && walk.next(a, g)) {
-                for (int t = g.t0; ok && t < g.t1; ++t, ++it) {
-                    const int st = it % S, bf = it & 1;
-                    // (4 bits: the stage itself may be in its next use by now)
-                    ok = BITS == 8 ? wait(&full[st], (it / S) & 1, vfail, a.wait_ns)
-                                   : wait(&v_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
-                    ok = ok && wait(&p_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
-                    if (!ok) break;
-                    umma::tc_fence_after();
-                    // d = 64: the accumulator's upper 64 rows repeat the lower ones and are not read
-                    const uint64_t dv = desc_rows8<D>(BITS == 8 ? st0 + st * C::kStage + C::kRaw : v80 + bf * C::kOp);
-                    const uint64_t dp = desc_rows8<128>(p0 + bf * C::kP, kTile * 128);
-                    const bool fresh = t - g.t0 < NSTR;  // the stream's first tile of the unit
-#pragma unroll
-                    for (int s = 0; s < kTile / 32; ++s)
-                        mma_f8(t_o + (NSTR == 2 ? bf * 3 * NB : 0), dv + s * (32 * D / 16), dp + s * 256, id, !(fresh && s == 0));
-                    umma::mma_commit(&pv_done[bf]);
-                    if (BITS == 8) umma::mma_commit(&empty[st]);
-                }
-            }
-            // all products issued, S's too, complete before TMEM goes back
-            umma::mma_commit(&drain);
-            umma::mbar_wait(&drain, 0, kDrainNs);
-        }
-    } else if (warp >= 12) {
-        // ---- 4-bit codes into e4m3 operands: one (row, 32-channel group) a step, its scale relative to the row's largest
-        const int w = tid - 384;
-        constexpr int GR = D / 32;
-        for (int it = 0; it < n_tiles; ++it) {
-            const int st = it % S, bf = it & 1;
-            const uint8_t *src = base + (st0 - sm) + st * C::kStage;
-            bool ok = wait(&full[st], (it / S) & 1, vfail, a.wait_ns);
-#pragma unroll 1
-            for (int which = 0; which < 2; ++which) {
-                if (it >= 2) ok = ok && wait(which ? &pv_done[bf] : &k_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
-                if (!__all_sync(0xFFFFFFFFu, ok)) break;
-                uint8_t *dst = base + ((which ? v80 : k80) - sm) + bf * C::kOp;
-#pragma unroll 2
-                for (int i = 0; i < GR; ++i) {
-                    const int idx = w + 128 * i, row = idx / GR, gq = idx % GR;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(src + which * C::kRaw + idx * 16);
-                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-                    const uint8_t *sc = src + 2 * C::kRaw + which * 512 + row * GR;
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int j = 0; j < GR; ++j) top = max(top, static_cast<uint32_t>(sc[j]));
-                    const uint2 lv = levels_of(static_cast<int>(top) - sc[gq]);
-                    uint32_t o[8];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t mg = vw[j] & 0x77777777u, sg = vw[j] & 0x88888888u;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t m = __byte_perm(lv.x, lv.y, mg >> (16 * k));
-                            // 0xFF where the sign is set, 0x80 elsewhere: its low bit is the sign
-                            uint32_t s;
-                            asm("prmt.b32 %0, %1, 0, %2;" : "=r"(s) : "r"(0x80u), "r"(sg >> (16 * k)));
-                            o[2 * j + k] = m | ((s << 7) & 0x80808080u);
-                        }
-                    }
-                    *reinterpret_cast<uint4 *>(dst + swizzle8<D>(row * D + gq * 32)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(dst + swizzle8<D>(row * D + gq * 32 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
-                }
-                umma::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) umma::mbar_arrive(which ? &v_full[bf] : &k_full[bf]);
-            }
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            if (lane == 0) umma::mbar_arrive(&empty[st]);
-        }
-    } else if (warp >= 4) {
+        return true;
+    };
+
+    if (warp >= 4 && warp < 12) {
         // ---- softmax: thread = key (S^T's row), columns [c0, c0 + NC) --------------------------
-        const int wg = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane, c0 = NSTR == 2 ? 0 : wg * NC;
-        const int own = NSTR == 2 ? wg : 0;  // the stream
+        constexpr int kAll = 1 + C::kSoft, kAllThreads = 128 * C::kSoft;  // the barrier of all softmax warps
+        const int wg = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
+        const int own = wg * NSTR / C::kSoft;  // the stream
+        const int c0 = (wg % (C::kSoft / NSTR)) * NC;
         const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t t_own = t_o + t_lane + own * 3 * NB;
-        Walk<NB> walk(a, pos0, pos1, b_at, f_at);
         Segment g;
-        int it = 0;
+        Ring<SV> rv;
+        int it = 0, n_seg = 0;
         bool dead = false;
-        while (!dead && walk.next(a, g)) {
-            // Q rows: two fp8 numbers a channel
-            {
-                constexpr int LR = D / 8, RP = 256 / LR;  // lanes a row, rows a pass
-                const int me = wg * 128 + r;
-#pragma unroll 1
-                for (int n = me / LR; n < NB; n += RP) {
-                    const long long gi = static_cast<long long>(g.r) * NB + n;
-                    const int tq = static_cast<int>(gi / a.grp), j = static_cast<int>(gi - static_cast<long long>(tq) * a.grp);
-                    const bool live = tq < g.s.nq;
-                    const int ch = (me % LR) * 8;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (live)
-                        v = *reinterpret_cast<const uint4 *>(a.q + (g.s.q0 + tq) * a.q_stride +
-                                                             static_cast<long long>(g.h * a.grp + j) * D + ch);
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t m2 = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, x[i] & 0x7FFF7FFFu);
-                    uint32_t amax = max(m2 & 0xFFFFu, m2 >> 16);
-#pragma unroll
-                    for (int o = 1; o < LR; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-                    const uint32_t sb = scale_byte<8>(amax);
-                    const float inv = sb == 255u ? 0.0f : scale_inverse(sb);
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float f0 = __uint_as_float(x[i] << 16) * inv, f1 = __uint_as_float(x[i] & 0xFFFF0000u) * inv;
-                        hi[i] = e4m3x2(f0, f1);
-                        const uint32_t hh = e4m3x2_to_f16x2(hi[i]);
-                        const float2 b2 = __half22float2(*reinterpret_cast<const __half2 *>(&hh));
-                        lo[i] = e4m3x2((f0 - b2.x) * 16.0f, (f1 - b2.y) * 16.0f);
-                        if (sb == 255u) hi[i] = 0x7F7Fu, lo[i] = 0;  // an infinity or a NaN: the row is NaN
-                    }
-                    const uint32_t oh = swizzle8<D>(n * D + ch), ol = swizzle8<D>((NB + n) * D + ch);
-                    *reinterpret_cast<uint2 *>(base + (q0 - sm) + oh) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-                    *reinterpret_cast<uint2 *>(base + (q0 - sm) + ol) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-                    if (me % LR == 0) {
-                        s_qs[n] = sb == 255u ? 1.0f : scale_of(sb);
-#pragma unroll
-                        for (int z = 0; z < NSTR; ++z) s_nm[z][n] = 0.0f;
-                        s_tok[n] = live ? tq : 0;
-                        s_row[n] = live ? static_cast<long long>(g.s.q0 + tq) * a.Hq + g.h * a.grp + j : -1;
-                    }
-                }
-            }
-            umma::fence_proxy_async_smem();
-            any_of(3, 256, false);
-            if (lane == 0) umma::mbar_arrive(&q_full);
-
+        while (!dead && next_segment(g, n_seg)) {
+            const int qb = n_seg & 1;
+            const bool q_ok = wait(&q_full[qb], (n_seg >> 1) & 1, vfail, a.wait_ns);
+            ++n_seg;
             uint64_t l2[NC / 2];
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) l2[i] = 0;
-            const int hist = g.s.kv - g.s.nq;  // keys before the new tokens
-            const int clear = a.mode == QVG_MASK_NONE ? g.s.kv : min(g.s.kv, hist);
-            int last = -1;  // this warpgroup's latest tile of the segment
-            for (int t = g.t0; t < g.t1; ++t, ++it) {
-                const int st = it % S, bf = it & 1;
-                if (NSTR == 2 && bf != wg) continue;
+            const int hist = g.kv - g.nq;  // keys before the new tokens
+            const int clear = a.mode == QVG_MASK_NONE ? g.kv : min(g.kv, hist);
+            int last = -1;      // this warpgroup's latest tile of the segment
+            bool late = false;  // this thread gave up a wait: all agree on that at the next barrier
+            for (int t = g.t0; t < g.t1; ++t, ++it, rv.next()) {
+                const int bf = it & 1;
+                if (NSTR == 2 && bf != own) continue;
                 const bool first = last < 0;
-                bool ok = wait(&s_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
-                if (it >= 2) ok = ok && wait(&pv_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
-                ok = ok && wait(&full[st], (it / S) & 1, vfail, a.wait_ns);  // (the scales: written by the async proxy)
-                umma::tc_fence_after();
-                const uint8_t *sc = base + (st0 - sm) + st * C::kStage + 2 * C::kRaw;
+                bool ok = q_ok && !late && wait(&v_full[rv.i], rv.parity, vfail, a.wait_ns);  // (the scales)
+                uint8_t *slot_v = base + (vr0 - sm) + rv.i * C::kVSlot;
+                const uint8_t *sc = slot_v + C::kRaw;
                 uint32_t kb = 0, vb = 0;
                 if constexpr (BITS == 8) {
                     kb = sc[r];
@@ -723,25 +705,31 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                         vb = max(vb, static_cast<uint32_t>(sc[512 + r * C::G + j]));
                     }
                 }
-                __syncwarp();
-                if (lane == 0) umma::mbar_arrive(&empty[st]);
                 // 4 bits: the operands are 2^6 times the values over the largest scale
-                const float ka = scale_of(kb) * (BITS == 8 ? a.scale_log2 : a.scale_log2 * 0x1p-6f);
-                const float sv = scale_of(vb) * (BITS == 8 ? 1.0f : 0x1p-6f);
-                const float lsv = static_cast<float>(static_cast<int>(vb) - (BITS == 8 ? 127 : 133));
                 const int key = t * kTile + r;
+                if (key >= g.kv) kb = vb = 127u;  // (whatever is there)
+                const float ka = scale_of(kb) * (BITS == 8 ? a.scale_log2 : a.scale_log2 * 0x1p-6f);
+                const bool v_nan = vb == 255u;  // weighed as 1, and made a NaN below
+                const float sv = v_nan ? 1.0f : scale_of(vb) * (BITS == 8 ? 1.0f : 0x1p-6f);
+                const float lsv = v_nan ? 0.0f : static_cast<float>(static_cast<int>(vb) - (BITS == 8 ? 127 : 133));
                 const bool part = (t + 1) * kTile > clear;
                 const uint64_t ka2 = pk2(ka, ka), lo2 = pk2(0.0625f, 0.0625f);
-                float y[NC];
-                // logits (base 2) less the reference; -inf where the row does not see the key
-                auto logits = [&]() {
+                ok = ok && wait(&s_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                umma::tc_fence_after();
+                const uint32_t t_s = tmem + t_lane + bf * 2 * NB + c0;
+                uint32_t hidden = 0;  // columns that do not see this key, where that can be
+                if (part)
+                    hidden = hide_keys<NC>(a, t_s, NB, &s_tok[qb][c0], s_mw[wg], wg, r, g.q0, key, g.kv, key - hist,
+                                           max(0, t * kTile - hist) >> 5);
+                float y[NC];  // logits (base 2) less the reference
+                for (bool settled = false;;) {
 #pragma unroll
                     for (int c = 0; c < NC; c += 16) {
-                        uint32_t v[16], u[16];
-                        tmem_ld16x2(tmem + t_lane + bf * 2 * NB + c0 + c, tmem + t_lane + bf * 2 * NB + NB + c0 + c, v, u);
+                        uint32_t v[16], u[16];  // against Q's hi and lo rows
+                        tmem_ld_pair(t_s + c, NB, v, u);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float4 qs = *reinterpret_cast<const float4 *>(&s_qs[c0 + c + 4 * i]);
+                            const float4 qs = *reinterpret_cast<const float4 *>(&s_qs[qb][c0 + c + 4 * i]);
                             const float4 nm = *reinterpret_cast<const float4 *>(&s_nm[own][c0 + c + 4 * i]);
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
@@ -754,87 +742,34 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                             }
                         }
                     }
-                    if (part) {
-                        const int j = key - hist;
+                    if (settled) break;
+                    float top4[4] = {y[0], y[1], y[2], y[3]};
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) {
-                            const int tq = s_tok[c0 + c];
-                            bool see = key < g.s.kv;
-                            if (see && j >= 0) {
-                                if (a.mode == QVG_MASK_CAUSAL) see = j <= tq;
-                                if (a.mode == QVG_MASK_TREE)
-                                    see = (a.mask[static_cast<long long>(g.s.q0 + tq) * a.words + (j >> 5)] >> (j & 31)) & 1u;
-                            }
-                            if (!see) y[c] = -INFINITY;
-                        }
-                    }
-                };
-                logits();
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < NC; ++c) top = fmaxf(top, y[c]);
-                if (any_of(wg + 1, 128, first || !ok || top + lsv > kTop)) {
-                    // set or raise references: the column maxima of w over the tile
-                    float v[NC];
-                    const float lw = fmaxf(lsv, -64.0f);
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) v[c] = y[c] + lw;
-                    const float m = across_lanes<NC, true>(v);
-                    if (lane < NC) s_red[wg][quad][c0 + lane] = m;
-                    // (two streams: the last product into these sums is the one whose weights were here before)
-                    if (!first && NSTR == 1) ok = ok && wait(&pv_done[bf ^ 1], ((it - 1) >> 1) & 1, vfail, a.wait_ns);
-                    dead = any_of(wg + 1, 128, !ok);
+                    for (int c = 4; c < NC; ++c) top4[c & 3] = fmaxf(top4[c & 3], y[c]);
+                    const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                    if (!any_of(wg + 1, 128, first || !ok || top + lsv > kTop)) break;
+                    if (!first) ok = ok && wait(&pv_done[(it - NSTR) & 1], ((it - NSTR) >> 1) & 1, vfail, a.wait_ns);  // O's latest
+                    dead = !set_references<NC, NB>(t_s, t_own + c0, &s_qs[qb][c0], &s_nm[own][c0],
+                                                   reinterpret_cast<float *>(base + (p0 - sm) + bf * C::kP + (NSTR == 1 ? wg * 16384 : 0)),
+                                                   s_red[wg], s_dl[wg], wg, r, ka,
+                                                   lsv, first, ok);
                     if (dead) break;
-                    umma::tc_fence_after();
-                    if (r < NC) {
-                        const int n = c0 + r;
-                        const float mx = fmaxf(fmaxf(s_red[wg][0][n], s_red[wg][1][n]), fmaxf(s_red[wg][2][n], s_red[wg][3][n]));
-                        const bool move = first ? mx > -INFINITY : mx > kTop;
-                        const float d = move ? mx - kTarget : 0.0f;
-                        s_nm[own][n] -= d;
-                        s_dl[wg][n] = ex2(-d);
-                    }
-                    any_of(wg + 1, 128, false);
-                    if (!first) {
-#pragma unroll 1
-                        for (int z = 0; z < 3; ++z)
-#pragma unroll 1
-                            for (int c = 0; c < NC; c += 16) {
-                                uint32_t o[16];
-                                tmem_ld16(t_own + z * NB + c0 + c, o);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * s_dl[wg][c0 + c + i]);
-                                umma::tmem_st16(t_own + z * NB + c0 + c, o);
-                            }
-                        umma::tmem_st_wait();
-#pragma unroll
-                        for (int i = 0; i < NC / 2; ++i)
-                            l2[i] = mul2(l2[i], pk2(s_dl[wg][c0 + 2 * i], s_dl[wg][c0 + 2 * i + 1]));
-                    }
-                    logits();
+                    for (int i = 0; i < NC / 2; ++i) l2[i] = mul2(l2[i], pk2(s_dl[wg][2 * i], s_dl[wg][2 * i + 1]));
+                    settled = true;
                 }
+                if (dead) break;
                 last = it;
                 umma::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive(&s_free[bf]);
-                // 8 bits: V's rows meet weights of 0 where a row does not see them, but 0 times a code that is no
-                // number would be one more NaN: slots past the end become 0, and so does such a code in the rows of
-                // the new tokens, which are the ones that a mask can hide (a slot that was never written)
-                if (BITS == 8 && part && (NSTR == 2 || wg == 0) && key >= hist) {
-                    uint4 *vr = reinterpret_cast<uint4 *>(base + (st0 - sm) + st * C::kStage + C::kRaw + r * D);
-#pragma unroll 1
-                    for (int i = 0; i < D / 16; ++i) {
-                        uint4 v = vr[i];
-                        uint32_t *w = &v.x;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t no = ((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes 0x7F, 0xFF
-                            w[j] = key < g.s.kv ? w[j] & ~((no >> 7) * 0xFFu) : 0u;
-                        }
-                        vr[i] = v;
-                    }
-                }
+                if (BITS == 8 && part && c0 == 0) clean_values<D>(slot_v, max(0, min(hist, g.kv) - t * kTile), g.kv - t * kTile, r);
                 uint8_t *prow = base + (p0 - sm) + bf * C::kP + r * 128;
+                auto place = [&](int z, int c) {  // part z of this thread's columns c .. c + 15 in its row of weights
+                    const int n = z * NB + c0 + c;
+                    return prow + (n >> 7) * (kTile * 128) + ((((n >> 4) & 7) ^ (r & 7)) << 4);
+                };
+                const uint64_t sv2 = pk2(sv, sv);
 #pragma unroll
                 for (int c = 0; c < NC; c += 16) {
                     uint32_t h[3][4];
@@ -844,39 +779,43 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const int e = c + 4 * k + 2 * i;
-                            const float pa = ex2(y[e]), pb = ex2(y[e + 1]);
-                            l2[e / 2] = add2(l2[e / 2], pk2(pa, pb));
-                            float wa = pa * sv, wb = pb * sv;
-                            if (part) {  // an unseen key has weight 0 whatever its scale is
-                                wa = y[e] == -INFINITY ? 0.0f : wa;
-                                wb = y[e + 1] == -INFINITY ? 0.0f : wb;
-                            }
+                            const uint64_t p = pk2(ex2(y[e]), ex2(y[e + 1]));
+                            l2[e / 2] = add2(l2[e / 2], p);
+                            float wa, wb;
+                            up2(mul2(p, sv2), wa, wb);
                             w[i] = f16x2(wa, wb);
                         }
                         three_parts(w[0], w[1], h[0][k], h[1][k], h[2][k]);
                     }
+                    // (the buffer's last weights have been used up by now)
+                    if (c == 0 && it >= 2 && !wait(&pv_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns)) late = true;
 #pragma unroll
-                    for (int z = 0; z < 3; ++z) {
-                        const int n = z * NB + c0 + c;
-                        *reinterpret_cast<uint4 *>(prow + (n >> 7) * (kTile * 128) + ((((n >> 4) & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(h[z][0], h[z][1], h[z][2], h[z][3]);
-                    }
+                    for (int z = 0; z < 3; ++z) *reinterpret_cast<uint4 *>(place(z, c)) = make_uint4(h[z][0], h[z][1], h[z][2], h[z][3]);
+                }
+                if (v_nan) {  // a NaN for the rows that see this key, and only for them
+#pragma unroll 1
+                    for (int c = 0; c < NC; ++c)
+                        if (!((hidden >> c) & 1u)) place(0, c & 16)[c & 15] = 0x7F;
                 }
                 umma::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) umma::mbar_arrive(&p_full[bf]);
+                if (lane == 0) {
+                    umma::mbar_arrive(&p_full[bf]);
+                    umma::mbar_arrive(&v_empty[rv.i]);
+                }
             }
-            // ---- the segment's sums (both warpgroups come here, also after a failure) ------------
-            bool ok = !dead;
+            // ---- the segment's sums (all warpgroups come here, also after a failure) ------------
+            bool ok = !dead && !late && q_ok;
             if (ok && last >= 0) ok = wait(&pv_done[last & 1], (last >> 1) & 1, vfail, a.wait_ns);
             {
-                float v[NC];
+                // the weights' buffers are free now: l's column sums go through them
+                float *scratch = reinterpret_cast<float *>(base + (p0 - sm) + wg * 16384);
 #pragma unroll
-                for (int i = 0; i < NC / 2; ++i) up2(l2[i], v[2 * i], v[2 * i + 1]);
-                const float s = across_lanes<NC, false>(v);
-                if (lane < NC) s_red[wg][quad][c0 + lane] = s;
+                for (int i = 0; i < NC / 2; ++i) *reinterpret_cast<uint64_t *>(scratch + r * NC + 2 * i) = l2[i];
+                dead = any_of(wg + 1, 128, !ok);
+                if (!dead) reduce_columns<NC, false>(scratch, s_red[wg], r);
             }
-            dead = any_of(3, 256, !ok);
+            dead = any_of(kAll, kAllThreads, dead);
             if (dead) break;
             umma::tc_fence_after();
             const int slot = cta * 2 + (g.t0 > 0 ? 0 : 1);
@@ -885,8 +824,9 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                 float l[NSTR], m = -INFINITY, sum = 0.0f;
 #pragma unroll
                 for (int z = 0; z < NSTR; ++z) {
-                    const int w = NSTR == 2 ? z : (r >= NC ? 1 : 0);
-                    l[z] = (s_red[w][0][r] + s_red[w][1][r]) + (s_red[w][2][r] + s_red[w][3][r]);
+                    const float(&red)[128 / NC][NC] = s_red[z * (C::kSoft / NSTR) + r / NC];
+                    l[z] = 0.0f;
+                    for (int i = 0; i < 128 / NC; ++i) l[z] += red[i][r % NC];
                     if (l[z] != 0.0f) m = fmaxf(m, -s_nm[z][r]);
                 }
                 float wt[NSTR];
@@ -898,7 +838,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                 const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
                 for (int z = 0; z < NSTR; ++z) s_wt[z][r] = wt[z] * inv;
-                const long long row = s_row[r];
+                const long long row = s_row[qb][r];
                 if (!whole) {
                     a.pm[static_cast<long long>(slot) * NB + r] = m;
                     a.pl[static_cast<long long>(slot) * NB + r] = sum;
@@ -906,9 +846,12 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                     a.lse[(row % a.Hq) * a.total_q + row / a.Hq] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
                 }
             }
-            any_of(3, 256, false);
+            any_of(kAll, kAllThreads, false);
+            if (wg < NSTR)
+                for (int n = r; n < NB; n += 128) s_nm[wg][n] = 0.0f;  // for the next unit
+            constexpr int kShare = NB / C::kSoft;  // columns of O a warpgroup hands out
 #pragma unroll 1
-            for (int c = wg * (NB / 2); c < (wg + 1) * (NB / 2); c += 8) {
+            for (int c = wg * kShare; c < (wg + 1) * kShare; c += 8) {
                 float o[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] = 0.0f;
@@ -919,7 +862,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float w = s_wt[z][c + i];
-                        const float f = fmaf(__uint_as_float(x[2][i]), 0x1p-6f, fmaf(__uint_as_float(x[1][i]), 0x1p-3f, __uint_as_float(x[0][i])));
+                        const float f = (__uint_as_float(x[2][i]) + __uint_as_float(x[1][i])) + __uint_as_float(x[0][i]);
                         if (w != 0.0f) o[i] = fmaf(f, w, o[i]);  // (a stream without a tile holds anything)
                     }
                 }
@@ -927,7 +870,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int n = c + i;
-                        const long long row = s_row[n];
+                        const long long row = s_row[qb][n];
                         if (row < 0) continue;
                         if (!whole)
                             a.po[(static_cast<long long>(slot) * NB + n) * D + r] = o[i];
@@ -939,7 +882,271 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                 }
             }
             umma::tc_fence_before();
-            any_of(3, 256, false);  // everything of this segment has been read
+            any_of(kAll, kAllThreads, false);  // everything of this segment has been read
+            if (lane == 0) umma::mbar_arrive(&q_free[qb]);
+        }
+    } else if (warp == 0 || (BITS == 8 && warp == 12)) {
+        // ---- loads: warp 0 K (4 bits: and V), warp 12 V ---------------------------------------------
+        Segment g;
+        Ring<SK> rk;
+        Ring<SV> rv;
+        int it = 0, n_seg = 0;
+        bool ok = true;
+        while (ok && next_segment(g, n_seg)) {
+            ++n_seg;
+            for (int t = g.t0; ok && t < g.t1; ++t, ++it) {
+                if (warp == 0) {
+                    ok = load_tile(g, t, true, &k_full[rk.i], &k_empty[rk.i], kr0 + rk.i * C::kRaw, rk.parity, it >= SK);
+                    rk.next();
+                }
+                if (BITS == 4 || warp != 0) {
+                    ok = ok && load_tile(g, t, false, &v_full[rv.i], &v_empty[rv.i], vr0 + rv.i * C::kVSlot, rv.parity, it >= SV);
+                    rv.next();
+                }
+                if (!ok) break;
+            }
+        }
+        if (lane == 0) {
+            if (warp == 0) s_issued[0] = it;
+            if (BITS == 4 || warp != 0) s_issued[1] = it;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 1) {
+        // ---- S = K Q^T -------------------------------------------------------------------
+        constexpr uint32_t id = idesc_f8(128, 2 * NB, 0);
+        Segment g;
+        Ring<SK> rk;
+        int it = 0, n_seg = 0;
+        bool ok = true;
+        while (ok && next_segment(g, n_seg)) {
+            if (lane == 0) {
+                ok = wait(&q_full[n_seg & 1], (n_seg >> 1) & 1, vfail, a.wait_ns);
+                const uint64_t dq = desc_rows8<D>(q0 + (n_seg & 1) * C::kQ);
+                for (int t = g.t0; ok && t < g.t1; ++t, ++it, rk.next()) {
+                    const int bf = it & 1;
+                    ok = BITS == 8 ? wait(&k_full[rk.i], rk.parity, vfail, a.wait_ns)
+                                   : wait(&ko_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                    if (it >= 2) ok = ok && wait(&s_free[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
+                    if (!ok) break;
+                    umma::tc_fence_after();
+                    const uint64_t dk = desc_rows8<D>(BITS == 8 ? kr0 + rk.i * C::kRaw : k80 + bf * C::kOp);
+#pragma unroll
+                    for (int s = 0; s < D / 32; ++s) mma_f8(tmem + bf * 2 * NB, dk + 2 * s, dq + 2 * s, id, s != 0);
+                    umma::mma_commit(&s_full[bf]);
+                    umma::mma_commit(BITS == 8 ? &k_empty[rk.i] : &ko_done[bf]);
+                    // test hook: with S in flight, wait for what never comes
+                    if (it == 0 && a.inject) ok = wait(&never, 0, vfail, a.wait_ns);
+                }
+                umma::mma_commit(&q_free[n_seg & 1]);
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            ++n_seg;
+        }
+        if (lane == 0) umma::mma_commit(&drain);
+    } else if (warp == 2) {
+        // ---- O += V^T P^T (its own warp: starting a batch of products takes longer than the batch) ----
+        constexpr uint32_t id = idesc_f8(128, 3 * NB, 1) | (1u << 15) | (1u << 16);  // both MN-major
+        Segment g;
+        Ring<SV> rv;
+        int it = 0, n_seg = 0;
+        bool ok = true;
+        while (ok && next_segment(g, n_seg)) {
+            ++n_seg;
+            if (lane == 0) {
+                for (int t = g.t0; ok && t < g.t1; ++t, ++it, rv.next()) {
+                    const int bf = it & 1;
+                    // (4 bits: the loaded codes' buffer may be in its next use by now)
+                    ok = BITS == 8 ? wait(&v_full[rv.i], rv.parity, vfail, a.wait_ns)
+                                   : wait(&vo_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                    ok = ok && wait(&p_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                    if (!ok) break;
+                    umma::tc_fence_after();
+                    // d = 64: the accumulator's upper 64 rows repeat the lower ones and are not read
+                    const uint64_t dv = desc_rows8<D>(BITS == 8 ? vr0 + rv.i * C::kVSlot : v80 + bf * C::kOp);
+                    const uint64_t dp = desc_rows8<128>(p0 + bf * C::kP, kTile * 128);
+                    const bool fresh = t - g.t0 < NSTR;  // the stream's first tile of the unit
+#pragma unroll
+                    for (int s = 0; s < kTile / 32; ++s)
+                        mma_f8(t_o + (NSTR == 2 ? bf * 3 * NB : 0), dv + s * (32 * D / 16), dp + s * 256, id, !(fresh && s == 0));
+                    umma::mma_commit(&pv_done[bf]);
+                    if (BITS == 8) umma::mma_commit(&v_empty[rv.i]);
+                }
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+        }
+        // all products issued, S's too, complete before TMEM goes back
+        if (lane == 0) {
+            umma::mma_commit(&drain);
+            umma::mbar_wait(&drain, 0, kDrainNs);
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        // ---- this CTA's part of the line, unit by unit (4 bits: and the unit's Q rows) ---------------
+        // tiles of all sequences, by chunks of `span` sequences
+        const int span = ((a.B + kChunks - 1) / kChunks + 31) & ~31;
+        long long total = 0;
+        for (int k = 0, b0 = 0; b0 < a.B; ++k, b0 += span) {
+            long long mine = 0;
+            for (int b = b0 + lane; b < min(a.B, b0 + span); b += 32) mine += seq_of<NB>(a, b, cta == 0).tiles(a.H);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+            if (lane == 0) s_chunk[k] = mine;
+            total += mine;
+        }
+        __syncwarp();
+        const long long per = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+        long long pos = min(total, cta * per);
+        const long long end = min(total, pos + per);
+        // the sequence that holds `pos`: its chunk, then by a scan over 32 at a time
+        long long first = 0;  // where sequence b begins
+        int b = 0;
+        if (pos < end) {
+            int k = 0;
+            while (pos >= first + s_chunk[k]) first += s_chunk[k++];
+            for (b = k * span;; b += 32) {
+                const long long w = b + lane < a.B ? seq_of<NB>(a, b + lane, false).tiles(a.H) : 0;
+                long long x = w;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                    if (lane >= o) x += y;
+                }
+                const uint32_t hit = __ballot_sync(0xFFFFFFFFu, pos < first + x);
+                const int l = hit ? __ffs(hit) - 1 : 31;
+                const long long upto = __shfl_sync(0xFFFFFFFFu, x, l), own = __shfl_sync(0xFFFFFFFFu, w, l);
+                if (hit) {
+                    first += upto - own;
+                    b += l;
+                    break;
+                }
+                first += upto;
+            }
+        }
+        int4 cut = make_int4(-1, 0, 0, 0);  // the unit that begins here and goes on: its CTAs
+        Seq s = seq_of<NB>(a, min(b, a.B - 1), false);
+        bool ok = true;
+        for (int n_seg = 0; ok; ++n_seg) {
+            Segment g;
+            g.t1 = 0;
+            if (pos < end) {
+                while (pos >= first + s.tiles(a.H)) {
+                    first += s.tiles(a.H);
+                    s = seq_of<NB>(a, ++b, false);
+                }
+                const uint32_t rel = static_cast<uint32_t>(pos - first), u = rel / static_cast<uint32_t>(s.nt);
+                g.b = b;
+                g.h = static_cast<int>(u / static_cast<uint32_t>(s.rb));
+                g.r = static_cast<int>(u % static_cast<uint32_t>(s.rb));
+                g.t0 = static_cast<int>(rel - u * s.nt);
+                g.t1 = static_cast<int>(min(static_cast<long long>(s.nt), g.t0 + (end - pos)));
+                g.q0 = s.q0;
+                g.nq = s.nq;
+                g.kv = s.kv;
+                g.nt = s.nt;
+                const long long unit_end = pos + (s.nt - g.t0);
+                if (g.t0 == 0 && g.t1 < s.nt) cut = make_int4(b, g.h, g.r, static_cast<int>((unit_end - 1) / per));
+                pos += g.t1 - g.t0;
+            } else if (lane == 0) {
+                a.desc[cta] = cut;
+            }
+            const int i = n_seg & (kRing - 1);
+            if (n_seg >= kRing) ok = wait(&seg_free[i], ((n_seg / kRing) - 1) & 1, vfail, a.wait_ns);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                s_seg[i] = g;
+                umma::mbar_arrive(&seg_full[i]);
+            }
+            if (g.t1 == 0) break;
+            if constexpr (BITS == 4) {
+                const int qb = n_seg & 1;
+                if (n_seg >= 2) ok = wait(&q_free[qb], ((n_seg >> 1) - 1) & 1, vfail, a.wait_ns);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                make_q<D, NB>(a, g, base + (q0 - sm) + qb * C::kQ, s_qs[qb], s_tok[qb], s_row[qb], 0, 256 / D);
+                if (lane == 0) umma::mbar_arrive(&q_full[qb]);
+            }
+        }
+        if (!ok && lane == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
+    } else if (BITS == 8 && warp >= 13) {
+        // ---- Q rows of the coming units ----------------------------------------------------------
+        Segment g;
+        int n_seg = 0;
+        bool ok = true;
+        while (ok && next_segment(g, n_seg)) {
+            const int qb = n_seg & 1;
+            if (n_seg >= 2) ok = wait(&q_free[qb], ((n_seg >> 1) - 1) & 1, vfail, a.wait_ns);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            make_q<D, NB>(a, g, base + (q0 - sm) + qb * C::kQ, s_qs[qb], s_tok[qb], s_row[qb], (warp - 13) * (256 / D), 3 * (256 / D));
+            if (lane == 0) umma::mbar_arrive(&q_full[qb]);
+            ++n_seg;
+        }
+    } else if (BITS == 4 && warp >= 12) {
+        // ---- 4-bit codes into e4m3 operands: one (row, 32-channel group) a step, its scale relative to the row's
+        // largest.  A word's eight magnitudes are two byte permutes of the group's eight levels.
+        // (two warps for K, two for V: V's operand waits for weights, K's must not)
+        const int which = (warp - 12) >> 1, w = tid - 384 - which * 64;
+        constexpr int GR = D / 32, kThreads = 64;
+        Ring<SK> rk;
+        Ring<SV> rv;
+        Segment g;
+        int it = 0, n_seg = 0;
+        bool ok = true;
+        while (ok && next_segment(g, n_seg)) {
+            ++n_seg;
+            for (int t = g.t0; t < g.t1; ++t, ++it, rk.next(), rv.next()) {
+            const int bf = it & 1;
+            ok = wait(&v_full[rv.i], rv.parity, vfail, a.wait_ns);  // (K's scales come with V's codes)
+            if (!which) ok = ok && wait(&k_full[rk.i], rk.parity, vfail, a.wait_ns);
+            if (it >= 2) ok = ok && wait(which ? &pv_done[bf] : &ko_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            const uint8_t *src = base + ((which ? vr0 + rv.i * C::kVSlot : kr0 + rk.i * C::kRaw) - sm);
+            const uint8_t *scales = base + (vr0 - sm) + rv.i * C::kVSlot + C::kRaw + which * 512;
+            uint8_t *dst = base + ((which ? v80 : k80) - sm) + bf * C::kOp;
+#pragma unroll 4
+            for (int i = 0; i < kTile * GR / kThreads; ++i) {
+                const int idx = w + kThreads * i, row = idx / GR, gq = idx % GR;
+                const uint4 v = *reinterpret_cast<const uint4 *>(src + idx * 16);
+                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+                const uint8_t *sc = scales + row * GR;
+                uint32_t top, mine;
+                if constexpr (GR == 4) {
+                    const uint32_t all = *reinterpret_cast<const uint32_t *>(sc);
+                    const uint32_t m = __vmaxu4(all, all >> 16);
+                    top = max(m & 0xFFu, (m >> 8) & 0xFFu);
+                    mine = (all >> (8 * gq)) & 0xFFu;
+                } else {
+                    const uint32_t all = *reinterpret_cast<const uint16_t *>(sc);
+                    top = max(all & 0xFFu, all >> 8);
+                    mine = (all >> (8 * gq)) & 0xFFu;
+                }
+                const uint2 lv = s_lv[min(top - mine, 15u)];
+                uint32_t o[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t mg = vw[j] & 0x77777777u, sg = vw[j] & 0x88888888u;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t m = __byte_perm(lv.x, lv.y, mg >> (16 * k));
+                        // 0xFF where the sign is set, 0x80 elsewhere: its low bit is the sign
+                        uint32_t s;
+                        asm("prmt.b32 %0, %1, 0, %2;" : "=r"(s) : "r"(0x80u), "r"(sg >> (16 * k)));
+                        o[2 * j + k] = m | ((s << 7) & 0x80808080u);
+                    }
+                }
+                *reinterpret_cast<uint4 *>(dst + swizzle8<D>(row * D + gq * 32)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(dst + swizzle8<D>(row * D + gq * 32 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            umma::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                umma::mbar_arrive(which ? &vo_full[bf] : &ko_full[bf]);
+                if (!which) umma::mbar_arrive(&k_empty[rk.i]);
+                umma::mbar_arrive(&v_empty[rv.i]);
+            }
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
         }
     }
     __syncwarp();
@@ -948,7 +1155,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
     if (tid == 0 && *vfail) {
         raise_error(a.err, QVG_ERR_TIMEOUT);
         // the copies in flight land before the CTA ends
-        for (int j = max(0, s_issued - S); j < s_issued; ++j) umma::mbar_wait(&full[j % S], (j / S) & 1, kDrainNs);
+        for (int j = max(0, s_issued[0] - SK); j < s_issued[0]; ++j) umma::mbar_wait(&k_full[j % SK], (j / SK) & 1, kDrainNs);
+        for (int j = max(0, s_issued[1] - SV); j < s_issued[1]; ++j) umma::mbar_wait(&v_full[j % SV], (j / SV) & 1, kDrainNs);
     }
     if (warp == 3) {
         umma::tc_fence_after();
