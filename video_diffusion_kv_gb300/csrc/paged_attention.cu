@@ -102,9 +102,13 @@ __global__ void k_tree_mask(const int32_t *__restrict__ parents, const int32_t *
 
 constexpr int kMaxTree = 8192;  // new tokens of one sequence whose parents fit 32 KB of shared memory
 
-// Query rows of a unit: the smallest block that holds a sequence's rows, at
-// most 64.
-int rows_of_block(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Query rows of a unit: 16 where that holds a sequence's rows, else blocks of
+// 32 (4-bit caches: blocks of 16, as their converters need registers too).  A
+// block of 32 costs a tile about 1.3 times a block of 16's time.
+int rows_of_block(long long rows, int bits) { return rows <= 16 || bits == 4 ? 16 : 32; }
+
+// Two CTAs an SM (see the kernel).
+int cta_count() { return 2 * sm_count_current(); }
 
 struct Workspace {
     size_t po, pm, pl, desc, bytes;  // offsets
@@ -152,13 +156,6 @@ qvg_status launch(const CUtensorMap (&map)[2], const pa::Args &a, int ctas, cuda
     return QVG_OK;
 }
 
-template <int D, int BITS>
-qvg_status launch_nb(int NB, const CUtensorMap (&map)[2], const pa::Args &a, int ctas, cudaStream_t st) {
-    if (NB == 16) return launch<D, BITS, 16>(map, a, ctas, st);
-    if (NB == 32) return launch<D, BITS, 32>(map, a, ctas, st);
-    return launch<D, BITS, 64>(map, a, ctas, st);
-}
-
 bool misaligned(const void *p, uintptr_t to) { return !p || reinterpret_cast<uintptr_t>(p) % to != 0; }
 
 }  // namespace
@@ -184,7 +181,7 @@ qvg_status qvg_tree_mask(const int32_t *parents, const int32_t *cu_q, int32_t B,
 qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B, int32_t max_q, size_t *bytes) {
     if (!bytes || H < 1 || Hq < 1 || Hq % H != 0 || B < 0 || max_q < 0) return QVG_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return QVG_ERR_UNSUPPORTED;
-    *bytes = carve(sm_count_current(), rows_of_block(static_cast<long long>(max_q) * (Hq / H)), d).bytes;
+    *bytes = carve(cta_count(), rows_of_block(static_cast<long long>(max_q) * (Hq / H), 8), d).bytes;  // (4 bits: no more)
     return QVG_OK;
 }
 
@@ -208,8 +205,8 @@ qvg_status qvg_paged_attention(const qvg_paged *cache, const void *q_bf16, int64
         (cu_q && misaligned(cu_q, 4)) || (lse && misaligned(lse, 4)))
         return QVG_ERR_INVALID_ARG;
     if (mask_mode == QVG_MASK_TREE && (misaligned(mask, 4) || mask_words < ceil_div(max_q, 32))) return QVG_ERR_INVALID_ARG;
-    const int ctas = sm_count_current();
-    const int NB = rows_of_block(static_cast<long long>(max_q) * (Hq / H));
+    const int ctas = cta_count();
+    const int NB = rows_of_block(static_cast<long long>(max_q) * (Hq / H), cache->bits);
     const Workspace w = carve(ctas, NB, d);
     if (!workspace || ws_bytes < w.bytes || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return QVG_ERR_WORKSPACE;
     CUtensorMap map[2] = {};
@@ -250,9 +247,9 @@ qvg_status qvg_paged_attention(const qvg_paged *cache, const void *q_bf16, int64
     a.wait_ns = wait_limit_ns();
     a.inject = wait_inject();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (d == 64)
-        return cache->bits == 8 ? launch_nb<64, 8>(NB, map, a, ctas, st) : launch_nb<64, 4>(NB, map, a, ctas, st);
-    return cache->bits == 8 ? launch_nb<128, 8>(NB, map, a, ctas, st) : launch_nb<128, 4>(NB, map, a, ctas, st);
+    if (cache->bits == 4) return d == 64 ? launch<64, 4, 16>(map, a, ctas, st) : launch<128, 4, 16>(map, a, ctas, st);
+    if (NB == 16) return d == 64 ? launch<64, 8, 16>(map, a, ctas, st) : launch<128, 8, 16>(map, a, ctas, st);
+    return d == 64 ? launch<64, 8, 32>(map, a, ctas, st) : launch<128, 8, 32>(map, a, ctas, st);
 }
 
 }  // extern "C"

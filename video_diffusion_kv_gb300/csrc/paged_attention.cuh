@@ -6,9 +6,14 @@
 // query row is a (new token, query head of the group) pair, so the group's
 // heads share each key and value that is read.  A unit walks its sequence in
 // tiles of 128 keys.  All units' tiles form one line, which is cut into equal
-// parts, one per CTA (one CTA per SM): ragged batches and single long
-// sequences fill the GPU alike.  A unit cut by a border leaves fp32 partial
-// sums that k_paged_merge joins.
+// parts, one per CTA: ragged batches and single long sequences fill the GPU
+// alike.  A unit cut by a border leaves fp32 partial sums that k_paged_merge
+// joins.
+//
+// Two CTAs share an SM (8 warps, half of the shared and tensor memory each), so
+// that one's latencies -- a tile is a chain of S, softmax and PV, a unit begins
+// and ends with its own -- pass while the other works.  (One CTA with two
+// softmax groups and twice the rows took 1.7 to 2.4 times as long.)
 //
 // The product runs transposed, keys on the tensor core's 128 rows, and takes
 // the cache's fp8 codes as they lie there (4-bit codes become fp8 first):
@@ -34,9 +39,6 @@
 // takes p in fp32.  The loop's code is kept small (one instance of each part):
 // with copies for the rare cases it outgrew the instruction cache and took
 // 1.5 times as long.
-// Up to 32 query rows, two softmax warpgroups take the tiles in turn, each
-// with its own references and sums (two streams, joined at the unit's end);
-// with 64 rows they share every tile, 32 columns each.
 #pragma once
 
 #include <cuda.h>
@@ -332,27 +334,25 @@ __device__ __forceinline__ void reduce_columns(const float *scratch, float (*red
 
 template <int D, int BITS, int NB>
 struct Cfg {
-    static constexpr int NSTR = NB <= 32 ? 2 : 1;  // streams (see above)
-    static constexpr int NC = NB <= 32 ? NB : 32;   // columns of a softmax thread
-    static constexpr int kSoft = 2;                 // softmax warpgroups
-    static constexpr int kParty = 8 / NSTR;         // softmax warps on one tile
+    static constexpr int NC = NB;              // columns of a softmax thread
     static constexpr int G = BITS == 8 ? 1 : D / 32;
-    static constexpr int kRow = D * BITS / 8;       // bytes of a row of codes
-    static constexpr int kRaw = kTile * kRow;       // a tile's codes (K or V)
-    static constexpr int kOp = BITS == 4 ? kTile * D : 0;   // K or V as e4m3 (4 bits), two buffers each
-    static constexpr int kP = 16384 * ((3 * NB + 127) / 128);  // weights, two buffers
-    static constexpr int kQ = 2 * NB * D;           // Q: hi rows, lo rows; two buffers
-    static constexpr int kFixed = 4 * kOp + 2 * kP + 2 * kQ;
-    static constexpr int kVSlot = kRaw + 1024;      // V's codes, K's and V's scales
+    static constexpr int kRow = D * BITS / 8;  // bytes of a row of codes
+    static constexpr int kRaw = kTile * kRow;  // a tile's codes (K or V)
+    static constexpr int kScales = 256 * G;    // and K's and V's scales
+    static constexpr int kOp = BITS == 4 ? kTile * D : 0;  // K or V as e4m3 (4 bits)
+    static constexpr int kP = 16384;           // weights: 128 rows of 3 NB (at most 128) bytes
+    static constexpr int kQ = 2 * NB * D;      // Q: hi rows, lo rows
+    static constexpr int kFixed = 2 * kOp + kP + kQ;
     // K's and V's copies in flight: a K buffer is free once S is there, a V buffer once O has it
-    static constexpr int kSlots = (224 * 1024 - 8192 - kFixed - 8 * 1024) / kRaw;
-    static constexpr int kSK = kSlots / 2 > 6 ? 6 : kSlots / 2, kSV = kSlots - kSK > 8 ? 8 : kSlots - kSK;
-    static constexpr int kSmem = kFixed + kSK * kRaw + kSV * kVSlot + 1024;
-    static constexpr int kWarps = 16;  // K's loads, S, PV, segments (4 bits: and Q); softmax 4 - 11; 12 V's loads, 13 - 15 Q, or (4 bits) converters
-    static constexpr int kQWarps = BITS == 8 ? 3 : 1;
-    static constexpr int kTmemUsed = 2 * 2 * NB + NSTR * 3 * NB;
-    static constexpr int kTmem = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-    static_assert(kSK >= 3 && kSV >= 3, "shared memory");
+    static constexpr int kRoom = 106 * 1024 - kFixed;
+    static constexpr int kSlots = kRoom / (kRaw + kScales / 2);
+    static constexpr int kSK = kSlots / 2 > 4 ? 4 : kSlots / 2, kSV = kSlots - kSK > 5 ? 5 : kSlots - kSK;
+    static constexpr int kSmem = kFixed + (kSK + kSV) * kRaw + kSV * kScales + 1024;
+    static constexpr int kConv = BITS == 4 ? 2 : 0;  // converter warps
+    static constexpr int kWarps = 8 + kConv;   // loads, S, PV, segments and Q; softmax 4 - 7; converters
+    static constexpr int kTmemUsed = 2 * 2 * NB + 3 * NB;
+    static constexpr int kTmem = kTmemUsed <= 128 ? 128 : 256;
+    static_assert(kSK >= 2 && kSV >= 2, "shared memory");
 };
 
 // e2m1 magnitudes times 2^(6 - k) as e4m3 bytes, for a group whose scale is
@@ -381,49 +381,29 @@ __device__ __forceinline__ void logits16(uint32_t t_hi, uint32_t t_lo, const flo
         y[i] = fmaf(fmaf(__uint_as_float(u[i]), 0.0625f, __uint_as_float(v[i])) * ka, qs[i], nm[i]);
 }
 
-// The rows (columns of S) that do not see this thread's key: their logits
-// become -inf in tensor memory.  Returns them as bits.
-//   t_s: S's column c0 (hi; lo is `lo` columns on); tok: the rows' new tokens;
-// mw: room for the tile's mask words; j: the key's number among the new
-// tokens; w0: the first mask word that the tile needs.
+// The rows (columns of S) that do not see this thread's key, as bits.
+//   row0: the first column's row; tok: the rows' new tokens; mw: room for the
+// tile's mask words; j: the key's number among the new tokens; w0: the first
+// mask word that the tile needs.
 template <int NC>
-__device__ __noinline__ uint32_t hide_keys(const Args &a, uint32_t t_s, uint32_t lo, const int *tok, uint32_t (*mw)[5], int wg,
-                                           int r, int q0, int key, int kv, int j, int w0) {
+__device__ __noinline__ uint32_t hidden_rows(const Args &a, int row0, const int *tok, uint32_t (*mw)[5], int r, int q0, bool past, int j,
+                                             int w0) {
     if (a.mode == QVG_MASK_TREE) {
         for (int i = r; i < NC * 5; i += 128) {
             const int c = i / 5, k = w0 + i % 5;
             mw[c][i % 5] = k < a.words ? a.mask[static_cast<long long>(q0 + tok[c]) * a.words + k] : 0u;
         }
-        any_of(wg + 1, 128, false);
+        any_of(1, 128, false);
+    }
+    if (past) return 0xFFFFFFFFu;
+    if (j < 0 || a.mode == QVG_MASK_NONE) return 0u;
+    if (a.mode == QVG_MASK_CAUSAL) {  // row i is token i / grp: it sees token j from row j grp on
+        const long long n = static_cast<long long>(j) * a.grp - row0;
+        return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
     }
     uint32_t hidden = 0;
-#pragma unroll 1
-    for (int c = 0; c < NC; ++c) {
-        bool see = key < kv;
-        if (see && j >= 0) {
-            if (a.mode == QVG_MASK_CAUSAL) see = j <= tok[c];
-            if (a.mode == QVG_MASK_TREE) see = (mw[c][(j >> 5) - w0] >> (j & 31)) & 1u;
-        }
-        if (__any_sync(0xFFFFFFFFu, !see)) {
-            uint32_t v, u;
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%2];\n\t"
-                "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%3];\n\t"
-                "tcgen05.wait::ld.sync.aligned;"
-                : "=r"(v), "=r"(u)
-                : "r"(t_s + c), "r"(t_s + lo + c)
-                : "memory");
-            v = see ? v : 0xFF800000u;
-            u = see ? u : 0u;
-            asm volatile(
-                "tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%2};\n\t"
-                "tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%3};" ::"r"(t_s + c),
-                "r"(t_s + lo + c), "r"(v), "r"(u)
-                : "memory");
-        }
-        hidden |= (see ? 0u : 1u) << c;
-    }
-    umma::tmem_st_wait();
+#pragma unroll 4
+    for (int c = 0; c < NC; ++c) hidden |= (~(mw[c][(j >> 5) - w0] >> (j & 31)) & 1u) << c;
     return hidden;
 }
 
@@ -453,19 +433,21 @@ __device__ __noinline__ void clean_values(uint8_t *v, int from, int past, int r)
 // dl gets the factors for l.  False: some thread has given up.
 template <int NC, int NB>
 __device__ __noinline__ bool set_references(uint32_t t_s, uint32_t t_own, const float *qs, float *nm, float *scratch, float (*red)[NC],
-                                            float *dl, int wg, int r, float ka, float lsv, bool first, bool ok) {
+                                            float *dl, int r, float ka, float lsv, const uint32_t hidden, bool first, bool ok) {
     const float lw = fmaxf(lsv, -64.0f);
 #pragma unroll 1
     for (int c = 0; c < NC; c += 16) {
         float y[16];
         logits16(t_s + c, t_s + NB + c, qs + c, nm + c, ka, y);
 #pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = (hidden >> (c + i)) & 1u ? -INFINITY : y[i] + lw;
+#pragma unroll
         for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4 *>(scratch + r * NC + c + i) = make_float4(y[i] + lw, y[i + 1] + lw, y[i + 2] + lw, y[i + 3] + lw);
+            *reinterpret_cast<float4 *>(scratch + r * NC + c + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
     }
-    if (any_of(wg + 1, 128, !ok)) return false;
+    if (any_of(1, 128, !ok)) return false;
     reduce_columns<NC, true>(scratch, red, r);
-    any_of(wg + 1, 128, false);
+    any_of(1, 128, false);
     umma::tc_fence_after();
     if (r < NC) {
         float mx = -INFINITY;
@@ -475,7 +457,7 @@ __device__ __noinline__ bool set_references(uint32_t t_s, uint32_t t_own, const 
         nm[r] -= d;
         dl[r] = ex2(-d);
     }
-    any_of(wg + 1, 128, false);
+    any_of(1, 128, false);
     if (!first) {
 #pragma unroll 1
         for (int z = 0; z < 3 * (NC / 16); ++z) {
@@ -491,11 +473,11 @@ __device__ __noinline__ bool set_references(uint32_t t_s, uint32_t t_own, const 
     return true;
 }
 
-// Q rows n0, n0 + step, .. of a unit (step rows at a time are a warp's share)
-// as pairs of fp8 numbers into dst, with their scales, tokens and out rows.
+// A unit's Q rows as pairs of fp8 numbers into dst, with their scales, tokens
+// and out rows; by one warp.
 template <int D, int NB>
-__device__ __noinline__ void make_q(const Args &a, const Segment &g, uint8_t *dst, float *qs, int *tok, long long *rows, int n0, int step) {
-    constexpr int LR = D / 8;  // lanes a row; 32 / LR rows a pass
+__device__ __noinline__ void make_q(const Args &a, const Segment &g, uint8_t *dst, float *qs, int *tok, long long *rows) {
+    constexpr int LR = D / 8, step = 32 / LR;  // lanes a row, rows a pass
     const int lane = threadIdx.x & 31, ch = (lane % LR) * 8;
     auto fetch = [&](int n, int &tq, int &j) {
         const uint32_t gi = static_cast<uint32_t>(g.r) * NB + n;  // (the call has made sure that it fits)
@@ -504,7 +486,7 @@ __device__ __noinline__ void make_q(const Args &a, const Segment &g, uint8_t *ds
         if (n >= NB || tq >= g.nq) return make_uint4(0, 0, 0, 0);
         return *reinterpret_cast<const uint4 *>(a.q + (g.q0 + tq) * a.q_stride + static_cast<long long>(g.h * a.grp + j) * D + ch);
     };
-    int n = n0 + lane / LR, tq, j, tq1, j1, tq2, j2;
+    int n = lane / LR, tq, j, tq1, j1, tq2, j2;
     uint4 v = fetch(n, tq, j), v1 = fetch(n + step, tq1, j1), v2;
 #pragma unroll 1
     for (; n < NB; n += step, v = v1, tq = tq1, j = j1, v1 = v2, tq1 = tq2, j1 = j2) {
@@ -543,74 +525,74 @@ __device__ __noinline__ void make_q(const Args &a, const Segment &g, uint8_t *ds
 }
 
 template <int D, int BITS, int NB>
-__global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
+__global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
     k_paged_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ Args a) {
     using C = Cfg<D, BITS, NB>;
-    constexpr int SK = C::kSK, SV = C::kSV, NSTR = C::NSTR, NC = C::NC;
+    constexpr int SK = C::kSK, SV = C::kSV, NC = C::NC;
     extern __shared__ uint8_t dyn[];
     __shared__ uint64_t k_full[SK], k_empty[SK], v_full[SV], v_empty[SV];  // codes (and scales, with V's) as loaded
-    __shared__ uint64_t ko_full[2], ko_done[2], vo_full[2];                // 4 bits: operands made of them
-    __shared__ uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full[2], q_free[2], drain, never;
+    __shared__ uint64_t ko_full, ko_done, vo_full;                         // 4 bits: operands made of them
+    __shared__ uint64_t s_full[2], s_free[2], p_full, pv_done, q_full[2], q_free, m_free[2], drain, never;
+    __shared__ uint64_t seg_full[kRing], seg_free[kRing];
+    __shared__ Segment s_seg[kRing];
+    __shared__ long long s_chunk[kChunks];
     __shared__ uint32_t tmem_base;
-    __shared__ int fail, s_issued[2];
-    __shared__ __align__(16) float s_qs[2][NB], s_nm[NSTR][NB];  // per column: Q's scale, minus the reference
-    __shared__ __align__(16) float s_red[C::kSoft][128 / NC][NC], s_dl[C::kSoft][NC], s_wt[NSTR][NB];
+    __shared__ int fail, s_issued;
+    __shared__ __align__(16) float s_qs[2][NB], s_nm[NB];  // per column: Q's scale, minus the reference
+    __shared__ __align__(16) float s_red[128 / NC][NC], s_dl[NC];
     __shared__ int s_tok[2][NB];        // new token of each row
     __shared__ long long s_row[2][NB];  // out row, or -1
-    __shared__ uint32_t s_mw[C::kSoft][NC][5];  // the mask words of a tile's new tokens
+    __shared__ uint32_t s_mw[NC][5];    // the mask words of a tile's new tokens
     __shared__ uint2 s_lv[BITS == 4 ? 16 : 1];
-    __shared__ Segment s_seg[kRing];
-    __shared__ uint64_t seg_full[kRing], seg_free[kRing];
-    __shared__ long long s_chunk[kChunks];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x;
-
     uint8_t *base = dyn + ((1024u - (umma::smem_u32(dyn) & 1023u)) & 1023u);
     const uint32_t sm = umma::smem_u32(base);
-    const uint32_t p0 = sm, k80 = p0 + 2 * C::kP, v80 = k80 + 2 * C::kOp, q0 = v80 + 2 * C::kOp, kr0 = q0 + 2 * C::kQ,
-                   vr0 = kr0 + SK * C::kRaw;
+    const uint32_t p0 = sm, k80 = p0 + C::kP, v80 = k80 + C::kOp, q0 = v80 + C::kOp, kr0 = q0 + C::kQ, vr0 = kr0 + SK * C::kRaw,
+                   sc0 = vr0 + SV * C::kRaw;
     if (tid == 0) {
         fail = 0;
-        s_issued[0] = s_issued[1] = 0;
+        s_issued = 0;
         for (int i = 0; i < kRing; ++i) {
             umma::mbar_init(&seg_full[i], 1);
-            umma::mbar_init(&seg_free[i], 15);  // every other warp
+            umma::mbar_init(&seg_free[i], C::kWarps - 1);  // every other warp
         }
         for (int i = 0; i < SK; ++i) {
             umma::mbar_init(&k_full[i], 1);
-            umma::mbar_init(&k_empty[i], BITS == 8 ? 1 : 2);  // S done, or the converters
+            umma::mbar_init(&k_empty[i], 1);  // S done, or the converter
         }
         for (int i = 0; i < SV; ++i) {
             umma::mbar_init(&v_full[i], 33);  // the codes; each lane's part of the scales
-            umma::mbar_init(&v_empty[i], (BITS == 8 ? 1 : 4) + C::kParty);  // O done, or the converters; scales read
+            umma::mbar_init(&v_empty[i], (BITS == 8 ? 1 : C::kConv) + 4);  // O done, or the converters; softmax warps
         }
         for (int i = 0; i < 2; ++i) {
-            umma::mbar_init(&ko_full[i], 2);
-            umma::mbar_init(&vo_full[i], 2);
-            umma::mbar_init(&ko_done[i], 1);
             umma::mbar_init(&s_full[i], 1);
-            umma::mbar_init(&s_free[i], C::kParty);
-            umma::mbar_init(&p_full[i], C::kParty);
-            umma::mbar_init(&pv_done[i], 1);
-            umma::mbar_init(&q_full[i], C::kQWarps);
-            umma::mbar_init(&q_free[i], 1 + 4 * C::kSoft);  // S done, softmax warps done
+            umma::mbar_init(&s_free[i], 4);
+            umma::mbar_init(&m_free[i], 4);
+            umma::mbar_init(&q_full[i], 1);
         }
+        umma::mbar_init(&ko_full, 1);
+        umma::mbar_init(&ko_done, 1);
+        umma::mbar_init(&vo_full, 1);
+        umma::mbar_init(&p_full, 4);
+        umma::mbar_init(&pv_done, 1);
+        umma::mbar_init(&q_free, 1);
         umma::mbar_init(&drain, 2);
         umma::mbar_init(&never, 1);
         umma::fence_barrier_init();
     }
-    if (warp == 3) {
+    if (warp == 2) {
         umma::tmem_alloc(&tmem_base, C::kTmem);
         umma::tmem_relinquish();
     }
-    for (int i = tid; i < NSTR * NB; i += C::kWarps * 32) (&s_nm[0][0])[i] = 0.0f;
+    if (tid < NB) s_nm[tid] = 0.0f;
     if (BITS == 4 && tid < 16) s_lv[tid] = levels_of(tid);
     __syncthreads();
     umma::tc_fence_after();
     const uint32_t tmem = tmem_base;
-    const uint32_t t_o = tmem + 4 * NB;  // S: two buffers of 2 NB columns; O: 3 NB per stream
+    const uint32_t t_o = tmem + 4 * NB;  // S: two buffers of 2 NB columns; O: 3 NB
     volatile int *vfail = &fail;
     // The next segment for this warp (n of them so far); false: no more, or gave up.
     auto next_segment = [&](Segment &g, int n) {
@@ -621,106 +603,58 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
         if (lane == 0) umma::mbar_arrive(&seg_free[i]);
         return __all_sync(0xFFFFFFFFu, ok) && g.t1 > 0;
     };
-    // One tile's K or V, by a whole warp: lane i fetches the tile's i-th piece (a page, or 128 tokens of one).
-    // Issuing a copy takes a warp about 90 clocks, so K and V have a warp each where they can, and the scales, 16
-    // bytes at a time, go by plain asynchronous copies of all lanes.  Waits for the buffer; false: gave up.
-    auto load_tile = [&](const Segment &g, int t, bool is_k, uint64_t *full, uint64_t *empty, uint32_t dst, uint32_t parity, bool used) {
-        const int pr_log2 = min(a.page_log2, 7), pr = 1 << pr_log2;
-        const int tok = t * kTile + (lane << pr_log2);
-        const bool there = lane < (kTile >> pr_log2) && tok < g.kv;
-        const int page = there ? a.table[g.b * a.table_stride + (tok >> a.page_log2)] : 0;
-        const bool good = there && page >= 0 && page < a.num_pages;
-        if (there && !good) raise_error(a.err, QVG_ERR_INVALID_ARG);
-        const int off = tok & ((1 << a.page_log2) - 1);
-        const long long at = good ? ((static_cast<long long>(page) * a.H + g.h) << a.page_log2) + off : -1;  // first row
-        const bool ok = !used || wait(empty, parity ^ 1u, vfail, a.wait_ns);
-        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
-        const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
-        if (lane == 0) umma::mbar_arrive_expect_tx(full, n * C::kRow * pr);
-        __syncwarp();
-        if (good) {
-            if constexpr (BITS == 8)
-                tma_load_4d(dst + lane * pr * C::kRow, is_k ? &kmap : &vmap, off, g.h, page, full);
-            else
-                bulk_copy(dst + lane * pr * C::kRow, (is_k ? a.kc : a.vc) + at * C::kRow, pr * C::kRow, full);
-        }
-        __syncwarp();
-        if (!is_k) {
-            // the scales: 128 G bytes each of K's and V's, in 16-byte parts
-#pragma unroll
-            for (int i0 = 0; i0 < 16 * C::G; i0 += 32) {
-                const int i = i0 + lane;
-                const bool v = i >= 8 * C::G;
-                const int c = v ? i - 8 * C::G : i, first = c * (16 / C::G);  // part c begins with this key's
-                const long long piece_at = __shfl_sync(0xFFFFFFFFu, at, (first >> pr_log2) & 31);
-                if (i < 16 * C::G && piece_at >= 0) {
-                    const uint8_t *from = (v ? a.vs : a.ks) + (piece_at + (first & (pr - 1))) * C::G;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst + C::kRaw + (v ? 512 : 0) + c * 16), "l"(from)
-                                 : "memory");
-                }
-            }
-            umma::cp_async_arrive_noinc(full);
-        }
-        return true;
-    };
 
-    if (warp >= 4 && warp < 12) {
-        // ---- softmax: thread = key (S^T's row), columns [c0, c0 + NC) --------------------------
-        constexpr int kAll = 1 + C::kSoft, kAllThreads = 128 * C::kSoft;  // the barrier of all softmax warps
-        const int wg = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
-        const int own = wg * NSTR / C::kSoft;  // the stream
-        const int c0 = (wg % (C::kSoft / NSTR)) * NC;
+    if (warp >= 4 && warp < 8) {
+        // ---- softmax: thread = key (S^T's row), all columns -------------------------------------
+        const int quad = warp & 3, r = quad * 32 + lane;
         const uint32_t t_lane = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t t_own = t_o + t_lane + own * 3 * NB;
+        uint8_t *p_base = base + (p0 - sm), *prow = p_base + r * 128;
         Segment g;
         Ring<SV> rv;
         int it = 0, n_seg = 0;
         bool dead = false;
         while (!dead && next_segment(g, n_seg)) {
             const int qb = n_seg & 1;
-            const bool q_ok = wait(&q_full[qb], (n_seg >> 1) & 1, vfail, a.wait_ns);
+            const bool q_ok = wait(&q_full[n_seg & 1], (n_seg >> 1) & 1, vfail, a.wait_ns);
             ++n_seg;
             uint64_t l2[NC / 2];
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) l2[i] = 0;
             const int hist = g.kv - g.nq;  // keys before the new tokens
             const int clear = a.mode == QVG_MASK_NONE ? g.kv : min(g.kv, hist);
-            int last = -1;      // this warpgroup's latest tile of the segment
             bool late = false;  // this thread gave up a wait: all agree on that at the next barrier
             for (int t = g.t0; t < g.t1; ++t, ++it, rv.next()) {
                 const int bf = it & 1;
-                if (NSTR == 2 && bf != own) continue;
-                const bool first = last < 0;
+                const bool first = t == g.t0;
                 bool ok = q_ok && !late && wait(&v_full[rv.i], rv.parity, vfail, a.wait_ns);  // (the scales)
-                uint8_t *slot_v = base + (vr0 - sm) + rv.i * C::kVSlot;
-                const uint8_t *sc = slot_v + C::kRaw;
+                const uint8_t *sc = base + (sc0 - sm) + rv.i * C::kScales;
                 uint32_t kb = 0, vb = 0;
                 if constexpr (BITS == 8) {
                     kb = sc[r];
-                    vb = sc[512 + r];
+                    vb = sc[128 + r];
                 } else {
 #pragma unroll
                     for (int j = 0; j < C::G; ++j) {
                         kb = max(kb, static_cast<uint32_t>(sc[r * C::G + j]));
-                        vb = max(vb, static_cast<uint32_t>(sc[512 + r * C::G + j]));
+                        vb = max(vb, static_cast<uint32_t>(sc[128 * C::G + r * C::G + j]));
                     }
                 }
-                // 4 bits: the operands are 2^6 times the values over the largest scale
                 const int key = t * kTile + r;
                 if (key >= g.kv) kb = vb = 127u;  // (whatever is there)
+                // 4 bits: the operands are 2^6 times the values over the largest scale
                 const float ka = scale_of(kb) * (BITS == 8 ? a.scale_log2 : a.scale_log2 * 0x1p-6f);
                 const bool v_nan = vb == 255u;  // weighed as 1, and made a NaN below
                 const float sv = v_nan ? 1.0f : scale_of(vb) * (BITS == 8 ? 1.0f : 0x1p-6f);
                 const float lsv = v_nan ? 0.0f : static_cast<float>(static_cast<int>(vb) - (BITS == 8 ? 127 : 133));
                 const bool part = (t + 1) * kTile > clear;
                 const uint64_t ka2 = pk2(ka, ka), lo2 = pk2(0.0625f, 0.0625f);
-                ok = ok && wait(&s_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
-                umma::tc_fence_after();
-                const uint32_t t_s = tmem + t_lane + bf * 2 * NB + c0;
                 uint32_t hidden = 0;  // columns that do not see this key, where that can be
                 if (part)
-                    hidden = hide_keys<NC>(a, t_s, NB, &s_tok[qb][c0], s_mw[wg], wg, r, g.q0, key, g.kv, key - hist,
-                                           max(0, t * kTile - hist) >> 5);
+                    hidden = hidden_rows<NC>(a, g.r * NB, s_tok[qb], s_mw, r, g.q0, key >= g.kv, key - hist,
+                                             max(0, t * kTile - hist) >> 5);
+                ok = ok && wait(&s_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                umma::tc_fence_after();
+                const uint32_t t_s = tmem + t_lane + bf * 2 * NB;
                 float y[NC];  // logits (base 2) less the reference
                 for (bool settled = false;;) {
 #pragma unroll
@@ -729,8 +663,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                         tmem_ld_pair(t_s + c, NB, v, u);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float4 qs = *reinterpret_cast<const float4 *>(&s_qs[qb][c0 + c + 4 * i]);
-                            const float4 nm = *reinterpret_cast<const float4 *>(&s_nm[own][c0 + c + 4 * i]);
+                            const float4 qs = *reinterpret_cast<const float4 *>(&s_qs[qb][c + 4 * i]);
+                            const float4 nm = *reinterpret_cast<const float4 *>(&s_nm[c + 4 * i]);
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const int k = 4 * i + 2 * h;
@@ -742,32 +676,32 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                             }
                         }
                     }
+                    if (part) {
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) y[c] = (hidden >> c) & 1u ? -INFINITY : y[c];
+                    }
                     if (settled) break;
                     float top4[4] = {y[0], y[1], y[2], y[3]};
 #pragma unroll
                     for (int c = 4; c < NC; ++c) top4[c & 3] = fmaxf(top4[c & 3], y[c]);
                     const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-                    if (!any_of(wg + 1, 128, first || !ok || top + lsv > kTop)) break;
-                    if (!first) ok = ok && wait(&pv_done[(it - NSTR) & 1], ((it - NSTR) >> 1) & 1, vfail, a.wait_ns);  // O's latest
-                    dead = !set_references<NC, NB>(t_s, t_own + c0, &s_qs[qb][c0], &s_nm[own][c0],
-                                                   reinterpret_cast<float *>(base + (p0 - sm) + bf * C::kP + (NSTR == 1 ? wg * 16384 : 0)),
-                                                   s_red[wg], s_dl[wg], wg, r, ka,
-                                                   lsv, first, ok);
+                    if (!any_of(1, 128, first || !ok || top + lsv > kTop)) break;
+                    if (!first) ok = ok && wait(&pv_done, (it - 1) & 1, vfail, a.wait_ns);  // O's latest
+                    dead = !set_references<NC, NB>(t_s, t_o + t_lane, s_qs[qb], s_nm, reinterpret_cast<float *>(p_base), s_red, s_dl, r,
+                                                   ka, lsv, hidden, first, ok);
                     if (dead) break;
 #pragma unroll
-                    for (int i = 0; i < NC / 2; ++i) l2[i] = mul2(l2[i], pk2(s_dl[wg][2 * i], s_dl[wg][2 * i + 1]));
+                    for (int i = 0; i < NC / 2; ++i) l2[i] = mul2(l2[i], pk2(s_dl[2 * i], s_dl[2 * i + 1]));
                     settled = true;
                 }
                 if (dead) break;
-                last = it;
                 umma::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive(&s_free[bf]);
-                if (BITS == 8 && part && c0 == 0) clean_values<D>(slot_v, max(0, min(hist, g.kv) - t * kTile), g.kv - t * kTile, r);
-                uint8_t *prow = base + (p0 - sm) + bf * C::kP + r * 128;
-                auto place = [&](int z, int c) {  // part z of this thread's columns c .. c + 15 in its row of weights
-                    const int n = z * NB + c0 + c;
-                    return prow + (n >> 7) * (kTile * 128) + ((((n >> 4) & 7) ^ (r & 7)) << 4);
+                if (BITS == 8 && part)
+                    clean_values<D>(base + (vr0 - sm) + rv.i * C::kRaw, max(0, min(hist, g.kv) - t * kTile), g.kv - t * kTile, r);
+                auto place = [&](int z, int c) {  // part z of columns c .. c + 15 in this thread's row of weights
+                    return prow + ((((z * NB + c) >> 4) ^ (r & 7)) << 4);
                 };
                 const uint64_t sv2 = pk2(sv, sv);
 #pragma unroll
@@ -787,8 +721,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                         }
                         three_parts(w[0], w[1], h[0][k], h[1][k], h[2][k]);
                     }
-                    // (the buffer's last weights have been used up by now)
-                    if (c == 0 && it >= 2 && !wait(&pv_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns)) late = true;
+                    // (the last tile's weights have been used up by now)
+                    if (c == 0 && it > 0 && !wait(&pv_done, (it - 1) & 1, vfail, a.wait_ns)) late = true;
 #pragma unroll
                     for (int z = 0; z < 3; ++z) *reinterpret_cast<uint4 *>(place(z, c)) = make_uint4(h[z][0], h[z][1], h[z][2], h[z][3]);
                 }
@@ -800,93 +734,66 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                 umma::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    umma::mbar_arrive(&p_full[bf]);
+                    umma::mbar_arrive(&p_full);
                     umma::mbar_arrive(&v_empty[rv.i]);
                 }
             }
-            // ---- the segment's sums (all warpgroups come here, also after a failure) ------------
-            bool ok = !dead && !late && q_ok;
-            if (ok && last >= 0) ok = wait(&pv_done[last & 1], (last >> 1) & 1, vfail, a.wait_ns);
-            {
-                // the weights' buffers are free now: l's column sums go through them
-                float *scratch = reinterpret_cast<float *>(base + (p0 - sm) + wg * 16384);
+            if (dead) break;
+            // ---- the segment's sums; the weights' buffer is free: l's column sums go through it ----
+            bool ok = !late && q_ok && wait(&pv_done, (it - 1) & 1, vfail, a.wait_ns);
+            float *scratch = reinterpret_cast<float *>(p_base);
+            if (ok) {
 #pragma unroll
                 for (int i = 0; i < NC / 2; ++i) *reinterpret_cast<uint64_t *>(scratch + r * NC + 2 * i) = l2[i];
-                dead = any_of(wg + 1, 128, !ok);
-                if (!dead) reduce_columns<NC, false>(scratch, s_red[wg], r);
             }
-            dead = any_of(kAll, kAllThreads, dead);
+            dead = any_of(1, 128, !ok);
             if (dead) break;
+            reduce_columns<NC, false>(scratch, s_red, r);
+            any_of(1, 128, false);
             umma::tc_fence_after();
             const int slot = cta * 2 + (g.t0 > 0 ? 0 : 1);
             const bool whole = g.whole();
-            if (wg == 0 && r < NB) {
-                float l[NSTR], m = -INFINITY, sum = 0.0f;
-#pragma unroll
-                for (int z = 0; z < NSTR; ++z) {
-                    const float(&red)[128 / NC][NC] = s_red[z * (C::kSoft / NSTR) + r / NC];
-                    l[z] = 0.0f;
-                    for (int i = 0; i < 128 / NC; ++i) l[z] += red[i][r % NC];
-                    if (l[z] != 0.0f) m = fmaxf(m, -s_nm[z][r]);
-                }
-                float wt[NSTR];
-#pragma unroll
-                for (int z = 0; z < NSTR; ++z) {
-                    wt[z] = l[z] != 0.0f ? (NSTR == 2 ? ex2(-s_nm[z][r] - m) : 1.0f) : 0.0f;
-                    if (wt[z] != 0.0f) sum = fmaf(l[z], wt[z], sum);
-                }
-                const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-                for (int z = 0; z < NSTR; ++z) s_wt[z][r] = wt[z] * inv;
+            if (r < NB) {
+                float l = 0.0f;
+                for (int i = 0; i < 128 / NC; ++i) l += s_red[i][r];
+                const float m = -s_nm[r];
+                s_dl[r] = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+                s_nm[r] = 0.0f;  // for the next unit
                 const long long row = s_row[qb][r];
                 if (!whole) {
                     a.pm[static_cast<long long>(slot) * NB + r] = m;
-                    a.pl[static_cast<long long>(slot) * NB + r] = sum;
+                    a.pl[static_cast<long long>(slot) * NB + r] = l;
                 } else if (a.lse && row >= 0) {
-                    a.lse[(row % a.Hq) * a.total_q + row / a.Hq] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+                    a.lse[(row % a.Hq) * a.total_q + row / a.Hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
                 }
             }
-            any_of(kAll, kAllThreads, false);
-            if (wg < NSTR)
-                for (int n = r; n < NB; n += 128) s_nm[wg][n] = 0.0f;  // for the next unit
-            constexpr int kShare = NB / C::kSoft;  // columns of O a warpgroup hands out
+            any_of(1, 128, false);
 #pragma unroll 1
-            for (int c = wg * kShare; c < (wg + 1) * kShare; c += 8) {
-                float o[8];
+            for (int c = 0; c < NB; c += 8) {
+                uint32_t x[3][8];
+                tmem_ld8x3(t_o + t_lane + c, NB, x[0], x[1], x[2]);
+                if (r >= D) continue;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = 0.0f;
-#pragma unroll
-                for (int z = 0; z < NSTR; ++z) {
-                    uint32_t x[3][8];
-                    tmem_ld8x3(t_o + t_lane + z * 3 * NB + c, NB, x[0], x[1], x[2]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float w = s_wt[z][c + i];
-                        const float f = (__uint_as_float(x[2][i]) + __uint_as_float(x[1][i])) + __uint_as_float(x[0][i]);
-                        if (w != 0.0f) o[i] = fmaf(f, w, o[i]);  // (a stream without a tile holds anything)
-                    }
-                }
-                if (r < D) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int n = c + i;
-                        const long long row = s_row[qb][n];
-                        if (row < 0) continue;
-                        if (!whole)
-                            a.po[(static_cast<long long>(slot) * NB + n) * D + r] = o[i];
-                        else if (a.out32)
-                            a.out32[row * D + r] = o[i];
-                        else
-                            a.out16[row * D + r] = f32_to_bf16(o[i]);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const long long row = s_row[qb][c + i];
+                    if (row < 0) continue;
+                    const float o = ((__uint_as_float(x[2][i]) + __uint_as_float(x[1][i])) + __uint_as_float(x[0][i])) * s_dl[c + i];
+                    if (!whole)
+                        a.po[(static_cast<long long>(slot) * NB + c + i) * D + r] = o;
+                    else if (a.out32)
+                        a.out32[row * D + r] = o;
+                    else
+                        a.out16[row * D + r] = f32_to_bf16(o);
                 }
             }
             umma::tc_fence_before();
-            any_of(kAll, kAllThreads, false);  // everything of this segment has been read
-            if (lane == 0) umma::mbar_arrive(&q_free[qb]);
+            any_of(1, 128, false);  // everything of this segment has been read
+            if (lane == 0) umma::mbar_arrive(&m_free[qb]);
         }
-    } else if (warp == 0 || (BITS == 8 && warp == 12)) {
-        // ---- loads: warp 0 K (4 bits: and V), warp 12 V ---------------------------------------------
+    } else if (warp == 0) {
+        // ---- loads: lane i fetches a tile's i-th piece (a page, or 128 tokens of one); the scales, 16 bytes at a
+        // time, go by plain asynchronous copies of all lanes (issuing a bulk copy takes a warp about 90 clocks) ----
+        const int pr_log2 = min(a.page_log2, 7), pr = 1 << pr_log2;
         Segment g;
         Ring<SK> rk;
         Ring<SV> rv;
@@ -894,26 +801,54 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
         bool ok = true;
         while (ok && next_segment(g, n_seg)) {
             ++n_seg;
-            for (int t = g.t0; ok && t < g.t1; ++t, ++it) {
-                if (warp == 0) {
-                    ok = load_tile(g, t, true, &k_full[rk.i], &k_empty[rk.i], kr0 + rk.i * C::kRaw, rk.parity, it >= SK);
-                    rk.next();
-                }
-                if (BITS == 4 || warp != 0) {
-                    ok = ok && load_tile(g, t, false, &v_full[rv.i], &v_empty[rv.i], vr0 + rv.i * C::kVSlot, rv.parity, it >= SV);
-                    rv.next();
+            for (int t = g.t0; t < g.t1; ++t, ++it, rk.next(), rv.next()) {
+                const int tok = t * kTile + (lane << pr_log2);
+                const bool there = lane < (kTile >> pr_log2) && tok < g.kv;
+                const int page = there ? a.table[g.b * a.table_stride + (tok >> a.page_log2)] : 0;
+                const bool good = there && page >= 0 && page < a.num_pages;
+                if (there && !good) raise_error(a.err, QVG_ERR_INVALID_ARG);
+                const int off = tok & ((1 << a.page_log2) - 1);
+                const long long at = good ? ((static_cast<long long>(page) * a.H + g.h) << a.page_log2) + off : -1;  // first row
+                const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, good)) * C::kRow * pr;
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {  // K, V
+                    uint64_t *full = which ? &v_full[rv.i] : &k_full[rk.i];
+                    const uint32_t dst = (which ? vr0 + rv.i * C::kRaw : kr0 + rk.i * C::kRaw) + lane * pr * C::kRow;
+                    if (it >= (which ? SV : SK))
+                        ok = ok && wait(which ? &v_empty[rv.i] : &k_empty[rk.i], (which ? rv.parity : rk.parity) ^ 1u, vfail, a.wait_ns);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    if (lane == 0) umma::mbar_arrive_expect_tx(full, bytes);
+                    __syncwarp();
+                    if (good) {
+                        if constexpr (BITS == 8)
+                            tma_load_4d(dst, which ? &vmap : &kmap, off, g.h, page, full);
+                        else
+                            bulk_copy(dst, (which ? a.vc : a.kc) + at * C::kRow, pr * C::kRow, full);
+                    }
+                    __syncwarp();
                 }
                 if (!ok) break;
+#pragma unroll
+                for (int i0 = 0; i0 < 16 * C::G; i0 += 32) {
+                    const int i = i0 + lane;
+                    const bool v = i >= 8 * C::G;
+                    const int c = v ? i - 8 * C::G : i, first = c * (16 / C::G);  // part c begins with this key's
+                    const long long piece_at = __shfl_sync(0xFFFFFFFFu, at, (first >> pr_log2) & 31);
+                    if (i < 16 * C::G && piece_at >= 0)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(sc0 + rv.i * C::kScales + i * 16),
+                                     "l"((v ? a.vs : a.ks) + (piece_at + (first & (pr - 1))) * C::G)
+                                     : "memory");
+                }
+                umma::cp_async_arrive_noinc(&v_full[rv.i]);
             }
         }
-        if (lane == 0) {
-            if (warp == 0) s_issued[0] = it;
-            if (BITS == 4 || warp != 0) s_issued[1] = it;
-        }
+        if (lane == 0) s_issued = it;
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 1) {
         // ---- S = K Q^T -------------------------------------------------------------------
         constexpr uint32_t id = idesc_f8(128, 2 * NB, 0);
+        const uint64_t dq = desc_rows8<D>(q0);
         Segment g;
         Ring<SK> rk;
         int it = 0, n_seg = 0;
@@ -921,31 +856,31 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
         while (ok && next_segment(g, n_seg)) {
             if (lane == 0) {
                 ok = wait(&q_full[n_seg & 1], (n_seg >> 1) & 1, vfail, a.wait_ns);
-                const uint64_t dq = desc_rows8<D>(q0 + (n_seg & 1) * C::kQ);
                 for (int t = g.t0; ok && t < g.t1; ++t, ++it, rk.next()) {
                     const int bf = it & 1;
-                    ok = BITS == 8 ? wait(&k_full[rk.i], rk.parity, vfail, a.wait_ns)
-                                   : wait(&ko_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                    ok = BITS == 8 ? wait(&k_full[rk.i], rk.parity, vfail, a.wait_ns) : wait(&ko_full, it & 1, vfail, a.wait_ns);
                     if (it >= 2) ok = ok && wait(&s_free[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
                     if (!ok) break;
                     umma::tc_fence_after();
-                    const uint64_t dk = desc_rows8<D>(BITS == 8 ? kr0 + rk.i * C::kRaw : k80 + bf * C::kOp);
+                    const uint64_t dk = desc_rows8<D>(BITS == 8 ? kr0 + rk.i * C::kRaw : k80);
 #pragma unroll
                     for (int s = 0; s < D / 32; ++s) mma_f8(tmem + bf * 2 * NB, dk + 2 * s, dq + 2 * s, id, s != 0);
                     umma::mma_commit(&s_full[bf]);
-                    umma::mma_commit(BITS == 8 ? &k_empty[rk.i] : &ko_done[bf]);
+                    umma::mma_commit(BITS == 8 ? &k_empty[rk.i] : &ko_done);
                     // test hook: with S in flight, wait for what never comes
                     if (it == 0 && a.inject) ok = wait(&never, 0, vfail, a.wait_ns);
                 }
-                umma::mma_commit(&q_free[n_seg & 1]);
+                umma::mma_commit(&q_free);
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
             ++n_seg;
         }
         if (lane == 0) umma::mma_commit(&drain);
+        __syncwarp();
     } else if (warp == 2) {
         // ---- O += V^T P^T (its own warp: starting a batch of products takes longer than the batch) ----
         constexpr uint32_t id = idesc_f8(128, 3 * NB, 1) | (1u << 15) | (1u << 16);  // both MN-major
+        const uint64_t dp = desc_rows8<128>(p0);
         Segment g;
         Ring<SV> rv;
         int it = 0, n_seg = 0;
@@ -954,21 +889,16 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
             ++n_seg;
             if (lane == 0) {
                 for (int t = g.t0; ok && t < g.t1; ++t, ++it, rv.next()) {
-                    const int bf = it & 1;
                     // (4 bits: the loaded codes' buffer may be in its next use by now)
-                    ok = BITS == 8 ? wait(&v_full[rv.i], rv.parity, vfail, a.wait_ns)
-                                   : wait(&vo_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
-                    ok = ok && wait(&p_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                    ok = BITS == 8 ? wait(&v_full[rv.i], rv.parity, vfail, a.wait_ns) : wait(&vo_full, it & 1, vfail, a.wait_ns);
+                    ok = ok && wait(&p_full, it & 1, vfail, a.wait_ns);
                     if (!ok) break;
                     umma::tc_fence_after();
                     // d = 64: the accumulator's upper 64 rows repeat the lower ones and are not read
-                    const uint64_t dv = desc_rows8<D>(BITS == 8 ? vr0 + rv.i * C::kVSlot : v80 + bf * C::kOp);
-                    const uint64_t dp = desc_rows8<128>(p0 + bf * C::kP, kTile * 128);
-                    const bool fresh = t - g.t0 < NSTR;  // the stream's first tile of the unit
+                    const uint64_t dv = desc_rows8<D>(BITS == 8 ? vr0 + rv.i * C::kRaw : v80);
 #pragma unroll
-                    for (int s = 0; s < kTile / 32; ++s)
-                        mma_f8(t_o + (NSTR == 2 ? bf * 3 * NB : 0), dv + s * (32 * D / 16), dp + s * 256, id, !(fresh && s == 0));
-                    umma::mma_commit(&pv_done[bf]);
+                    for (int s = 0; s < kTile / 32; ++s) mma_f8(t_o, dv + s * (32 * D / 16), dp + s * 256, id, !(t == g.t0 && s == 0));
+                    umma::mma_commit(&pv_done);
                     if (BITS == 8) umma::mma_commit(&v_empty[rv.i]);
                 }
             }
@@ -981,7 +911,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
         }
         __syncwarp();
     } else if (warp == 3) {
-        // ---- this CTA's part of the line, unit by unit (4 bits: and the unit's Q rows) ---------------
+        // ---- this CTA's part of the line, unit by unit, and each unit's Q rows ------------------------
         // tiles of all sequences, by chunks of `span` sequences
         const int span = ((a.B + kChunks - 1) / kChunks + 31) & ~31;
         long long total = 0;
@@ -1058,95 +988,80 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
                 umma::mbar_arrive(&seg_full[i]);
             }
             if (g.t1 == 0) break;
-            if constexpr (BITS == 4) {
-                const int qb = n_seg & 1;
-                if (n_seg >= 2) ok = wait(&q_free[qb], ((n_seg >> 1) - 1) & 1, vfail, a.wait_ns);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                make_q<D, NB>(a, g, base + (q0 - sm) + qb * C::kQ, s_qs[qb], s_tok[qb], s_row[qb], 0, 256 / D);
-                if (lane == 0) umma::mbar_arrive(&q_full[qb]);
-            }
-        }
-        if (!ok && lane == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
-    } else if (BITS == 8 && warp >= 13) {
-        // ---- Q rows of the coming units ----------------------------------------------------------
-        Segment g;
-        int n_seg = 0;
-        bool ok = true;
-        while (ok && next_segment(g, n_seg)) {
+            // Q's rows, once the last unit's products with its own are done
             const int qb = n_seg & 1;
-            if (n_seg >= 2) ok = wait(&q_free[qb], ((n_seg >> 1) - 1) & 1, vfail, a.wait_ns);
+            if (n_seg >= 1) ok = wait(&q_free, (n_seg - 1) & 1, vfail, a.wait_ns);
+            if (n_seg >= 2) ok = ok && wait(&m_free[qb], ((n_seg >> 1) - 1) & 1, vfail, a.wait_ns);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
-            make_q<D, NB>(a, g, base + (q0 - sm) + qb * C::kQ, s_qs[qb], s_tok[qb], s_row[qb], (warp - 13) * (256 / D), 3 * (256 / D));
+            make_q<D, NB>(a, g, base + (q0 - sm), s_qs[qb], s_tok[qb], s_row[qb]);
             if (lane == 0) umma::mbar_arrive(&q_full[qb]);
-            ++n_seg;
         }
-    } else if (BITS == 4 && warp >= 12) {
-        // ---- 4-bit codes into e4m3 operands: one (row, 32-channel group) a step, its scale relative to the row's
-        // largest.  A word's eight magnitudes are two byte permutes of the group's eight levels.
-        // (two warps for K, two for V: V's operand waits for weights, K's must not)
-        const int which = (warp - 12) >> 1, w = tid - 384 - which * 64;
-        constexpr int GR = D / 32, kThreads = 64;
+        if (!ok && lane == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
+    } else if (BITS == 4) {
+        // ---- 4-bit codes into e4m3 operands, a warp for K and one for V: one (row, 32-channel group) a step, its
+        // scale relative to the row's largest.  A word's eight magnitudes are two byte permutes of the group's eight
+        // levels. ----
+        const int which = warp - 8;
+        constexpr int GR = D / 32;
+        Segment g;
         Ring<SK> rk;
         Ring<SV> rv;
-        Segment g;
         int it = 0, n_seg = 0;
         bool ok = true;
         while (ok && next_segment(g, n_seg)) {
             ++n_seg;
             for (int t = g.t0; t < g.t1; ++t, ++it, rk.next(), rv.next()) {
-            const int bf = it & 1;
-            ok = wait(&v_full[rv.i], rv.parity, vfail, a.wait_ns);  // (K's scales come with V's codes)
-            if (!which) ok = ok && wait(&k_full[rk.i], rk.parity, vfail, a.wait_ns);
-            if (it >= 2) ok = ok && wait(which ? &pv_done[bf] : &ko_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            const uint8_t *src = base + ((which ? vr0 + rv.i * C::kVSlot : kr0 + rk.i * C::kRaw) - sm);
-            const uint8_t *scales = base + (vr0 - sm) + rv.i * C::kVSlot + C::kRaw + which * 512;
-            uint8_t *dst = base + ((which ? v80 : k80) - sm) + bf * C::kOp;
+                ok = wait(&v_full[rv.i], rv.parity, vfail, a.wait_ns);  // (K's scales come with V's codes)
+                if (!which) ok = ok && wait(&k_full[rk.i], rk.parity, vfail, a.wait_ns);
+                if (it >= 1) ok = ok && wait(which ? &pv_done : &ko_done, (it - 1) & 1, vfail, a.wait_ns);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const uint8_t *src = base + ((which ? vr0 + rv.i * C::kRaw : kr0 + rk.i * C::kRaw) - sm);
+                const uint8_t *scales = base + (sc0 - sm) + rv.i * C::kScales + which * 128 * GR;
+                uint8_t *dst = base + ((which ? v80 : k80) - sm);
 #pragma unroll 4
-            for (int i = 0; i < kTile * GR / kThreads; ++i) {
-                const int idx = w + kThreads * i, row = idx / GR, gq = idx % GR;
-                const uint4 v = *reinterpret_cast<const uint4 *>(src + idx * 16);
-                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-                const uint8_t *sc = scales + row * GR;
-                uint32_t top, mine;
-                if constexpr (GR == 4) {
-                    const uint32_t all = *reinterpret_cast<const uint32_t *>(sc);
-                    const uint32_t m = __vmaxu4(all, all >> 16);
-                    top = max(m & 0xFFu, (m >> 8) & 0xFFu);
-                    mine = (all >> (8 * gq)) & 0xFFu;
-                } else {
-                    const uint32_t all = *reinterpret_cast<const uint16_t *>(sc);
-                    top = max(all & 0xFFu, all >> 8);
-                    mine = (all >> (8 * gq)) & 0xFFu;
-                }
-                const uint2 lv = s_lv[min(top - mine, 15u)];
-                uint32_t o[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t mg = vw[j] & 0x77777777u, sg = vw[j] & 0x88888888u;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t m = __byte_perm(lv.x, lv.y, mg >> (16 * k));
-                        // 0xFF where the sign is set, 0x80 elsewhere: its low bit is the sign
-                        uint32_t s;
-                        asm("prmt.b32 %0, %1, 0, %2;" : "=r"(s) : "r"(0x80u), "r"(sg >> (16 * k)));
-                        o[2 * j + k] = m | ((s << 7) & 0x80808080u);
+                for (int i = 0; i < kTile * GR / 32; ++i) {
+                    const int idx = lane + 32 * i, row = idx / GR, gq = idx % GR;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(src + idx * 16);
+                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+                    const uint8_t *sc = scales + row * GR;
+                    uint32_t top, mine;
+                    if constexpr (GR == 4) {
+                        const uint32_t all = *reinterpret_cast<const uint32_t *>(sc);
+                        const uint32_t m = __vmaxu4(all, all >> 16);
+                        top = max(m & 0xFFu, (m >> 8) & 0xFFu);
+                        mine = (all >> (8 * gq)) & 0xFFu;
+                    } else {
+                        const uint32_t all = *reinterpret_cast<const uint16_t *>(sc);
+                        top = max(all & 0xFFu, all >> 8);
+                        mine = (all >> (8 * gq)) & 0xFFu;
                     }
+                    const uint2 lv = s_lv[min(top - mine, 15u)];
+                    uint32_t o[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t mg = vw[j] & 0x77777777u, sg = vw[j] & 0x88888888u;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t m = __byte_perm(lv.x, lv.y, mg >> (16 * k));
+                            // 0xFF where the sign is set, 0x80 elsewhere: its low bit is the sign
+                            uint32_t s;
+                            asm("prmt.b32 %0, %1, 0, %2;" : "=r"(s) : "r"(0x80u), "r"(sg >> (16 * k)));
+                            o[2 * j + k] = m | ((s << 7) & 0x80808080u);
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(dst + swizzle8<D>(row * D + gq * 32)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(dst + swizzle8<D>(row * D + gq * 32 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
-                *reinterpret_cast<uint4 *>(dst + swizzle8<D>(row * D + gq * 32)) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4 *>(dst + swizzle8<D>(row * D + gq * 32 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+                umma::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    umma::mbar_arrive(which ? &vo_full : &ko_full);
+                    if (!which) umma::mbar_arrive(&k_empty[rk.i]);
+                    umma::mbar_arrive(&v_empty[rv.i]);
+                }
             }
-            umma::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                umma::mbar_arrive(which ? &vo_full[bf] : &ko_full[bf]);
-                if (!which) umma::mbar_arrive(&k_empty[rk.i]);
-                umma::mbar_arrive(&v_empty[rv.i]);
-            }
-            }
-            ok = __all_sync(0xFFFFFFFFu, ok);
         }
     }
     __syncwarp();
@@ -1155,10 +1070,10 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 1)
     if (tid == 0 && *vfail) {
         raise_error(a.err, QVG_ERR_TIMEOUT);
         // the copies in flight land before the CTA ends
-        for (int j = max(0, s_issued[0] - SK); j < s_issued[0]; ++j) umma::mbar_wait(&k_full[j % SK], (j / SK) & 1, kDrainNs);
-        for (int j = max(0, s_issued[1] - SV); j < s_issued[1]; ++j) umma::mbar_wait(&v_full[j % SV], (j / SV) & 1, kDrainNs);
+        for (int j = max(0, s_issued - SK); j < s_issued; ++j) umma::mbar_wait(&k_full[j % SK], (j / SK) & 1, kDrainNs);
+        for (int j = max(0, s_issued - SV); j < s_issued; ++j) umma::mbar_wait(&v_full[j % SV], (j / SV) & 1, kDrainNs);
     }
-    if (warp == 3) {
+    if (warp == 2) {
         umma::tc_fence_after();
         umma::tmem_dealloc(tmem, C::kTmem);
     }
