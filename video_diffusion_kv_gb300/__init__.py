@@ -393,20 +393,29 @@ class _Device:
     __slots__ = ("dev", "was")
 
     def __init__(self, dev):
-        import torch
-        if dev.type != "cuda":
-            raise ValueError("CUDA tensors are wanted, got one on %s" % dev)
-        self.dev, self.was = dev.index, torch.cuda.current_device()
+        self.dev, self.was = dev, None
 
     def __enter__(self):
-        if self.dev != self.was:
-            import torch
+        import torch
+        if self.dev.type != "cuda":
+            raise ValueError("CUDA tensors are wanted, got one on %s" % self.dev)
+        was = torch.cuda.current_device()
+        if self.dev.index != was:
+            self.was = was
             torch.cuda.set_device(self.dev)
 
     def __exit__(self, *exc):
-        if self.dev != self.was:
+        if self.was is not None:
             import torch
             torch.cuda.set_device(self.was)
+
+
+def _raw_stream(stream, dev):
+    """The CUDA stream of a call on `dev`: the given one, or torch's current."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _empty(shape, dtype, dev, stream):
@@ -445,7 +454,7 @@ def rope(plan: RopePlan, x, positions, transpose=False, out=None, stream=None):
     with _Device(x.device):
         _check(lib().qvg_rope(plan._ref, x.data_ptr(), QVG_OUT_F32 if x.dtype == torch.float32 else QVG_OUT_BF16, n, H,
                               d, xs, positions.data_ptr(), 1 if transpose else 0, out.data_ptr(), os_,
-                              _stream(stream)), "qvg_rope")
+                              _raw_stream(stream, x.device)), "qvg_rope")
     return out
 
 
@@ -501,7 +510,7 @@ def paged_append(cache: PagedKV, k, v, slots, plan=None, positions=None, stream=
     with _Device(cache.device):
         _check(lib().qvg_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), n, ks, vs, slots.data_ptr(),
                                       None if plan is None else plan._ref,
-                                      None if plan is None else positions.data_ptr(), _stream(stream)),
+                                      None if plan is None else positions.data_ptr(), _raw_stream(stream, cache.device)),
                "qvg_paged_append")
 
 
@@ -519,7 +528,7 @@ def paged_read(cache: PagedKV, slots, out_dtype=QVG_OUT_BF16, k_out=None, v_out=
     _on(cache.device, "paged_read", slots=(slots, torch.int64), k_out=(k_out, dt), v_out=(v_out, dt))
     with _Device(cache.device):
         _check(lib().qvg_paged_read(cache._ref, slots.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(), out_dtype,
-                                    _stream(stream)), "qvg_paged_read")
+                                    _raw_stream(stream, cache.device)), "qvg_paged_read")
     return k_out, v_out
 
 
@@ -540,11 +549,12 @@ def tree_mask(parents, max_q, cu_q=None, out=None, stream=None):
     _on(parents.device, "tree_mask", parents=(parents, torch.int32), cu_q=(cu_q, torch.int32), out=(out, torch.int32))
     with _Device(parents.device):
         _check(lib().qvg_tree_mask(parents.data_ptr(), None if cu_q is None else cu_q.data_ptr(), B, max_q, out.shape[1],
-                                   out.data_ptr(), _stream(stream)), "qvg_tree_mask")
+                                   out.data_ptr(), _raw_stream(stream, parents.device)), "qvg_tree_mask")
     return out
 
 
 def paged_workspace_size(cache: PagedKV, Hq, B, max_q):
+    """Scratch bytes of paged_attention."""
     b = ct.c_size_t(0)
     with _Device(cache.device):
         _check(lib().qvg_paged_workspace_size(cache.H, cache.d, Hq, B, max_q, ct.byref(b)), "qvg_paged_workspace_size")
@@ -584,7 +594,7 @@ def paged_attention(cache: PagedKV, q, block_table, kv_len, max_q, cu_q=None, ma
             block_table.data_ptr(), block_table.shape[1], kv_len.data_ptr(), mask_mode,
             None if mask is None else mask.data_ptr(), 0 if mask is None else mask.shape[1], scale, out.data_ptr(),
             out_dtype, None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-            _stream(stream)), "qvg_paged_attention")
+            _raw_stream(stream, q.device)), "qvg_paged_attention")
     return out, lse
 
 

@@ -93,23 +93,29 @@ __device__ __forceinline__ void quantise16(const uint32_t (&x)[8], uint8_t *code
     }
 }
 
+// How K is rotated on its way: not at all, pairs of neighbouring channels
+// (a lane has both), halves whose 16-byte pieces line up (pairs % 8 == 0), or
+// any halves.
+enum { kNoRope = 0, kPairs = 1, kHalves = 2, kAnyHalves = 3 };
+
 // One warp per token (blockIdx.y: a share of its heads); a lane holds 16
 // consecutive channels, D / 16 lanes a head, 512 / D heads side by side.
-//   ROPE: the token's cosines and sines are made once per warp (pairs / 32
-// angles a lane) and kept in registers for the lane's 16 channels; the K row
-// goes through shared memory, from which each lane takes its channels'
-// partners.  The rotated row is rounded to bf16, as qvg_rope would store it.
+//   The token's cosines and sines are made once per warp (pairs / 32 angles a
+// lane) and kept in registers for the lane's 16 channels.  With halves the K
+// row goes through shared memory, from which each lane takes its channels'
+// partners, 16 bytes at a time where they line up (2 bytes at a time, it took
+// 2.3 times as long).  The rotated row is rounded to bf16, as qvg_rope would
+// store it.
 // Bound by HBM: reads 4 H D bytes a token, writes 2 H D bits / 8 + scales.
-template <int D, int BITS, bool ROPE>
-__global__ void __launch_bounds__(kWarps * 32) k_paged_append(const __grid_constant__ RopeArgs r, PagedArgs a,
-                                                             const uint16_t *__restrict__ k,
-                                                             const uint16_t *__restrict__ v, int n, long long ks,
-                                                             long long vs, const int64_t *__restrict__ slots,
-                                                             const int32_t *__restrict__ positions,
-                                                             int heads_per_block) {
+template <int D, int BITS, int ROPE>
+__global__ void __launch_bounds__(kWarps * 32, ROPE == kNoRope ? 5 : 3)
+    k_paged_append(const __grid_constant__ RopeArgs r, PagedArgs a, const uint16_t *__restrict__ k, const uint16_t *__restrict__ v, int n,
+                   long long ks, long long vs, const int64_t *__restrict__ slots, const int32_t *__restrict__ positions,
+                   int heads_per_block) {
     constexpr int LANES = D / 16, SIDE = 32 / LANES;
+    constexpr bool SHARED = ROPE == kHalves || ROPE == kAnyHalves;
     __shared__ float2 s_cs[ROPE ? kWarps : 1][ROPE ? QVG_ROPE_MAX_PAIRS : 1];
-    __shared__ __align__(16) uint16_t s_row[ROPE ? kWarps : 1][ROPE ? SIDE * D : 8];
+    __shared__ __align__(16) uint16_t s_row[SHARED ? kWarps : 1][SHARED ? SIDE * D : 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * kWarps + warp;
     if (t >= n) return;
@@ -120,55 +126,89 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_append(const __grid_const
         return;
     }
     const int u = lane % LANES, hs = lane / LANES;
-    float co[16], si[16];  // of the lane's channels; si with the sign of the channel's place in its pair
-    int partner[16];       // in the row
-    if constexpr (ROPE) {
+    float co[ROPE == kPairs ? 8 : 16], si[ROPE == kPairs ? 8 : 16];  // si with the sign of the channel's place in its pair
+    int from[2];  // where the lane's two runs of 8 channels have their partners in the row
+    if constexpr (ROPE != kNoRope) {
         for (int i = lane; i < r.pairs; i += 32)
             s_cs[warp][i] = rope_cos_sin(r.step[i], positions[static_cast<long long>(t) * r.axes + r.axis[i]], r.mscale, false);
         __syncwarp();
+        if constexpr (ROPE == kPairs) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int c = u * 16 + i;
-            co[i] = 1.0f;
-            si[i] = 0.0f;
-            partner[i] = c;
-            if (c < 2 * r.pairs) {
-                const bool half = r.layout == QVG_ROPE_HALF;
-                const int pair = half ? (c < r.pairs ? c : c - r.pairs) : c >> 1;
-                const bool second = half ? c >= r.pairs : (c & 1);
-                const float2 cs = s_cs[warp][pair];
+            for (int i = 0; i < 8; ++i) {
+                const float2 cs = u * 8 + i < r.pairs ? s_cs[warp][u * 8 + i] : make_float2(1.0f, 0.0f);
+                co[i] = cs.x;
+                si[i] = cs.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int c = u * 16 + i;
+                const bool second = c >= r.pairs;
+                const float2 cs = c < 2 * r.pairs ? s_cs[warp][second ? c - r.pairs : c] : make_float2(1.0f, 0.0f);
                 co[i] = cs.x;
                 si[i] = second ? cs.y : -cs.y;
-                partner[i] = half ? (second ? c - r.pairs : c + r.pairs) : c ^ 1;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = u * 16 + 8 * h;
+                from[h] = c < r.pairs ? c + r.pairs : c < 2 * r.pairs ? c - r.pairs : c;
             }
         }
     }
     const int h0 = blockIdx.y * heads_per_block, h1 = min(a.H, h0 + heads_per_block);
     const uint16_t *kr = k + t * ks, *vr = v + t * vs;
-#pragma unroll 2
+    const uint4 zero = make_uint4(0, 0, 0, 0);
     for (int hb = h0; hb < h1; hb += SIDE) {
         const int h = hb + hs;
         const bool live = h < h1;
-        uint32_t xk[8], xv[8];
-        const uint4 zero = make_uint4(0, 0, 0, 0);
         const uint4 *pk = reinterpret_cast<const uint4 *>(kr + static_cast<long long>(h) * D + u * 16);
         const uint4 *pv = reinterpret_cast<const uint4 *>(vr + static_cast<long long>(h) * D + u * 16);
-        const uint4 k0 = live ? pk[0] : zero, k1 = live ? pk[1] : zero, v0 = live ? pv[0] : zero, v1 = live ? pv[1] : zero;
-        xk[0] = k0.x, xk[1] = k0.y, xk[2] = k0.z, xk[3] = k0.w, xk[4] = k1.x, xk[5] = k1.y, xk[6] = k1.z, xk[7] = k1.w;
-        xv[0] = v0.x, xv[1] = v0.y, xv[2] = v0.z, xv[3] = v0.w, xv[4] = v1.x, xv[5] = v1.y, xv[6] = v1.z, xv[7] = v1.w;
-        if constexpr (ROPE) {
+        const uint4 k0 = live ? __ldcs(pk) : zero, k1 = live ? __ldcs(pk + 1) : zero;
+        const uint4 v0 = live ? __ldcs(pv) : zero, v1 = live ? __ldcs(pv + 1) : zero;
+        uint32_t xk[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+        const uint32_t xv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        if constexpr (ROPE == kPairs) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x0 = __uint_as_float(xk[i] << 16), x1 = __uint_as_float(xk[i] & 0xFFFF0000u);
+                const __nv_bfloat162 y = __floats2bfloat162_rn(x0 * co[i] - x1 * si[i], x1 * co[i] + x0 * si[i]);
+                xk[i] = *reinterpret_cast<const uint32_t *>(&y);
+            }
+        }
+        if constexpr (SHARED) {
             uint16_t *row = s_row[warp] + hs * D;
             __syncwarp();  // the previous heads' partners have been read
             reinterpret_cast<uint4 *>(row + u * 16)[0] = k0;
             reinterpret_cast<uint4 *>(row + u * 16)[1] = k1;
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x0 = __uint_as_float(xk[i] << 16), x1 = __uint_as_float(xk[i] & 0xFFFF0000u);
-                const float p0 = bf16_to_f32(row[partner[2 * i]]), p1 = bf16_to_f32(row[partner[2 * i + 1]]);
-                const __nv_bfloat162 y = __floats2bfloat162_rn(x0 * co[2 * i] + p0 * si[2 * i],
-                                                               x1 * co[2 * i + 1] + p1 * si[2 * i + 1]);
-                xk[i] = *reinterpret_cast<const uint32_t *>(&y);
+            for (int half = 0; half < 2; ++half) {
+                uint32_t pw[4];
+                if constexpr (ROPE == kHalves) {
+                    const uint4 p = *reinterpret_cast<const uint4 *>(row + from[half]);
+                    pw[0] = p.x, pw[1] = p.y, pw[2] = p.z, pw[3] = p.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w = 0;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int c = u * 16 + 8 * half + 2 * i + e;
+                            const int q = c < r.pairs ? c + r.pairs : c < 2 * r.pairs ? c - r.pairs : c;
+                            w |= static_cast<uint32_t>(row[q]) << (16 * e);
+                        }
+                        pw[i] = w;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = 8 * half + 2 * i;
+                    const uint32_t x = xk[e / 2];
+                    const __nv_bfloat162 y =
+                        __floats2bfloat162_rn(__uint_as_float(x << 16) * co[e] + __uint_as_float(pw[i] << 16) * si[e],
+                                              __uint_as_float(x & 0xFFFF0000u) * co[e + 1] + __uint_as_float(pw[i] & 0xFFFF0000u) * si[e + 1]);
+                    xk[e / 2] = *reinterpret_cast<const uint32_t *>(&y);
+                }
             }
         }
         const size_t at = live ? row_of(a, slot, h) : 0;
@@ -193,7 +233,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_paged_read(PagedArgs a, const i
     if (slot >= a.n_slots && lane == 0 && blockIdx.y == 0) raise_error(a.err, QVG_ERR_INVALID_ARG);
     const int u = lane % LANES, hs = lane / LANES;
     const int h0 = blockIdx.y * heads_per_block, h1 = min(a.H, h0 + heads_per_block);
-#pragma unroll 2
+#pragma unroll 4
     for (int h = h0 + hs; h < h1; h += SIDE) {
         const size_t row = in ? row_of(a, slot, h) : 0;
 #pragma unroll
@@ -262,10 +302,15 @@ qvg_status launch_append(const qvg_paged *c, const uint16_t *k, const uint16_t *
     const PagedArgs a = paged_args(c);
     int per;
     const dim3 grid = token_grid(n, c->H, 512 / D, &per);
-    if (plan)
-        k_paged_append<D, BITS, true><<<grid, kWarps * 32, 0, st>>>(rope_args(plan, false), a, k, v, n, ks, vs, slots, positions, per);
+    const RopeArgs r = plan ? rope_args(plan, false) : RopeArgs{};
+    if (!plan)
+        k_paged_append<D, BITS, kNoRope><<<grid, kWarps * 32, 0, st>>>(r, a, k, v, n, ks, vs, slots, positions, per);
+    else if (r.layout == QVG_ROPE_INTERLEAVED)
+        k_paged_append<D, BITS, kPairs><<<grid, kWarps * 32, 0, st>>>(r, a, k, v, n, ks, vs, slots, positions, per);
+    else if (r.pairs % 8 == 0)
+        k_paged_append<D, BITS, kHalves><<<grid, kWarps * 32, 0, st>>>(r, a, k, v, n, ks, vs, slots, positions, per);
     else
-        k_paged_append<D, BITS, false><<<grid, kWarps * 32, 0, st>>>(RopeArgs{}, a, k, v, n, ks, vs, slots, positions, per);
+        k_paged_append<D, BITS, kAnyHalves><<<grid, kWarps * 32, 0, st>>>(r, a, k, v, n, ks, vs, slots, positions, per);
     QVG_LAUNCH_CHECK();
     return QVG_OK;
 }

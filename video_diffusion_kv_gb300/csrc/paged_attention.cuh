@@ -177,13 +177,23 @@ __device__ __forceinline__ bool any_of(int id, int count, bool p) {
 // Bounded wait that also ends when another role has failed.  (Out of line but
 // for the first try: a tile's loop has many waits, and its code has to stay
 // small.)
+__device__ __forceinline__ bool try_wait_long(uint64_t *bar, uint32_t parity) {  // suspended for up to 20 us
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(umma::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *fail, uint64_t limit_ns) {
-    for (int i = 0; i < 32; ++i)
-        if (umma::mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < 4; ++i)
+        if (try_wait_long(bar, parity)) return true;
     const uint64_t t0 = umma::globaltimer_ns();
     for (;;) {
-        for (int i = 0; i < 32; ++i)
-            if (umma::mbar_try_wait(bar, parity)) return true;
+        if (try_wait_long(bar, parity)) return true;
         if (*fail) return false;
         if (umma::globaltimer_ns() - t0 > limit_ns) {
             *fail = 1;
@@ -348,7 +358,7 @@ struct Cfg {
     static constexpr int kSlots = kRoom / (kRaw + kScales / 2);
     static constexpr int kSK = kSlots / 2 > 4 ? 4 : kSlots / 2, kSV = kSlots - kSK > 5 ? 5 : kSlots - kSK;
     static constexpr int kSmem = kFixed + (kSK + kSV) * kRaw + kSV * kScales + 1024;
-    static constexpr int kConv = BITS == 4 ? 2 : 0;  // converter warps
+    static constexpr int kConv = BITS == 4 ? 4 : 0;  // converter warps, half for K and half for V
     static constexpr int kWarps = 8 + kConv;   // loads, S, PV, segments and Q; softmax 4 - 7; converters
     static constexpr int kTmemUsed = 2 * 2 * NB + 3 * NB;
     static constexpr int kTmem = kTmemUsed <= 128 ? 128 : 256;
@@ -561,7 +571,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
         }
         for (int i = 0; i < SK; ++i) {
             umma::mbar_init(&k_full[i], 1);
-            umma::mbar_init(&k_empty[i], 1);  // S done, or the converter
+            umma::mbar_init(&k_empty[i], BITS == 8 ? 1 : C::kConv / 2);  // S done, or the converters
         }
         for (int i = 0; i < SV; ++i) {
             umma::mbar_init(&v_full[i], 33);  // the codes; each lane's part of the scales
@@ -573,9 +583,9 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
             umma::mbar_init(&m_free[i], 4);
             umma::mbar_init(&q_full[i], 1);
         }
-        umma::mbar_init(&ko_full, 1);
+        umma::mbar_init(&ko_full, BITS == 8 ? 1 : C::kConv / 2);
         umma::mbar_init(&ko_done, 1);
-        umma::mbar_init(&vo_full, 1);
+        umma::mbar_init(&vo_full, BITS == 8 ? 1 : C::kConv / 2);
         umma::mbar_init(&p_full, 4);
         umma::mbar_init(&pv_done, 1);
         umma::mbar_init(&q_free, 1);
@@ -801,10 +811,21 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
         bool ok = true;
         while (ok && next_segment(g, n_seg)) {
             ++n_seg;
+            // the block table, 32 entries at a time, the next 32 on their way while these are used
+            const int32_t *row = a.table + g.b * a.table_stride;
+            const int pages = (g.kv + (1 << a.page_log2) - 1) >> a.page_log2;
+            int have = (g.t0 * kTile) >> a.page_log2 & ~31;  // entry of lane 0's `now`
+            auto entries = [&](int e) { return e + lane < pages ? row[e + lane] : 0; };
+            int now = entries(have), then = entries(have + 32);
             for (int t = g.t0; t < g.t1; ++t, ++it, rk.next(), rv.next()) {
+                if ((t * kTile) >> a.page_log2 >= have + 32) {  // (a tile's entries never straddle 32)
+                    have += 32;
+                    now = then;
+                    then = entries(have + 32);
+                }
                 const int tok = t * kTile + (lane << pr_log2);
                 const bool there = lane < (kTile >> pr_log2) && tok < g.kv;
-                const int page = there ? a.table[g.b * a.table_stride + (tok >> a.page_log2)] : 0;
+                const int page = __shfl_sync(0xFFFFFFFFu, now, (tok >> a.page_log2) & 31);
                 const bool good = there && page >= 0 && page < a.num_pages;
                 if (there && !good) raise_error(a.err, QVG_ERR_INVALID_ARG);
                 const int off = tok & ((1 << a.page_log2) - 1);
@@ -999,11 +1020,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
         }
         if (!ok && lane == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
     } else if (BITS == 4) {
-        // ---- 4-bit codes into e4m3 operands, a warp for K and one for V: one (row, 32-channel group) a step, its
+        // ---- 4-bit codes into e4m3 operands, two warps for K and two for V: one (row, 32-channel group) a step, its
         // scale relative to the row's largest.  A word's eight magnitudes are two byte permutes of the group's eight
         // levels. ----
-        const int which = warp - 8;
-        constexpr int GR = D / 32;
+        constexpr int GR = D / 32, kThreads = C::kConv > 0 ? C::kConv * 16 : 32;
+        const int which = (warp - 8) / (kThreads / 32), w = (warp - 8) % (kThreads / 32) * 32 + lane;
         Segment g;
         Ring<SK> rk;
         Ring<SV> rv;
@@ -1021,8 +1042,8 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
                 const uint8_t *scales = base + (sc0 - sm) + rv.i * C::kScales + which * 128 * GR;
                 uint8_t *dst = base + ((which ? v80 : k80) - sm);
 #pragma unroll 4
-                for (int i = 0; i < kTile * GR / 32; ++i) {
-                    const int idx = lane + 32 * i, row = idx / GR, gq = idx % GR;
+                for (int i = 0; i < kTile * GR / kThreads; ++i) {
+                    const int idx = w + kThreads * i, row = idx / GR, gq = idx % GR;
                     const uint4 v = *reinterpret_cast<const uint4 *>(src + idx * 16);
                     const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
                     const uint8_t *sc = scales + row * GR;

@@ -84,61 +84,78 @@ __global__ void __launch_bounds__(kWarps * 32) k_rope(const __grid_constant__ Ro
     const int t = blockIdx.x * kWarps + warp;
     if (t >= n) return;
     float2 *cs = s_cs[warp];
-    for (int i = lane; i < r.pairs; i += 32)
-        cs[i] = rope_cos_sin(r.step[i], positions[static_cast<long long>(t) * r.axes + r.axis[i]], r.mscale, r.transpose);
-    __syncwarp();
     const int h0 = blockIdx.y * heads_per_block, h1 = min(H, h0 + heads_per_block);
     const T *xr = x + t * xs;
     T *yr = out + t * os;
     const bool half = r.layout == QVG_ROPE_HALF;
+    auto angles = [&]() {
+        for (int i = lane; i < r.pairs; i += 32)
+            cs[i] = rope_cos_sin(r.step[i], positions[static_cast<long long>(t) * r.axes + r.axis[i]], r.mscale, r.transpose);
+        __syncwarp();
+    };
     if constexpr (VEC) {
         const int units = d / (2 * E);  // lanes on one head; 32 / units heads side by side
         const int u = lane % units, step = 32 / units;
         const int rot = r.pairs / E;  // units that rotate; the others copy
-        const bool turn = u < rot;
+        const bool turn = u < rot, live = turn || x != out;
         const int c0 = half && turn ? u * E : 2 * E * u, c1 = half && turn ? r.pairs + u * E : c0 + E;
-        float2 a[E];
-        if (turn)
+        constexpr int AHEAD = 4;  // heads on their way at once, the first ones while the angles are made
+        uint4 v0[AHEAD], v1[AHEAD];
+        auto fetch = [&](int h) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) a[i] = cs[u * E + i];
-        if (!turn && x == out) return;
-#pragma unroll 4
-        for (int h = h0 + lane / units; h < h1; h += step) {
-            const T *p = xr + static_cast<long long>(h) * d;
-            T *q = yr + static_cast<long long>(h) * d;
-            uint4 v0 = *reinterpret_cast<const uint4 *>(p + c0), v1 = *reinterpret_cast<const uint4 *>(p + c1);
-            if (turn) {
-                float f0[E], f1[E];
-                unpack(v0, f0);
-                unpack(v1, f1);
-                if (half) {
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        const float y0 = f0[i] * a[i].x - f1[i] * a[i].y, y1 = f1[i] * a[i].x + f0[i] * a[i].y;
-                        f0[i] = y0;
-                        f1[i] = y1;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < E / 2; ++i) {
-                        float y0 = f0[2 * i] * a[i].x - f0[2 * i + 1] * a[i].y;
-                        float y1 = f0[2 * i + 1] * a[i].x + f0[2 * i] * a[i].y;
-                        f0[2 * i] = y0;
-                        f0[2 * i + 1] = y1;
-                        const float2 b = a[E / 2 + i];
-                        y0 = f1[2 * i] * b.x - f1[2 * i + 1] * b.y;
-                        y1 = f1[2 * i + 1] * b.x + f1[2 * i] * b.y;
-                        f1[2 * i] = y0;
-                        f1[2 * i + 1] = y1;
-                    }
+            for (int i = 0; i < AHEAD; ++i)
+                if (live && h + i * step < h1) {
+                    const T *p = xr + static_cast<long long>(h + i * step) * d;
+                    v0[i] = __ldcs(reinterpret_cast<const uint4 *>(p + c0));
+                    v1[i] = __ldcs(reinterpret_cast<const uint4 *>(p + c1));
                 }
-                v0 = pack(f0);
-                v1 = pack(f1);
+        };
+        int h = h0 + lane / units;
+        fetch(h);
+        angles();
+        float2 a[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) a[i] = turn ? cs[u * E + i] : make_float2(1.0f, 0.0f);
+        for (; h < h1; h += AHEAD * step) {
+#pragma unroll
+            for (int b = 0; b < AHEAD; ++b) {
+                if (!live || h + b * step >= h1) break;
+                if (turn) {
+                    float f0[E], f1[E];
+                    unpack(v0[b], f0);
+                    unpack(v1[b], f1);
+                    if (half) {
+#pragma unroll
+                        for (int i = 0; i < E; ++i) {
+                            const float y0 = f0[i] * a[i].x - f1[i] * a[i].y, y1 = f1[i] * a[i].x + f0[i] * a[i].y;
+                            f0[i] = y0;
+                            f1[i] = y1;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < E / 2; ++i) {
+                            float y0 = f0[2 * i] * a[i].x - f0[2 * i + 1] * a[i].y;
+                            float y1 = f0[2 * i + 1] * a[i].x + f0[2 * i] * a[i].y;
+                            f0[2 * i] = y0;
+                            f0[2 * i + 1] = y1;
+                            const float2 e = a[E / 2 + i];
+                            y0 = f1[2 * i] * e.x - f1[2 * i + 1] * e.y;
+                            y1 = f1[2 * i + 1] * e.x + f1[2 * i] * e.y;
+                            f1[2 * i] = y0;
+                            f1[2 * i + 1] = y1;
+                        }
+                    }
+                    v0[b] = pack(f0);
+                    v1[b] = pack(f1);
+                }
+                T *q = yr + static_cast<long long>(h + b * step) * d;
+                *reinterpret_cast<uint4 *>(q + c0) = v0[b];
+                *reinterpret_cast<uint4 *>(q + c1) = v1[b];
             }
-            *reinterpret_cast<uint4 *>(q + c0) = v0;
-            *reinterpret_cast<uint4 *>(q + c1) = v1;
+            fetch(h + AHEAD * step);
         }
     } else {
+        angles();
         for (int h = h0; h < h1; ++h) {
             const T *p = xr + static_cast<long long>(h) * d;
             T *q = yr + static_cast<long long>(h) * d;
