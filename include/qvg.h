@@ -650,11 +650,14 @@ qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B,
  *   workspace  at least qvg_paged_workspace_size(H, d, Hq, B, max_q) bytes.
  * Keys that a token does not see, and slots past kv_len, have no influence
  * on it, whatever they hold.  Q enters the product as the sum of two fp8
- * numbers (exact for channels down to 2^-14 of the row's largest, off by at
- * most 2^-21 of the largest below), K and V as their codes; the weights times
- * V's scale enter as the sum of three fp8 numbers (off by at most 2^-9 of
- * themselves, or 2^-25 of the largest); all sums are fp32.  (4 bits: groups
- * whose scale is below 2^-14 of their row's largest count as 0.)
+ * numbers, K and V as their codes, the weights times V's scale as the sum of
+ * three fp8 numbers or as fp16; all sums are fp32.
+ *   max_q * Hq / H <= 32 (16 with 4 bits): a channel of q is exact down to
+ *     2^-13 of its row's largest and off by at most 2^-21 of the largest
+ *     below; a weight is off by at most 2^-9 of itself or 2^-25 of the largest.
+ *   more rows: 2^-9 and 2^-17; 2^-11.
+ *   4 bits: K groups (with few rows V's too) whose scale is below 2^-14 of
+ *     their row's largest count as 0 (with many rows V's below 2^-24).
  * A row of q
  * with an infinity or a NaN gives NaN.  The results do not depend on what
  * else the GPU runs: the split of the work follows from the sizes alone.

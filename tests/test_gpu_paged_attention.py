@@ -70,7 +70,7 @@ class Batch:
         """Every row against the plain form.  Bounds, per row (p: the weights):
         a logit is off by
           D = scale (2^-21 max|q| sum|k| + 2 d 2^-23 sum |q||k|) + 8 2^-24 |s|
-        (Q's fp8 pair; fp32 sums of 2 d products; the base-2 form's roundings
+        (Q's fp8 pair, 2^-17 with many rows; fp32 sums of 2 d products; the base-2 form's roundings
         of the logit), so a weight by 2 D + 2^-20 (2^x) of itself; a weight
         times V's scale by 2^-11 (fp16) and 2^-9 (three e5m2 parts) more or,
         far below the largest, by 2^-25 of the largest (half of e5m2's smallest
@@ -80,6 +80,8 @@ class Batch:
         got, q = out.double().cpu().numpy(), self.q.double().cpu().numpy()
         got_lse = None if lse is None else lse.double().cpu().numpy()
         scale = 1 / math.sqrt(self.d) if scale is None else scale
+        rows_in_block = max(self.nq) * self.G
+        q_step = 2.0 ** -21 if rows_in_block <= (32 if self.cache.bits == 8 else 16) else 2.0 ** -17
         half = 2.0 ** -8 if out.dtype == torch.bfloat16 else 2.0 ** -24
         first = 0
         for b, T in enumerate(self.nq):
@@ -98,7 +100,7 @@ class Batch:
                 p = np.exp(s - m)
                 den = p.sum(-1, keepdims=True)
                 want, want_lse = ((p / den)[..., None] * vv).sum(1), (m + np.log(den))[:, 0]
-                dd = scale * (2.0 ** -21 * np.abs(qq).max(-1) * np.abs(kk).sum(-1) + 2 * self.d * 2.0 ** -23 * np.abs(kk * qq).sum(-1))
+                dd = scale * (q_step * np.abs(qq).max(-1) * np.abs(kk).sum(-1) + 2 * self.d * 2.0 ** -23 * np.abs(kk * qq).sum(-1))
                 dd = (dd + 8 * 2.0 ** -24 * np.abs(s)).max(-1, keepdims=True)
                 rel = 2 * dd + 2.0 ** -20 + 2.0 ** -11 + 2.0 ** -9 + len(js) * 2.0 ** -24
                 mean = ((p / den)[..., None] * np.abs(vv)).sum(1)

@@ -5,7 +5,7 @@
 
 #include <cmath>
 
-#include "paged_attention.cuh"
+#include "paged_attention_wide.cuh"
 
 namespace qvg {
 
@@ -102,13 +102,13 @@ __global__ void k_tree_mask(const int32_t *__restrict__ parents, const int32_t *
 
 constexpr int kMaxTree = 8192;  // new tokens of one sequence whose parents fit 32 KB of shared memory
 
-// Query rows of a unit: 16 where that holds a sequence's rows, else blocks of
-// 32 (4-bit caches: blocks of 16, as their converters need registers too).  A
-// block of 32 costs a tile about 1.3 times a block of 16's time.
-int rows_of_block(long long rows, int bits) { return rows <= 16 || bits == 4 ? 16 : 32; }
+// Query rows of a unit: 16 or 32 (narrow kernel) where that holds a sequence's
+// rows, else 256 (wide kernel).  4-bit caches have no blocks of 32: the narrow
+// kernel's converters need registers too.
+int rows_of_block(long long rows, int bits) { return rows <= 16 ? 16 : rows <= 32 && bits == 8 ? 32 : pa::kWideRows; }
 
-// Two CTAs an SM (see the kernel).
-int cta_count() { return 2 * sm_count_current(); }
+// The narrow kernel has two CTAs an SM, the wide one has one.
+int cta_count(int NB) { return (NB == pa::kWideRows ? 1 : 2) * sm_count_current(); }
 
 struct Workspace {
     size_t po, pm, pl, desc, bytes;  // offsets
@@ -139,6 +139,17 @@ bool codes_map(CUtensorMap *m, const qvg_paged *c, const uint8_t *codes) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int D, int NB>
+qvg_status launch_merge(const pa::Args &a, int ctas, cudaStream_t st) {
+    const cudaError_t e = launch_pdl(k_paged_merge<D, NB>, dim3(ctas, NB / 8), dim3(256), 0, st, a);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        note_cuda_error(e);
+        return QVG_ERR_CUDA;
+    }
+    return QVG_OK;
+}
+
 template <int D, int BITS, int NB>
 qvg_status launch(const CUtensorMap (&map)[2], const pa::Args &a, int ctas, cudaStream_t st) {
     using C = pa::Cfg<D, BITS, NB>;
@@ -147,13 +158,18 @@ qvg_status launch(const CUtensorMap (&map)[2], const pa::Args &a, int ctas, cuda
     if (s != QVG_OK) return s;
     pa::k_paged_attention<D, BITS, NB><<<ctas, C::kWarps * 32, C::kSmem, st>>>(map[0], map[1], a);
     QVG_LAUNCH_CHECK();
-    const cudaError_t e = launch_pdl(k_paged_merge<D, NB>, dim3(ctas, NB / 8), dim3(256), 0, st, a);
-    if (e != cudaSuccess) {
-        (void)cudaGetLastError();
-        note_cuda_error(e);
-        return QVG_ERR_CUDA;
-    }
-    return QVG_OK;
+    return launch_merge<D, NB>(a, ctas, st);
+}
+
+template <int D, int BITS>
+qvg_status launch_wide(const CUtensorMap (&map)[2], const pa::Args &a, int ctas, cudaStream_t st) {
+    using C = pa::Wide<D, BITS>;
+    static std::atomic<uint64_t> done{0};
+    const qvg_status s = smem_limit_once(done, reinterpret_cast<const void *>(pa::k_paged_attention_wide<D, BITS>), C::kSmem);
+    if (s != QVG_OK) return s;
+    pa::k_paged_attention_wide<D, BITS><<<ctas, C::kWarps * 32, C::kSmem, st>>>(map[0], a);
+    QVG_LAUNCH_CHECK();
+    return launch_merge<D, pa::kWideRows>(a, ctas, st);
 }
 
 bool misaligned(const void *p, uintptr_t to) { return !p || reinterpret_cast<uintptr_t>(p) % to != 0; }
@@ -181,7 +197,11 @@ qvg_status qvg_tree_mask(const int32_t *parents, const int32_t *cu_q, int32_t B,
 qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B, int32_t max_q, size_t *bytes) {
     if (!bytes || H < 1 || Hq < 1 || Hq % H != 0 || B < 0 || max_q < 0) return QVG_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return QVG_ERR_UNSUPPORTED;
-    *bytes = carve(cta_count(), rows_of_block(static_cast<long long>(max_q) * (Hq / H), 8), d).bytes;  // (4 bits: no more)
+    *bytes = 0;  // (of a cache of either bit width)
+    for (int bits = 4; bits <= 8; bits += 4) {
+        const int NB = rows_of_block(static_cast<long long>(max_q) * (Hq / H), bits);
+        *bytes = std::max(*bytes, carve(cta_count(NB), NB, d).bytes);
+    }
     return QVG_OK;
 }
 
@@ -199,14 +219,13 @@ qvg_status qvg_paged_attention(const qvg_paged *cache, const void *q_bf16, int64
     if (out_dtype != QVG_OUT_F32 && out_dtype != QVG_OUT_BF16) return QVG_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return QVG_ERR_INVALID_ARG;
     if (!cu_q && static_cast<int64_t>(B) * max_q > total_q) return QVG_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(max_q) * (Hq / H) > INT32_MAX - 64) return QVG_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_q) * (Hq / H) > INT32_MAX - pa::kWideRows) return QVG_ERR_UNSUPPORTED;
     if (B == 0 || max_q == 0 || total_q == 0) return QVG_OK;
     if (misaligned(q_bf16, 16) || misaligned(out, 16) || misaligned(table, 4) || misaligned(kv_len, 4) ||
         (cu_q && misaligned(cu_q, 4)) || (lse && misaligned(lse, 4)))
         return QVG_ERR_INVALID_ARG;
     if (mask_mode == QVG_MASK_TREE && (misaligned(mask, 4) || mask_words < ceil_div(max_q, 32))) return QVG_ERR_INVALID_ARG;
-    const int ctas = cta_count();
-    const int NB = rows_of_block(static_cast<long long>(max_q) * (Hq / H), cache->bits);
+    const int NB = rows_of_block(static_cast<long long>(max_q) * (Hq / H), cache->bits), ctas = cta_count(NB);
     const Workspace w = carve(ctas, NB, d);
     if (!workspace || ws_bytes < w.bytes || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return QVG_ERR_WORKSPACE;
     CUtensorMap map[2] = {};
@@ -247,6 +266,10 @@ qvg_status qvg_paged_attention(const qvg_paged *cache, const void *q_bf16, int64
     a.wait_ns = wait_limit_ns();
     a.inject = wait_inject();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (NB == pa::kWideRows) {
+        if (cache->bits == 4) return d == 64 ? launch_wide<64, 4>(map, a, ctas, st) : launch_wide<128, 4>(map, a, ctas, st);
+        return d == 64 ? launch_wide<64, 8>(map, a, ctas, st) : launch_wide<128, 8>(map, a, ctas, st);
+    }
     if (cache->bits == 4) return d == 64 ? launch<64, 4, 16>(map, a, ctas, st) : launch<128, 4, 16>(map, a, ctas, st);
     if (NB == 16) return d == 64 ? launch<64, 8, 16>(map, a, ctas, st) : launch<128, 8, 16>(map, a, ctas, st);
     return d == 64 ? launch<64, 8, 32>(map, a, ctas, st) : launch<128, 8, 32>(map, a, ctas, st);

@@ -25,7 +25,7 @@
 // own accumulator columns; a product with N <= 64 takes the tensor core the
 // same 45 clocks whatever N is, so the extra columns are free there:
 //   - Q as two: hi + lo / 16 in e4m3 (4 significant bits each, a bf16 number
-//     has 8: exact while the channel is within 2^-14 of the row's largest);
+//     has 8: exact down to 2^-13 of the row's largest);
 //   - P as three: h1 + h2 + h3 in e5m2, which is the upper byte of an fp16
 //     number: the first two cut off, the last rounded: at most 2^-9 of the
 //     weight off, and nearly fp16's range, which e4m3 lacks.
@@ -123,6 +123,82 @@ struct __align__(16) Segment {
 };
 constexpr int kRing = 8;  // segments ahead; a copy can run that far ahead in one-tile units
 constexpr int kChunks = 256;
+
+// The CTA's part of the line, made by one whole warp.
+template <int NB>
+struct Line {
+    long long pos, end, first, per;  // first: where sequence b begins
+    int b;
+    int4 cut;  // the unit that begins here and goes on, and the last of the CTAs that share it
+    Seq s;
+
+    // chunk [kChunks]: room in shared memory
+    __device__ __forceinline__ Line(const Args &a, long long *chunk) {
+        const int lane = threadIdx.x & 31, cta = blockIdx.x;
+        // tiles of all sequences, by chunks of `span` sequences
+        const int span = ((a.B + kChunks - 1) / kChunks + 31) & ~31;
+        long long total = 0;
+        for (int k = 0, b0 = 0; b0 < a.B; ++k, b0 += span) {
+            long long mine = 0;
+            for (int i = b0 + lane; i < min(a.B, b0 + span); i += 32) mine += seq_of<NB>(a, i, cta == 0).tiles(a.H);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+            if (lane == 0) chunk[k] = mine;
+            total += mine;
+        }
+        __syncwarp();
+        per = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+        pos = min(total, cta * per);
+        end = min(total, pos + per);
+        first = 0;
+        b = 0;
+        if (pos < end) {  // the sequence that holds `pos`: its chunk, then by a scan over 32 at a time
+            int k = 0;
+            while (pos >= first + chunk[k]) first += chunk[k++];
+            for (b = k * span;; b += 32) {
+                const long long w = b + lane < a.B ? seq_of<NB>(a, b + lane, false).tiles(a.H) : 0;
+                long long x = w;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                    if (lane >= o) x += y;
+                }
+                const uint32_t hit = __ballot_sync(0xFFFFFFFFu, pos < first + x);
+                const int l = hit ? __ffs(hit) - 1 : 31;
+                const long long upto = __shfl_sync(0xFFFFFFFFu, x, l), own = __shfl_sync(0xFFFFFFFFu, w, l);
+                first += hit ? upto - own : upto;
+                if (hit) {
+                    b += l;
+                    break;
+                }
+            }
+        }
+        cut = make_int4(-1, 0, 0, 0);
+        s = seq_of<NB>(a, min(b, a.B - 1), false);
+    }
+
+    // t1 = 0: no more.
+    __device__ __forceinline__ void next(const Args &a, Segment &g) {
+        g.t1 = 0;
+        if (pos >= end) return;
+        while (pos >= first + s.tiles(a.H)) {
+            first += s.tiles(a.H);
+            s = seq_of<NB>(a, ++b, false);
+        }
+        const uint32_t rel = static_cast<uint32_t>(pos - first), u = rel / static_cast<uint32_t>(s.nt);
+        g.b = b;
+        g.h = static_cast<int>(u / static_cast<uint32_t>(s.rb));
+        g.r = static_cast<int>(u % static_cast<uint32_t>(s.rb));
+        g.t0 = static_cast<int>(rel - u * s.nt);
+        g.t1 = static_cast<int>(min(static_cast<long long>(s.nt), g.t0 + (end - pos)));
+        g.q0 = s.q0;
+        g.nq = s.nq;
+        g.kv = s.kv;
+        g.nt = s.nt;
+        if (g.t0 == 0 && g.t1 < s.nt) cut = make_int4(b, g.h, g.r, static_cast<int>((pos + s.nt - 1) / per));
+        pos += g.t1 - g.t0;
+    }
+};
 
 // ---- small pieces ---------------------------------------------------------------
 
@@ -933,73 +1009,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
         __syncwarp();
     } else if (warp == 3) {
         // ---- this CTA's part of the line, unit by unit, and each unit's Q rows ------------------------
-        // tiles of all sequences, by chunks of `span` sequences
-        const int span = ((a.B + kChunks - 1) / kChunks + 31) & ~31;
-        long long total = 0;
-        for (int k = 0, b0 = 0; b0 < a.B; ++k, b0 += span) {
-            long long mine = 0;
-            for (int b = b0 + lane; b < min(a.B, b0 + span); b += 32) mine += seq_of<NB>(a, b, cta == 0).tiles(a.H);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-            if (lane == 0) s_chunk[k] = mine;
-            total += mine;
-        }
-        __syncwarp();
-        const long long per = max(1ll, (total + gridDim.x - 1) / gridDim.x);
-        long long pos = min(total, cta * per);
-        const long long end = min(total, pos + per);
-        // the sequence that holds `pos`: its chunk, then by a scan over 32 at a time
-        long long first = 0;  // where sequence b begins
-        int b = 0;
-        if (pos < end) {
-            int k = 0;
-            while (pos >= first + s_chunk[k]) first += s_chunk[k++];
-            for (b = k * span;; b += 32) {
-                const long long w = b + lane < a.B ? seq_of<NB>(a, b + lane, false).tiles(a.H) : 0;
-                long long x = w;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-                    if (lane >= o) x += y;
-                }
-                const uint32_t hit = __ballot_sync(0xFFFFFFFFu, pos < first + x);
-                const int l = hit ? __ffs(hit) - 1 : 31;
-                const long long upto = __shfl_sync(0xFFFFFFFFu, x, l), own = __shfl_sync(0xFFFFFFFFu, w, l);
-                if (hit) {
-                    first += upto - own;
-                    b += l;
-                    break;
-                }
-                first += upto;
-            }
-        }
-        int4 cut = make_int4(-1, 0, 0, 0);  // the unit that begins here and goes on: its CTAs
-        Seq s = seq_of<NB>(a, min(b, a.B - 1), false);
+        Line<NB> line(a, s_chunk);
         bool ok = true;
         for (int n_seg = 0; ok; ++n_seg) {
             Segment g;
-            g.t1 = 0;
-            if (pos < end) {
-                while (pos >= first + s.tiles(a.H)) {
-                    first += s.tiles(a.H);
-                    s = seq_of<NB>(a, ++b, false);
-                }
-                const uint32_t rel = static_cast<uint32_t>(pos - first), u = rel / static_cast<uint32_t>(s.nt);
-                g.b = b;
-                g.h = static_cast<int>(u / static_cast<uint32_t>(s.rb));
-                g.r = static_cast<int>(u % static_cast<uint32_t>(s.rb));
-                g.t0 = static_cast<int>(rel - u * s.nt);
-                g.t1 = static_cast<int>(min(static_cast<long long>(s.nt), g.t0 + (end - pos)));
-                g.q0 = s.q0;
-                g.nq = s.nq;
-                g.kv = s.kv;
-                g.nt = s.nt;
-                const long long unit_end = pos + (s.nt - g.t0);
-                if (g.t0 == 0 && g.t1 < s.nt) cut = make_int4(b, g.h, g.r, static_cast<int>((unit_end - 1) / per));
-                pos += g.t1 - g.t0;
-            } else if (lane == 0) {
-                a.desc[cta] = cut;
-            }
+            line.next(a, g);
             const int i = n_seg & (kRing - 1);
             if (n_seg >= kRing) ok = wait(&seg_free[i], ((n_seg / kRing) - 1) & 1, vfail, a.wait_ns);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -1018,7 +1032,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
             make_q<D, NB>(a, g, base + (q0 - sm), s_qs[qb], s_tok[qb], s_row[qb]);
             if (lane == 0) umma::mbar_arrive(&q_full[qb]);
         }
-        if (!ok && lane == 0) a.desc[cta] = make_int4(-1, 0, 0, 0);
+        if (lane == 0) a.desc[cta] = ok ? line.cut : make_int4(-1, 0, 0, 0);
     } else if (BITS == 4) {
         // ---- 4-bit codes into e4m3 operands, two warps for K and two for V: one (row, 32-channel group) a step, its
         // scale relative to the row's largest.  A word's eight magnitudes are two byte permutes of the group's eight
