@@ -165,8 +165,25 @@ template <int D, int BITS>
 qvg_status launch_wide(const CUtensorMap (&map)[2], const pa::Args &a, int ctas, cudaStream_t st) {
     using C = pa::Wide<D, BITS>;
     static std::atomic<uint64_t> done{0};
-    const qvg_status s = smem_limit_once(done, reinterpret_cast<const void *>(pa::k_paged_attention_wide<D, BITS>), C::kSmem);
+    const void *kernel = reinterpret_cast<const void *>(pa::k_paged_attention_wide<D, BITS>);
+    const qvg_status s = smem_limit_once(done, kernel, C::kSmem);
     if (s != QVG_OK) return s;
+    // The kernel's register split is made for what it is compiled to have at
+    // launch: with fewer, its softmax warps would wait for registers that never
+    // come.
+    static std::atomic<int> regs{0};
+    int n = regs.load(std::memory_order_acquire);
+    if (n == 0) {
+        cudaFuncAttributes at{};
+        const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+        if (e != cudaSuccess) {
+            (void)cudaGetLastError();
+            note_cuda_error(e);
+            return QVG_ERR_CUDA;
+        }
+        regs.store(n = at.numRegs, std::memory_order_release);
+    }
+    if (n != pa::kWideRegs) return QVG_ERR_UNSUPPORTED;
     pa::k_paged_attention_wide<D, BITS><<<ctas, C::kWarps * 32, C::kSmem, st>>>(map[0], a);
     QVG_LAUNCH_CHECK();
     return launch_merge<D, pa::kWideRows>(a, ctas, st);

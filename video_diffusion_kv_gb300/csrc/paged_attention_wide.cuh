@@ -25,7 +25,7 @@
 namespace qvg {
 namespace pa {
 
-constexpr int kWideRows = 256;
+constexpr int kWideRows = 256, kWideRegs = 128;  // rows of a unit; registers a thread at launch
 
 template <int D, int BITS>
 struct Wide {
@@ -42,8 +42,26 @@ struct Wide {
     static_assert(kSmem <= 224 * 1024, "shared memory");
 };
 
+// (This kernel splits its registers unevenly, which the compiler does not
+// combine with calls: everything is inlined, the waits too.)
+__device__ __forceinline__ bool wait_here(uint64_t *bar, uint32_t parity, volatile int *fail, uint64_t limit_ns) {
+    if (umma::mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (int i = 0;; ++i) {
+        if (try_wait_long(bar, parity)) return true;
+        if (i < 4) continue;
+        if (i == 4) t0 = umma::globaltimer_ns();
+        if (*fail) return false;
+        if (umma::globaltimer_ns() - t0 > limit_ns) {
+            *fail = 1;
+            return false;
+        }
+    }
+}
+
 // Which of the tile's 128 keys the row of new token tq sees, as bits.
-__device__ __noinline__ uint4 seen_keys(const Args &a, int t, int kv, int nq, int q0, int tq) {
+__device__ __forceinline__ uint4 seen_keys(const Args &a, int t, int kv, int nq, int q0, int tq) {
     const int k0 = t * kTile, hist = kv - nq;
     int end = min(kv - k0, kTile);  // keys of the sequence in this tile
     if (a.mode == QVG_MASK_CAUSAL) end = min(end, hist + tq + 1 - k0);
@@ -70,7 +88,7 @@ __device__ __noinline__ uint4 seen_keys(const Args &a, int t, int kv, int nq, in
 
 // A warp's rows of O times their factors (the references of some have moved).
 template <int D>
-__device__ __noinline__ void rescale_rows(uint32_t t_o, float f) {
+__device__ __forceinline__ void rescale_rows(uint32_t t_o, float f) {
 #pragma unroll 1
     for (int c = 0; c < D; c += 16) {
         uint32_t o[16];
@@ -84,7 +102,7 @@ __device__ __noinline__ void rescale_rows(uint32_t t_o, float f) {
 
 // A thread's Q row as two rows of e4m3 numbers; returns its scale.
 template <int D>
-__device__ __noinline__ float make_q_row(const uint16_t *q, uint8_t *hi, uint8_t *lo, int r) {
+__device__ __forceinline__ float make_q_row(const uint16_t *q, uint8_t *hi, uint8_t *lo, int r) {
     uint4 v[D / 8];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) v[i] = q ? reinterpret_cast<const uint4 *>(q)[i] : make_uint4(0, 0, 0, 0);
@@ -177,7 +195,7 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
     volatile int *vfail = &fail;
     auto next_segment = [&](Segment &g, int n) {
         const int i = n & (kRing - 1);
-        const bool ok = wait(&seg_full[i], (n / kRing) & 1, vfail, a.wait_ns);
+        const bool ok = wait_here(&seg_full[i], (n / kRing) & 1, vfail, a.wait_ns);
         g = s_seg[i];
         __syncwarp();
         if (lane == 0) umma::mbar_arrive(&seg_free[i]);
@@ -186,7 +204,10 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
     // Whether group 1 has rows in this unit.
     auto both = [&](const Segment &g) { return static_cast<long long>(g.nq) * a.grp - static_cast<long long>(g.r) * NB > 128; };
 
+    // Registers: 2 x 128 softmax threads take 200, the other 2 x 128 keep 56; the sum is what the block was launched
+    // with (512 x 128, which the launch makes sure of).
     if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---- softmax: thread = row ---------------------------------------------------------------
         const int grp = warp >> 2, r = tid & 127;
         const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -217,45 +238,51 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
             for (int t = g.t0; t < g.t1; ++t, ++it, ++mine) {
                 const int bf = it & 1;
                 const bool first = t == g.t0, part = (t + 1) * kTile > clear;
-                ok = wait(&s_full[grp], mine & 1, vfail, a.wait_ns);
+                ok = wait_here(&s_full[grp], mine & 1, vfail, a.wait_ns);
                 // The keys' scales.  (After S: group 1 may have left tiles out, and only once S(t) is there has its
                 // buffer's last use but one surely begun, which the parity cannot tell.)
-                ok = ok && wait(&vo_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                ok = ok && wait_here(&vo_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 umma::tc_fence_after();
-                uint4 see = make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);
-                if (part) see = seen_keys(a, t, g.kv, g.nq, g.q0, live ? tq : 0);
-                // the row's largest logit plus log of V's scale
-                float top = -INFINITY;
-                const uint64_t qs2 = pk2(qs, qs);
-                uint4 sw = see;
-#pragma unroll 1
-                for (int c = 0; c < kTile; c += 32) {
-                    uint32_t v[32];
-                    umma::tmem_ld32(t_s + c, v);
-                    umma::tmem_ld_wait_regs(v);
-                    float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                // the row's logits less qs, in registers: x = S ka
+                float x[kTile];
+                {
+                    uint32_t v[4][32];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 ka = *reinterpret_cast<const float4 *>(&s_ka[bf][c + 4 * i]);
-                        const float4 ls = *reinterpret_cast<const float4 *>(&s_lsv[bf][c + 4 * i]);
-                        float x[4];
-                        up2(fma2(mul2(pk2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), pk2(ka.x, ka.y)), qs2, pk2(ls.x, ls.y)),
-                            x[0], x[1]);
-                        up2(fma2(mul2(pk2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), pk2(ka.z, ka.w)), qs2,
-                                 pk2(ls.z, ls.w)),
-                            x[2], x[3]);
-                        if (part) {
+                    for (int c = 0; c < 4; ++c) umma::tmem_ld32(t_s + 32 * c, v[c]);
+                    umma::tmem_ld_wait_regs(v[0]);
+                    umma::reg_fence32(v[1]);
+                    umma::reg_fence32(v[2]);
+                    umma::reg_fence32(v[3]);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) x[e] = (sw.x >> (4 * i + e)) & 1u ? x[e] : -INFINITY;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) top4[e] = fmaxf(top4[e], x[e]);
+                    for (int i = 0; i < kTile / 4; ++i) {
+                        const float4 ka = *reinterpret_cast<const float4 *>(&s_ka[bf][4 * i]);
+                        const uint32_t(&w)[32] = v[i / 8];
+                        const int e = 4 * (i % 8);
+                        up2(mul2(pk2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), pk2(ka.x, ka.y)), x[4 * i], x[4 * i + 1]);
+                        up2(mul2(pk2(__uint_as_float(w[e + 2]), __uint_as_float(w[e + 3])), pk2(ka.z, ka.w)), x[4 * i + 2], x[4 * i + 3]);
                     }
-                    top = fmaxf(fmaxf(fmaxf(top, top4[0]), fmaxf(top4[1], top4[2])), top4[3]);
-                    sw = make_uint4(sw.y, sw.z, sw.w, 0u);
                 }
+                if (part) {
+                    const uint4 see = seen_keys(a, t, g.kv, g.nq, g.q0, live ? tq : 0);
+                    const uint32_t sw[4] = {see.x, see.y, see.z, see.w};
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c) x[c] = (sw[c / 32] >> (c & 31)) & 1u ? x[c] : -INFINITY;
+                }
+                // the row's largest logit plus log of V's scale
+                const uint64_t qs2 = pk2(qs, qs);
+                float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < kTile / 4; ++i) {
+                    const float4 ls = *reinterpret_cast<const float4 *>(&s_lsv[bf][4 * i]);
+                    float y0, y1, y2, y3;
+                    up2(fma2(pk2(x[4 * i], x[4 * i + 1]), qs2, pk2(ls.x, ls.y)), y0, y1);
+                    up2(fma2(pk2(x[4 * i + 2], x[4 * i + 3]), qs2, pk2(ls.z, ls.w)), y2, y3);
+                    top4[i & 1] = fmaxf(fmaxf(top4[i & 1], y0), y1);
+                    top4[2 + (i & 1)] = fmaxf(fmaxf(top4[2 + (i & 1)], y2), y3);
+                }
+                const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
                 // the reference: set by the first tile that the row sees a key of, raised where a weight would pass 2^kTop
                 const bool fresh = (l2[0] | l2[1]) == 0;
                 const bool move = top > -INFINITY && (fresh || top + nm > kTop);
@@ -267,39 +294,24 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                     if (!first && __any_sync(0xFFFFFFFFu, f != 1.0f)) rescale_rows<D>(t_o, f);  // (the last product is done: S came after it)
                 }
                 const uint64_t nm2 = pk2(nm, nm);
-                sw = see;
-#pragma unroll 1
+#pragma unroll
                 for (int c = 0; c < kTile; c += 32) {
-                    uint32_t v[32], w[16];
-                    umma::tmem_ld32(t_s + c, v);
-                    umma::tmem_ld_wait_regs(v);
+                    uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float4 ka = *reinterpret_cast<const float4 *>(&s_ka[bf][c + 4 * i]);
                         const float4 sv = *reinterpret_cast<const float4 *>(&s_sv[bf][c + 4 * i]);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int e = 4 * i + 2 * h;
                             float y0, y1, w0, w1;
-                            up2(fma2(mul2(pk2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), h ? pk2(ka.z, ka.w) : pk2(ka.x, ka.y)),
-                                     qs2, nm2),
-                                y0, y1);
-                            if (part) {
-                                y0 = (sw.x >> e) & 1u ? y0 : -INFINITY;
-                                y1 = (sw.x >> (e + 1)) & 1u ? y1 : -INFINITY;
-                            }
+                            up2(fma2(pk2(x[c + e], x[c + e + 1]), qs2, nm2), y0, y1);
                             const uint64_t p = pk2(ex2(y0), ex2(y1));
                             l2[h] = add2(l2[h], p);
                             up2(mul2(p, h ? pk2(sv.z, sv.w) : pk2(sv.x, sv.y)), w0, w1);
-                            if (part) {  // an unseen key has weight 0 whatever its scale is
-                                w0 = (sw.x >> e) & 1u ? w0 : 0.0f;
-                                w1 = (sw.x >> (e + 1)) & 1u ? w1 : 0.0f;
-                            }
                             w[e / 2] = f16x2(w0, w1);
                         }
                     }
-                    umma::tmem_st16(t_s + c / 2, w);  // over logits already read
-                    sw = make_uint4(sw.y, sw.z, sw.w, 0u);
+                    umma::tmem_st16(t_s + c / 2, w);  // over the logits
                 }
                 umma::tmem_st_wait();
                 umma::tc_fence_before();
@@ -307,7 +319,7 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                 if (lane == 0) umma::mbar_arrive(&p_full[grp]);
             }
             if (!ok) break;
-            ok = wait(&o_done[grp], (mine - 1) & 1, vfail, a.wait_ns);
+            ok = wait_here(&o_done[grp], (mine - 1) & 1, vfail, a.wait_ns);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             umma::tc_fence_after();
@@ -351,7 +363,9 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
             }
             umma::tc_fence_before();
         }
-    } else if (warp < 12) {
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp < 12) {
         // ---- converters: V's codes into fp16, the scales into floats (4 bits: K's codes into e4m3) ----
         const int w = tid - 256;
         constexpr int GR = D / 32;
@@ -364,10 +378,10 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
             ++n_seg;
             for (int t = g.t0; t < g.t1; ++t, ++it, rk.next(), rv.next()) {
                 const int bf = it & 1;
-                ok = wait(&v_full[rv.i], rv.parity, vfail, a.wait_ns);
+                ok = wait_here(&v_full[rv.i], rv.parity, vfail, a.wait_ns);
                 if (BITS == 4) {
-                    ok = ok && wait(&k_full[rk.i], rk.parity, vfail, a.wait_ns);
-                    if (it >= 2) ok = ok && wait(&ko_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
+                    ok = ok && wait_here(&k_full[rk.i], rk.parity, vfail, a.wait_ns);
+                    if (it >= 2) ok = ok && wait_here(&ko_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
                 }
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
@@ -406,7 +420,7 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                         umma::mbar_arrive(&k_empty[rk.i]);
                     }
                 }
-                if (it >= 2) ok = wait(&vo_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
+                if (it >= 2) ok = wait_here(&vo_done[bf], ((it >> 1) - 1) & 1, vfail, a.wait_ns);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 {
@@ -419,7 +433,8 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                     if (t * kTile + w >= g.kv) kb = vb = 127u;  // (whatever is there)
                     // 4 bits: K's operand is 2^6 times the values over the largest scale
                     s_ka[bf][w] = scale_of(kb) * (BITS == 8 ? a.scale_log2 : a.scale_log2 * 0x1p-6f);
-                    s_sv[bf][w] = vb == 255u ? NAN : scale_of(vb);
+                    s_sv[bf][w] = vb == 255u ? 1.0f : scale_of(vb);
+                    if (vb == 255u) s_ka[bf][w] = NAN;  // (its V row is 0: the rows that see it become NaN this way)
                     s_lsv[bf][w] = vb == 255u ? 0.0f : fmaxf(static_cast<float>(static_cast<int>(vb) - 127), -64.0f);
                 }
                 const uint8_t *src = base + (vr0 - sm) + rv.i * C::kRaw;
@@ -514,7 +529,7 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                     uint64_t *full = which ? &v_full[rv.i] : &k_full[rk.i];
                     const uint32_t dst = (which ? vr0 + rv.i * C::kRaw : kr0 + rk.i * C::kRaw) + lane * pr * C::kRow;
                     if (it >= (which ? SV : SK))
-                        ok = ok && wait(which ? &v_empty[rv.i] : &k_empty[rk.i], (which ? rv.parity : rk.parity) ^ 1u, vfail, a.wait_ns);
+                        ok = ok && wait_here(which ? &v_empty[rv.i] : &k_empty[rk.i], (which ? rv.parity : rk.parity) ^ 1u, vfail, a.wait_ns);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     if (lane == 0) umma::mbar_arrive_expect_tx(full, bytes);
@@ -560,15 +575,15 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                 // no rows here: K's and V's buffers are given back as they come
                 for (int t = g.t0; ok && t < g.t1; ++t, ++it, rk.next()) {
                     const int bf = it & 1;
-                    ok = BITS == 8 ? wait(&k_full[rk.i], rk.parity, vfail, a.wait_ns) : wait(&ko_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
-                    ok = ok && wait(&vo_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                    ok = BITS == 8 ? wait_here(&k_full[rk.i], rk.parity, vfail, a.wait_ns) : wait_here(&ko_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                    ok = ok && wait_here(&vo_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
                     if (!ok) break;
                     umma::mbar_arrive(BITS == 8 ? &k_empty[rk.i] : &ko_done[bf]);
                     umma::mbar_arrive(&vo_done[bf]);
                 }
             } else if (lane == 0) {
                 auto scores = [&](int i, const Ring<SK> &k) {
-                    ok = ok && (BITS == 8 ? wait(&k_full[k.i], k.parity, vfail, a.wait_ns) : wait(&ko_full[i & 1], (i >> 1) & 1, vfail, a.wait_ns));
+                    ok = ok && (BITS == 8 ? wait_here(&k_full[k.i], k.parity, vfail, a.wait_ns) : wait_here(&ko_full[i & 1], (i >> 1) & 1, vfail, a.wait_ns));
                     if (!ok) return;
                     umma::tc_fence_after();
                     const uint64_t dk = desc_rows8<D>(BITS == 8 ? kr0 + k.i * C::kRaw : k80 + (i & 1) * C::kK8);
@@ -579,14 +594,14 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                     umma::mma_commit(&s_full[grp]);
                     umma::mma_commit(BITS == 8 ? &k_empty[k.i] : &ko_done[i & 1]);
                 };
-                ok = wait(&q_full[grp], n_own & 1, vfail, a.wait_ns);
+                ok = wait_here(&q_full[grp], n_own & 1, vfail, a.wait_ns);
                 scores(it, rk);
                 // test hook: with S in flight, wait for what never comes
-                if (ok && mine == 0 && a.inject) ok = wait(&never, 0, vfail, a.wait_ns);
+                if (ok && mine == 0 && a.inject) ok = wait_here(&never, 0, vfail, a.wait_ns);
                 for (int t = g.t0; ok && t < g.t1; ++t, ++it, ++mine) {
                     const int bf = it & 1;
-                    ok = wait(&vo_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
-                    ok = ok && wait(&p_full[grp], mine & 1, vfail, a.wait_ns);
+                    ok = wait_here(&vo_full[bf], (it >> 1) & 1, vfail, a.wait_ns);
+                    ok = ok && wait_here(&p_full[grp], mine & 1, vfail, a.wait_ns);
                     if (!ok) break;
                     umma::tc_fence_after();
                     const uint64_t dv = umma::desc_sw128_mn(vf0 + bf * C::kVf, kTile * 128);
@@ -597,7 +612,7 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                     rk.next();
                     if (t + 1 < g.t1) {
                         // (products of two kinds into different accumulators need not run in the order of issue)
-                        ok = wait(&o_done[grp], mine & 1, vfail, a.wait_ns);
+                        ok = wait_here(&o_done[grp], mine & 1, vfail, a.wait_ns);
                         scores(it + 1, rk);
                     }
                 }
@@ -619,7 +634,7 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
             Segment g;
             line.next(a, g);
             const int i = n_seg & (kRing - 1);
-            if (n_seg >= kRing) ok = wait(&seg_free[i], ((n_seg / kRing) - 1) & 1, vfail, a.wait_ns);
+            if (n_seg >= kRing) ok = wait_here(&seg_free[i], ((n_seg / kRing) - 1) & 1, vfail, a.wait_ns);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             if (lane == 0) {
@@ -629,6 +644,7 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
             if (g.t1 == 0) break;
         }
         if (lane == 0) a.desc[cta] = ok ? line.cut : make_int4(-1, 0, 0, 0);
+    }
     }
     __syncwarp();
     umma::tc_fence_before();
