@@ -656,6 +656,8 @@ qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B,
  *     2^-13 of its row's largest and off by at most 2^-21 of the largest
  *     below; a weight is off by at most 2^-9 of itself or 2^-25 of the largest.
  *   more rows: 2^-9 and 2^-17; 2^-11.
+ *   Where V is so small that it matters, an output over n keys is off by at
+ *   most n 2^-106 more (the weights' range ends).
  *   4 bits: K groups (with few rows V's too) whose scale is below 2^-14 of
  *     their row's largest count as 0 (with many rows V's below 2^-24).
  * A row of q

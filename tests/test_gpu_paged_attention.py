@@ -473,3 +473,210 @@ def test_joins_the_compressed_history():
     want, _ = ref.attention(b.q.double().cpu().numpy(), np.concatenate([kh, k_all]), np.concatenate([vh, v_all]), see)
     # the compressed side's own bar: 2e-3 of the largest output (fp16 operands)
     assert np.abs(got.cpu().numpy() - want).max() <= 2e-3 * np.abs(want).max()
+
+
+# ---- many rows a sequence -------------------------------------------------------------------------
+
+
+def check_on_device(b, out, lse, mode, rows=None):
+    """Batch.check's plain form and bounds, sequence by sequence on the GPU in
+    64 bits (for batches that are too long for the host's loop).  Below 2^-90
+    V's scale is not in the reference: a weight, of up to 2^98 of its row's
+    sum, is off by at most 2^-17 (half of e5m2's smallest step) against codes
+    up to 448, n 2^-106 over n keys."""
+    k_all, v_all = (torch.from_numpy(x).cuda().transpose(1, 2).reshape(-1, b.H, b.d) for x in ref.held(b.cache))
+    q_step = 2.0 ** -21 if max(b.nq) * b.G <= (32 if b.cache.bits == 8 else 16) else 2.0 ** -17
+    half = 2.0 ** -8 if out.dtype == torch.bfloat16 else 2.0 ** -24
+    scale, first = 1 / math.sqrt(b.d), 0
+    for i, (T, L) in enumerate(zip(b.nq, b.kv)):
+        if T == 0:
+            continue
+        at = torch.from_numpy(b.slots[i]).cuda()
+        see = torch.from_numpy(b.see(i, mode, None if rows is None else rows[i])).cuda()
+        q = b.q[first:first + T].double().view(T, b.H, b.G, b.d)
+        got, got_lse = out[first:first + T].double().view(T, b.H, b.G, b.d), lse[:, first:first + T].double().view(b.H, b.G, T)
+        first += T
+        k, v = k_all[at], v_all[at]
+        s = torch.einsum("thgd,lhd->hgtl", q, k) * scale
+        s = s.masked_fill(~see, -math.inf)
+        m = s.amax(-1, keepdim=True).clamp(min=-1e300)
+        p = torch.exp(s - m)
+        den = p.sum(-1, keepdim=True)
+        want_lse = (m + den.log())[..., 0]
+        w = p / den.clamp(min=1e-300)
+        n = see.sum(-1).double()
+        absqk = torch.einsum("thgd,lhd->hgtl", q.abs(), k.abs())
+        dd = scale * (q_step * q.abs().amax(-1).permute(1, 2, 0)[..., None] * k.abs().sum(-1).t()[:, None, None] + 2 * b.d * 2.0 ** -23 * absqk)
+        dd = (dd + 8 * 2.0 ** -24 * s.abs().masked_fill(~see, 0)).masked_fill(~see, 0).amax(-1)
+        rel = 2 * dd + 2.0 ** -20 + 2.0 ** -11 + 2.0 ** -9 + n * 2.0 ** -24
+        back = lambda x: x.permute(2, 0, 1)[..., None]  # noqa: E731
+        want = torch.einsum("hgtl,lhd->thgd", w, v)
+        mean = torch.einsum("hgtl,lhd->thgd", w, v.abs())
+        lost = n * 2.0 ** -24 * (w * v.abs().amax(-1).t()[:, None, None]).amax(-1)
+        bound = back(rel) * mean + back(lost) + half * want.abs() + back(n.expand_as(rel)) * 2.0 ** -106
+        err = (got - want).abs()
+        assert bool((err <= bound).all()), (i, float((err / bound).max()))
+        some = n > 0
+        assert bool((got_lse[:, :, ~some] == -math.inf).all()) and bool((got[~some] == 0).all())
+        lb = dd + 2.0 ** -20 + n * 2.0 ** -24 + 2.0 ** -21 * want_lse.abs()
+        assert bool(((got_lse - want_lse).abs() <= lb)[:, :, some].all())
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mode", [qvg.QVG_MASK_NONE, qvg.QVG_MASK_CAUSAL, qvg.QVG_MASK_TREE])
+def test_many_rows_many_units(bits, d, mode):
+    """Several row blocks in one CTA's run, second halves of them with and
+    without rows, sequences without new tokens, without history, without keys."""
+    g = np.random.default_rng(100 + d)
+    nq = [int(x) for x in g.choice([0, 1, 31, 32, 33, 64, 65, 75, 97], size=230)]
+    kv = [max(n, int(x)) for n, x in zip(nq, g.integers(0, 500, size=230))]
+    nq[0], kv[0], nq[7], kv[7] = 97, 97, 64, 64
+    b = Batch(2, 4, d, bits, 32, nq, kv, seed=22)
+    mask = rows = None
+    if mode == qvg.QVG_MASK_TREE:
+        rows = [np.eye(T, dtype=bool) | (g.random((T, T)) < 0.5) for T in nq]
+        rows[0][[0, 40, 96]] = False  # no history: rows that see nothing
+        words = np.zeros((sum(nq), (max(nq) + 31) // 32), np.uint32)
+        first = 0
+        for T, r in zip(nq, rows):
+            for j in range(T):
+                words[first:first + T, j >> 5] |= r[:, j].astype(np.uint32) << np.uint32(j & 31)
+            first += T
+        mask = torch.from_numpy(words.view(np.int32)).cuda()
+    out, lse = b.run(mode, mask=mask)
+    assert qvg.get_status() == qvg.QVG_OK
+    check_on_device(b, out, lse, mode, rows)
+    again, lse2 = b.run(mode, mask=mask)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("rows", [15, 16, 17, 31, 32, 33, 127, 128, 129, 255, 256, 257, 600])
+def test_row_counts(bits, rows):
+    """Either side of every size at which another kernel or block begins."""
+    b = Batch(1, 1, 128, bits, 64, (rows, 1, rows // 2), (rows + 300, 200, rows), seed=23)
+    out, lse = b.run()
+    check_on_device(b, out, lse, qvg.QVG_MASK_CAUSAL)
+    b = Batch(2, 3, 64, bits, 16, (-(-rows // 3),), (3000,), seed=24)
+    out, lse = b.run()
+    check_on_device(b, out, lse, qvg.QVG_MASK_CAUSAL)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("G", [4, 16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_unseen_keys_have_no_influence_on_many_rows(bits, G, d):
+    """The same with 17 to 32 rows and more: masked drafts that are not finite,
+    and slots that were never written."""
+    b = Batch(2, G, d, bits, 32, (6, 3), (70, 200), seed=25)
+    mask = torch.tensor([[1 << t] for t in range(6)] + [[1], [3], [7]], dtype=torch.int32, device="cuda")
+    want, want_lse = b.run(qvg.QVG_MASK_TREE, mask=mask)
+    bad = torch.full((2, 2, d), 1.0, dtype=torch.bfloat16, device="cuda")
+    bad[0, :, 3], bad[1, :, 60] = math.inf, math.nan
+    at = torch.from_numpy(b.slots[0][[64 + 1, 64 + 4]]).cuda()
+    good = torch.zeros_like(bad)
+    keep = [i for i in range(9) if i not in (1, 4)]
+    for k, v in ((bad, good), (good, bad), (bad, bad)):
+        qvg.paged_append(b.cache, k, v, at)
+        out, lse = b.run(qvg.QVG_MASK_TREE, mask=mask)
+        assert torch.equal(out[keep], want[keep]) and torch.equal(lse[:, keep], want_lse[:, keep])
+        assert out[[1, 4]].isnan().all()
+    for s in b.slots[0][[64 + 1, 64 + 4]]:
+        for t in (b.cache.k_codes, b.cache.v_codes):
+            t[s // 32, :, s % 32] = torch.randint(0, 256, t.shape[-1:], device="cuda").to(torch.uint8) | 0x7E
+        for t in (b.cache.k_scales, b.cache.v_scales):
+            t[s // 32, :, s % 32] = int(s) * 37 % 256
+    out, lse = b.run(qvg.QVG_MASK_TREE, mask=mask)
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[:, keep], want_lse[:, keep])
+    assert qvg.get_status() == qvg.QVG_OK
+
+
+@pytest.mark.parametrize("T", [7, 60])
+def test_non_finite_query_among_many_rows(T):
+    b = Batch(2, 4, 128, 8, 16, (T,), (300,), seed=26)
+    want, _ = b.run()
+    b.q[1, 2, 7], b.q[2, 5, 0], b.q[T - 1, 7, 127] = math.nan, math.inf, -math.inf
+    out, lse = b.run()
+    nan = torch.zeros(T, 8, dtype=torch.bool)
+    nan[1, 2], nan[2, 5], nan[T - 1, 7] = True, True, True
+    assert (out.cpu().isnan().all(-1) == nan).all() and (lse.cpu().isnan().t() == nan).all()
+    assert torch.equal(out.cpu()[~nan], want.cpu()[~nan])
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("T", [12, 70])
+@pytest.mark.parametrize("kw", [dict(k_scale=30.0), dict(v_scale=2.0 ** -20), dict(v_scale=2.0 ** -80), dict(v_scale=2.0 ** 30),
+                                dict(q_scale=2.0 ** 20, k_scale=2.0 ** -18), dict(k_scale=2.0 ** -30)])
+def test_magnitudes_with_many_rows(bits, T, kw):
+    b = Batch(1, 2, 128, bits, 64, (T, 1), (900, 300), seed=27, **kw)
+    out, lse = b.run()
+    check_on_device(b, out, lse, qvg.QVG_MASK_CAUSAL)
+
+
+@pytest.mark.parametrize("T", [12, 70])
+@pytest.mark.parametrize("v_scale", [1.0, 2.0 ** -70, 2.0 ** -122])
+def test_growing_logits_with_many_rows(T, v_scale):
+    """References raised from tile to tile, by a little and by far more than
+    the weights' types hold; with V so small that the sum would overflow first."""
+    for L, top in ((3000, 400.0), (9000, 3e4)):
+        b = Batch(1, 2, 128, 8, 64, (T,), (L,), seed=28, v_scale=v_scale)
+        t = torch.arange(L, device="cuda")
+        k = torch.randn(L, 1, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+        k[:, 0, 0] = t / L * top
+        qvg.paged_append(b.cache, k.bfloat16(), b.v, torch.from_numpy(b.slots[0]).cuda())
+        b.q[:, 0, 0], b.q[:, 1, 0] = 1.0, -2.0
+        out, lse = b.run()
+        check_on_device(b, out, lse, qvg.QVG_MASK_CAUSAL)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("T", [6, 80])
+def test_many_rows_padded_captured_and_out_of_time(bits, T):
+    """A padded batch, several streams at once, a replayed graph, and the
+    library's bounded-wait hook, for the kernels of more than 16 rows."""
+    b = Batch(2, 4, 128, bits, 32, (T, 0, T // 2), (1500, 40, 700), seed=29)
+    want, want_lse = b.run()
+    check_on_device(b, want, want_lse, qvg.QVG_MASK_CAUSAL)
+    n = sum(b.nq)
+    q = torch.full((n + 5, 8, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    q[:n] = b.q
+    out = torch.full_like(q, 5.0)
+    qvg.paged_attention(b.cache, q, b.table, b.kv_len, T, cu_q=b.cu_q, out=out)
+    assert (out[n:] == 5).all() and torch.equal(out[:n], want)
+    side = [torch.cuda.Stream() for _ in range(2)]
+    for s in side:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [b.run(stream=s) for _ in range(3) for s in side]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) and torch.equal(l, want_lse) for o, l in got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, l = b.run()
+    for _ in range(2):
+        o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(l, want_lse)
+    qvg.debug_set_wait(1_000_000, True)
+    try:
+        b.run()
+    finally:
+        qvg.debug_set_wait(0, False)
+    assert qvg.get_status() == qvg.QVG_ERR_TIMEOUT
+    again, _ = b.run()
+    assert qvg.get_status() == qvg.QVG_OK and torch.equal(again, want)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("T", [1, 12, 70])
+def test_logits_far_below_zero(bits, T):
+    """Every key's logit far below 0, in every cut of the sequence: the first
+    reference is as far below."""
+    b = Batch(1, 2, 128, bits, 64, (T,), (5000,), seed=30)
+    k = torch.randn(5000, 1, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+    k[:, 0, 0] = 3000.0
+    qvg.paged_append(b.cache, k.bfloat16(), b.v, torch.from_numpy(b.slots[0]).cuda())
+    b.q[:, :, 0] = -4.0
+    out, lse = b.run()
+    check_on_device(b, out, lse, qvg.QVG_MASK_CAUSAL)

@@ -51,6 +51,9 @@ namespace pa {
 
 constexpr int kTile = 128;
 constexpr float kTarget = 8.0f, kTop = 15.0f;
+// V's scale enters the reference, so that w = p sv spans its type's range; from 2^kLeastV down only p does, whose sums
+// (up to 2^(kTop - kLeastV) a key) stay in fp32.
+constexpr float kLeastV = -90.0f;
 constexpr uint64_t kDrainNs = 2000000000ull;
 
 struct Args {
@@ -520,13 +523,12 @@ __device__ __noinline__ void clean_values(uint8_t *v, int from, int past, int r)
 template <int NC, int NB>
 __device__ __noinline__ bool set_references(uint32_t t_s, uint32_t t_own, const float *qs, float *nm, float *scratch, float (*red)[NC],
                                             float *dl, int r, float ka, float lsv, const uint32_t hidden, bool first, bool ok) {
-    const float lw = fmaxf(lsv, -64.0f);
 #pragma unroll 1
     for (int c = 0; c < NC; c += 16) {
         float y[16];
         logits16(t_s + c, t_s + NB + c, qs + c, nm + c, ka, y);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = (hidden >> (c + i)) & 1u ? -INFINITY : y[i] + lw;
+        for (int i = 0; i < 16; ++i) y[i] = (hidden >> (c + i)) & 1u ? -INFINITY : y[i] + lsv;
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
             *reinterpret_cast<float4 *>(scratch + r * NC + c + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
@@ -541,7 +543,7 @@ __device__ __noinline__ bool set_references(uint32_t t_s, uint32_t t_own, const 
         const bool move = first ? mx > -INFINITY : mx > kTop;
         const float d = move ? mx - kTarget : 0.0f;
         nm[r] -= d;
-        dl[r] = ex2(-d);
+        dl[r] = first ? 1.0f : ex2(-d);  // (a first reference may lie far below 0, and l is 0 yet)
     }
     any_of(1, 128, false);
     if (!first) {
@@ -731,7 +733,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
                 const float ka = scale_of(kb) * (BITS == 8 ? a.scale_log2 : a.scale_log2 * 0x1p-6f);
                 const bool v_nan = vb == 255u;  // weighed as 1, and made a NaN below
                 const float sv = v_nan ? 1.0f : scale_of(vb) * (BITS == 8 ? 1.0f : 0x1p-6f);
-                const float lsv = v_nan ? 0.0f : static_cast<float>(static_cast<int>(vb) - (BITS == 8 ? 127 : 133));
+                const float lsv = v_nan ? 0.0f : fmaxf(static_cast<float>(static_cast<int>(vb) - (BITS == 8 ? 127 : 133)), kLeastV);
                 const bool part = (t + 1) * kTile > clear;
                 const uint64_t ka2 = pk2(ka, ka), lo2 = pk2(0.0625f, 0.0625f);
                 uint32_t hidden = 0;  // columns that do not see this key, where that can be

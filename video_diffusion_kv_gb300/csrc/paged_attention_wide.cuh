@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                     s_ka[bf][w] = scale_of(kb) * (BITS == 8 ? a.scale_log2 : a.scale_log2 * 0x1p-6f);
                     s_sv[bf][w] = vb == 255u ? 1.0f : scale_of(vb);
                     if (vb == 255u) s_ka[bf][w] = NAN;  // (its V row is 0: the rows that see it become NaN this way)
-                    s_lsv[bf][w] = vb == 255u ? 0.0f : fmaxf(static_cast<float>(static_cast<int>(vb) - 127), -64.0f);
+                    s_lsv[bf][w] = vb == 255u ? 0.0f : fmaxf(static_cast<float>(static_cast<int>(vb) - 127), kLeastV);
                 }
                 const uint8_t *src = base + (vr0 - sm) + rv.i * C::kRaw;
                 if constexpr (BITS == 8) {
