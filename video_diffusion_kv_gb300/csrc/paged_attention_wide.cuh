@@ -270,48 +270,66 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
 #pragma unroll
                     for (int c = 0; c < kTile; ++c) x[c] = (sw[c / 32] >> (c & 31)) & 1u ? x[c] : -INFINITY;
                 }
-                // the row's largest logit plus log of V's scale
-                const uint64_t qs2 = pk2(qs, qs);
-                float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < kTile / 4; ++i) {
-                    const float4 ls = *reinterpret_cast<const float4 *>(&s_lsv[bf][4 * i]);
-                    float y0, y1, y2, y3;
-                    up2(fma2(pk2(x[4 * i], x[4 * i + 1]), qs2, pk2(ls.x, ls.y)), y0, y1);
-                    up2(fma2(pk2(x[4 * i + 2], x[4 * i + 3]), qs2, pk2(ls.z, ls.w)), y2, y3);
-                    top4[i & 1] = fmaxf(fmaxf(top4[i & 1], y0), y1);
-                    top4[2 + (i & 1)] = fmaxf(fmaxf(top4[2 + (i & 1)], y2), y3);
-                }
-                const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-                // the reference: set by the first tile that the row sees a key of, raised where a weight would pass 2^kTop
+                const uint64_t qs2 = pk2(qs, qs), l_was[2] = {l2[0], l2[1]};
                 const bool fresh = (l2[0] | l2[1]) == 0;
-                const bool move = top > -INFINITY && (fresh || top + nm > kTop);
-                if (__any_sync(0xFFFFFFFFu, move)) {
-                    const float to = move ? kTarget - top : nm, f = move && !fresh ? ex2(to - nm) : 1.0f;
-                    nm = to;
-                    l2[0] = mul2(l2[0], pk2(f, f));
-                    l2[1] = mul2(l2[1], pk2(f, f));
-                    if (!first && __any_sync(0xFFFFFFFFu, f != 1.0f)) rescale_rows<D>(t_o, f);  // (the last product is done: S came after it)
-                }
-                const uint64_t nm2 = pk2(nm, nm);
+                // The reference is set by the first tile that the row sees a key of, and raised where a weight passes
+                // 2^kTop: then the weights are made once more.
+                bool look = __any_sync(0xFFFFFFFFu, fresh);
+                for (bool again = true; again;) {
+                    uint64_t lp[2] = {l_was[0], l_was[1]};
+                    if (look) {
+                        // the row's largest logit plus log of V's scale
+                        float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 sv = *reinterpret_cast<const float4 *>(&s_sv[bf][c + 4 * i]);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int e = 4 * i + 2 * h;
-                            float y0, y1, w0, w1;
-                            up2(fma2(pk2(x[c + e], x[c + e + 1]), qs2, nm2), y0, y1);
-                            const uint64_t p = pk2(ex2(y0), ex2(y1));
-                            l2[h] = add2(l2[h], p);
-                            up2(mul2(p, h ? pk2(sv.z, sv.w) : pk2(sv.x, sv.y)), w0, w1);
-                            w[e / 2] = f16x2(w0, w1);
+                        for (int i = 0; i < kTile / 4; ++i) {
+                            const float4 ls = *reinterpret_cast<const float4 *>(&s_lsv[bf][4 * i]);
+                            float y0, y1, y2, y3;
+                            up2(fma2(pk2(x[4 * i], x[4 * i + 1]), qs2, pk2(ls.x, ls.y)), y0, y1);
+                            up2(fma2(pk2(x[4 * i + 2], x[4 * i + 3]), qs2, pk2(ls.z, ls.w)), y2, y3);
+                            top4[i & 1] = fmaxf(fmaxf(top4[i & 1], y0), y1);
+                            top4[2 + (i & 1)] = fmaxf(fmaxf(top4[2 + (i & 1)], y2), y3);
                         }
+                        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+                        const bool move = top > -INFINITY && (fresh || top + nm > kTop);
+                        const float to = move ? kTarget - top : nm, f = move && !fresh ? ex2(to - nm) : 1.0f;
+                        nm = to;
+                        lp[0] = mul2(lp[0], pk2(f, f));
+                        lp[1] = mul2(lp[1], pk2(f, f));
+                        if (!first && __any_sync(0xFFFFFFFFu, f != 1.0f)) rescale_rows<D>(t_o, f);  // (the last product is done: S came after it)
                     }
-                    umma::tmem_st16(t_s + c / 2, w);  // over the logits
+                    const uint64_t nm2 = pk2(nm, nm);
+                    __half2 high = __half2half2(__ushort_as_half(0));  // the largest weights
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 32) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 sv = *reinterpret_cast<const float4 *>(&s_sv[bf][c + 4 * i]);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int e = 4 * i + 2 * h;
+                                float y0, y1, w0, w1;
+                                up2(fma2(pk2(x[c + e], x[c + e + 1]), qs2, nm2), y0, y1);
+                                const uint64_t p = pk2(ex2(y0), ex2(y1));
+                                lp[h] = add2(lp[h], p);
+                                up2(mul2(p, h ? pk2(sv.z, sv.w) : pk2(sv.x, sv.y)), w0, w1);
+                                w[e / 2] = f16x2(w0, w1);
+                                high = __hmax2(high, *reinterpret_cast<const __half2 *>(&w[e / 2]));
+                            }
+                        }
+                        umma::tmem_st16(t_s + c / 2, w);  // over the logits
+                    }
+                    l2[0] = lp[0];
+                    l2[1] = lp[1];
+                    const uint32_t hb = *reinterpret_cast<const uint32_t *>(&high);
+                    float a0, a1, a2, a3;
+                    up2(l2[0], a0, a1);
+                    up2(l2[1], a2, a3);
+                    // (the sum has no V scale in it: where V's is below 2^kLeastV it could overflow before a weight does)
+                    again = !look && __any_sync(0xFFFFFFFFu, max(hb & 0xFFFFu, hb >> 16) >= 0x7800u ||  // 2^kTop
+                                                                 fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) > 0x1p120f);
+                    if (again) umma::tmem_st_wait();
+                    look = true;
                 }
                 umma::tmem_st_wait();
                 umma::tc_fence_before();
