@@ -20,8 +20,10 @@
  *   - Every call returns a qvg_status.  Argument errors are found on the
  *     host before anything is launched and leave all buffers untouched.
  *     A failed launch returns QVG_ERR_CUDA.  Errors found on the device
- *     (an exceeded wait bound) are latched in a per-device status word and
- *     reported by qvg_get_status(stream).
+ *     (an exceeded wait bound; in the token-wise operators also values in
+ *     device arrays that are out of range: slots, pages, lengths, parents)
+ *     are latched in a per-device status word and reported by
+ *     qvg_get_status(stream).
  *   - bf16 / fp16 values travel as their 16-bit patterns (uint16_t).
  *   - Layouts are row-major; "[a][b][c]" lists dimensions outermost first.
  *   - Thread safety: calls on different streams, from any host threads, may
@@ -419,7 +421,7 @@ qvg_status qvg_get_status(void *stream);
 /*
  * Device-side waits, a test hook for the failure path (the pages have no
  * counterpart).  Every wait of a kernel on a barrier (the k-means
- * assignment's tile and MMA hand-offs, the attention pipeline's) is bounded;
+ * assignment's tile and MMA hand-offs, the attention pipelines') is bounded;
  * when the bound runs out the kernel stops its work, waits at the default
  * bound for the tensor-core work it has issued, frees its tensor memory,
  * latches QVG_ERR_TIMEOUT in the device word and returns, leaving the
@@ -601,15 +603,20 @@ qvg_status qvg_paged_read(const qvg_paged *cache, const int64_t *slots, int32_t 
  *            (the token follows the history).  Another value latches
  *            QVG_ERR_INVALID_ARG and counts as -1.
  *   cu_q     int32 [B + 1] device: sequence b's new tokens are rows
- *            cu_q[b] .. cu_q[b + 1] - 1; NULL: max_q rows each.
+ *            cu_q[b] .. cu_q[b + 1] - 1; NULL: max_q rows each.  A sequence
+ *            of more than max_q, or with rows outside total_q, latches
+ *            QVG_ERR_INVALID_ARG; rows past its max_q, or all of its rows,
+ *            are left as they were.
+ *   total_q  rows of parents and mask.
  *   mask     uint32 [total_q][words] device, words >= ceil(max_q / 32);
  *            bit j % 32 of word j / 32 is new token j.  Every word of the
  *            rows cu_q[0] .. cu_q[B] - 1 is written.
- * Errors: QVG_ERR_INVALID_ARG for B < 0, max_q < 0, too few words, missing
- * or misaligned pointers.
+ * Errors: QVG_ERR_INVALID_ARG for B < 0, max_q < 0, total_q < 0 or (without
+ * cu_q) below B * max_q, too few words, missing or misaligned pointers;
+ * QVG_ERR_UNSUPPORTED for max_q > 8192.
  */
-qvg_status qvg_tree_mask(const int32_t *parents, const int32_t *cu_q, int32_t B, int32_t max_q, int32_t words,
-                         uint32_t *mask, void *stream);
+qvg_status qvg_tree_mask(const int32_t *parents, const int32_t *cu_q, int32_t B, int32_t max_q, int32_t total_q,
+                         int32_t words, uint32_t *mask, void *stream);
 
 /*
  * Scratch bytes of qvg_paged_attention on the current device (256-byte
@@ -622,7 +629,8 @@ qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B,
  * (decoding), a drafted tree, or the tokens of a chunk.  The new tokens' K
  * and V have been appended: they are the last tokens of the sequence.  With
  * L = kv_len[b] tokens and T new ones, key j < L - T is history and key
- * L - T + i is new token i; new token t sees what mask_mode says, and
+ * L - T + i is new token i (T > L: the first T - L have none); new token t
+ * sees what mask_mode says, and
  *   O = softmax(scale * Q K^T) V   over the keys it sees.
  *   q          bf16 [total_q][Hq][d], 16-byte aligned; token t starts at
  *              element t * q_stride (a multiple of 8, >= Hq d).  Query head
@@ -652,7 +660,7 @@ qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B,
  * on it, whatever they hold.  Q enters the product as the sum of two fp8
  * numbers, K and V as their codes, the weights times V's scale as the sum of
  * three fp8 numbers or as fp16; all sums are fp32.
- *   max_q * Hq / H <= 32 (16 with 4 bits): a channel of q is exact down to
+ *   max_q * Hq / H <= 64 (32 with 4 bits): a channel of q is exact down to
  *     2^-13 of its row's largest and off by at most 2^-21 of the largest
  *     below; a weight is off by at most 2^-9 of itself or 2^-25 of the largest.
  *   more rows: 2^-9 and 2^-17; 2^-11.
@@ -660,9 +668,10 @@ qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B,
  *   most n 2^-106 more (the weights' range ends).
  *   4 bits: K groups (with few rows V's too) whose scale is below 2^-14 of
  *     their row's largest count as 0 (with many rows V's below 2^-24).
- * A row of q
- * with an infinity or a NaN gives NaN.  The results do not depend on what
- * else the GPU runs: the split of the work follows from the sizes alone.
+ * A row of q with an infinity or a NaN, and one that sees a K or V row marked
+ * with scale 255, gives NaN (with many rows its lse is NaN too where only V is
+ * marked).  The results do not depend on what else the GPU runs: the split of
+ * the work follows from the sizes and the number of SMs alone.
  * All sizes on the device are read when the kernels run: a captured call can
  * be replayed with other lengths, tables and masks.
  */

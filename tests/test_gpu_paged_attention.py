@@ -81,7 +81,7 @@ class Batch:
         got_lse = None if lse is None else lse.double().cpu().numpy()
         scale = 1 / math.sqrt(self.d) if scale is None else scale
         rows_in_block = max(self.nq) * self.G
-        q_step = 2.0 ** -21 if rows_in_block <= (32 if self.cache.bits == 8 else 16) else 2.0 ** -17
+        q_step = 2.0 ** -21 if rows_in_block <= (64 if self.cache.bits == 8 else 32) else 2.0 ** -17
         half = 2.0 ** -8 if out.dtype == torch.bfloat16 else 2.0 ** -24
         first = 0
         for b, T in enumerate(self.nq):
@@ -485,7 +485,7 @@ def check_on_device(b, out, lse, mode, rows=None):
     sum, is off by at most 2^-17 (half of e5m2's smallest step) against codes
     up to 448, n 2^-106 over n keys."""
     k_all, v_all = (torch.from_numpy(x).cuda().transpose(1, 2).reshape(-1, b.H, b.d) for x in ref.held(b.cache))
-    q_step = 2.0 ** -21 if max(b.nq) * b.G <= (32 if b.cache.bits == 8 else 16) else 2.0 ** -17
+    q_step = 2.0 ** -21 if max(b.nq) * b.G <= (64 if b.cache.bits == 8 else 32) else 2.0 ** -17
     half = 2.0 ** -8 if out.dtype == torch.bfloat16 else 2.0 ** -24
     scale, first = 1 / math.sqrt(b.d), 0
     for i, (T, L) in enumerate(zip(b.nq, b.kv)):
@@ -552,7 +552,7 @@ def test_many_rows_many_units(bits, d, mode):
 
 
 @pytest.mark.parametrize("bits", [8, 4])
-@pytest.mark.parametrize("rows", [15, 16, 17, 31, 32, 33, 127, 128, 129, 255, 256, 257, 600])
+@pytest.mark.parametrize("rows", [15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 600])
 def test_row_counts(bits, rows):
     """Either side of every size at which another kernel or block begins."""
     b = Batch(1, 1, 128, bits, 64, (rows, 1, rows // 2), (rows + 300, 200, rows), seed=23)
@@ -680,3 +680,43 @@ def test_logits_far_below_zero(bits, T):
     b.q[:, :, 0] = -4.0
     out, lse = b.run()
     check_on_device(b, out, lse, qvg.QVG_MASK_CAUSAL)
+
+
+def test_tree_masks_of_long_trees():
+    """Chains and bushes up to the largest tree, rows wider than they need be,
+    and row counts that do not fit the tensors."""
+    g = np.random.default_rng(31)
+    T = 8192
+    chain = torch.arange(T, dtype=torch.int32, device="cuda") - 1
+    m = qvg.tree_mask(chain, T).cpu().numpy().view(np.uint32)
+    t, w = np.arange(T)[:, None], np.arange(T // 32)[None]
+    full = np.clip(t + 1 - 32 * w, 0, 32)
+    assert (m == ((1 << full.astype(np.uint64)) - 1).astype(np.uint32)).all()
+    parents = np.array([-1] + [int(g.integers(max(-1, i - 40), i)) for i in range(1, 700)], np.int32)
+    rows = ref.tree_rows(parents)
+    out = torch.full((700, 30), -1, dtype=torch.int32, device="cuda")
+    qvg.tree_mask(torch.from_numpy(parents).cuda(), 700, out=out)
+    bits = np.unpackbits(out.cpu().numpy().view(np.uint8), axis=1, bitorder="little")
+    assert (bits[:, :700] == rows).all() and not bits[:, 700:].any()
+    assert qvg.get_status() == qvg.QVG_OK
+    for cu in ([0, 5, 900], [0, 5, 3], [-3, 2, 4], [2**31 - 1, -2**31, 7]):
+        out.fill_(-1)
+        qvg.tree_mask(torch.from_numpy(parents).cuda(), 20, cu_q=torch.tensor(cu, dtype=torch.int32, device="cuda"), out=out)
+        assert qvg.get_status() == qvg.QVG_ERR_INVALID_ARG, cu
+        assert (out[20:] == -1).all()
+
+
+@pytest.mark.parametrize("G", [1, 8, 64])
+def test_nothing_to_do(G):
+    """No new tokens in any sequence; no keys in any; pages shared by sequences."""
+    b = Batch(1, G, 64, 8, 16, (2, 1), (40, 30), seed=32)
+    out = torch.full((3, G, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    qvg.paged_attention(b.cache, b.q, b.table, b.kv_len, 2, cu_q=torch.zeros_like(b.cu_q), out=out)
+    assert (out == 5).all()
+    out, lse = qvg.paged_attention(b.cache, b.q, b.table, torch.zeros_like(b.kv_len), 2, cu_q=b.cu_q, want_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    b.table[1] = b.table[0]
+    b.slots[1] = b.slots[0][:30]
+    out, lse = b.run()
+    check_on_device(b, out, lse, qvg.QVG_MASK_CAUSAL)
+    assert qvg.get_status() == qvg.QVG_OK

@@ -154,11 +154,11 @@ def test_python_refusals(lib):
 
 
 def test_tree_mask_refusals(lib):
-    call = lambda par=P, cu=None, B=2, mq=40, w=2, m=P: lib.qvg_tree_mask(par, cu, B, mq, w, m, None)  # noqa: E731
+    call = lambda par=P, cu=None, B=2, mq=40, tq=80, w=2, m=P: lib.qvg_tree_mask(par, cu, B, mq, tq, w, m, None)  # noqa: E731
     for kw in (dict(B=-1), dict(mq=-1), dict(w=1), dict(par=None), dict(m=None), dict(m=ct.c_void_p(0x10002)),
-               dict(cu=ct.c_void_p(0x10001))):
+               dict(tq=-1), dict(tq=79), dict(cu=ct.c_void_p(0x10001))):
         assert call(**kw) == BAD, kw
-    assert call(mq=8193, w=300) == UNS
+    assert call(mq=8193, tq=20000, w=300) == UNS
     assert call(B=0, par=None, m=None) == qvg.QVG_OK
 
 

@@ -1,8 +1,9 @@
 """Python binding of libqvg: compressed video KV cache (QVG / QVG-Pro with
-QuantWM QSAC / PSAC) on one GB300.
+QuantWM QSAC / PSAC) on one GB300, and the operators of single tokens: rotary
+positions, a paged 8-bit / 4-bit cache, and attention over its pages.
 
 Argument marshalling only: every step of compression, reconstruction,
-attention and the QuantWM statistics runs in the CUDA kernels of
+attention, the QuantWM statistics and the token-wise operators runs in the CUDA kernels of
 ``libqvg.so``; PyTorch provides device memory and streams.  There is no
 fallback: if the library is missing or no CUDA device is present, the calls
 raise.
@@ -108,7 +109,7 @@ def lib():
         L.qvg_paged_bytes.argtypes = [i32, i32, i32, i32, i32, vp, vp]
         L.qvg_paged_append.argtypes = [vp, vp, vp, i32, i64, i64, vp, vp, vp, vp]
         L.qvg_paged_read.argtypes = [vp, vp, i32, vp, vp, i32, vp]
-        L.qvg_tree_mask.argtypes = [vp, vp, i32, i32, i32, vp, vp]
+        L.qvg_tree_mask.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp]
         L.qvg_paged_workspace_size.argtypes = [i32, i32, i32, i32, i32, vp]
         L.qvg_paged_attention.argtypes = [vp, vp, i64, i32, i32, i32, i32, vp, vp, i32, vp, i32, vp, i32, ct.c_float,
                                           vp, i32, vp, vp, sz, vp]
@@ -487,6 +488,7 @@ class PagedKV:
         self._c = _Paged(H, d, page_size, num_pages, bits, self.k_codes.data_ptr(), self.k_scales.data_ptr(),
                          self.v_codes.data_ptr(), self.v_scales.data_ptr())
         self._ref = ct.byref(self._c)
+        self._workspace = {}  # paged_attention's scratch bytes by (Hq, max_q): no sequence count changes them
 
     @property
     def nbytes(self):
@@ -548,8 +550,8 @@ def tree_mask(parents, max_q, cu_q=None, out=None, stream=None):
     B = total // max_q if cu_q is None else cu_q.numel() - 1
     _on(parents.device, "tree_mask", parents=(parents, torch.int32), cu_q=(cu_q, torch.int32), out=(out, torch.int32))
     with _Device(parents.device):
-        _check(lib().qvg_tree_mask(parents.data_ptr(), None if cu_q is None else cu_q.data_ptr(), B, max_q, out.shape[1],
-                                   out.data_ptr(), _raw_stream(stream, parents.device)), "qvg_tree_mask")
+        _check(lib().qvg_tree_mask(parents.data_ptr(), None if cu_q is None else cu_q.data_ptr(), B, max_q, total,
+                                   out.shape[1], out.data_ptr(), _raw_stream(stream, parents.device)), "qvg_tree_mask")
     return out
 
 
@@ -587,7 +589,10 @@ def paged_attention(cache: PagedKV, q, block_table, kv_len, max_q, cu_q=None, ma
         cu_q=(cu_q, torch.int32), mask=(mask, torch.int32), out=(out, dt), workspace=(workspace, torch.uint8))
     lse = _empty((Hq, total), torch.float32, q.device, stream) if want_lse else None
     if workspace is None:
-        workspace = _empty((paged_workspace_size(cache, Hq, B, max_q),), torch.uint8, q.device, stream)
+        need = cache._workspace.get((Hq, max_q))
+        if need is None:
+            need = cache._workspace[Hq, max_q] = paged_workspace_size(cache, Hq, B, max_q)
+        workspace = _empty((need,), torch.uint8, q.device, stream)
     with _Device(q.device):
         _check(lib().qvg_paged_attention(
             cache._ref, q.data_ptr(), qs, total, Hq, B, max_q, None if cu_q is None else cu_q.data_ptr(),

@@ -107,6 +107,9 @@ enum { kNoRope = 0, kPairs = 1, kHalves = 2, kAnyHalves = 3 };
 // 2.3 times as long).  The rotated row is rounded to bf16, as qvg_rope would
 // store it.
 // Bound by HBM: reads 4 H D bytes a token, writes 2 H D bits / 8 + scales.
+// 37,440 tokens of 16 heads of 128 into the 4-bit cache with K rotated, and back
+// as bf16 (0.78 GB in all): 196 us, 4.0 TB/s, 58 % of a plain copy's rate; 48
+// tokens of 8 heads take no longer than their launch.
 template <int D, int BITS, int ROPE>
 __global__ void __launch_bounds__(kWarps * 32, ROPE == kNoRope ? 5 : 3)
     k_paged_append(const __grid_constant__ RopeArgs r, PagedArgs a, const uint16_t *__restrict__ k, const uint16_t *__restrict__ v, int n,
@@ -219,7 +222,8 @@ __global__ void __launch_bounds__(kWarps * 32, ROPE == kNoRope ? 5 : 3)
 
 // One warp per token, lanes as in k_paged_append; K and V one after the
 // other.  Bound by HBM: reads the codes and scales, writes n H D elements
-// for each of K and V.
+// for each of K and V.  37,440 tokens of 16 heads of 128, 8 bits, as bf16 (0.46
+// GB): 80 us, 5.8 TB/s, 85 % of a plain copy's rate.
 template <int D, int BITS, bool BF16>
 __global__ void __launch_bounds__(kWarps * 32) k_paged_read(PagedArgs a, const int64_t *__restrict__ slots, int n,
                                                            void *__restrict__ k_out, void *__restrict__ v_out,

@@ -73,14 +73,18 @@ __global__ void __launch_bounds__(256) k_paged_merge(const __grid_constant__ pa:
 }
 
 // One block per sequence: parents in shared memory, a thread walks up from
-// its token.  A parent is below its child, so a walk has at most T steps.
-__global__ void k_tree_mask(const int32_t *__restrict__ parents, const int32_t *__restrict__ cu_q, int max_q, int words,
-                            uint32_t *__restrict__ mask, int *err) {
+// its token.  A parent is below its child, so a walk has at most T steps and
+// meets the row's words in falling order: each is written once it is left.
+// What bounds it is the walk (one shared load a step), T of them for a chain.
+__global__ void k_tree_mask(const int32_t *__restrict__ parents, const int32_t *__restrict__ cu_q, int max_q, int total_q,
+                            int words, uint32_t *__restrict__ mask, int *err) {
     extern __shared__ int32_t s_up[];
     const int b = blockIdx.x;
     const long long q0 = cu_q ? cu_q[b] : static_cast<long long>(b) * max_q;
-    const int n = cu_q ? min(cu_q[b + 1] - cu_q[b], max_q) : max_q;
-    if (cu_q && threadIdx.x == 0 && cu_q[b + 1] - cu_q[b] > max_q) raise_error(err, QVG_ERR_INVALID_ARG);
+    const long long all = cu_q ? static_cast<long long>(cu_q[b + 1]) - q0 : max_q;
+    const bool good = q0 >= 0 && all >= 0 && q0 + all <= total_q;
+    const int n = good ? static_cast<int>(min(all, static_cast<long long>(max_q))) : 0;
+    if (threadIdx.x == 0 && (!good || all > max_q)) raise_error(err, QVG_ERR_INVALID_ARG);
     for (int t = threadIdx.x; t < n; t += blockDim.x) {
         int p = parents[q0 + t];
         if (p < -1 || p >= t) {
@@ -90,22 +94,36 @@ __global__ void k_tree_mask(const int32_t *__restrict__ parents, const int32_t *
         s_up[t] = p;
     }
     __syncthreads();
-    // a thread makes one word of one row: bits [32 w, 32 w + 32)
-    for (long long i = threadIdx.x; i < static_cast<long long>(n) * words; i += blockDim.x) {
-        const int t = static_cast<int>(i / words), w = static_cast<int>(i % words);
-        uint32_t m = 0;
-        for (int j = t; j >= 32 * w; j = s_up[j])
-            if ((j >> 5) == w) m |= 1u << (j & 31);
-        mask[(q0 + t) * words + w] = m;
+    for (int t = threadIdx.x; t < n; t += blockDim.x) {
+        uint32_t *row = mask + (q0 + t) * words;
+        int j = t;
+        for (int w = words - 1; w >= 0; --w) {
+            uint32_t m = 0;
+            for (; j >= 32 * w; j = s_up[j]) m |= 1u << (j & 31);
+            row[w] = m;
+        }
     }
 }
 
 constexpr int kMaxTree = 8192;  // new tokens of one sequence whose parents fit 32 KB of shared memory
 
-// Query rows of a unit: 16 or 32 (narrow kernel) where that holds a sequence's
-// rows, else 256 (wide kernel).  4-bit caches have no blocks of 32: the narrow
-// kernel's converters need registers too.
-int rows_of_block(long long rows, int bits) { return rows <= 16 ? 16 : rows <= 32 && bits == 8 ? 32 : pa::kWideRows; }
+// Query rows of a unit, from a sequence's rows (max_q new tokens times the
+// query heads of a KV head): 16 or 32 (narrow kernel) up to two blocks of
+// them, else 256 (wide kernel), whose time hardly depends on them.  4-bit caches
+// have no blocks of 32: the narrow kernel's converters need registers too.
+// Microseconds for 16 sequences of 2,000 to 12,000 keys (8 KV heads, d = 128):
+//            rows     16   32   64   96  128
+//   8 bits   16       62   88  147
+//            32       74   82  124  172
+//            256     140  144  148  155  160
+//   4 bits   16      101  173  309
+//            256     185  188  195  199  203
+// One sequence of 150,000: 64 rows 126 (32 each) against 169, 4 bits and 32 rows
+// 188 (16 each) against 218.  Only where a call is as short as its launch is the
+// order the other way (40 sequences of 300 to 2,000, 2 KV heads: 50 against 41).
+int rows_of_block(long long rows, int bits) {
+    return rows <= (bits == 8 ? 16 : 32) ? 16 : rows <= 64 && bits == 8 ? 32 : pa::kWideRows;
+}
 
 // The narrow kernel has two CTAs an SM, the wide one has one.
 int cta_count(int NB) { return (NB == pa::kWideRows ? 1 : 2) * sm_count_current(); }
@@ -198,15 +216,16 @@ using namespace qvg;
 
 extern "C" {
 
-qvg_status qvg_tree_mask(const int32_t *parents, const int32_t *cu_q, int32_t B, int32_t max_q, int32_t words,
-                         uint32_t *mask, void *stream) {
-    if (B < 0 || max_q < 0 || words < ceil_div(max_q, 32)) return QVG_ERR_INVALID_ARG;
+qvg_status qvg_tree_mask(const int32_t *parents, const int32_t *cu_q, int32_t B, int32_t max_q, int32_t total_q,
+                         int32_t words, uint32_t *mask, void *stream) {
+    if (B < 0 || max_q < 0 || total_q < 0 || words < ceil_div(max_q, 32)) return QVG_ERR_INVALID_ARG;
+    if (!cu_q && static_cast<int64_t>(B) * max_q > total_q) return QVG_ERR_INVALID_ARG;
     if (max_q > kMaxTree) return QVG_ERR_UNSUPPORTED;
     if (B == 0 || max_q == 0) return QVG_OK;
     if (misaligned(parents, 4) || misaligned(mask, 4) || (cu_q && misaligned(cu_q, 4))) return QVG_ERR_INVALID_ARG;
-    const int threads = static_cast<int>(std::min<long long>(1024, (static_cast<long long>(max_q) * words + 31) / 32 * 32));
+    const int threads = std::min(1024, ceil_div(max_q, 32) * 32);
     k_tree_mask<<<B, threads, static_cast<size_t>(max_q) * sizeof(int32_t), static_cast<cudaStream_t>(stream)>>>(
-        parents, cu_q, max_q, words, mask, device_error_word());
+        parents, cu_q, max_q, total_q, words, mask, device_error_word());
     QVG_LAUNCH_CHECK();
     return QVG_OK;
 }

@@ -13,7 +13,7 @@
 // Two CTAs share an SM (8 warps, half of the shared and tensor memory each), so
 // that one's latencies -- a tile is a chain of S, softmax and PV, a unit begins
 // and ends with its own -- pass while the other works.  (One CTA with two
-// softmax groups and twice the rows took 1.7 to 2.4 times as long.)
+// softmax groups: 305 us for the batch below, where two CTAs took 265.)
 //
 // The product runs transposed, keys on the tensor core's 128 rows, and takes
 // the cache's fp8 codes as they lie there (4-bit codes become fp8 first):
@@ -39,6 +39,15 @@
 // takes p in fp32.  The loop's code is kept small (one instance of each part):
 // with copies for the rare cases it outgrew the instruction cache and took
 // 1.5 times as long.
+//
+// Bound: HBM for single tokens.  One token over 449,280 (8 KV heads, d = 128,
+// 4 query heads each, 8 bits; 0.93 GB): 157 us, 5.9 TB/s, 87 % of a plain copy's
+// rate.  48 tokens over 700 to 24,000 each (8 query heads a KV head, pages of
+// 16): 229 us, 5.35 TB/s; pages of 16 mean 8 copies a tile for each of K and V,
+// about 100 clocks of issue each, and every sequence's ends leave a part tile.
+// 4 bits are bound by the conversion into fp8 (four warps, about 500
+// instructions a thread and tile): 24 trees of 5 to 13 tokens over 4,000 to
+// 16,000, 16 KV heads: 302 us, 1.8 TB/s.
 #pragma once
 
 #include <cuda.h>
@@ -523,12 +532,13 @@ __device__ __noinline__ void clean_values(uint8_t *v, int from, int past, int r)
 template <int NC, int NB>
 __device__ __noinline__ bool set_references(uint32_t t_s, uint32_t t_own, const float *qs, float *nm, float *scratch, float (*red)[NC],
                                             float *dl, int r, float ka, float lsv, const uint32_t hidden, bool first, bool ok) {
+    const float lw = fmaxf(lsv, kLeastV);
 #pragma unroll 1
     for (int c = 0; c < NC; c += 16) {
         float y[16];
         logits16(t_s + c, t_s + NB + c, qs + c, nm + c, ka, y);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = (hidden >> (c + i)) & 1u ? -INFINITY : y[i] + lsv;
+        for (int i = 0; i < 16; ++i) y[i] = (hidden >> (c + i)) & 1u ? -INFINITY : y[i] + lw;
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
             *reinterpret_cast<float4 *>(scratch + r * NC + c + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
@@ -733,7 +743,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
                 const float ka = scale_of(kb) * (BITS == 8 ? a.scale_log2 : a.scale_log2 * 0x1p-6f);
                 const bool v_nan = vb == 255u;  // weighed as 1, and made a NaN below
                 const float sv = v_nan ? 1.0f : scale_of(vb) * (BITS == 8 ? 1.0f : 0x1p-6f);
-                const float lsv = v_nan ? 0.0f : fmaxf(static_cast<float>(static_cast<int>(vb) - (BITS == 8 ? 127 : 133)), kLeastV);
+                const float lsv = v_nan ? 0.0f : static_cast<float>(static_cast<int>(vb) - (BITS == 8 ? 127 : 133));
                 const bool part = (t + 1) * kTile > clear;
                 const uint64_t ka2 = pk2(ka, ka), lo2 = pk2(0.0625f, 0.0625f);
                 uint32_t hidden = 0;  // columns that do not see this key, where that can be
@@ -773,7 +783,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
 #pragma unroll
                     for (int c = 4; c < NC; ++c) top4[c & 3] = fmaxf(top4[c & 3], y[c]);
                     const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-                    if (!any_of(1, 128, first || !ok || top + lsv > kTop)) break;
+                    if (!any_of(1, 128, first || !ok || top + fmaxf(lsv, kLeastV) > kTop)) break;
                     if (!first) ok = ok && wait(&pv_done, (it - 1) & 1, vfail, a.wait_ns);  // O's latest
                     dead = !set_references<NC, NB>(t_s, t_o + t_lane, s_qs[qb], s_nm, reinterpret_cast<float *>(p_base), s_red, s_dl, r,
                                                    ka, lsv, hidden, first, ok);

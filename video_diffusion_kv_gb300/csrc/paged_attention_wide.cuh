@@ -12,12 +12,22 @@
 //   O [rows x d]   += P V      P in fp16 in tensor memory, over S; V's codes as
 //                              fp16, made by four converter warps (4 bits: K's
 //                              codes become e4m3 on the way as well)
-// A softmax thread owns a row, so its maximum and sum need no other thread,
-// and the per-weight work is half of the narrow kernel's (no three parts, no
-// weights through shared memory); a key's scales are read from shared memory.
-// One group's products run while the other group is at its softmax.  Tensor
-// core: 8 + 8 products of 64 clocks a group and tile; the softmax's issue slots
-// are the tighter bound (about 900 instructions a warp, row tile and key tile).
+// A softmax thread owns a row, so its maximum and sum need no other thread, and
+// there are no three parts and no weights through shared memory; a key's scales
+// are read from shared memory.  A row's 128 logits stay in registers from the
+// one read of S to the weights, for which the softmax warps take registers from
+// the others (with two reads of S and 128 registers: 510 us for the frame
+// below, where this takes 366); the largest logit is looked for only where a
+// weight overflows (375 us with the search in every tile).
+// One group's products run while the other group is at its softmax.
+//
+// Bound: the chain of a group and tile, about 6000 clocks: its softmax (read
+// 800, weights 1300, waits for S) and then its products, PV(t) and S(t + 1), 8
+// each of 64 clocks, which share the tensor core with the other group's and
+// start on an idle pipe.  880 causal tokens over 21,120 (24 heads, d = 128, 8
+// bits; 2.3e11 operations): 366 us, 624 TFLOP/s, 33 % of a large bf16 product's
+// rate.  16 trees of 17 to 48 tokens (4 query heads each) over 2,000 to 12,000:
+// 199 us; a unit there has 68 to 192 of the 256 rows.
 #pragma once
 
 #include "paged_attention.cuh"
