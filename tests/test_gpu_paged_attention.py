@@ -496,6 +496,9 @@ def check_on_device(b, out, lse, mode, rows=None):
         q = b.q[first:first + T].double().view(T, b.H, b.G, b.d)
         got, got_lse = out[first:first + T].double().view(T, b.H, b.G, b.d), lse[:, first:first + T].double().view(b.H, b.G, T)
         first += T
+        if L == 0:
+            assert bool((got_lse == -math.inf).all()) and bool((got == 0).all())
+            continue
         k, v = k_all[at], v_all[at]
         s = torch.einsum("thgd,lhd->hgtl", q, k) * scale
         s = s.masked_fill(~see, -math.inf)
@@ -720,3 +723,32 @@ def test_nothing_to_do(G):
     out, lse = b.run()
     check_on_device(b, out, lse, qvg.QVG_MASK_CAUSAL)
     assert qvg.get_status() == qvg.QVG_OK
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("mode", [qvg.QVG_MASK_NONE, qvg.QVG_MASK_CAUSAL, qvg.QVG_MASK_TREE])
+@pytest.mark.parametrize("nq,kv", [((5, 16), (3, 1)), ((40, 7), (10, 6)), ((200, 140), (150, 1))])
+def test_more_new_tokens_than_keys(bits, mode, nq, kv):
+    """The first T - L new tokens have no key of their own."""
+    g = np.random.default_rng(33)
+    b = Batch(2, 1, 128, bits, 16, nq, kv, seed=33)
+    mask = rows = None
+    if mode == qvg.QVG_MASK_TREE:
+        parents = [np.array([g.integers(-1, t) if t else -1 for t in range(T)], np.int32) for T in nq]
+        rows = [ref.tree_rows(p) for p in parents]
+        mask = qvg.tree_mask(torch.from_numpy(np.concatenate(parents)).cuda(), max(nq), cu_q=b.cu_q)
+    out, lse = b.run(mode, mask=mask)
+    assert qvg.get_status() == qvg.QVG_OK
+    check_on_device(b, out, lse, mode, rows)
+
+
+def test_thousands_of_sequences():
+    """More sequences than a warp's list holds at once, some without keys,
+    some without new tokens."""
+    g = np.random.default_rng(34)
+    kv = [int(x) for x in g.choice([0, 1, 17, 128, 129, 300], size=2500)]
+    nq = [int(x) for x in g.integers(0, 3, size=2500)]
+    b = Batch(1, 2, 64, 8, 16, nq, kv, seed=34)
+    out, lse = b.run()
+    assert qvg.get_status() == qvg.QVG_OK
+    check_on_device(b, out, lse, qvg.QVG_MASK_CAUSAL)
