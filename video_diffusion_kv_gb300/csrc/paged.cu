@@ -108,10 +108,11 @@ enum { kNoRope = 0, kPairs = 1, kHalves = 2, kAnyHalves = 3 };
 // store it.
 // Bound by HBM: reads 4 H D bytes a token, writes 2 H D bits / 8 + scales.
 // 37,440 tokens of 16 heads of 128 into the 4-bit cache with K rotated, and back
-// as bf16 (0.78 GB in all): 196 us, 4.0 TB/s, 58 % of a plain copy's rate; 48
+// as bf16 (0.78 GB in all): 189 us, 4.1 TB/s, 61 % of a plain copy's rate (the
+// rotation in 64 registers, four blocks an SM; three: 197 us, five: 209 us); 48
 // tokens of 8 heads take no longer than their launch.
 template <int D, int BITS, int ROPE>
-__global__ void __launch_bounds__(kWarps * 32, ROPE == kNoRope ? 5 : 3)
+__global__ void __launch_bounds__(kWarps * 32, ROPE == kNoRope ? 5 : 4)
     k_paged_append(const __grid_constant__ RopeArgs r, PagedArgs a, const uint16_t *__restrict__ k, const uint16_t *__restrict__ v, int n,
                    long long ks, long long vs, const int64_t *__restrict__ slots, const int32_t *__restrict__ positions,
                    int heads_per_block) {
