@@ -638,8 +638,9 @@ qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B,
  *   cu_q       int32 [B + 1] device, ascending from 0: first row of each
  *              sequence's new tokens; NULL: max_q rows each.  Rows from
  *              cu_q[B] on are neither read nor written.
- *   max_q      at least the largest T.  A longer sequence's tokens beyond it
- *              are left out and latch QVG_ERR_INVALID_ARG.
+ *   max_q      at least the largest T.  A longer sequence latches
+ *              QVG_ERR_INVALID_ARG: its tokens beyond max_q are left out, and
+ *              what the others get is undefined.
  *   table      int32 [B][table_stride] device: page of tokens
  *              p * page_size .. of sequence b.  Entries past the sequence's
  *              last page are not read.
