@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(256) k_paged_merge(const __grid_constant__ pa:
     const long long gi = static_cast<long long>(u.z) * NB + n;
     const int tq = static_cast<int>(gi / a.grp), j = static_cast<int>(gi - static_cast<long long>(tq) * a.grp);
     if (tq >= s.nq) return;
-    const int first = blockIdx.x, last = u.w;
+    const int first = blockIdx.x, last = min(u.w, static_cast<int>(gridDim.x) - 1);
     auto at = [&](int z) { return static_cast<size_t>(2 * z + (z == first ? 1 : 0)) * NB + n; };
     float m = -INFINITY;
     for (int z = first + lane; z <= last; z += 32)
