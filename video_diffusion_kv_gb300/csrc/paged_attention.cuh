@@ -47,7 +47,7 @@
 // about 100 clocks of issue each, and every sequence's ends leave a part tile.
 // 4 bits are bound by the conversion into fp8 (four warps, about 500
 // instructions a thread and tile): 24 trees of 5 to 13 tokens over 4,000 to
-// 16,000, 16 KV heads: 277 us, 1.9 TB/s.
+// 16,000, 16 KV heads: 272 us, 1.9 TB/s.
 #pragma once
 
 #include <cuda.h>
@@ -1070,7 +1070,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
                 const uint8_t *src = base + ((which ? vr0 + rv.i * C::kRaw : kr0 + rk.i * C::kRaw) - sm);
                 const uint8_t *scales = base + (sc0 - sm) + rv.i * C::kScales + which * 128 * GR;
                 uint8_t *dst = base + ((which ? v80 : k80) - sm);
-#pragma unroll 4
+#pragma unroll 2
                 for (int i = 0; i < kTile * GR / kThreads; ++i) {
                     const int idx = w + kThreads * i, row = idx / GR, gq = idx % GR;
                     const uint4 v = *reinterpret_cast<const uint4 *>(src + idx * 16);
