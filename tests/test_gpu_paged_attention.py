@@ -752,3 +752,34 @@ def test_thousands_of_sequences():
     out, lse = b.run()
     assert qvg.get_status() == qvg.QVG_OK
     check_on_device(b, out, lse, qvg.QVG_MASK_CAUSAL)
+
+
+# ---- waits that run out ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("G", [1, 32, 128])
+def test_wait_that_ends_while_the_work_is_handed_out(bits, G):
+    """A bound of a nanosecond, and lists of sequences that take from some ten
+    to a thousand microseconds to go through, so that waits run out before,
+    while and after the first unit is handed out: each call ends, and the
+    next one is whole."""
+    b = Batch(1, G, 64, bits, 16, (1, 1), (20, 16), seed=35)
+    want, want_lse = b.run()
+    status = None
+    for n in [int(2 ** (11 + i / 8)) for i in range(33)] + [1 << 16]:
+        kv = torch.zeros(n, dtype=torch.int32, device="cuda")  # one new token each, and hardly any keys
+        kv[:8] = 16
+        table = b.table[:1, :1].expand(n, 1).contiguous()
+        q = b.q[:1].expand(n, G, 64).contiguous()
+        qvg.debug_set_wait(1, False)
+        try:
+            qvg.paged_attention(b.cache, q, table, kv, 1)
+        finally:
+            qvg.debug_set_wait(0, False)
+        status = qvg.get_status()
+        assert status in (qvg.QVG_OK, qvg.QVG_ERR_TIMEOUT), n
+    assert status == qvg.QVG_ERR_TIMEOUT
+    out, lse = b.run()
+    assert qvg.get_status() == qvg.QVG_OK
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)

@@ -714,7 +714,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
         Ring<SV> rv;
         int it = 0, n_seg = 0;
         bool dead = false;
-        while (!dead && next_segment(g, n_seg)) {
+        while (!dead) {
+            // The four warps vote: the segment may be handed out while a wait runs out, after some have given up, and
+            // the barriers below have no bound.
+            const bool got = next_segment(g, n_seg);
+            if (any_of(1, 128, !got)) break;
             const int qb = n_seg & 1;
             const bool q_ok = wait(&q_full[n_seg & 1], (n_seg >> 1) & 1, vfail, a.wait_ns);
             ++n_seg;
