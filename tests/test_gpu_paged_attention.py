@@ -783,3 +783,28 @@ def test_wait_that_ends_while_the_work_is_handed_out(bits, G):
     out, lse = b.run()
     assert qvg.get_status() == qvg.QVG_OK
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("G", [1, 8, 32])
+def test_wait_that_ends_among_short_trees(bits, G):
+    """Trees of four tokens in sequences of one tile: the wait runs out with
+    the first unit's products in flight and the next units' rows not there
+    yet, while every tile needs mask rows.  The status says so, the next call is whole."""
+    g = np.random.default_rng(36)
+    n = 900
+    b = Batch(2, G, 64, bits, 16, [4] * n, [int(x) for x in g.integers(4, 129, size=n)], seed=36)
+    parents = torch.from_numpy(np.concatenate([[-1] + [g.integers(-1, t) for t in range(1, 4)] for _ in range(n)]).astype(np.int32)).cuda()
+    mask = qvg.tree_mask(parents, 4, cu_q=b.cu_q)
+    want, want_lse = b.run(qvg.QVG_MASK_TREE, mask=mask)
+    assert qvg.get_status() == qvg.QVG_OK
+    for limit, inject in ((1_000_000, True), (20_000, True), (1, True), (1, False)):
+        qvg.debug_set_wait(limit, inject)
+        try:
+            b.run(qvg.QVG_MASK_TREE, mask=mask)
+        finally:
+            qvg.debug_set_wait(0, False)
+        assert qvg.get_status() in ((qvg.QVG_ERR_TIMEOUT,) if inject else (qvg.QVG_OK, qvg.QVG_ERR_TIMEOUT))
+        out, lse = b.run(qvg.QVG_MASK_TREE, mask=mask)
+        assert qvg.get_status() == qvg.QVG_OK
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)

@@ -716,11 +716,11 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
         bool dead = false;
         while (!dead) {
             // The four warps vote: the segment may be handed out while a wait runs out, after some have given up, and
-            // the barriers below have no bound.
-            const bool got = next_segment(g, n_seg);
-            if (any_of(1, 128, !got)) break;
+            // the barriers below have no bound.  Nor does any of them go on without the unit's rows (s_tok leads into
+            // the mask).
             const int qb = n_seg & 1;
-            const bool q_ok = wait(&q_full[n_seg & 1], (n_seg >> 1) & 1, vfail, a.wait_ns);
+            const bool got = next_segment(g, n_seg) && wait(&q_full[qb], (n_seg >> 1) & 1, vfail, a.wait_ns);
+            if (any_of(1, 128, !got)) break;
             ++n_seg;
             uint64_t l2[NC / 2];
 #pragma unroll
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
             for (int t = g.t0; t < g.t1; ++t, ++it, rv.next()) {
                 const int bf = it & 1;
                 const bool first = t == g.t0;
-                bool ok = q_ok && !late && wait(&v_full[rv.i], rv.parity, vfail, a.wait_ns);  // (the scales)
+                bool ok = !late && wait(&v_full[rv.i], rv.parity, vfail, a.wait_ns);  // (the scales)
                 const uint8_t *sc = base + (sc0 - sm) + rv.i * C::kScales;
                 uint32_t kb = 0, vb = 0;
                 if constexpr (BITS == 8) {
@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
             }
             if (dead) break;
             // ---- the segment's sums; the weights' buffer is free: l's column sums go through it ----
-            bool ok = !late && q_ok && wait(&pv_done, (it - 1) & 1, vfail, a.wait_ns);
+            bool ok = !late && wait(&pv_done, (it - 1) & 1, vfail, a.wait_ns);
             float *scratch = reinterpret_cast<float *>(p_base);
             if (ok) {
 #pragma unroll
