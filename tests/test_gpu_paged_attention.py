@@ -808,3 +808,28 @@ def test_wait_that_ends_among_short_trees(bits, G):
         out, lse = b.run(qvg.QVG_MASK_TREE, mask=mask)
         assert qvg.get_status() == qvg.QVG_OK
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 70])
+def test_wait_that_ends_with_copies_in_flight(bits, d, T):
+    """Long sequences, whose copies run ahead of the products: K's of a tile
+    may be out when the wait for V's room ends (4 bits and many rows: K's room
+    is free once converted, V's waits for products).  The calls right behind,
+    on the same and on another stream, get their own bytes."""
+    b = Batch(2, 1, d, bits, 16, (T, T), (30000, 20000), seed=37)
+    want, want_lse = b.run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for limit in (1, 30_000, 200_000, 1_000_000):
+        qvg.debug_set_wait(limit, True)
+        try:
+            b.run()
+        finally:
+            qvg.debug_set_wait(0, False)
+        got += [b.run(), b.run(stream=side)]
+    assert qvg.get_status() == qvg.QVG_ERR_TIMEOUT
+    for o, l in got:
+        assert torch.equal(o, want) and torch.equal(l, want_lse)

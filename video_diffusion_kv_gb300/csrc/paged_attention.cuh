@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
     __shared__ Segment s_seg[kRing];
     __shared__ long long s_chunk[kChunks];
     __shared__ uint32_t tmem_base;
-    __shared__ int fail, s_issued;
+    __shared__ int fail, s_issued[2];  // tiles of K and of V whose copies have been issued
     __shared__ __align__(16) float s_qs[2][NB], s_nm[NB];  // per column: Q's scale, minus the reference
     __shared__ __align__(16) float s_red[128 / NC][NC], s_dl[NC];
     __shared__ int s_tok[2][NB];        // new token of each row
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
                    sc0 = vr0 + SV * C::kRaw;
     if (tid == 0) {
         fail = 0;
-        s_issued = 0;
+        s_issued[0] = s_issued[1] = 0;
         for (int i = 0; i < kRing; ++i) {
             umma::mbar_init(&seg_full[i], 1);
             umma::mbar_init(&seg_free[i], C::kWarps - 1);  // every other warp
@@ -942,6 +942,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
                         else
                             bulk_copy(dst, (which ? a.vc : a.kc) + at * C::kRow, pr * C::kRow, full);
                     }
+                    if (lane == 0) s_issued[which] = it + 1;
                     __syncwarp();
                 }
                 if (!ok) break;
@@ -959,7 +960,6 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
                 umma::cp_async_arrive_noinc(&v_full[rv.i]);
             }
         }
-        if (lane == 0) s_issued = it;
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 1) {
         // ---- S = K Q^T -------------------------------------------------------------------
@@ -1123,9 +1123,9 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
     __syncthreads();
     if (tid == 0 && *vfail) {
         raise_error(a.err, QVG_ERR_TIMEOUT);
-        // the copies in flight land before the CTA ends
-        for (int j = max(0, s_issued - SK); j < s_issued; ++j) umma::mbar_wait(&k_full[j % SK], (j / SK) & 1, kDrainNs);
-        for (int j = max(0, s_issued - SV); j < s_issued; ++j) umma::mbar_wait(&v_full[j % SV], (j / SV) & 1, kDrainNs);
+        // the copies in flight land before the CTA ends (K's of a tile may be out without V's)
+        for (int j = max(0, s_issued[0] - SK); j < s_issued[0]; ++j) umma::mbar_wait(&k_full[j % SK], (j / SK) & 1, kDrainNs);
+        for (int j = max(0, s_issued[1] - SV); j < s_issued[1]; ++j) umma::mbar_wait(&v_full[j % SV], (j / SV) & 1, kDrainNs);
     }
     if (warp == 2) {
         umma::tc_fence_after();

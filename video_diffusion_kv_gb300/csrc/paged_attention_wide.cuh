@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
     __shared__ Segment s_seg[kRing];
     __shared__ long long s_chunk[kChunks];
     __shared__ uint32_t tmem_base;
-    __shared__ int fail, s_issued;
+    __shared__ int fail, s_issued[2];  // tiles of K and of V whose copies have been issued
     __shared__ __align__(16) float s_ka[2][kTile], s_sv[2][kTile], s_lsv[2][kTile];  // per key: K's scale, V's, its log
     __shared__ uint2 s_lv[BITS == 4 ? 16 : 1];
 
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                    sc0 = vr0 + SV * C::kRaw;
     if (tid == 0) {
         fail = 0;
-        s_issued = 0;
+        s_issued[0] = s_issued[1] = 0;
         for (int i = 0; i < kRing; ++i) {
             umma::mbar_init(&seg_full[i], 1);
             umma::mbar_init(&seg_free[i], C::kWarps - 1);
@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                         else
                             bulk_copy(dst, (which ? a.vc : a.kc) + at * C::kRow, pr * C::kRow, full);
                     }
+                    if (lane == 0) s_issued[which] = it + 1;
                     __syncwarp();
                 }
                 if (!ok) break;
@@ -585,7 +586,6 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                 umma::cp_async_arrive_noinc(&v_full[rv.i]);
             }
         }
-        if (lane == 0) s_issued = it;
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp < 15) {
         // ---- a group's products: PV(t) and then S(t + 1), so that S is only written once its weights have been used
@@ -679,9 +679,9 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
     __syncthreads();
     if (tid == 0 && *vfail) {
         raise_error(a.err, QVG_ERR_TIMEOUT);
-        // the copies in flight land before the CTA ends
-        for (int j = max(0, s_issued - SK); j < s_issued; ++j) umma::mbar_wait(&k_full[j % SK], (j / SK) & 1, kDrainNs);
-        for (int j = max(0, s_issued - SV); j < s_issued; ++j) umma::mbar_wait(&v_full[j % SV], (j / SV) & 1, kDrainNs);
+        // the copies in flight land before the CTA ends (K's of a tile may be out without V's)
+        for (int j = max(0, s_issued[0] - SK); j < s_issued[0]; ++j) umma::mbar_wait(&k_full[j % SK], (j / SK) & 1, kDrainNs);
+        for (int j = max(0, s_issued[1] - SV); j < s_issued[1]; ++j) umma::mbar_wait(&v_full[j % SV], (j / SV) & 1, kDrainNs);
     }
     if (warp == 15) {
         umma::tc_fence_after();
