@@ -667,6 +667,7 @@ qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B,
  *   more rows: 2^-9 and 2^-17; 2^-11.
  *   Where V is so small that it matters, an output over n keys is off by at
  *   most n 2^-106 more (the weights' range ends).
+ *   Where V passes 2^111, a weight below 2^-8 of the largest may count as 0.
  *   4 bits: K groups (with few rows V's too) whose scale is below 2^-14 of
  *     their row's largest count as 0 (with many rows V's below 2^-24).
  * A row of q with an infinity or a NaN, and one that sees a K or V row marked

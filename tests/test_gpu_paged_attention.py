@@ -833,3 +833,25 @@ def test_wait_that_ends_with_copies_in_flight(bits, d, T):
     assert qvg.get_status() == qvg.QVG_ERR_TIMEOUT
     for o, l in got:
         assert torch.equal(o, want) and torch.equal(l, want_lse)
+
+
+# ---- V of very unlike sizes -----------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("T", [1, 12, 70])
+@pytest.mark.parametrize("e", [60, 118])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+def test_values_of_very_unlike_size(bits, T, e, order):
+    """Keys of equal weight whose V rows are 0 or around 2^e: the reference of
+    the weights follows V's scale, by more than 2^126, and every key still
+    counts in the sum; within a CTA's run (many sequences) and across cuts."""
+    for n, L in ((60, 1000), (1, 20000)):
+        b = Batch(2, 2, 64, bits, 64, [T] * n, [L] * n, seed=38)
+        t = torch.arange(L, device="cuda")
+        big = {"rising": t >= L // 2, "falling": t < L // 2, "mixed": t % 777 == 500}[order].repeat(n)
+        v = torch.randn(L * n, 2, 64, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6)) * 2.0 ** e
+        qvg.paged_append(b.cache, torch.zeros_like(b.k), (v * big[:, None, None]).bfloat16(), torch.from_numpy(np.concatenate(b.slots)).cuda())
+        out, lse = b.run(out_dtype=qvg.QVG_OUT_F32)
+        check_on_device(b, out, lse, qvg.QVG_MASK_CAUSAL)
+    assert qvg.get_status() == qvg.QVG_OK

@@ -43,8 +43,11 @@ __global__ void __launch_bounds__(256) k_paged_merge(const __grid_constant__ pa:
     for (int z0 = first; z0 <= last; z0 += 32) {
         const int z = z0 + lane;
         float lz = z <= last ? a.pl[at(z)] : 0.0f;
-        const float w = lz == 0.0f ? 0.0f : exp2f(a.pm[at(z)] - m);  // 0: no key of this part is seen
-        lz *= w;
+        // in two factors: references follow V's scale, and may lie further apart than fp32's range reaches while l_z
+        // still counts (up to 2^120 apart the second is 1); 0: no key of this part is seen
+        const float e = lz == 0.0f ? -INFINITY : a.pm[at(z)] - m, e1 = fmaxf(e, -120.0f);
+        const float w1 = exp2f(e1), w2 = exp2f(e - e1), w = w1 * w2;
+        lz = lz * w1 * w2;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) lz += __shfl_xor_sync(0xFFFFFFFFu, lz, o);
         l += lz;

@@ -531,10 +531,13 @@ __device__ __noinline__ void clean_values(uint8_t *v, int from, int past, int r)
 
 // Set (first) or raise the references of this warpgroup's columns after the
 // tile's logits: from the columns' largest w over the tile.  O's sums follow;
-// dl gets the factors for l.  False: some thread has given up.
+// dl gets the factors for l.  A reference follows V's scale and may rise by
+// more than 2^126, which is no factor, while l, up to 2^120, still counts: a
+// rise of most .. 2 most is left at `most`, to be done again.  (A larger one
+// leaves nothing of l.)  0: some thread has given up; 1: done; 2: once more.
 template <int NC, int NB>
-__device__ __noinline__ bool set_references(uint32_t t_s, uint32_t t_own, const float *qs, float *nm, float *scratch, float (*red)[NC],
-                                            float *dl, int r, float ka, float lsv, const uint32_t hidden, bool first, bool ok) {
+__device__ __noinline__ int set_references(uint32_t t_s, uint32_t t_own, const float *qs, float *nm, float *scratch, float (*red)[NC],
+                                            float *dl, int r, float ka, float lsv, const uint32_t hidden, bool first, bool ok, float most) {
     const float lw = fmaxf(lsv, kLeastV);
 #pragma unroll 1
     for (int c = 0; c < NC; c += 16) {
@@ -546,7 +549,8 @@ __device__ __noinline__ bool set_references(uint32_t t_s, uint32_t t_own, const 
         for (int i = 0; i < 16; i += 4)
             *reinterpret_cast<float4 *>(scratch + r * NC + c + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
     }
-    if (any_of(1, 128, !ok)) return false;
+    if (any_of(1, 128, !ok)) return 0;
+    bool more = false;
     reduce_columns<NC, true>(scratch, red, r);
     any_of(1, 128, false);
     umma::tc_fence_after();
@@ -554,11 +558,13 @@ __device__ __noinline__ bool set_references(uint32_t t_s, uint32_t t_own, const 
         float mx = -INFINITY;
         for (int i = 0; i < 128 / NC; ++i) mx = fmaxf(mx, red[i][r]);
         const bool move = first ? mx > -INFINITY : mx > kTop;
-        const float d = move ? mx - kTarget : 0.0f;
+        float d = move ? mx - kTarget : 0.0f;
+        more = !first && d > most && d <= 2.0f * most;
+        d = more ? most : d;
         nm[r] -= d;
         dl[r] = first ? 1.0f : ex2(-d);  // (a first reference may lie far below 0, and l is 0 yet)
     }
-    any_of(1, 128, false);
+    more = any_of(1, 128, more);
     if (!first) {
 #pragma unroll 1
         for (int z = 0; z < 3 * (NC / 16); ++z) {
@@ -571,7 +577,7 @@ __device__ __noinline__ bool set_references(uint32_t t_s, uint32_t t_own, const 
         }
         umma::tmem_st_wait();
     }
-    return true;
+    return more ? 2 : 1;
 }
 
 // A unit's Q rows as pairs of fp8 numbers into dst, with their scales, tokens
@@ -761,7 +767,7 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
                 umma::tc_fence_after();
                 const uint32_t t_s = tmem + t_lane + bf * 2 * NB;
                 float y[NC];  // logits (base 2) less the reference
-                for (bool settled = false;;) {
+                for (int set = 0;;) {  // (the answer of set_references)
 #pragma unroll
                     for (int c = 0; c < NC; c += 16) {
                         uint32_t v[16], u[16];  // against Q's hi and lo rows
@@ -785,19 +791,19 @@ __global__ void __launch_bounds__(Cfg<D, BITS, NB>::kWarps * 32, 2)
 #pragma unroll
                         for (int c = 0; c < NC; ++c) y[c] = (hidden >> c) & 1u ? -INFINITY : y[c];
                     }
-                    if (settled) break;
+                    if (set == 1) break;
                     float top4[4] = {y[0], y[1], y[2], y[3]};
 #pragma unroll
                     for (int c = 4; c < NC; ++c) top4[c & 3] = fmaxf(top4[c & 3], y[c]);
                     const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
                     if (!any_of(1, 128, first || !ok || top + fmaxf(lsv, kLeastV) > kTop)) break;
                     if (!first) ok = ok && wait(&pv_done, (it - 1) & 1, vfail, a.wait_ns);  // O's latest
-                    dead = !set_references<NC, NB>(t_s, t_o + t_lane, s_qs[qb], s_nm, reinterpret_cast<float *>(p_base), s_red, s_dl, r,
-                                                   ka, lsv, hidden, first, ok);
+                    set = set_references<NC, NB>(t_s, t_o + t_lane, s_qs[qb], s_nm, reinterpret_cast<float *>(p_base), s_red, s_dl, r,
+                                                 ka, lsv, hidden, first, ok, set == 0 ? 120.0f : INFINITY);
+                    dead = set == 0;
                     if (dead) break;
 #pragma unroll
                     for (int i = 0; i < NC / 2; ++i) l2[i] = mul2(l2[i], pk2(s_dl[2 * i], s_dl[2 * i + 1]));
-                    settled = true;
                 }
                 if (dead) break;
                 umma::tc_fence_before();

@@ -110,6 +110,14 @@ __device__ __forceinline__ void rescale_rows(uint32_t t_o, float f) {
     umma::tmem_st_wait();
 }
 
+// 2^-d (d >= 0) as two factors, each within fp32's range up to d = 246: the
+// references follow V's scale, which may rise by more than 2^126 while the
+// sum l, up to 2^120, still counts.  (up to d = 120 the second is 1)
+__device__ __forceinline__ float2 fall(float d) {
+    const float a = fminf(d, 120.0f);
+    return make_float2(ex2(-a), ex2(a - d));
+}
+
 // A thread's Q row as two rows of e4m3 numbers; returns its scale.
 template <int D>
 __device__ __forceinline__ float make_q_row(const uint16_t *q, uint8_t *hi, uint8_t *lo, int r) {
@@ -301,11 +309,12 @@ __global__ void __launch_bounds__(Wide<D, BITS>::kWarps * 32, 1)
                         }
                         const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
                         const bool move = top > -INFINITY && (fresh || top + nm > kTop);
-                        const float to = move ? kTarget - top : nm, f = move && !fresh ? ex2(to - nm) : 1.0f;
+                        const float to = move ? kTarget - top : nm;
+                        const float2 f = fall(move && !fresh ? nm - to : 0.0f);
                         nm = to;
-                        lp[0] = mul2(lp[0], pk2(f, f));
-                        lp[1] = mul2(lp[1], pk2(f, f));
-                        if (!first && __any_sync(0xFFFFFFFFu, f != 1.0f)) rescale_rows<D>(t_o, f);  // (the last product is done: S came after it)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) lp[h] = mul2(mul2(lp[h], pk2(f.x, f.x)), pk2(f.y, f.y));
+                        if (!first && __any_sync(0xFFFFFFFFu, f.x != 1.0f)) rescale_rows<D>(t_o, f.x * f.y);  // (the last product is done: S came after it)
                     }
                     const uint64_t nm2 = pk2(nm, nm);
                     __half2 high = __half2half2(__ushort_as_half(0));  // the largest weights
