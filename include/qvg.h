@@ -663,7 +663,8 @@ qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B,
  * three fp8 numbers or as fp16; all sums are fp32.
  *   max_q * Hq / H <= 64 (32 with 4 bits): a channel of q is exact down to
  *     2^-13 of its row's largest and off by at most 2^-21 of the largest
- *     below; a weight is off by at most 2^-9 of itself or 2^-25 of the largest.
+ *     below; a weight is off by at most 2^-9 + 2^-11 of itself or 2^-25 of the
+ *     largest.
  *   more rows: 2^-9 and 2^-17; 2^-11.
  *   Where V is so small that it matters, an output over n keys is off by at
  *   most n 2^-106 more (the weights' range ends).

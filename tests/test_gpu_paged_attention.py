@@ -855,3 +855,49 @@ def test_values_of_very_unlike_size(bits, T, e, order):
         out, lse = b.run(out_dtype=qvg.QVG_OUT_F32)
         check_on_device(b, out, lse, qvg.QVG_MASK_CAUSAL)
     assert qvg.get_status() == qvg.QVG_OK
+
+
+# ---- the weights' own precision --------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("T", [16, 30, 200])
+def test_precision_of_a_weight(bits, T):
+    """Each row sees two keys that share no channel of V, so that an fp32
+    output is one weight times one value.  Q has four significant bits (exact
+    in its fp8 pair).  Bounds: the logits' fp32 sums (of 2 d products, 2^-23
+    each; the base-2 form 8 2^-24 of the logit), twice for two of them; ex2 2^-20; the weight as fp16,
+    2^-11 of itself, and with few rows as three e5m2 parts, 2^-9 more; fp32
+    roundings of the result 2^-22; far below the largest 2^-25 of it."""
+    H, d = 8, 64
+    b = Batch(H, 1, d, bits, 16, (T,), (T,), seed=39, k_scale=0.4)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    b.q.copy_(torch.randint(-15, 16, b.q.shape, device="cuda", generator=g) / 8)
+    v = torch.ones(T, H, d, device="cuda")
+    v[:, :, 0] = 0.0
+    v[0] = 0.0
+    v[0, :, 0] = 1.0
+    k = b.k.clone()
+    k[0] = (b.q.float().mean(0) * 4).bfloat16()  # often the larger logit, not always
+    qvg.paged_append(b.cache, k, v.bfloat16(), torch.from_numpy(b.slots[0]).cuda())
+    words = torch.zeros(T, -(-T // 32), dtype=torch.int64, device="cuda")
+    t = torch.arange(T, device="cuda")
+    words[t, t // 32] |= 1 << (t % 32)
+    words[:, 0] |= 1
+    mask = torch.where(words >= 2 ** 31, words - 2 ** 32, words).int()
+    out, lse = b.run(qvg.QVG_MASK_TREE, mask=mask, out_dtype=qvg.QVG_OUT_F32)
+    assert qvg.get_status() == qvg.QVG_OK
+    kk, vv = (x.transpose(0, 2, 1, 3).reshape(-1, H, d)[b.slots[0]] for x in ref.held(b.cache))
+    q = b.q.double().cpu().numpy()
+    see = np.eye(T, dtype=bool)
+    see[:, 0] = True
+    want, want_lse = ref.attention(q, kk, vv, see)
+    s0, st = np.abs(q * kk[:1]).sum(-1), np.abs(q * kk).sum(-1)
+    logit = (2 * d * 2.0 ** -23 + 8 * 2.0 ** -24) * np.maximum(s0, st) / math.sqrt(d)
+    few = T <= (64 if bits == 8 else 32)
+    rel = 2 * logit + 2.0 ** -20 + 2.0 ** -11 + (2.0 ** -9 if few else 0) + 2.0 ** -22
+    bound = rel[..., None] * np.abs(want) + 2.0 ** -25 * np.abs(want).max()
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert (err <= bound).all(), float((err / bound).max())
+    lb = logit.T + 2.0 ** -20 + 2.0 ** -21 * np.abs(want_lse)
+    assert (np.abs(lse.double().cpu().numpy() - want_lse) <= lb).all()
