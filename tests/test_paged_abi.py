@@ -211,3 +211,20 @@ def test_python_attention_refusals(lib):
                      ((par, 2), {})):
         with pytest.raises(ValueError):
             qvg.tree_mask(*args, **kw)
+
+
+def test_positions_by_axis_are_refused(lib):
+    """positions are [n, axes]: [axes, n] has as many elements, and would be
+    read in the wrong order."""
+    plan = qvg.RopePlan((24, 20, 20))
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    cache, slots = qvg.PagedKV(2, 64, 16, 4, device="cpu"), torch.zeros(4, dtype=torch.int64)
+    for shape, good in (((4, 3), True), ((2, 2, 3), True), ((3, 4), False), ((12,), False), ((4, 3, 1), False)):
+        pos = torch.zeros(*shape, dtype=torch.int32)
+        for call in (lambda: qvg.rope(plan, x, pos), lambda: qvg.paged_append(cache, x, x, slots, plan=plan, positions=pos)):
+            with pytest.raises(ValueError, match="CUDA tensors" if good else "positions must be"):
+                call()
+    one = qvg.RopePlan((64,))
+    for shape in ((4,), (4, 1), (1, 4)):
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            qvg.rope(one, x, torch.zeros(*shape, dtype=torch.int32))

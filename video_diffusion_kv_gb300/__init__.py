@@ -433,7 +433,7 @@ def _empty(shape, dtype, dev, stream):
 def _positions(plan, positions, n, where):
     if positions is None:
         raise ValueError("%s: a plan needs positions" % where)
-    if positions.numel() != n * plan.axes:
+    if positions.numel() != n * plan.axes or (n > 0 and plan.axes > 1 and positions.shape[-1] != plan.axes):
         raise ValueError("%s: positions must be int32 [%d, %d]" % (where, n, plan.axes))
 
 
