@@ -228,3 +228,17 @@ def test_positions_by_axis_are_refused(lib):
     for shape in ((4,), (4, 1), (1, 4)):
         with pytest.raises(ValueError, match="CUDA tensors"):
             qvg.rope(one, x, torch.zeros(*shape, dtype=torch.int32))
+
+
+def test_paged_buffers_given(lib):
+    """Four buffers that share no byte; they may be parts of one allocation."""
+    codes, scales = qvg.paged_bytes(2, 64, 16, 4, 8)
+    sizes = [codes, scales, codes, scales]
+    arena = torch.zeros(sum(sizes) + 16, dtype=torch.uint8)
+    parts = list(arena[:sum(sizes)].split(sizes))
+    c = qvg.PagedKV(2, 64, 16, 4, buffers=parts)
+    assert c.v_codes.data_ptr() == parts[2].data_ptr() and c.nbytes == sum(sizes)
+    for bad in (parts[:3], parts + [parts[0].clone()], [parts[0], parts[1], parts[0], parts[3]],
+                [parts[0], parts[1], arena[codes:2 * codes], parts[3]], [parts[0], parts[1], parts[2], parts[1]]):
+        with pytest.raises(ValueError, match="four buffers|overlap"):
+            qvg.PagedKV(2, 64, 16, 4, buffers=bad)

@@ -480,9 +480,14 @@ class PagedKV:
         shapes = [rows + (d * bits // 8,), rows + (1 if bits == 8 else d // 32,)] * 2
         if buffers is None:
             buffers = [torch.zeros(s, dtype=torch.uint8, device=device) for s in shapes]
+        if len(buffers) != 4:
+            raise ValueError("PagedKV: four buffers are wanted (k codes, k scales, v codes, v scales), got %d" % len(buffers))
         for t, need in zip(buffers, sizes * 2):
             if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != need or t.device != buffers[0].device:
                 raise ValueError("PagedKV: each buffer must be contiguous uint8 of the size paged_bytes reports")
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel()) for t in buffers)
+        if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
+            raise ValueError("PagedKV: the buffers overlap")
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = (t.view(s) for t, s in zip(buffers, shapes))
         self.device = self.k_codes.device
         self._c = _Paged(H, d, page_size, num_pages, bits, self.k_codes.data_ptr(), self.k_scales.data_ptr(),
