@@ -162,6 +162,89 @@ def test_rope_autograd():
     assert np.abs(x.grad.double().cpu().numpy() - want).max() <= bound
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_rope_keeps_the_gradient(dtype, transpose):
+    """The gradient of a loss over qvg.rope of a part of a fused projection
+    reaches the projection and is the transposed rotation, for dy as a tensor
+    and as an expanded scalar; no_grad and inputs without one are as before."""
+    plan = qvg.RopePlan((24, 20, 20), layout=qvg.QVG_ROPE_INTERLEAVED, mscale=1.25)
+    pos = torch.from_numpy(positions_of(30, 3, 5, 500)[3:]).cuda()
+    wide = values((27, 6, 128), 8, dtype).cuda().requires_grad_()
+    x = wide[:, 2:5]
+    y = qvg.rope(plan, x, pos, transpose=transpose)
+    assert y.requires_grad and torch.equal(y.detach(), qvg.rope(plan, x.detach(), pos, transpose=transpose))
+    dy = values((27, 3, 128), 9, dtype).cuda()
+    y.backward(dy)
+    want = torch.zeros_like(wide)
+    want[:, 2:5] = qvg.rope(plan, dy, pos, transpose=not transpose)
+    assert torch.equal(wide.grad, want)
+    f, axis = ref.frequencies((24, 20, 20))
+    formula = ref.rope(dy.double().cpu().numpy(), pos.cpu().numpy(), f, axis, 1, 1.25, not transpose)
+    err = np.abs(want[:, 2:5].double().cpu().numpy() - formula)
+    assert (err <= rope_bound(dy.double().cpu().numpy(), formula, 1.25, dtype)).all()
+    wide.grad = None
+    qvg.rope(plan, x, pos, transpose=transpose).sum().backward()
+    assert torch.equal(wide.grad[:, 2:5], qvg.rope(plan, torch.ones_like(dy), pos, transpose=not transpose))
+    with torch.no_grad():
+        assert not qvg.rope(plan, x, pos).requires_grad
+        out = torch.empty_like(y)
+        assert torch.equal(qvg.rope(plan, x, pos, transpose=transpose, out=out), y)
+    assert not qvg.rope(plan, dy, pos).requires_grad
+
+
+def test_rope_gradient_by_differences():
+    """A loss that is not linear: autograd against central differences in
+    64 bits of the plain form, and the second derivative through the graph."""
+    plan = qvg.RopePlan((64,))
+    pos = torch.arange(5, dtype=torch.int32, device="cuda") * 77
+    x = values((5, 2, 64), 10, torch.float32).cuda().requires_grad_()
+    g, = torch.autograd.grad(qvg.rope(plan, x, pos).pow(3).sum(), x, create_graph=True)
+    f, axis = ref.frequencies((64,))
+    xd, pn = x.detach().double().cpu().numpy(), pos.cpu().numpy()[:, None]
+    loss = lambda a: (ref.rope(a, pn, f, axis, 0) ** 3).sum()  # noqa: E731
+    top = np.abs(xd).max() * np.sqrt(2)
+    for i, h, c in ((0, 0, 0), (3, 1, 17), (4, 0, 63)):
+        e = np.zeros_like(xd)
+        e[i, h, c] = 1e-4
+        # a cubic's central difference is off by its third derivative's step: 1e-8 times a few; g as in test_rope_autograd
+        bound = 2 * (6 * top * 16 * 2.0 ** -24 * top + 3 * top ** 2 * 20 * 2.0 ** -24) + 1e-6
+        assert abs((loss(xd + e) - loss(xd - e)) / 2e-4 - float(g[i, h, c].detach())) <= bound
+    # H u for u = 1: R^T (6 y R u), each rotation off by 16 2^-24 of its largest input, products by 2^-24
+    hu, = torch.autograd.grad(g.sum(), x)
+    ones = np.ones_like(xd)
+    mid = 6 * ref.rope(xd, pn, f, axis, 0) * ref.rope(ones, pn, f, axis, 0)
+    want = ref.rope(mid, pn, f, axis, 0, transpose=True)
+    assert np.abs(hu.double().cpu().numpy() - want).max() <= 64 * 2.0 ** -24 * 6 * top * 2 * 2
+
+
+def test_rope_gradient_on_a_stream_and_captured():
+    """Forward and backward on a side stream, and captured into a graph that
+    is replayed with other inputs while the eager graph of the leaf lives."""
+    plan = qvg.RopePlan((128,))
+    pos = torch.arange(40, dtype=torch.int32, device="cuda")
+    x = values((40, 3, 128), 11, torch.float32).cuda().requires_grad_()
+    step = lambda t: torch.autograd.grad(qvg.rope(plan, t, pos).pow(2).sum(), t)[0]  # noqa: E731
+    want = step(x)
+    alive = qvg.rope(plan, x, pos)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step(x)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)
+    other = torch.zeros_like(x).requires_grad_()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        captured = step(other)
+    with torch.no_grad():
+        other.copy_(x)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(captured, want) and alive.requires_grad
+
+
 # ---- the cache --------------------------------------------------------------------------
 
 def rows(n, H, d, seed):

@@ -242,3 +242,17 @@ def test_paged_buffers_given(lib):
                 [parts[0], parts[1], arena[codes:2 * codes], parts[3]], [parts[0], parts[1], parts[2], parts[1]]):
         with pytest.raises(ValueError, match="four buffers|overlap"):
             qvg.PagedKV(2, 64, 16, 4, buffers=bad)
+
+
+def test_rope_refuses_out_where_a_gradient_is_wanted(lib):
+    plan = qvg.RopePlan((64,))
+    x = torch.zeros(4, 2, 64, requires_grad=True)
+    pos = torch.zeros(4, 1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="no gradient through out"):
+        qvg.rope(plan, x, pos, out=torch.zeros(4, 2, 64))
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        qvg.rope(plan, x, pos)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensors"):
+        qvg.rope(plan, x, pos, out=torch.zeros(4, 2, 64))
+    with pytest.raises(ValueError, match="a plan needs positions"):
+        qvg.rope(plan, x, None)

@@ -6,7 +6,7 @@ Argument marshalling only: every step of compression, reconstruction,
 attention, the QuantWM statistics and the token-wise operators runs in the CUDA kernels of
 ``libqvg.so``; PyTorch provides device memory and streams.  There is no
 fallback: if the library is missing or no CUDA device is present, the calls
-raise.
+raise.  rope() carries gradients; nothing else here does.
 
 Names follow the C ABI in ``include/qvg.h``.
 """
@@ -437,11 +437,42 @@ def _positions(plan, positions, n, where):
         raise ValueError("%s: positions must be int32 [%d, %d]" % (where, n, plan.axes))
 
 
+_rope_autograd = None
+
+
+def _rope_with_gradient(plan, x, positions, transpose, stream):
+    """rope as a node of torch's graph (the class is made at its first use:
+    torch is imported by the calls)."""
+    global _rope_autograd
+    if _rope_autograd is None:
+        import torch
+
+        class Rope(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, positions, plan, transpose, stream):
+                ctx.plan, ctx.transpose = plan, transpose
+                ctx.save_for_backward(positions)
+                return rope(plan, x, positions, transpose=transpose, stream=stream)
+
+            @staticmethod
+            def backward(ctx, dy):  # torch runs it on the stream that was current in forward
+                positions, = ctx.saved_tensors
+                return rope(ctx.plan, dy.contiguous(), positions, transpose=not ctx.transpose), None, None, None, None
+
+        _rope_autograd = Rope
+    return _rope_autograd.apply(x, positions, plan, transpose, stream)
+
+
 def rope(plan: RopePlan, x, positions, transpose=False, out=None, stream=None):
     """Rotate x (bf16 or fp32 [n, H, d]; tokens may be strided) at positions
     (int32 [n, axes], or [n] with one axis).  transpose=True turns the angles'
-    signs: the gradient with respect to x.  out may be x itself."""
+    signs: the gradient with respect to x.  out may be x itself.  Where x
+    requires a gradient, the result has one (without `out`)."""
     import torch
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("rope: no gradient through out; leave it out, or call under torch.no_grad()")
+        return _rope_with_gradient(plan, x, positions, transpose, stream)
     if x.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("rope: bf16 or fp32 is wanted, got %s" % x.dtype)
     n, H, d, xs = _heads(x, "rope")
