@@ -345,6 +345,25 @@ def test_append_rotates(bits, layout, d, dims):
         assert torch.equal(getattr(a, n), getattr(b, n)), n
 
 
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("layout", [qvg.QVG_ROPE_HALF, qvg.QVG_ROPE_INTERLEAVED])
+@pytest.mark.parametrize("d,dims", [(128, (128,)), (128, (44, 20)), (64, (22,)), (128, (96,))])
+def test_append_rotates_zeros_of_either_sign(bits, layout, d, dims):
+    """The same where many channels are 0 or -0 beside values of either sign,
+    among the rotated channels and the others."""
+    plan = qvg.RopePlan(dims, layout=layout)
+    g = torch.Generator().manual_seed(12)
+    x = torch.randn(300, 2, d, generator=g)
+    x = torch.where(torch.rand(x.shape, generator=g) < 0.6, torch.copysign(torch.zeros(()), x), x).bfloat16().cuda()
+    pos = torch.from_numpy(positions_of(300, len(dims), 13, 1000)).cuda()
+    slots = torch.arange(300, device="cuda")
+    a, b = make(2, d, 16, 20, bits), make(2, d, 16, 20, bits)
+    qvg.paged_append(a, x, x, slots, plan=plan, positions=pos)
+    qvg.paged_append(b, qvg.rope(plan, x, pos), x, slots)
+    for n in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        assert torch.equal(getattr(a, n), getattr(b, n)), n
+
+
 def test_slots_beyond_the_cache():
     """A slot past the end is skipped (append) or zeros (read) and reported
     once; the other tokens are served."""

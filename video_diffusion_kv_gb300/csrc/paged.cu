@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kWarps * 32, ROPE == kNoRope ? 5 : 4)
     }
     const int u = lane % LANES, hs = lane / LANES;
     float co[ROPE == kPairs ? 8 : 16], si[ROPE == kPairs ? 8 : 16];  // si with the sign of the channel's place in its pair
+    const int turned = r.pairs - u * 8;  // kPairs: the lane's pairs that turn, from its first on
     int from[2];  // where the lane's two runs of 8 channels have their partners in the row
     if constexpr (ROPE != kNoRope) {
         for (int i = lane; i < r.pairs; i += 32)
@@ -174,9 +175,10 @@ __global__ void __launch_bounds__(kWarps * 32, ROPE == kNoRope ? 5 : 4)
         if constexpr (ROPE == kPairs) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float x0 = __uint_as_float(xk[i] << 16), x1 = __uint_as_float(xk[i] & 0xFFFF0000u);
-                const __nv_bfloat162 y = __floats2bfloat162_rn(x0 * co[i] - x1 * si[i], x1 * co[i] + x0 * si[i]);
-                xk[i] = *reinterpret_cast<const uint32_t *>(&y);
+                const float2 t = rope_turn(__uint_as_float(xk[i] << 16), __uint_as_float(xk[i] & 0xFFFF0000u), co[i], si[i]);
+                const __nv_bfloat162 y = __floats2bfloat162_rn(t.x, t.y);
+                // (a pair that does not turn stays as it is: 0 times its partner would make +0 of -0)
+                xk[i] = i < turned ? *reinterpret_cast<const uint32_t *>(&y) : xk[i];
             }
         }
         if constexpr (SHARED) {
@@ -209,8 +211,8 @@ __global__ void __launch_bounds__(kWarps * 32, ROPE == kNoRope ? 5 : 4)
                     const int e = 8 * half + 2 * i;
                     const uint32_t x = xk[e / 2];
                     const __nv_bfloat162 y =
-                        __floats2bfloat162_rn(__uint_as_float(x << 16) * co[e] + __uint_as_float(pw[i] << 16) * si[e],
-                                              __uint_as_float(x & 0xFFFF0000u) * co[e + 1] + __uint_as_float(pw[i] & 0xFFFF0000u) * si[e + 1]);
+                        __floats2bfloat162_rn(fmaf(__uint_as_float(x << 16), co[e], __fmul_rn(__uint_as_float(pw[i] << 16), si[e])),  // as rope_turn
+                                              fmaf(__uint_as_float(x & 0xFFFF0000u), co[e + 1], __fmul_rn(__uint_as_float(pw[i] & 0xFFFF0000u), si[e + 1])));
                     xk[e / 2] = *reinterpret_cast<const uint32_t *>(&y);
                 }
             }

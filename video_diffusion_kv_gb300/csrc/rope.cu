@@ -130,22 +130,20 @@ __global__ void __launch_bounds__(kWarps * 32) k_rope(const __grid_constant__ Ro
                     if (half) {
 #pragma unroll
                         for (int i = 0; i < E; ++i) {
-                            const float y0 = f0[i] * a[i].x - f1[i] * a[i].y, y1 = f1[i] * a[i].x + f0[i] * a[i].y;
-                            f0[i] = y0;
-                            f1[i] = y1;
+                            const float2 y = rope_turn(f0[i], f1[i], a[i].x, a[i].y);
+                            f0[i] = y.x;
+                            f1[i] = y.y;
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < E / 2; ++i) {
-                            float y0 = f0[2 * i] * a[i].x - f0[2 * i + 1] * a[i].y;
-                            float y1 = f0[2 * i + 1] * a[i].x + f0[2 * i] * a[i].y;
-                            f0[2 * i] = y0;
-                            f0[2 * i + 1] = y1;
                             const float2 e = a[E / 2 + i];
-                            y0 = f1[2 * i] * e.x - f1[2 * i + 1] * e.y;
-                            y1 = f1[2 * i + 1] * e.x + f1[2 * i] * e.y;
-                            f1[2 * i] = y0;
-                            f1[2 * i + 1] = y1;
+                            const float2 y0 = rope_turn(f0[2 * i], f0[2 * i + 1], a[i].x, a[i].y);
+                            const float2 y1 = rope_turn(f1[2 * i], f1[2 * i + 1], e.x, e.y);
+                            f0[2 * i] = y0.x;
+                            f0[2 * i + 1] = y0.y;
+                            f1[2 * i] = y1.x;
+                            f1[2 * i + 1] = y1.y;
                         }
                     }
                     v0[b] = pack(f0);
@@ -165,9 +163,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_rope(const __grid_constant__ Ro
             for (int i = lane; i < d / 2; i += 32) {
                 if (i < r.pairs) {
                     const int c0 = half ? i : 2 * i, c1 = half ? r.pairs + i : 2 * i + 1;
-                    const float f0 = load1(p + c0), f1 = load1(p + c1);
-                    store1(q + c0, f0 * cs[i].x - f1 * cs[i].y);
-                    store1(q + c1, f1 * cs[i].x + f0 * cs[i].y);
+                    const float2 y = rope_turn(load1(p + c0), load1(p + c1), cs[i].x, cs[i].y);
+                    store1(q + c0, y.x);
+                    store1(q + c1, y.y);
                 } else if (x != out) {
                     q[2 * i] = p[2 * i];
                     q[2 * i + 1] = p[2 * i + 1];

@@ -35,6 +35,12 @@ __device__ __forceinline__ float2 rope_cos_sin(uint64_t step, int32_t position, 
     return make_float2(mscale * co, transpose ? -mscale * si : mscale * si);
 }
 
+// The pair (x0, x1) turned by (cos, sin).  The products' roundings are spelt
+// out: the rotation and the cache's write path give the same bits.
+__device__ __forceinline__ float2 rope_turn(float x0, float x1, float c, float s) {
+    return make_float2(fmaf(x0, c, -__fmul_rn(x1, s)), fmaf(x1, c, __fmul_rn(x0, s)));
+}
+
 // Host: whether a plan can be used with heads of d channels, and its
 // by-value form.
 bool rope_plan_ok(const qvg_rope_plan *plan, int d);
