@@ -645,9 +645,10 @@ qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B,
  *              p * page_size .. of sequence b.  Entries past the sequence's
  *              last page are not read.
  *   kv_len     int32 [B] device, the new tokens included; 0: no keys.  A
- *              sequence longer than its table row, and a page outside the
- *              cache, latch QVG_ERR_INVALID_ARG and make the sequence's
- *              output undefined.
+ *              sequence longer than its table row or than 2^31 - 4096, one
+ *              with more than 2^32 tiles (128 keys each, for every KV head and
+ *              block of query rows), and a page outside the cache, latch
+ *              QVG_ERR_INVALID_ARG and make the sequence's output undefined.
  *   mask       QVG_MASK_TREE: uint32 [total_q][mask_words] (qvg_tree_mask, or
  *              any bits); mask_words >= ceil(max_q / 32).
  *   scale      as in qvg_attention.

@@ -901,3 +901,33 @@ def test_precision_of_a_weight(bits, T):
     assert (err <= bound).all(), float((err / bound).max())
     lb = logit.T + 2.0 ** -20 + 2.0 ** -21 * np.abs(want_lse)
     assert (np.abs(lse.double().cpu().numpy() - want_lse) <= lb).all()
+
+
+@pytest.mark.parametrize("bits,G", [(8, 1), (4, 1), (8, 70)])
+def test_longest_sequence(bits, G):
+    """One page that a whole block table points to.  2^31 - 4096 keys are
+    served: the page's own attention, with log of the repeats in the lse.
+    One more is reported (the numbers of a tile's keys would pass 32 bits).
+    Bounds: a CTA has up to 2^24 / 152 tiles.  With few rows a thread owns a
+    key of each tile, so a sum has one addition a tile; with many a thread owns a row and keeps
+    four sums of 32 keys a tile each; 2^-24 an addition.  The products go
+    into O in eight steps a tile, 2^-23 each."""
+    b = Batch(1, G, 64, bits, 256, (1,), (256,), seed=40)
+    most = 2 ** 31 - 4096
+    table = b.table[:, :1].expand(1, (1 << 23)).contiguous()
+    kv = torch.tensor([most], dtype=torch.int32, device="cuda")
+    out, lse = qvg.paged_attention(b.cache, b.q, table, kv, 1, out_dtype=qvg.QVG_OUT_F32, want_lse=True)
+    assert qvg.get_status() == qvg.QVG_OK
+    k, v = (x.transpose(0, 2, 1, 3).reshape(-1, 1, 64)[b.slots[0]] for x in ref.held(b.cache))
+    want, want_lse = ref.attention(b.q.double().cpu().numpy(), k, v, np.ones((1, 256), bool))
+    tiles = 2.0 ** 24 / 152
+    sums = tiles * (32 if G > 64 else 1) * 2.0 ** -24
+    assert np.abs(lse.double().cpu().numpy() - want_lse - math.log(most / 256)).max() <= sums + 2.0 ** -9
+    bound = (sums + tiles * 8 * 2.0 ** -23 + 2.0 ** -8) * np.abs(v).max()
+    assert np.abs(out.double().cpu().numpy() - want).max() <= bound
+    for n in (most + 1, 2 ** 31 - 128, 2 ** 31 - 1):
+        kv.fill_(n)
+        qvg.paged_attention(b.cache, b.q, table, kv, 1)
+        assert qvg.get_status() == qvg.QVG_ERR_INVALID_ARG, n
+    again, _ = b.run()
+    assert qvg.get_status() == qvg.QVG_OK

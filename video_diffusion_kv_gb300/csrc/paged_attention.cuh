@@ -63,6 +63,7 @@ constexpr float kTarget = 8.0f, kTop = 15.0f;
 // V's scale enters the reference, so that w = p sv spans its type's range; from 2^kLeastV down only p does, whose sums
 // (up to 2^(kTop - kLeastV) a key) stay in fp32.
 constexpr float kLeastV = -90.0f;
+constexpr long long kMostKeys = (1ll << 31) - 4096;  // of a sequence: key numbers and what a tile adds to them stay in 32 bits
 constexpr uint64_t kDrainNs = 2000000000ull;
 
 struct Args {
@@ -110,7 +111,7 @@ __device__ __forceinline__ Seq seq_of(const Args &a, int b, bool report) {
         if (q0 < 0 || q0 > a.total_q) q0 = nq = 0;
         nq = max(0, min(min(nq, a.max_q), a.total_q - q0));
     }
-    const long long most = a.table_stride << a.page_log2;
+    const long long most = min(a.table_stride << a.page_log2, kMostKeys);
     int kv = a.kv_len[b];
     bad = bad || kv < 0 || kv > most;
     kv = static_cast<int>(max(0ll, min(static_cast<long long>(kv), most)));
