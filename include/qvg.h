@@ -543,8 +543,8 @@ qvg_status qvg_rope(const qvg_rope_plan *plan, const void *x, int32_t dtype, int
  * into bf16 adds nothing.  (A value within the last step below 2^128 takes the
  * code below it, so that every finite value stays finite.)
  * All four buffers are caller-allocated, 16-byte aligned device memory of the
- * size that qvg_paged_bytes reports.  H >= 1, d = 64 or 128, page_size 16,
- * 32, 64, 128 or 256.
+ * size that qvg_paged_bytes reports, and share no byte.  H >= 1, d = 64 or
+ * 128, page_size 16, 32, 64, 128 or 256.
  */
 typedef struct {
     int32_t H;
@@ -668,7 +668,8 @@ qvg_status qvg_paged_workspace_size(int32_t H, int32_t d, int32_t Hq, int32_t B,
  *     largest.
  *   more rows: 2^-9 and 2^-17; 2^-11.
  *   Where V is so small that it matters, an output over n keys is off by at
- *   most n 2^-106 more (the weights' range ends).
+ *   most n 2^-106 more (the weights' range ends), and from 2^23 keys on lse
+ *   may be infinite.
  *   Where V passes 2^111, a weight below 2^-8 of the largest may count as 0.
  *   4 bits: K groups (with few rows V's too) whose scale is below 2^-14 of
  *     their row's largest count as 0 (with many rows V's below 2^-24).

@@ -1,6 +1,7 @@
 // common.cuh -- device helpers shared by the libqvg kernels (sm_103a).
 #pragma once
 
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -120,6 +121,9 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
+
+// cuTensorMapEncodeTiled from the driver, or NULL (compress.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Device address of the current device's error word (looked up once per
 // device, race-free), or NULL if the current device cannot be determined.

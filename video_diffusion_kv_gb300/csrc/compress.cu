@@ -1150,7 +1150,6 @@ __global__ void k_chunk_table(int chunk, int slot0, int N, int32_t *chunk_start,
 static int sm_count() { return sm_count_current(); }
 
 // cuTensorMapEncodeTiled from the driver (looked up once; no link to libcuda).
-// paged_attention.cu uses it too.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

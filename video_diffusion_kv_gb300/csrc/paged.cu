@@ -108,9 +108,11 @@ enum { kNoRope = 0, kPairs = 1, kHalves = 2, kAnyHalves = 3 };
 // store it.
 // Bound by HBM: reads 4 H D bytes a token, writes 2 H D bits / 8 + scales.
 // 37,440 tokens of 16 heads of 128 into the 4-bit cache with K rotated, and back
-// as bf16 (0.78 GB in all): 189 us, 4.1 TB/s, 61 % of a plain copy's rate (the
+// as bf16 (0.78 GB in all): 188 us, 4.1 TB/s, 61 % of a plain copy's rate, 109 us of
+// it this kernel (3.5 TB/s: neither HBM nor, at 65 %, the issue slots are full; a warp
+// loads a few heads, works on them and stores them before it loads the next; the
 // rotation in 64 registers, four blocks an SM; three: 197 us, five: 209 us); 48
-// tokens of 8 heads take no longer than their launch.
+// tokens of 8 heads: 6 us.
 template <int D, int BITS, int ROPE>
 __global__ void __launch_bounds__(kWarps * 32, ROPE == kNoRope ? 5 : 4)
     k_paged_append(const __grid_constant__ RopeArgs r, PagedArgs a, const uint16_t *__restrict__ k, const uint16_t *__restrict__ v, int n,
@@ -226,7 +228,8 @@ __global__ void __launch_bounds__(kWarps * 32, ROPE == kNoRope ? 5 : 4)
 // One warp per token, lanes as in k_paged_append; K and V one after the
 // other.  Bound by HBM: reads the codes and scales, writes n H D elements
 // for each of K and V.  37,440 tokens of 16 heads of 128, 8 bits, as bf16 (0.46
-// GB): 80 us, 5.8 TB/s, 85 % of a plain copy's rate.
+// GB): 79 us, 5.8 TB/s, 86 % of a plain copy's rate; 4 bits (0.39 GB): 78 us, 5 TB/s,
+// as long, so there the instructions of the conversion count too.
 template <int D, int BITS, bool BF16>
 __global__ void __launch_bounds__(kWarps * 32) k_paged_read(PagedArgs a, const int64_t *__restrict__ slots, int n,
                                                            void *__restrict__ k_out, void *__restrict__ v_out,

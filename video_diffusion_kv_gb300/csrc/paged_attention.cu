@@ -1,15 +1,11 @@
 // paged_attention.cu -- attention over a paged cache: launch, the join of
 // units that several CTAs shared, the mask rows of drafted trees, and the
 // entry points.  The kernel is in paged_attention.cuh.
-#include <cudaTypedefs.h>
-
 #include <cmath>
 
 #include "paged_attention_wide.cuh"
 
 namespace qvg {
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // compress.cu
 
 namespace {
 
@@ -116,14 +112,16 @@ constexpr int kMaxTree = 8192;  // new tokens of one sequence whose parents fit 
 // have no blocks of 32: the narrow kernel's converters need registers too.
 // Microseconds for 16 sequences of 2,000 to 12,000 keys (8 KV heads, d = 128):
 //            rows     16   32   64   96  128
-//   8 bits   16       62   88  147
-//            32       74   82  124  172
-//            256     140  144  148  155  160
-//   4 bits   16      101  173  309
-//            256     185  188  195  199  203
-// One sequence of 150,000: 64 rows 126 (32 each) against 169, 4 bits and 32 rows
-// 188 (16 each) against 218.  Only where a call is as short as its launch is the
-// order the other way (40 sequences of 300 to 2,000, 2 KV heads: 50 against 41).
+//   8 bits   16       62   89  148
+//            32       74   81  124  171  214
+//            256     137  141  147  152  158
+//   4 bits   16       87  146  260
+//            256     186  191  195  200  203
+// At the borders, 64 rows of 8 bits (32 each) and 32 rows of 4 bits (16 each)
+// against 256: d = 64: 101 against 125, 100 against 153; 48 sequences: 311 against 382,
+// 386 against 516; one sequence of 150,000: 125 against 168, 175 against 220.  Only where a
+// call is as short as its launch is the order the other way (40 sequences of 300
+// to 2,000, 2 KV heads: 50 against 41, 44 against 41).
 int rows_of_block(long long rows, int bits) {
     return rows <= (bits == 8 ? 16 : 32) ? 16 : rows <= 64 && bits == 8 ? 32 : pa::kWideRows;
 }

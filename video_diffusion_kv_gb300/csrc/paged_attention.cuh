@@ -23,12 +23,12 @@
 // and V are touched once by the copy and once by the tensor core.  The other
 // operand is made of several fp8 numbers side by side along N, each with its
 // own accumulator columns; a product with N <= 64 takes the tensor core the
-// same 45 clocks whatever N is, so the extra columns are free there:
+// same 45 to 48 clocks whatever N is, so the extra columns are free there:
 //   - Q as two: hi + lo / 16 in e4m3 (4 significant bits each, a bf16 number
 //     has 8: exact down to 2^-13 of the row's largest);
 //   - P as three: h1 + h2 + h3 in e5m2, which is the upper byte of an fp16
 //     number: the first two cut off, the last rounded: at most 2^-9 of the
-//     weight off, and nearly fp16's range, which e4m3 lacks.
+//     weight off (and 2^-11 by fp16), and nearly fp16's range, which e4m3 lacks.
 // A key's scale is one number per row of S^T, i.e. per softmax thread; V's
 // scale goes into the weight: w = p sv.
 // Softmax: a thread owns one key and 16 or 32 columns.  The weights of a column
@@ -41,13 +41,13 @@
 // 1.5 times as long.
 //
 // Bound: HBM for single tokens.  One token over 449,280 (8 KV heads, d = 128,
-// 4 query heads each, 8 bits; 0.93 GB): 157 us, 5.9 TB/s, 87 % of a plain copy's
+// 4 query heads each, 8 bits; 0.93 GB): 158 us, 5.85 TB/s, 86 % of a plain copy's
 // rate.  48 tokens over 700 to 24,000 each (8 query heads a KV head, pages of
-// 16): 229 us, 5.35 TB/s; pages of 16 mean 8 copies a tile for each of K and V,
-// about 100 clocks of issue each, and every sequence's ends leave a part tile.
+// 16): 231 us, 5.3 TB/s; pages of 16 mean 8 copies a tile for each of K and V,
+// and every sequence's ends leave a part tile.
 // 4 bits are bound by the conversion into fp8 (four warps, about 500
 // instructions a thread and tile): 24 trees of 5 to 13 tokens over 4,000 to
-// 16,000, 16 KV heads: 272 us, 1.9 TB/s.
+// 16,000, 16 KV heads: 269 us, 1.95 TB/s.
 #pragma once
 
 #include <cuda.h>

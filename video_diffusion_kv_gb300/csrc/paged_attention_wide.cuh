@@ -17,17 +17,19 @@
 // are read from shared memory.  A row's 128 logits stay in registers from the
 // one read of S to the weights, for which the softmax warps take registers from
 // the others (with two reads of S and 128 registers: 510 us for the frame
-// below, where this takes 366); the largest logit is looked for only where a
+// below, where this takes 367); the largest logit is looked for only where a
 // weight overflows (375 us with the search in every tile).
 // One group's products run while the other group is at its softmax.
 //
-// Bound: the chain of a group and tile, about 6000 clocks: its softmax (read
-// 800, weights 1300, waits for S) and then its products, PV(t) and S(t + 1), 8
-// each of 64 clocks, which share the tensor core with the other group's and
-// start on an idle pipe.  880 causal tokens over 21,120 (24 heads, d = 128, 8
-// bits; 2.3e11 operations): 366 us, 624 TFLOP/s, 33 % of a large bf16 product's
+// Bound: the chain of a group and tile, about 6000 clocks in the frame below: a
+// thread waits for S 2400 (its own weights' products and then S's: eight each,
+// which one thread takes 820 and 560 clocks to issue and which end 350 and 260 later),
+// for V's operand 240, reads S in 610, masks and makes the weights in 2150; the
+// rest is the segments' ends.  880 causal tokens over 21,120 (24 heads, d = 128, 8
+// bits; 2.3e11 operations): 367 us, 623 TFLOP/s, 33 % of a large bf16 product's
 // rate.  16 trees of 17 to 48 tokens (4 query heads each) over 2,000 to 12,000:
-// 199 us; a unit there has 68 to 192 of the 256 rows.
+// 199 us; a unit there has 68 to 192 of the 256 rows, and with up to 128 of them
+// the second group has nothing to do.
 #pragma once
 
 #include "paged_attention.cuh"

@@ -74,9 +74,9 @@ constexpr int kWarps = 8;
 //   VEC: pieces line up (pairs a multiple of the elements in 16 bytes, all
 // rows 16-byte aligned).  Otherwise a lane owns single pairs.
 // Bound by HBM: 2 n H d bytes-per-element, each read and written once.  37,440
-// tokens of 16 heads of 128, bf16, three axes (0.31 GB): 57 us, 5.4 TB/s, 80 % of
-// a plain copy's rate; 2,639 fp32 tokens of 24 heads (65 MB): 14 us, a third
-// of it the launch and the waves' ends.
+// tokens of 16 heads of 128, bf16, three axes (0.31 GB): 56 us, 5.4 TB/s, 80 % of
+// a plain copy's rate; 2,639 fp32 tokens of 24 heads (65 MB): 12 us, 80 % too (a call
+// takes 13 to 20, the host's part); 64 tokens of 32 heads: 4 us.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) k_rope(const __grid_constant__ RopeArgs r, const T *x, int n, int H,
                                                      int d, long long xs, const int32_t *__restrict__ positions,
