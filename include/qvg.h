@@ -686,6 +686,257 @@ qvg_status qvg_paged_attention(const qvg_paged *cache, const void *q_bf16, int64
                                const uint32_t *mask, int32_t mask_words, float scale, void *out,
                                int32_t out_dtype, float *lse, void *workspace, size_t ws_bytes, void *stream);
 
+/* ======================================================================
+ * The latent cache: for models that keep one latent vector a token, from
+ * which every head's key and value are projected, and one key part that
+ * carries the rotary position and is shared by the heads.
+ * ====================================================================== */
+
+/*
+ * A paged cache of latents (one layer), slots and pages as in qvg_paged:
+ *   c    bf16 [num_pages][page_size][dc]   the latent;
+ *   kr   bf16 [num_pages][page_size][dr]   the shared key part, rotated.
+ * A token that held an infinity or a NaN is all NaN, both parts.
+ * dc = 64, 128, 192 or 256; dr a multiple of 8 up to 128 (0: none, kr NULL);
+ * page_size 16, 32, 64, 128 or 256.  Both buffers are caller-allocated,
+ * 16-byte aligned device memory of the size that qvg_latent_bytes reports, and
+ * share no byte.
+ */
+typedef struct {
+    int32_t dc;
+    int32_t dr;
+    int32_t page_size;
+    int32_t num_pages;
+    void *c;
+    void *kr;
+} qvg_latent;
+
+/* Bytes of the two buffers. */
+qvg_status qvg_latent_bytes(int32_t dc, int32_t dr, int32_t page_size, int32_t num_pages, size_t *c, size_t *kr);
+
+/*
+ * Write n tokens into their slots.
+ *   c, k_rope  bf16 [n][dc] and [n][dr], 16-byte aligned; token t starts at
+ *              element t * c_stride (t * kr_stride), a multiple of 8 and
+ *              >= dc (dr).  (Both may be parts of one wider row.)
+ *   slots      int64 [n] device, as in qvg_paged_append.
+ *   plan       NULL, or rotary positions that k_rope gets on the way (its
+ *              first plan->dims channels), in fp32 and rounded once, as
+ *              qvg_rope does.  positions int32 [n][axes] device.
+ * A slot at or beyond the cache's end is skipped and latches
+ * QVG_ERR_INVALID_ARG.  Nothing but the tokens' slots is written.
+ * Errors: QVG_ERR_INVALID_ARG for a bad cache or plan, n < 0, missing or
+ * misaligned pointers, bad strides; QVG_ERR_UNSUPPORTED for another dc.
+ */
+qvg_status qvg_latent_append(const qvg_latent *cache, const void *c_bf16, const void *k_rope_bf16, int32_t n,
+                             int64_t c_stride, int64_t kr_stride, const int64_t *slots, const qvg_rope_plan *plan,
+                             const int32_t *positions, void *stream);
+
+/*
+ * Read n slots back: c_out bf16 [n][dc], kr_out bf16 [n][dr], 16-byte aligned;
+ * either may be NULL.  A negative slot gives zeros; a slot beyond the cache
+ * gives zeros and latches QVG_ERR_INVALID_ARG.
+ */
+qvg_status qvg_latent_read(const qvg_latent *cache, const int64_t *slots, int32_t n, void *c_out, void *kr_out,
+                           void *stream);
+
+/*
+ * bf16 values [tokens][heads][channels] whose channels are contiguous: token t
+ * of head h starts at element t * token_stride + h * head_stride.  data is
+ * 16-byte aligned; the strides are multiples of 8 and at least the channels
+ * (a stride that is never taken, of one token or one head, may be anything).
+ */
+typedef struct {
+    const void *data;
+    int64_t token_stride;
+    int64_t head_stride;
+} qvg_view;
+
+/*
+ * Scratch bytes of qvg_latent_attention on the current device (256-byte
+ * aligned; no initialisation needed, dead after the call).
+ */
+qvg_status qvg_latent_workspace_size(int32_t dc, int32_t dr, size_t *bytes);
+
+/*
+ * Attention of B sequences' new tokens over a latent cache, in the absorbed
+ * form: the heads' key projections have been multiplied into the queries, and
+ * the value projections come after the call, so all Hq heads read the same
+ * latents.  Row (t, h) against token j:
+ *   S_j = scale * (q[t][h] . c_j + q_rope[t][h] . kr_j),   O[t][h] = softmax(S) c.
+ *   q       [total_q][Hq][dc];  q_rope [total_q][Hq][dr] (NULL where dr = 0).
+ *   scale   > 0 (it follows from the channels before the absorption).
+ *   out     [total_q][Hq][dc] fp32 or bf16, 16-byte aligned.
+ *   total_q, B, max_q, cu_q, table, table_stride, kv_len, mask_mode, mask,
+ *   mask_words, lse: as in qvg_paged_attention, here with one KV head.
+ *   workspace  at least qvg_latent_workspace_size(dc, dr) bytes.
+ * Products are of bf16 numbers with fp32 sums; a weight is off by at most
+ * 2^-9 of itself (it enters the product as bf16; lse takes it in fp32).
+ * Keys that a token does not see, and slots past kv_len, have no influence
+ * on it, whatever they hold.  A row of q with an infinity or a NaN, and one
+ * that sees a token that is NaN, gives NaN.  The results do not depend on what
+ * else the GPU runs.  All sizes on the device are read when the kernels run: a
+ * captured call can be replayed with other lengths, tables and masks.
+ */
+qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, const qvg_view *q_rope, int32_t total_q,
+                                int32_t Hq, int32_t B, int32_t max_q, const int32_t *cu_q, const int32_t *table,
+                                int32_t table_stride, const int32_t *kv_len, int32_t mask_mode, const uint32_t *mask,
+                                int32_t mask_words, float scale, void *out, int32_t out_dtype, float *lse,
+                                void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Attention of prompts in the expanded form: keys and values projected per
+ * head, the rotated key part still one for all heads.  For B sequences, with T
+ * new tokens (rows of q) that are the last of L keys,
+ *   S[t][h][j] = scale * (q[t][h] . k[j][h] + q_rope[t][h] . k_rope[j]),
+ *   O[t][h] = softmax(S) v[:][h].
+ *   q, k       [total_q][H][dn], [total_k][H][dn];  dn = 64 or 128.
+ *   q_rope, k_rope  [total_q][H][dr], [total_k][dr] (head_stride not used); dr
+ *              a multiple of 8 up to 64; 0: none, both NULL.
+ *   v          [total_k][H][dv];  dv = 64 or 128.
+ *   cu_q, cu_k int32 [B + 1] device, ascending from 0: first rows of each
+ *              sequence's new tokens and keys; NULL: max_q, max_k rows each.
+ *              A sequence with more than max_q new tokens, or rows outside
+ *              total_q or total_k, latches QVG_ERR_INVALID_ARG: its tokens
+ *              beyond max_q are left out, rows outside are not touched.
+ *   max_k      used where cu_k is NULL.
+ *   mask_mode  QVG_MASK_NONE, or QVG_MASK_CAUSAL: new token t sees the keys
+ *              0 .. L - T + t.
+ *   scale      <= 0: 1 / sqrt(dn + dr).
+ *   out        [total_q][H][dv] fp32 or bf16, 16-byte aligned; a row that
+ *              sees no key is 0.  Rows from cu_q[B] on are left as they were.
+ *   lse        fp32 [H][total_q] or NULL, as in qvg_paged_attention.
+ * Rounding, NaN and unseen keys as in qvg_latent_attention (a row that sees a
+ * value with an infinity or a NaN may be NaN in all its channels).
+ */
+qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, const qvg_view *k, const qvg_view *k_rope,
+                                  const qvg_view *v, int32_t total_q, int32_t total_k, int32_t H, int32_t dn, int32_t dr,
+                                  int32_t dv, int32_t B, int32_t max_q, int32_t max_k, const int32_t *cu_q,
+                                  const int32_t *cu_k, int32_t mask_mode, float scale, void *out, int32_t out_dtype,
+                                  float *lse, void *stream);
+
+/* ======================================================================
+ * Pages: which sequence holds which page of the paged caches, and moving what
+ * is in them.  One block table serves every layer's cache.
+ * ====================================================================== */
+
+/*
+ * The pages of a pool: refs int32 [num_pages] device, how many sequences hold
+ * each page (0: free).  It starts as zeros and is all the state there is.
+ */
+typedef struct {
+    int32_t num_pages;
+    int32_t *refs;
+} qvg_page_pool;
+
+/*
+ * A batch of sequences, device arrays that the calls read and change:
+ *   table   int32 [B][table_stride]  pages of sequence b in order; entries past
+ *           its last page mean nothing;
+ *   kv_len  int32 [B]                its tokens.
+ * Sequence b holds the first ceil(kv_len[b] / page_size) pages of its row.
+ * page_size 16, 32, 64, 128 or 256.
+ */
+typedef struct {
+    int32_t B;
+    int32_t page_size;
+    int32_t table_stride;
+    int32_t *table;
+    int32_t *kv_len;
+} qvg_sequences;
+
+/*
+ * Make children[i] a copy of sequence parents[i] that shares its pages (int32
+ * [n] device): the row's entries and the length are copied, and each page is
+ * held once more.  A child must be empty (kv_len 0), be named once, and not
+ * be a parent in the same call.  A pair that breaks this, names a sequence
+ * outside the batch, or a parent with more pages than its row, is left out and
+ * latches QVG_ERR_INVALID_ARG; so does a page outside the pool, whose entry is
+ * copied all the same.
+ */
+qvg_status qvg_pages_fork(const qvg_page_pool *pool, const qvg_sequences *seqs, const int32_t *parents,
+                          const int32_t *children, int32_t n, void *stream);
+
+/*
+ * Cut sequences ids[i] (int32 [n] device) to their first keep[i] tokens (keep
+ * NULL: 0, the whole sequence is freed): pages past those are held once less,
+ * and free where nobody holds them.  A sequence outside the batch, one named
+ * twice, and a keep outside 0 .. kv_len is left as it was and latches
+ * QVG_ERR_INVALID_ARG; a page outside the pool or held by nobody latches it and
+ * is passed over.
+ */
+qvg_status qvg_pages_release(const qvg_page_pool *pool, const qvg_sequences *seqs, const int32_t *ids,
+                             const int32_t *keep, int32_t n, void *stream);
+
+/* Scratch bytes of qvg_pages_reserve (16-byte aligned; dead after the call). */
+qvg_status qvg_pages_workspace_size(int32_t num_pages, int32_t B, size_t *bytes);
+
+/*
+ * Make room for new tokens at the sequences' ends and say where they go.
+ *   cu_new   int32 [B + 1] device, ascending from 0: sequence b gets
+ *            cu_new[b + 1] - cu_new[b] tokens (0 is allowed); NULL: n_new each.
+ *   slots    int64 [total] device: slot of each new token, sequence by sequence
+ *            (for the append calls).  total = cu_new[B] or B * n_new.
+ *   copies   int32 [B][2] device: (page, new page) where a sequence's last page
+ *            was partly filled and shared and so is replaced by a copy of its
+ *            own (to be filled by qvg_pages_copy in every layer's cache, before
+ *            the append); (-1, -1) elsewhere.
+ * Of k sequences that write to one shared page, in their order, each takes a
+ * copy while another holder is left; the last holder keeps the page.  New pages
+ * are the lowest free ones, in the order in which the sequences need them (a
+ * copy first); a page that becomes free in the call is not given out by it.
+ * kv_len grows by the new tokens.
+ * If the free pages or a table row do not suffice, nothing changes but slots
+ * and copies, which are -1 throughout, and QVG_ERR_CAPACITY is latched; if
+ * cu_new does not ascend from 0 to total, kv_len is negative or a
+ * shared page lies outside the pool, the same with QVG_ERR_INVALID_ARG.
+ *   workspace  at least qvg_pages_workspace_size(num_pages, B) bytes.
+ */
+qvg_status qvg_pages_reserve(const qvg_page_pool *pool, const qvg_sequences *seqs, const int32_t *cu_new, int32_t n_new,
+                             int32_t total, int64_t *slots, int32_t *copies, void *workspace, size_t ws_bytes,
+                             void *stream);
+
+/*
+ * What the next two calls move: the buffers of a cache as rows.  Buffer i is
+ * [num_pages][heads[i]][page_size][row_bytes[i]] bytes at base[i].
+ */
+typedef struct {
+    int32_t page_size;
+    int32_t num_pages;
+    int32_t n;
+    void *base[4];
+    int32_t heads[4];
+    int32_t row_bytes[4];
+} qvg_page_rows;
+
+qvg_status qvg_paged_rows(const qvg_paged *cache, qvg_page_rows *rows);
+qvg_status qvg_latent_rows(const qvg_latent *cache, qvg_page_rows *rows);
+
+/*
+ * Copy whole pages: copies int32 [n][2] device, (from, to); a pair with a
+ * negative page is passed over, one with a page beyond the cache latches
+ * QVG_ERR_INVALID_ARG and is passed over.  The copies run at the same time: no
+ * page may be written twice, or be both read and written.
+ */
+qvg_status qvg_pages_copy(const qvg_page_rows *rows, const int32_t *copies, int32_t n, void *stream);
+
+/*
+ * Move the tokens that are kept together, in place: token first[b] + i of
+ * sequence b becomes what token keep[b][i] was, for i < n_keep[b].
+ *   first, n_keep  int32 [B] device;  keep int32 [B][keep_stride] device,
+ *           ascending, and not below first[b] (accepted tokens of a drafted
+ *           tree, or what is left of a history).
+ * Tokens past those keep what they held (qvg_pages_release cuts them off).
+ * Pages that are written must not be shared with another sequence.
+ *   table, table_stride, B  as in qvg_paged_attention.
+ * n_keep outside 0 .. keep_stride, a negative first, a keep that does not
+ * ascend or is beyond the row, and a page outside the cache latch
+ * QVG_ERR_INVALID_ARG; that sequence is left as it was.
+ */
+qvg_status qvg_paged_compact(const qvg_page_rows *rows, const int32_t *table, int32_t table_stride, int32_t B,
+                             const int32_t *first, const int32_t *keep, int32_t keep_stride, const int32_t *n_keep,
+                             void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,8 @@
 """Python binding of libqvg: compressed video KV cache (QVG / QVG-Pro with
 QuantWM QSAC / PSAC) on one GB300, and the operators of single tokens: rotary
-positions, a paged 8-bit / 4-bit cache, and attention over its pages.
+positions, a paged 8-bit / 4-bit cache, and attention over its pages; a paged
+cache of latents with attention over it, attention of prompts, and the pages'
+bookkeeping (forks, room for new tokens, copies, compaction).
 
 Argument marshalling only: every step of compression, reconstruction,
 attention, the QuantWM statistics and the token-wise operators runs in the CUDA kernels of
@@ -39,6 +41,9 @@ EXPORTED = (
     "qvg_get_status", "qvg_last_cuda_error", "qvg_compress_chunk_noalloc", "qvg_attention_ar",
     "qvg_debug_set_wait", "qvg_rope_plan_init", "qvg_rope", "qvg_paged_bytes", "qvg_paged_append",
     "qvg_paged_read", "qvg_tree_mask", "qvg_paged_workspace_size", "qvg_paged_attention",
+    "qvg_latent_bytes", "qvg_latent_append", "qvg_latent_read", "qvg_latent_workspace_size", "qvg_latent_attention",
+    "qvg_expanded_attention", "qvg_pages_fork", "qvg_pages_release", "qvg_pages_workspace_size", "qvg_pages_reserve",
+    "qvg_paged_rows", "qvg_latent_rows", "qvg_pages_copy", "qvg_paged_compact",
 )
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -79,6 +84,29 @@ class _Paged(ct.Structure):
                 ("v_codes", ct.c_void_p), ("v_scales", ct.c_void_p)]
 
 
+class _Latent(ct.Structure):
+    _fields_ = [("dc", ct.c_int32), ("dr", ct.c_int32), ("page_size", ct.c_int32), ("num_pages", ct.c_int32),
+                ("c", ct.c_void_p), ("kr", ct.c_void_p)]
+
+
+class _View(ct.Structure):
+    _fields_ = [("data", ct.c_void_p), ("token_stride", ct.c_int64), ("head_stride", ct.c_int64)]
+
+
+class _PagePool(ct.Structure):
+    _fields_ = [("num_pages", ct.c_int32), ("refs", ct.c_void_p)]
+
+
+class _Sequences(ct.Structure):
+    _fields_ = [("B", ct.c_int32), ("page_size", ct.c_int32), ("table_stride", ct.c_int32), ("table", ct.c_void_p),
+                ("kv_len", ct.c_void_p)]
+
+
+class _PageRows(ct.Structure):
+    _fields_ = [("page_size", ct.c_int32), ("num_pages", ct.c_int32), ("n", ct.c_int32), ("base", ct.c_void_p * 4),
+                ("heads", ct.c_int32 * 4), ("row_bytes", ct.c_int32 * 4)]
+
+
 _lib = None
 
 
@@ -113,6 +141,22 @@ def lib():
         L.qvg_paged_workspace_size.argtypes = [i32, i32, i32, i32, i32, vp]
         L.qvg_paged_attention.argtypes = [vp, vp, i64, i32, i32, i32, i32, vp, vp, i32, vp, i32, vp, i32, ct.c_float,
                                           vp, i32, vp, vp, sz, vp]
+        L.qvg_latent_bytes.argtypes = [i32, i32, i32, i32, vp, vp]
+        L.qvg_latent_append.argtypes = [vp, vp, vp, i32, i64, i64, vp, vp, vp, vp]
+        L.qvg_latent_read.argtypes = [vp, vp, i32, vp, vp, vp]
+        L.qvg_latent_workspace_size.argtypes = [i32, i32, vp]
+        L.qvg_latent_attention.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp, i32, vp, i32, ct.c_float, vp, i32,
+                                           vp, vp, sz, vp]
+        L.qvg_expanded_attention.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, vp, vp, i32,
+                                             ct.c_float, vp, i32, vp, vp]
+        L.qvg_pages_fork.argtypes = [vp, vp, vp, vp, i32, vp]
+        L.qvg_pages_release.argtypes = [vp, vp, vp, vp, i32, vp]
+        L.qvg_pages_workspace_size.argtypes = [i32, i32, vp]
+        L.qvg_pages_reserve.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+        L.qvg_paged_rows.argtypes = [vp, vp]
+        L.qvg_latent_rows.argtypes = [vp, vp]
+        L.qvg_pages_copy.argtypes = [vp, vp, i32, vp]
+        L.qvg_paged_compact.argtypes = [vp, vp, i32, i32, vp, vp, i32, vp, vp]
         L.qvg_get_status.argtypes = [vp]
         L.qvg_debug_set_wait.argtypes = [ct.c_uint64, i32]
         L.qvg_last_cuda_error.restype = ct.c_char_p
@@ -637,6 +681,325 @@ def paged_attention(cache: PagedKV, q, block_table, kv_len, max_q, cu_q=None, ma
             out_dtype, None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
             _raw_stream(stream, q.device)), "qvg_paged_attention")
     return out, lse
+
+
+def latent_bytes(dc, dr, page_size, num_pages):
+    """(latents, key parts) bytes of a latent cache's two buffers."""
+    a, b = ct.c_size_t(0), ct.c_size_t(0)
+    _check(lib().qvg_latent_bytes(dc, dr, page_size, num_pages, ct.byref(a), ct.byref(b)), "qvg_latent_bytes")
+    return int(a.value), int(b.value)
+
+
+class LatentKV:
+    """One latent of dc channels and one rotated key part of dr channels a
+    token, bf16, in pages (qvg_latent in include/qvg.h).  `buffers`: the two
+    bf16 tensors where the caller allocates them."""
+
+    def __init__(self, dc, dr, page_size, num_pages, device="cuda", buffers=None):
+        import torch
+        sizes = latent_bytes(dc, dr, page_size, num_pages)
+        self.dc, self.dr, self.page_size, self.num_pages = dc, dr, page_size, num_pages
+        shapes = [(num_pages, page_size, dc), (num_pages, page_size, dr)]
+        if buffers is None:
+            buffers = [torch.zeros(s, dtype=torch.bfloat16, device=device) for s in shapes]
+        if len(buffers) != 2:
+            raise ValueError("LatentKV: two buffers are wanted (latents, key parts), got %d" % len(buffers))
+        for t, need in zip(buffers, sizes):
+            if t.dtype != torch.bfloat16 or not t.is_contiguous() or 2 * t.numel() != need or t.device != buffers[0].device:
+                raise ValueError("LatentKV: each buffer must be contiguous bf16 of the size latent_bytes reports")
+        (a0, a1), (b0, b1) = ((t.data_ptr(), t.data_ptr() + 2 * t.numel()) for t in buffers)
+        if a0 < b1 and b0 < a1:
+            raise ValueError("LatentKV: the buffers overlap")
+        self.c, self.kr = (t.view(s) for t, s in zip(buffers, shapes))
+        self.device = self.c.device
+        self._c = _Latent(dc, dr, page_size, num_pages, self.c.data_ptr(), self.kr.data_ptr() if dr else None)
+        self._ref = ct.byref(self._c)
+        self._workspace = None
+
+    @property
+    def nbytes(self):
+        return 2 * (self.c.numel() + self.kr.numel())
+
+
+def _rows2(x, channels, dev, where, name):
+    """Token stride of a bf16 [n, channels] tensor whose channels are contiguous."""
+    import torch
+    if x.dim() != 2 or x.shape[1] != channels or x.dtype != torch.bfloat16 or x.device != dev:
+        raise ValueError("%s: %s must be bf16 [n, %d] on %s" % (where, name, channels, dev))
+    if x.stride(1) != 1 and channels > 1:
+        raise ValueError("%s: %s's channels must be contiguous" % (where, name))
+    return x.stride(0) if x.shape[0] > 1 else channels
+
+
+def latent_append(cache: LatentKV, c, k_rope, slots, plan=None, positions=None, stream=None):
+    """Write tokens' latents c (bf16 [n, dc]) and key parts k_rope (bf16
+    [n, dr]; None where dr is 0) into the slots (int64 [n]; negative: skip);
+    both may be strided by token.  With a RopePlan, k_rope is rotated at
+    `positions` on the way.  A slot beyond the cache is reported by
+    get_status()."""
+    import torch
+    n = slots.numel()
+    cs, ks = _rows2(c, cache.dc, cache.device, "latent_append", "c"), 0
+    if cache.dr:
+        if k_rope is None:
+            raise ValueError("latent_append: k_rope is missing")
+        ks = _rows2(k_rope, cache.dr, cache.device, "latent_append", "k_rope")
+    if c.shape[0] != n or (cache.dr and k_rope.shape[0] != n):
+        raise ValueError("latent_append: c, k_rope and slots must be of as many tokens")
+    _on(cache.device, "latent_append", slots=(slots, torch.int64), positions=(positions, torch.int32))
+    if plan is not None:
+        _positions(plan, positions, n, "latent_append")
+    with _Device(cache.device):
+        _check(lib().qvg_latent_append(cache._ref, c.data_ptr(), k_rope.data_ptr() if cache.dr else None, n, cs, ks,
+                                       slots.data_ptr(), None if plan is None else plan._ref,
+                                       None if plan is None else positions.data_ptr(), _raw_stream(stream, cache.device)),
+               "qvg_latent_append")
+
+
+def latent_read(cache: LatentKV, slots, c_out=None, kr_out=None, stream=None):
+    """What the slots (int64 [n]; negative: zeros) hold: (latents bf16 [n, dc],
+    key parts bf16 [n, dr])."""
+    import torch
+    n = slots.numel()
+    c_out = _empty((n, cache.dc), torch.bfloat16, cache.device, stream) if c_out is None else c_out
+    kr_out = _empty((n, cache.dr), torch.bfloat16, cache.device, stream) if kr_out is None else kr_out
+    if c_out.shape != (n, cache.dc) or kr_out.shape != (n, cache.dr):
+        raise ValueError("latent_read: outputs must be [n, %d] and [n, %d]" % (cache.dc, cache.dr))
+    _on(cache.device, "latent_read", slots=(slots, torch.int64), c_out=(c_out, torch.bfloat16), kr_out=(kr_out, torch.bfloat16))
+    with _Device(cache.device):
+        _check(lib().qvg_latent_read(cache._ref, slots.data_ptr(), n, c_out.data_ptr(), kr_out.data_ptr() if cache.dr else None,
+                                     _raw_stream(stream, cache.device)), "qvg_latent_read")
+    return c_out, kr_out
+
+
+def latent_workspace_size(cache: LatentKV):
+    """Scratch bytes of latent_attention (of every batch)."""
+    b = ct.c_size_t(0)
+    with _Device(cache.device):
+        _check(lib().qvg_latent_workspace_size(cache.dc, cache.dr, ct.byref(b)), "qvg_latent_workspace_size")
+    return int(b.value)
+
+
+def _view(x, shape, dev, where, name):
+    """A qvg_view of a bf16 [tokens, heads, channels] tensor whose channels are
+    contiguous."""
+    import torch
+    if x is None or x.dim() != 3 or tuple(x.shape) != shape or x.dtype != torch.bfloat16 or x.device != dev:
+        raise ValueError("%s: %s must be bf16 [%d, %d, %d] on %s" % (where, name, *shape, dev))
+    s = x.stride()
+    if s[2] != 1 and shape[2] > 1:
+        raise ValueError("%s: %s's channels must be contiguous" % (where, name))
+    return ct.byref(_View(x.data_ptr(), s[0], s[1]))
+
+
+def latent_attention(cache: LatentKV, q, q_rope, block_table, kv_len, max_q, scale, cu_q=None, mask_mode=QVG_MASK_CAUSAL,
+                     mask=None, out_dtype=QVG_OUT_BF16, want_lse=False, out=None, workspace=None, stream=None):
+    """Attention of the new tokens over a latent cache, in the absorbed form:
+    q (bf16 [total_q, Hq, dc]: the heads' queries times their key projections)
+    and q_rope (bf16 [total_q, Hq, dr]; None where dr is 0), both strided by
+    token and head as they please; the result is in the latents' space
+    ([total_q, Hq, dc]).  scale has no default: it follows from the channels
+    before the absorption.  The rest as in paged_attention.  Returns (out, lse
+    or None).  Two calls that run at once need a workspace each (None: one per
+    call)."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError("latent_attention: q must be [total_q, Hq, %d]" % cache.dc)
+    total, Hq, B = q.shape[0], q.shape[1], kv_len.numel()
+    dt = torch.float32 if out_dtype == QVG_OUT_F32 else torch.bfloat16
+    qv = _view(q, (total, Hq, cache.dc), cache.device, "latent_attention", "q")
+    qr = _view(q_rope, (total, Hq, cache.dr), cache.device, "latent_attention", "q_rope") if cache.dr else None
+    if block_table.dim() != 2 or block_table.shape[0] != B or (cu_q is not None and cu_q.numel() != B + 1):
+        raise ValueError("latent_attention: block_table must be [B, pages], kv_len [B], cu_q [B + 1]")
+    if mask_mode == QVG_MASK_TREE and (mask is None or mask.dim() != 2 or mask.shape[0] < total):
+        raise ValueError("latent_attention: QVG_MASK_TREE needs mask rows [total_q, words]")
+    if out is None:
+        out = _empty((total, Hq, cache.dc), dt, q.device, stream)
+    elif out.shape != (total, Hq, cache.dc):
+        raise ValueError("latent_attention: out must be [total_q, Hq, %d]" % cache.dc)
+    _on(q.device, "latent_attention", block_table=(block_table, torch.int32), kv_len=(kv_len, torch.int32),
+        cu_q=(cu_q, torch.int32), mask=(mask, torch.int32), out=(out, dt), workspace=(workspace, torch.uint8))
+    lse = _empty((Hq, total), torch.float32, q.device, stream) if want_lse else None
+    if workspace is None:
+        if cache._workspace is None:
+            cache._workspace = latent_workspace_size(cache)
+        workspace = _empty((cache._workspace,), torch.uint8, q.device, stream)
+    with _Device(q.device):
+        _check(lib().qvg_latent_attention(
+            cache._ref, qv, qr, total, Hq, B, max_q, None if cu_q is None else cu_q.data_ptr(), block_table.data_ptr(),
+            block_table.shape[1], kv_len.data_ptr(), mask_mode, None if mask is None else mask.data_ptr(),
+            0 if mask is None else mask.shape[1], scale, out.data_ptr(), out_dtype, None if lse is None else lse.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), _raw_stream(stream, q.device)), "qvg_latent_attention")
+    return out, lse
+
+
+def expanded_attention(q, q_rope, k, k_rope, v, max_q, scale=0.0, cu_q=None, cu_k=None, max_k=0, mask_mode=QVG_MASK_CAUSAL,
+                       out_dtype=QVG_OUT_BF16, want_lse=False, out=None, stream=None):
+    """Attention of prompts with keys and values projected per head: q, k bf16
+    [tokens, H, dn], v bf16 [tokens, H, dv] (strided by token and head as they
+    please, such as parts of a fused projection), and the rotated parts q_rope
+    [tokens, H, dr] and k_rope [tokens, dr], which all heads share (both None:
+    no such part).  A sequence's new tokens (cu_q: int32 [B + 1]; None: max_q
+    each) are the last of its keys (cu_k; None: max_k each).  Returns (out
+    [total_q, H, dv], lse or None)."""
+    import torch
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("expanded_attention: q, k and v must be [tokens, heads, channels]")
+    (total, H, dn), total_k, dv = q.shape, k.shape[0], v.shape[2]
+    if (q_rope is None) != (k_rope is None) or (k_rope is not None and k_rope.dim() != 2):
+        raise ValueError("expanded_attention: q_rope [tokens, H, dr] and k_rope [tokens, dr] come together")
+    dr, dt, dev = 0 if k_rope is None else k_rope.shape[1], torch.float32 if out_dtype == QVG_OUT_F32 else torch.bfloat16, q.device
+    views = [_view(q, (total, H, dn), dev, "expanded_attention", "q"),
+             _view(q_rope, (total, H, dr), dev, "expanded_attention", "q_rope") if dr else None,
+             _view(k, (total_k, H, dn), dev, "expanded_attention", "k"),
+             _view(k_rope[:, None], (total_k, 1, dr), dev, "expanded_attention", "k_rope") if dr else None,
+             _view(v, (total_k, H, dv), dev, "expanded_attention", "v")]
+    if cu_q is not None:
+        B = cu_q.numel() - 1
+    elif cu_k is not None:
+        B = cu_k.numel() - 1
+    else:
+        B = total // max_q if max_q > 0 else 0
+    if B < 0 or (cu_q is None and total != B * max_q) or (cu_k is None and total_k != B * max_k) or \
+            (cu_k is not None and cu_k.numel() != B + 1):
+        raise ValueError("expanded_attention: cu_q and cu_k must be [B + 1]; without them every sequence has max_q, max_k rows")
+    if out is None:
+        out = _empty((total, H, dv), dt, dev, stream)
+    elif out.shape != (total, H, dv):
+        raise ValueError("expanded_attention: out must be [total_q, H, %d]" % dv)
+    _on(dev, "expanded_attention", cu_q=(cu_q, torch.int32), cu_k=(cu_k, torch.int32), out=(out, dt))
+    lse = _empty((H, total), torch.float32, dev, stream) if want_lse else None
+    with _Device(dev):
+        _check(lib().qvg_expanded_attention(
+            *views, total, total_k, H, dn, dr, dv, B, max_q, max_k, None if cu_q is None else cu_q.data_ptr(),
+            None if cu_k is None else cu_k.data_ptr(), mask_mode, scale, out.data_ptr(), out_dtype,
+            None if lse is None else lse.data_ptr(), _raw_stream(stream, dev)), "qvg_expanded_attention")
+    return out, lse
+
+
+class PagePool:
+    """How many sequences hold each page of the paged caches (qvg_page_pool in
+    include/qvg.h).  refs: int32 [num_pages] where the caller allocates it; 0:
+    free.  One pool and one block table serve every layer's cache."""
+
+    def __init__(self, num_pages, device="cuda", refs=None):
+        import torch
+        if num_pages < 1:
+            raise ValueError("PagePool: at least one page is wanted")
+        if refs is None:
+            refs = torch.zeros(num_pages, dtype=torch.int32, device=device)
+        if refs.dtype != torch.int32 or not refs.is_contiguous() or refs.numel() != num_pages:
+            raise ValueError("PagePool: refs must be contiguous int32 [%d]" % num_pages)
+        self.num_pages, self.refs, self.device = num_pages, refs, refs.device
+        self._c = _PagePool(num_pages, refs.data_ptr())
+        self._ref = ct.byref(self._c)
+
+
+def _sequences(pool, page_size, block_table, kv_len, where):
+    import torch
+    B = kv_len.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("%s: block_table must be [B, pages], kv_len [B]" % where)
+    _on(pool.device, where, block_table=(block_table, torch.int32), kv_len=(kv_len, torch.int32))
+    return ct.byref(_Sequences(B, page_size, block_table.shape[1], block_table.data_ptr(), kv_len.data_ptr()))
+
+
+def pages_fork(pool: PagePool, page_size, block_table, kv_len, parents, children, stream=None):
+    """Make the empty sequences children[i] (int32 [n]) copies of parents[i]
+    that share their pages; block_table and kv_len change in place."""
+    import torch
+    s = _sequences(pool, page_size, block_table, kv_len, "pages_fork")
+    if parents.numel() != children.numel():
+        raise ValueError("pages_fork: parents and children must be as many")
+    _on(pool.device, "pages_fork", parents=(parents, torch.int32), children=(children, torch.int32))
+    with _Device(pool.device):
+        _check(lib().qvg_pages_fork(pool._ref, s, parents.data_ptr(), children.data_ptr(), parents.numel(),
+                                    _raw_stream(stream, pool.device)), "qvg_pages_fork")
+
+
+def pages_release(pool: PagePool, page_size, block_table, kv_len, ids, keep=None, stream=None):
+    """Cut sequences ids[i] (int32 [n]) to their first keep[i] tokens (None: 0)
+    and give back the pages past those; kv_len changes in place."""
+    import torch
+    s = _sequences(pool, page_size, block_table, kv_len, "pages_release")
+    if keep is not None and keep.numel() != ids.numel():
+        raise ValueError("pages_release: ids and keep must be as many")
+    _on(pool.device, "pages_release", ids=(ids, torch.int32), keep=(keep, torch.int32))
+    with _Device(pool.device):
+        _check(lib().qvg_pages_release(pool._ref, s, ids.data_ptr(), None if keep is None else keep.data_ptr(), ids.numel(),
+                                       _raw_stream(stream, pool.device)), "qvg_pages_release")
+
+
+def pages_reserve(pool: PagePool, page_size, block_table, kv_len, n_new=1, cu_new=None, total=None, slots=None, copies=None,
+                  stream=None):
+    """Make room for new tokens: n_new of every sequence, or cu_new[b + 1] -
+    cu_new[b] (int32 [B + 1], `total` in all).  Returns (slots int64 [total] for
+    the append calls, copies int32 [B, 2] for pages_copy, to be made before
+    the append: (page, new page), or (-1, -1) where nothing is shared).
+    block_table and kv_len change in place.  A lack of room is reported by
+    get_status() as QVG_ERR_CAPACITY; slots and copies are -1 then."""
+    import torch
+    s = _sequences(pool, page_size, block_table, kv_len, "pages_reserve")
+    B = kv_len.numel()
+    if cu_new is not None and (cu_new.numel() != B + 1 or total is None):
+        raise ValueError("pages_reserve: cu_new must be [B + 1], with total")
+    total = B * n_new if cu_new is None else total
+    if total < 0:
+        raise ValueError("pages_reserve: a negative number of tokens")
+    slots = _empty((total,), torch.int64, pool.device, stream) if slots is None else slots
+    copies = _empty((B, 2), torch.int32, pool.device, stream) if copies is None else copies
+    if slots.numel() != total or copies.shape != (B, 2):
+        raise ValueError("pages_reserve: slots must be [%d], copies [%d, 2]" % (total, B))
+    _on(pool.device, "pages_reserve", cu_new=(cu_new, torch.int32), slots=(slots, torch.int64), copies=(copies, torch.int32))
+    need = ct.c_size_t(0)
+    _check(lib().qvg_pages_workspace_size(pool.num_pages, B, ct.byref(need)), "qvg_pages_workspace_size")
+    workspace = _empty((need.value,), torch.uint8, pool.device, stream)
+    with _Device(pool.device):
+        _check(lib().qvg_pages_reserve(pool._ref, s, None if cu_new is None else cu_new.data_ptr(), n_new, total,
+                                       slots.data_ptr(), copies.data_ptr(), workspace.data_ptr(), need.value,
+                                       _raw_stream(stream, pool.device)), "qvg_pages_reserve")
+    return slots, copies
+
+
+def _page_rows(cache, where):
+    rows = getattr(cache, "_rows", None)
+    if rows is None:
+        rows = _PageRows()
+        call = lib().qvg_latent_rows if isinstance(cache, LatentKV) else lib().qvg_paged_rows
+        _check(call(cache._ref, ct.byref(rows)), where)
+        cache._rows = rows
+    return ct.byref(rows)
+
+
+def pages_copy(cache, copies, stream=None):
+    """Copy whole pages of a PagedKV or LatentKV: copies int32 [n, 2] (from,
+    to), as pages_reserve returns them; a negative pair is passed over.  No
+    page may be written twice, or be both read and written."""
+    import torch
+    if copies.dim() != 2 or copies.shape[1] != 2:
+        raise ValueError("pages_copy: copies must be [n, 2]")
+    _on(cache.device, "pages_copy", copies=(copies, torch.int32))
+    with _Device(cache.device):
+        _check(lib().qvg_pages_copy(_page_rows(cache, "pages_copy"), copies.data_ptr(), copies.shape[0],
+                                    _raw_stream(stream, cache.device)), "qvg_pages_copy")
+
+
+def paged_compact(cache, block_table, first, keep, n_keep, stream=None):
+    """Move kept tokens of a PagedKV or LatentKV together, in place: token
+    first[b] + i becomes what token keep[b, i] was, for i < n_keep[b] (keep int32
+    [B, most], ascending, not below first[b]; first, n_keep int32 [B]).  The
+    accepted tokens of a drafted tree, or what is left of a history; the pages
+    written must not be shared.  (pages_release then cuts the sequence.)"""
+    import torch
+    B = n_keep.numel()
+    if block_table.dim() != 2 or keep.dim() != 2 or block_table.shape[0] != B or keep.shape[0] != B or first.numel() != B:
+        raise ValueError("paged_compact: block_table and keep must be [B, ...], first and n_keep [B]")
+    _on(cache.device, "paged_compact", block_table=(block_table, torch.int32), first=(first, torch.int32),
+        keep=(keep, torch.int32), n_keep=(n_keep, torch.int32))
+    with _Device(cache.device):
+        _check(lib().qvg_paged_compact(_page_rows(cache, "paged_compact"), block_table.data_ptr(), block_table.shape[1], B,
+                                       first.data_ptr(), keep.data_ptr(), keep.shape[1], n_keep.data_ptr(),
+                                       _raw_stream(stream, cache.device)), "qvg_paged_compact")
 
 
 def query_stats(q, H, M=None, w=None, count=None, accumulate=False, stream=None):
