@@ -770,8 +770,8 @@ qvg_status qvg_latent_workspace_size(int32_t dc, int32_t dr, size_t *bytes);
  *   total_q, B, max_q, cu_q, table, table_stride, kv_len, mask_mode, mask,
  *   mask_words, lse: as in qvg_paged_attention, here with one KV head.
  *   workspace  at least qvg_latent_workspace_size(dc, dr) bytes.
- * Products are of bf16 numbers with fp32 sums; a weight is off by at most
- * 2^-9 of itself (it enters the product as bf16; lse takes it in fp32).
+ * Products are of bf16 numbers with fp32 sums; a weight enters the second one
+ * rounded to bf16, i.e. off by at most 2^-8 of itself (lse takes it in fp32).
  * Keys that a token does not see, and slots past kv_len, have no influence
  * on it, whatever they hold.  A row of q with an infinity or a NaN, and one
  * that sees a token that is NaN, gives NaN.  The results do not depend on what

@@ -1,113 +1,147 @@
 // latent_attention.cu -- attention over a latent cache (absorbed form) and of
-// prompts (expanded form): a first form, one warp per query row and head.
+// prompts (expanded form): launch, the join of units that several CTAs shared,
+// and the entry points.  The kernel is in latent_attention.cuh.
 #include <cmath>
 
-#include "latent.cuh"
+#include "latent_attention.cuh"
 
 namespace qvg {
 namespace {
 
-struct Args {
-    const uint16_t *q, *qr, *k, *kr, *v;
-    long long q_t, q_h, qr_t, qr_h, k_t, k_h, kr_t, v_t, v_h;
-    int total_q, total_k, Hq, dk, dr, dv, B, max_q, max_k;
-    const int32_t *cu_q, *cu_k, *table, *kv_len;
-    long long table_stride;
-    int page_log2, num_pages;
-    int mode;
-    const uint32_t *mask;
-    int words;
-    float scale_log2;
-    float *out32;
-    uint16_t *out16;
-    float *lse;
-    int *err;
-};
-
-// Row t of sequence b: blockIdx.x = (b, t), a warp per head.
-__global__ void __launch_bounds__(128) k_rows(Args a) {
-    const int lane = threadIdx.x & 31, h = blockIdx.y * 4 + (threadIdx.x >> 5);
-    const int b = blockIdx.x / a.max_q, t = blockIdx.x - b * a.max_q;
-    int q0 = b * a.max_q, nq = a.max_q, k0 = b * a.max_k, kv = a.max_k;
-    bool bad = false;
-    if (a.cu_q) {
-        q0 = a.cu_q[b];
-        nq = a.cu_q[b + 1] - q0;
-        bad = nq < 0 || nq > a.max_q || q0 < 0 || q0 > a.total_q - nq;
-        if (q0 < 0 || q0 > a.total_q) q0 = nq = 0;
-        nq = max(0, min(min(nq, a.max_q), a.total_q - q0));
-    }
-    if (a.table) {
-        kv = a.kv_len[b];
-        bad = bad || kv < 0 || kv > a.table_stride << a.page_log2;
-        kv = static_cast<int>(max(0ll, min(static_cast<long long>(kv), a.table_stride << a.page_log2)));
-    } else if (a.cu_k) {
-        k0 = a.cu_k[b];
-        kv = a.cu_k[b + 1] - k0;
-        bad = bad || kv < 0 || k0 < 0 || k0 > a.total_k - kv;
-        if (k0 < 0 || k0 > a.total_k) k0 = kv = 0;
-        kv = max(0, min(kv, a.total_k - k0));
-    }
-    if (bad && t == 0 && h == 0 && lane == 0) raise_error(a.err, QVG_ERR_INVALID_ARG);
-    if (t >= nq || h >= a.Hq) return;
-    float q[8], qr[4], acc[8], m = -INFINITY, l = 0.0f;
+// The unit that begins in CTA i and goes on to CTA `last` left one partial
+// sum per CTA: slot 1 of CTA i, slot 0 of the others.  With references m_z,
+// sums l_z and O_z: m = max m_z, l = sum l_z 2^(m_z - m), O likewise.  One
+// warp per query row; lane z weighs part z, then the lanes share the channels
+// and go through the parts in CTA order, so the result is the same each time.
+template <int DC>
+__global__ void __launch_bounds__(256) k_latent_merge(const __grid_constant__ la::Args a) {
+    constexpr int E = DC / 32, V = E % 4 == 0 ? 4 : 2, NV = E / V;  // a lane's channels: NV runs of V, 32 V apart
+    pdl_wait();
+    const int4 u = a.desc[blockIdx.x];
+    if (u.x < 0) return;
+    const int n = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const pa::Seq s = pa::seq_of<la::kRows, la::kKeys>(a, u.x, false);
+    const long long gi = static_cast<long long>(u.z) * la::kRows + n;
+    const int tq = static_cast<int>(gi / a.grp), h = static_cast<int>(gi - static_cast<long long>(tq) * a.grp);
+    if (tq >= s.nq) return;
+    const int first = blockIdx.x, last = min(u.w, static_cast<int>(gridDim.x) - 1);
+    auto at = [&](int z) { return static_cast<size_t>(2 * z + (z == first ? 1 : 0)) * la::kRows + n; };
+    float m = -INFINITY;
+    for (int z = first + lane; z <= last; z += 32)
+        if (a.pl[at(z)] != 0.0f) m = fmaxf(m, a.pm[at(z)]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = lane + 32 * i;
-        q[i] = c < a.dk ? bf16_to_f32(a.q[(q0 + t) * a.q_t + h * a.q_h + c]) : 0.0f;
-        acc[i] = 0.0f;
-    }
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float acc[E], l = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = lane + 32 * i;
-        qr[i] = c < a.dr ? bf16_to_f32(a.qr[(q0 + t) * a.qr_t + h * a.qr_h + c]) : 0.0f;
-    }
-    const int hist = kv - nq;
-    for (int j = 0; j < kv; ++j) {
-        if (a.mode == QVG_MASK_CAUSAL && j > hist + t) break;
-        if (a.mode == QVG_MASK_TREE && j >= hist) {
-            const int i = j - hist;
-            if (!((a.mask[static_cast<long long>(q0 + t) * a.words + (i >> 5)] >> (i & 31)) & 1u)) continue;
-        }
-        long long at = k0 + j;
-        if (a.table) {
-            const int page = a.table[b * a.table_stride + (j >> a.page_log2)];
-            if (page < 0 || page >= a.num_pages) {
-                raise_error(a.err, QVG_ERR_INVALID_ARG);
-                continue;
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    for (int z0 = first; z0 <= last; z0 += 32) {
+        const int z = z0 + lane;
+        float lz = z <= last ? a.pl[at(z)] : 0.0f;
+        const float w = lz == 0.0f ? 0.0f : exp2f(a.pm[at(z)] - m);
+        lz *= w;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) lz += __shfl_xor_sync(0xFFFFFFFFu, lz, o);
+        l += lz;
+        const int parts = min(32, last - z0 + 1);
+#pragma unroll 8
+        for (int k = 0; k < parts; ++k) {
+            const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+            const float *o = a.po + at(z0 + k) * DC + lane * V;
+            if (wk != 0.0f) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int e = 0; e < V; e += 2) {
+                        const float2 x = *reinterpret_cast<const float2 *>(o + i * 32 * V + e);
+                        acc[i * V + e] = fmaf(wk, x.x, acc[i * V + e]);
+                        acc[i * V + e + 1] = fmaf(wk, x.y, acc[i * V + e + 1]);
+                    }
             }
-            at = (static_cast<long long>(page) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
         }
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (lane + 32 * i < a.dk) s = fmaf(q[i], bf16_to_f32(a.k[at * a.k_t + h * a.k_h + lane + 32 * i]), s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < a.dr) s = fmaf(qr[i], bf16_to_f32(a.kr[at * a.kr_t + lane + 32 * i]), s);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        s *= a.scale_log2;
-        const float top = fmaxf(m, s), f = m == -INFINITY ? 0.0f : exp2f(m - top), p = exp2f(s - top);
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (lane + 32 * i < a.dv) acc[i] = fmaf(p, bf16_to_f32(a.v[at * a.v_t + h * a.v_h + lane + 32 * i]), acc[i] * f);
-        m = top;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const long long row = static_cast<long long>(q0 + t) * a.Hq + h;
+    const long long row = static_cast<long long>(s.q0 + tq) * a.Hq + h;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = lane + 32 * i;
-        if (c >= a.dv) continue;
-        if (a.out32)
-            a.out32[row * a.dv + c] = acc[i] * inv;
-        else
-            a.out16[row * a.dv + c] = f32_to_bf16(acc[i] * inv);
-    }
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const long long c = row * DC + i * 32 * V + lane * V + e;
+            const float x = acc[i * V + e] * inv, y = acc[i * V + e + 1] * inv;
+            if (a.out32)
+                *reinterpret_cast<float2 *>(a.out32 + c) = make_float2(x, y);
+            else
+                *reinterpret_cast<uint32_t *>(a.out16 + c) = la::bf16x2(x, y);
+        }
     if (lane == 0 && a.lse)
-        a.lse[static_cast<long long>(h) * a.total_q + q0 + t] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        a.lse[static_cast<long long>(h) * a.total_q + s.q0 + tq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+struct Workspace {
+    size_t pm, pl, desc, bytes;  // offsets (the partial sums of O are first)
+};
+Workspace carve(int ctas, int dc) {
+    auto al = [](size_t b) { return (b + 255) & ~static_cast<size_t>(255); };
+    const size_t rows = static_cast<size_t>(ctas) * 2 * la::kRows;
+    Workspace w{};
+    w.pm = al(rows * dc * 4);
+    w.pl = w.pm + al(rows * 4);
+    w.desc = w.pl + al(rows * 4);
+    w.bytes = w.desc + al(static_cast<size_t>(ctas) * sizeof(int4));
+    return w;
+}
+
+// bf16 values as [rows][heads][channels] (heads 0: [rows][channels]); a box is
+// 64 channels of one head's `box` rows, swizzled as the tensor core reads them.
+// Channels beyond the last are filled with 0.
+bool rows_map(CUtensorMap *m, const void *data, int channels, int heads, int64_t rows, int64_t head_stride, int64_t row_stride, int box) {
+    const auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    const bool h = heads > 0;
+    if (rows == 1) row_stride = 128;  // (never taken)
+    if (heads == 1) head_stride = 128;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(channels), static_cast<cuuint64_t>(h ? heads : rows), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * (h ? head_stride : row_stride)), static_cast<cuuint64_t>(2 * row_stride)};
+    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(h ? 1 : box), static_cast<cuuint32_t>(box)};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, h ? 3 : 2, const_cast<void *>(data), dims, strides, boxes, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The rings' stages: what Q leaves of the shared memory.  Absorbed form: ring B
+// serves both products and gets all but two stages of the (small) ring A;
+// expanded form: as many of each.
+void stages(la::Args &a, bool latent) {
+    const int q = latent ? (a.na + a.nb) * la::kQChunk : 2 * a.na * la::kQChunk;
+    const int room = la::kSmem - 1024 - q, A = a.na * la::kChunk, B = a.nb * la::kChunk;
+    if (latent) {
+        a.sa = a.na ? 2 : 0;
+        a.sb = std::min(la::kMostStages, (room - a.sa * A) / B);
+    } else {
+        a.sb = std::min(la::kMostStages, room / (A + B));
+        a.sa = std::min(la::kMostStages, (room - a.sb * B) / A);
+    }
+}
+
+template <bool LATENT>
+qvg_status launch(const CUtensorMap (&map)[3], const la::Args &a, int grid, int blocks, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    const qvg_status s = smem_limit_once(done, reinterpret_cast<const void *>(la::k_latent_attention<LATENT>), la::kSmem);
+    if (s != QVG_OK) return s;
+    la::k_latent_attention<LATENT><<<grid, LATENT ? 384 : 512, la::kSmem, st>>>(map[0], map[1], map[2], a, blocks);
+    QVG_LAUNCH_CHECK();
+    return QVG_OK;
+}
+
+template <int DC>
+qvg_status launch_merge(const la::Args &a, int ctas, cudaStream_t st) {
+    const cudaError_t e = launch_pdl(k_latent_merge<DC>, dim3(ctas, la::kRows / 8), dim3(256), 0, st, a);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        note_cuda_error(e);
+        return QVG_ERR_CUDA;
+    }
+    return QVG_OK;
 }
 
 bool misaligned(const void *p, uintptr_t to) { return !p || reinterpret_cast<uintptr_t>(p) % to != 0; }
@@ -117,14 +151,6 @@ bool view_ok(const qvg_view *v, int channels, int64_t tokens, int heads) {
     if (!v || misaligned(v->data, 16)) return false;
     if (tokens > 1 && (v->token_stride < channels || v->token_stride % 8 != 0)) return false;
     return heads <= 1 || (v->head_stride >= channels && v->head_stride % 8 == 0);
-}
-
-qvg_status launch(const Args &a, cudaStream_t st) {
-    const int64_t rows = static_cast<int64_t>(a.B) * a.max_q;
-    if (rows > INT32_MAX) return QVG_ERR_UNSUPPORTED;
-    k_rows<<<dim3(static_cast<unsigned>(rows), ceil_div(a.Hq, 4)), 128, 0, st>>>(a);
-    QVG_LAUNCH_CHECK();
-    return QVG_OK;
 }
 
 }  // namespace
@@ -139,7 +165,7 @@ qvg_status qvg_latent_workspace_size(int32_t dc, int32_t dr, size_t *bytes) {
     const qvg_latent l{dc, dr, 16, 1, nullptr, nullptr};
     const qvg_status s = check_latent(&l, true);
     if (s != QVG_OK) return s;
-    *bytes = 256;
+    *bytes = carve(sm_count_current(), dc).bytes;
     return QVG_OK;
 }
 
@@ -162,24 +188,34 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
         (lse && misaligned(lse, 4)))
         return QVG_ERR_INVALID_ARG;
     if (mask_mode == QVG_MASK_TREE && (misaligned(mask, 4) || mask_words < ceil_div(max_q, 32))) return QVG_ERR_INVALID_ARG;
-    if (!workspace || ws_bytes < 256 || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return QVG_ERR_WORKSPACE;
-    Args a{};
+    if (static_cast<int64_t>(max_q) * Hq > INT32_MAX - la::kRows ||
+        static_cast<int64_t>(cache->num_pages) * cache->page_size > INT32_MAX)
+        return QVG_ERR_UNSUPPORTED;
+    const int ctas = sm_count_current();
+    const Workspace w = carve(ctas, dc);
+    if (!workspace || ws_bytes < w.bytes || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return QVG_ERR_WORKSPACE;
+    const int64_t slots = static_cast<int64_t>(cache->num_pages) * cache->page_size;
+    const int box = std::min(cache->page_size, la::kKeys);
+    CUtensorMap map[3] = {};
+    if (!rows_map(&map[0], cache->c, dc, 0, slots, 0, dc, box) || (dr > 0 && !rows_map(&map[1], cache->kr, dr, 0, slots, 0, dr, box)))
+        return QVG_ERR_CUDA;
+    la::Args a{};
     a.q = static_cast<const uint16_t *>(q->data);
-    a.q_t = q->token_stride;
+    a.q_stride = q->token_stride;
     a.q_h = q->head_stride;
     if (dr > 0) {
         a.qr = static_cast<const uint16_t *>(q_rope->data);
         a.qr_t = q_rope->token_stride;
         a.qr_h = q_rope->head_stride;
     }
-    a.k = a.v = static_cast<const uint16_t *>(cache->c);
-    a.kr = static_cast<const uint16_t *>(cache->kr);
-    a.k_t = a.v_t = dc;
-    a.kr_t = dr;
     a.total_q = total_q;
-    a.Hq = Hq;
+    a.Hq = a.grp = Hq;
+    a.H = 1;
     a.dk = a.dv = dc;
     a.dr = dr;
+    a.na = ceil_div(dr, 64);
+    a.nb = dc / 64;
+    stages(a, true);
     a.B = B;
     a.max_q = max_q;
     a.cu_q = cu_q;
@@ -195,8 +231,23 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
     a.out32 = out_dtype == QVG_OUT_F32 ? static_cast<float *>(out) : nullptr;
     a.out16 = out_dtype == QVG_OUT_BF16 ? static_cast<uint16_t *>(out) : nullptr;
     a.lse = lse;
+    char *base = static_cast<char *>(workspace);
+    a.po = reinterpret_cast<float *>(base);
+    a.pm = reinterpret_cast<float *>(base + w.pm);
+    a.pl = reinterpret_cast<float *>(base + w.pl);
+    a.desc = reinterpret_cast<int4 *>(base + w.desc);
     a.err = device_error_word();
-    return launch(a, static_cast<cudaStream_t>(stream));
+    a.wait_ns = wait_limit_ns();
+    a.inject = wait_inject();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    s = launch<true>(map, a, ctas, 0, st);
+    if (s != QVG_OK) return s;
+    switch (dc) {
+        case 64: return launch_merge<64>(a, ctas, st);
+        case 128: return launch_merge<128>(a, ctas, st);
+        case 192: return launch_merge<192>(a, ctas, st);
+        default: return launch_merge<256>(a, ctas, st);
+    }
 }
 
 qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, const qvg_view *k, const qvg_view *k_rope,
@@ -217,33 +268,32 @@ qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, con
         return QVG_ERR_INVALID_ARG;
     if (misaligned(out, 16) || (cu_q && misaligned(cu_q, 4)) || (cu_k && misaligned(cu_k, 4)) || (lse && misaligned(lse, 4)))
         return QVG_ERR_INVALID_ARG;
-    Args a{};
+    const int64_t blocks = ceil_div(max_q, 256), grid = blocks * B * H;
+    if (max_q > INT32_MAX - 256 || static_cast<int64_t>(B) * H > INT32_MAX || grid > INT32_MAX) return QVG_ERR_UNSUPPORTED;
+    CUtensorMap map[3] = {};
+    if (total_k > 0 && (!rows_map(&map[0], k->data, dn, H, total_k, k->head_stride, k->token_stride, la::kKeys) ||
+                        (dr > 0 && !rows_map(&map[1], k_rope->data, dr, 0, total_k, 0, k_rope->token_stride, la::kKeys)) ||
+                        !rows_map(&map[2], v->data, dv, H, total_k, v->head_stride, v->token_stride, la::kKeys)))
+        return QVG_ERR_CUDA;
+    la::Args a{};
     a.q = static_cast<const uint16_t *>(q->data);
-    a.q_t = q->token_stride;
+    a.q_stride = q->token_stride;
     a.q_h = q->head_stride;
-    if (total_k > 0) {
-        a.k = static_cast<const uint16_t *>(k->data);
-        a.k_t = k->token_stride;
-        a.k_h = k->head_stride;
-        a.v = static_cast<const uint16_t *>(v->data);
-        a.v_t = v->token_stride;
-        a.v_h = v->head_stride;
-    }
     if (dr > 0) {
         a.qr = static_cast<const uint16_t *>(q_rope->data);
         a.qr_t = q_rope->token_stride;
         a.qr_h = q_rope->head_stride;
-        if (total_k > 0) {
-            a.kr = static_cast<const uint16_t *>(k_rope->data);
-            a.kr_t = k_rope->token_stride;
-        }
     }
     a.total_q = total_q;
     a.total_k = total_k;
-    a.Hq = H;
+    a.Hq = a.H = H;
+    a.grp = 1;
     a.dk = dn;
     a.dv = dv;
     a.dr = dr;
+    a.na = dn / 64 + (dr > 0 ? 1 : 0);
+    a.nb = dv / 64;
+    stages(a, false);
     a.B = B;
     a.max_q = max_q;
     a.max_k = max_k;
@@ -255,7 +305,9 @@ qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, con
     a.out16 = out_dtype == QVG_OUT_BF16 ? static_cast<uint16_t *>(out) : nullptr;
     a.lse = lse;
     a.err = device_error_word();
-    return launch(a, static_cast<cudaStream_t>(stream));
+    a.wait_ns = wait_limit_ns();
+    a.inject = wait_inject();
+    return launch<false>(map, a, static_cast<int>(grid), static_cast<int>(blocks), static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

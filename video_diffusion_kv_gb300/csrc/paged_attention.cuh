@@ -99,7 +99,8 @@ struct Seq {
     __device__ __forceinline__ long long tiles(int H) const { return static_cast<long long>(H) * rb * nt; }
 };
 
-template <int NB>
+// (TILE: keys of a tile; the kernels over latents take smaller ones)
+template <int NB, int TILE = kTile>
 __device__ __forceinline__ Seq seq_of(const Args &a, int b, bool report) {
     Seq s;
     int q0 = b * a.max_q, nq = a.max_q;
@@ -118,7 +119,7 @@ __device__ __forceinline__ Seq seq_of(const Args &a, int b, bool report) {
     s.q0 = q0;
     s.nq = nq;
     s.kv = kv;
-    s.nt = max(1, static_cast<int>((static_cast<long long>(kv) + kTile - 1) / kTile));
+    s.nt = max(1, static_cast<int>((static_cast<long long>(kv) + TILE - 1) / TILE));
     s.rb = static_cast<int>((static_cast<long long>(nq) * a.grp + NB - 1) / NB);
     bad = bad || s.tiles(a.H) > 0xFFFFFFFFll;
     if (report && bad) raise_error(a.err, QVG_ERR_INVALID_ARG);
@@ -139,7 +140,7 @@ constexpr int kChunks = 256;
 
 // The CTA's part of the line, made by one whole warp.  (Its walks end with the
 // batch even if the lengths change meanwhile.)
-template <int NB>
+template <int NB, int TILE = kTile>
 struct Line {
     long long pos, end, first, per;  // first: where sequence b begins
     int b;
@@ -154,7 +155,7 @@ struct Line {
         long long total = 0;
         for (int k = 0, b0 = 0; b0 < a.B; ++k, b0 += span) {
             long long mine = 0;
-            for (int i = b0 + lane; i < min(a.B, b0 + span); i += 32) mine += seq_of<NB>(a, i, cta == 0).tiles(a.H);
+            for (int i = b0 + lane; i < min(a.B, b0 + span); i += 32) mine += seq_of<NB, TILE>(a, i, cta == 0).tiles(a.H);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
             if (lane == 0) chunk[k] = mine;
@@ -170,7 +171,7 @@ struct Line {
             int k = 0;
             while (pos >= first + chunk[k]) first += chunk[k++];
             for (b = k * span; b < a.B; b += 32) {
-                const long long w = b + lane < a.B ? seq_of<NB>(a, b + lane, false).tiles(a.H) : 0;
+                const long long w = b + lane < a.B ? seq_of<NB, TILE>(a, b + lane, false).tiles(a.H) : 0;
                 long long x = w;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -189,7 +190,7 @@ struct Line {
         }
         cut = make_int4(-1, 0, 0, 0);
         if (b >= a.B) pos = end;
-        s = seq_of<NB>(a, min(b, a.B - 1), false);
+        s = seq_of<NB, TILE>(a, min(b, a.B - 1), false);
     }
 
     // t1 = 0: no more.
@@ -198,7 +199,7 @@ struct Line {
         if (pos >= end) return;
         while (b < a.B && pos >= first + s.tiles(a.H)) {
             first += s.tiles(a.H);
-            s = seq_of<NB>(a, min(++b, a.B - 1), false);
+            s = seq_of<NB, TILE>(a, min(++b, a.B - 1), false);
         }
         if (b >= a.B) return;
         const uint32_t rel = static_cast<uint32_t>(pos - first), u = rel / static_cast<uint32_t>(s.nt);
@@ -280,7 +281,7 @@ __device__ __forceinline__ bool try_wait_long(uint64_t *bar, uint32_t parity) { 
         : "memory");
     return ok != 0;
 }
-__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *fail, uint64_t limit_ns) {
+static __device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *fail, uint64_t limit_ns) {
     for (int i = 0; i < 4; ++i)
         if (try_wait_long(bar, parity)) return true;
     const uint64_t t0 = umma::globaltimer_ns();
