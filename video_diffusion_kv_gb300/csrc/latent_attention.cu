@@ -90,22 +90,36 @@ Workspace carve(int ctas, int dc) {
     return w;
 }
 
-// bf16 values as [rows][heads][channels] (heads 0: [rows][channels]); a box is
-// 64 channels of one head's `box` rows, swizzled as the tensor core reads them.
-// Channels beyond the last are filled with 0.
-bool rows_map(CUtensorMap *m, const void *data, int channels, int heads, int64_t rows, int64_t head_stride, int64_t row_stride, int box) {
+// bf16 values [rows][heads][channels], channels by chunks of 64: dimensions
+// (channel of a chunk, row, chunk, head); a box is `box` rows of one head's
+// `chunks` chunks, laid out chunk after chunk and swizzled as the tensor core
+// reads them.
+bool chunk_map(CUtensorMap *m, const void *data, int channels, int heads, int64_t rows, int64_t head_stride, int64_t row_stride, int box, int chunks) {
     const auto fn = tensor_map_encoder();
     if (!fn) return false;
-    const bool h = heads > 0;
-    if (rows == 1) row_stride = 128;  // (never taken)
-    if (heads == 1) head_stride = 128;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(channels), static_cast<cuuint64_t>(h ? heads : rows), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * (h ? head_stride : row_stride)), static_cast<cuuint64_t>(2 * row_stride)};
-    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(h ? 1 : box), static_cast<cuuint32_t>(box)};
-    const cuuint32_t es[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, h ? 3 : 2, const_cast<void *>(data), dims, strides, boxes, es,
+    if (rows == 1) row_stride = 64;  // (never taken)
+    if (heads == 1) head_stride = 64;
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(channels / 64), static_cast<cuuint64_t>(heads)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(2 * row_stride), 128, static_cast<cuuint64_t>(2 * head_stride)};
+    const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(chunks), 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, heads > 0 ? 4 : 3, const_cast<void *>(data), dims, strides, boxes, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The rotated part, bf16 [rows][channels]; a box is 64 channels of `box` rows,
+// channels beyond the last are filled with 0.
+bool rotated_map(CUtensorMap *m, const void *data, int channels, int64_t rows, int64_t row_stride, int box) {
+    const auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    if (rows == 1) row_stride = 64;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(channels), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * row_stride)};
+    const cuuint32_t boxes[2] = {64, static_cast<cuuint32_t>(box)};
+    const cuuint32_t es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(data), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The rings' stages: what Q leaves of the shared memory.  Absorbed form: ring B
@@ -197,7 +211,9 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
     const int64_t slots = static_cast<int64_t>(cache->num_pages) * cache->page_size;
     const int box = std::min(cache->page_size, la::kKeys);
     CUtensorMap map[3] = {};
-    if (!rows_map(&map[0], cache->c, dc, 0, slots, 0, dc, box) || (dr > 0 && !rows_map(&map[1], cache->kr, dr, 0, slots, 0, dr, box)))
+    // (a page that holds a whole tile is copied in one go, a smaller one chunk by chunk)
+    if (!chunk_map(&map[0], cache->c, dc, 0, slots, 0, dc, box, box == la::kKeys ? dc / 64 : 1) ||
+        (dr > 0 && !rotated_map(&map[1], cache->kr, dr, slots, dr, box)))
         return QVG_ERR_CUDA;
     la::Args a{};
     a.q = static_cast<const uint16_t *>(q->data);
@@ -271,9 +287,9 @@ qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, con
     const int64_t blocks = ceil_div(max_q, 256), grid = blocks * B * H;
     if (max_q > INT32_MAX - 256 || static_cast<int64_t>(B) * H > INT32_MAX || grid > INT32_MAX) return QVG_ERR_UNSUPPORTED;
     CUtensorMap map[3] = {};
-    if (total_k > 0 && (!rows_map(&map[0], k->data, dn, H, total_k, k->head_stride, k->token_stride, la::kKeys) ||
-                        (dr > 0 && !rows_map(&map[1], k_rope->data, dr, 0, total_k, 0, k_rope->token_stride, la::kKeys)) ||
-                        !rows_map(&map[2], v->data, dv, H, total_k, v->head_stride, v->token_stride, la::kKeys)))
+    if (total_k > 0 && (!chunk_map(&map[0], k->data, dn, H, total_k, k->head_stride, k->token_stride, la::kKeys, dn / 64) ||
+                        (dr > 0 && !rotated_map(&map[1], k_rope->data, dr, total_k, k_rope->token_stride, la::kKeys)) ||
+                        !chunk_map(&map[2], v->data, dv, H, total_k, v->head_stride, v->token_stride, la::kKeys, dv / 64)))
         return QVG_ERR_CUDA;
     la::Args a{};
     a.q = static_cast<const uint16_t *>(q->data);

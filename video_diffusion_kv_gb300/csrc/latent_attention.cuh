@@ -77,6 +77,52 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int c
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *map, int c0, int c1, int c2, int c3, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(umma::smem_u32(bar))
+        : "memory");
+}
+
+// The issuing warps stay whole and name the thread that issues by a predicate:
+// addresses and counts are then the same for the warp as the compiler sees it, and
+// an instruction takes about 25 clocks to issue, where one under `if (lane == 0)` takes 90.
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, bool one) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc), "r"(one ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc, bool one) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(acc), "r"(one ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t *bar, bool one) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(umma::smem_u32(bar)),
+        "r"(one ? 1u : 0u)
+        : "memory");
+}
+
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
@@ -463,8 +509,11 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == W0 + 4) {
-        // ---- loads: a lane per (piece of pages, chunk) --------------------------------------------------
+        // ---- loads -------------------------------------------------------------------------------------
+        // A tile's latents (k, v) take one copy where a page holds the whole tile, else one for each piece of a page and
+        // chunk; the rotated part's chunks one copy each.
         const int pr_log2 = LATENT ? min(a.page_log2, 6) : 6, pr = 1 << pr_log2, pieces = kKeys >> pr_log2;
+        const bool one = elected();
         pa::Segment g;
         Ring ra, rb;
         int it = 0, n_seg = 0;
@@ -472,8 +521,8 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
         while (ok && next_segment(g, n_seg)) {
             ++n_seg;
             // first slot of piece `lane` of tile t (expanded form: first key); -1: no such page
-            auto first_of = [&](int t) -> long long {
-                if (!LATENT) return u.k0 + static_cast<long long>(t) * kKeys;
+            auto first_of = [&](int t) {
+                if (!LATENT) return u.k0 + t * kKeys;
                 const long long tok = static_cast<long long>(t) * kKeys + (lane << pr_log2);
                 if (lane >= pieces || tok >= g.kv || t >= g.t1) return -1;
                 const int page = a.table[g.b * a.table_stride + (tok >> a.page_log2)];
@@ -481,149 +530,160 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
                     raise_error(a.err, QVG_ERR_INVALID_ARG);
                     return -1;
                 }
-                return (static_cast<long long>(page) << a.page_log2) + (tok & ((1 << a.page_log2) - 1));
+                return (page << a.page_log2) + static_cast<int>(tok & ((1 << a.page_log2) - 1));
             };
-            long long now = first_of(g.t0);
+            int now = first_of(g.t0);
             for (int t = g.t0; t < g.t1; ++t, ++it) {
-                const long long then = LATENT ? first_of(t + 1) : u.k0 + static_cast<long long>(t + 1) * kKeys;
-                const uint32_t there = LATENT ? __popc(__ballot_sync(0xFFFFFFFFu, now >= 0)) : 1;
-#pragma unroll
-                for (int which = 0; which < 2; ++which) {  // A, B
-                    const int chunks = which ? a.nb : a.na;
-                    if (chunks == 0) continue;
-                    Ring &rg = which ? rb : ra;
-                    uint64_t *full = which ? &b_full[rg.i] : &a_full[rg.i];
-                    if (it >= (which ? a.sb : a.sa)) ok = ok && wait(which ? &b_empty[rg.i] : &a_empty[rg.i], rg.parity ^ 1u);
+                const int then = first_of(t + 1);
+                const int there = LATENT ? __popc(__ballot_sync(0xFFFFFFFFu, now >= 0)) : 1;
+                if (a.na > 0) {
+                    if (it >= a.sa) ok = wait(&a_empty[ra.i], ra.parity ^ 1u);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    if (lane == 0) umma::mbar_arrive_expect_tx(full, there * chunks * (pr * 128));
-                    __syncwarp();
-                    const int p = LATENT ? lane & (pieces - 1) : 0, c = LATENT ? lane / pieces : lane;
-                    const long long at = LATENT ? __shfl_sync(0xFFFFFFFFu, now, p) : now;
-                    if (c < chunks && at >= 0) {
-                        const uint32_t dst = (which ? b0 + rg.i * b_bytes : a0 + rg.i * a_bytes) + c * kChunk + p * (pr * 128);
-                        if constexpr (LATENT) {
-                            tma_load_2d(dst, which ? &kmap : &rmap, c * 64, static_cast<int>(at), full);
-                        } else if (which) {
-                            tma_load_3d(dst, &vmap, c * 64, u.h, static_cast<int>(at), full);
-                        } else if (c < a.dk / 64) {
-                            tma_load_3d(dst, &kmap, c * 64, u.h, static_cast<int>(at), full);
-                        } else {
-                            tma_load_2d(dst, &rmap, 0, static_cast<int>(at), full);
+                    const uint32_t dst = a0 + ra.i * a_bytes;
+                    if (one) umma::mbar_arrive_expect_tx(&a_full[ra.i], there * a.na * (pr * 128));
+                    if constexpr (LATENT) {
+                        for (int p = 0; p < pieces; ++p) {
+                            const int at = __shfl_sync(0xFFFFFFFFu, now, p);
+                            if (at >= 0)
+                                for (int c = 0; c < a.na; ++c)
+                                    if (one) tma_load_2d(dst + c * kChunk + p * (pr * 128), &rmap, c * 64, at, &a_full[ra.i]);
+                        }
+                    } else {
+                        if (one) tma_load_4d(dst, &kmap, 0, now, 0, u.h, &a_full[ra.i]);
+                        if (a.dr > 0 && one) tma_load_2d(dst + (a.na - 1) * kChunk, &rmap, 0, now, &a_full[ra.i]);
+                    }
+                    if (one) issued[0] = it + 1;
+                    ra.next(a.sa);
+                }
+                if (it >= a.sb) ok = wait(&b_empty[rb.i], rb.parity ^ 1u);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const uint32_t dst = b0 + rb.i * b_bytes;
+                if (one) umma::mbar_arrive_expect_tx(&b_full[rb.i], there * a.nb * (pr * 128));
+                if constexpr (LATENT) {
+                    if (pieces == 1) {
+                        const int at = __shfl_sync(0xFFFFFFFFu, now, 0);
+                        if (at >= 0 && one) tma_load_3d(dst, &kmap, 0, at, 0, &b_full[rb.i]);
+                    } else {
+                        for (int p = 0; p < pieces; ++p) {
+                            const int at = __shfl_sync(0xFFFFFFFFu, now, p);
+                            if (at >= 0)
+                                for (int c = 0; c < a.nb; ++c)
+                                    if (one) tma_load_3d(dst + c * kChunk + p * (pr * 128), &kmap, 0, at, c, &b_full[rb.i]);
                         }
                     }
-                    if (lane == 0) issued[which] = it + 1;
-                    rg.next(which ? a.sb : a.sa);
-                    __syncwarp();
+                } else {
+                    if (one) tma_load_4d(dst, &vmap, 0, now, 0, u.h, &b_full[rb.i]);
                 }
-                if (!ok) break;
+                if (one) issued[1] = it + 1;
+                rb.next(a.sb);
                 now = then;
             }
         }
+        __syncwarp();
     } else if (warp == W0 + 5) {
         // ---- S: the rotated part's chunks of ring A (expanded form: all of K), then the latents' ---------
         constexpr uint32_t id = umma::idesc_f16(kRows, kKeys, 1);
         const int plain = LATENT ? 0 : a.dk / 64;  // ring A: chunks of 64 channels each, then the rotated part's
+        const bool one = elected();
         pa::Segment g;
         Ring ra, rb;
         int mine[G] = {}, n_fix = 0, n_seg = 0;
         bool ok = true;
         while (ok && next_segment(g, n_seg)) {
-            if (lane == 0) {
-                const int clear = clear_of(g);
-                ok = wait(&q_full, n_seg & 1);
-                for (int t = g.t0; ok && t < g.t1; ++t) {
-                    if (a.na > 0) ok = wait(&a_full[ra.i], ra.parity);
-                    if (LATENT) {
-                        ok = ok && wait(&b_full[rb.i], rb.parity);
-                        if (partial(t, clear)) {
-                            ok = ok && wait(&fixed[n_fix % kFix], (n_fix / kFix) & 1);
-                            ++n_fix;
-                        }
-                    }
-#pragma unroll
-                    for (int grp = 0; grp < G; ++grp) {
-                        if (t >= tiles_end(g, grp)) continue;
-                        const int bf = mine[grp] & 1;
-                        if (mine[grp] >= 2) ok = ok && wait(&o_done[grp][bf], ((mine[grp] >> 1) - 1) & 1);  // the buffer's last weights have been used
-                        if (!ok) break;
-                        umma::tc_fence_after();
-                        const uint32_t t_s = tmem + 256 + grp * 128 + bf * 64;
-                        uint32_t acc = 0;
-                        const uint64_t dq = umma::desc_sw128(sm + grp * q_group);
-                        for (int c = 0; c < a.na; ++c) {
-                            const uint64_t dk = umma::desc_sw128(a0 + ra.i * a_bytes + c * kChunk), dqc = dq + c * (kQChunk >> 4);
-                            const int steps = c < plain ? 4 : min(4, (a.dr - (c - plain) * 64 + 15) / 16);
-                            for (int s = 0; s < steps; ++s, acc = 1) umma::mma_f16(t_s, dqc + 2 * s, dk + 2 * s, id, acc);
-                        }
-                        if (LATENT) {
-                            for (int c = 0; c < a.nb; ++c) {
-                                const uint64_t dk = umma::desc_sw128(b0 + rb.i * b_bytes + c * kChunk), dqc = dq + (a.na + c) * (kQChunk >> 4);
-#pragma unroll
-                                for (int s = 0; s < 4; ++s, acc = 1) umma::mma_f16(t_s, dqc + 2 * s, dk + 2 * s, id, acc);
-                            }
-                        }
-                        umma::mma_commit(&s_full[grp][bf]);
-                        // test hook: with S in flight, wait for what never comes
-                        if (a.inject && mine[grp] == 0) ok = ok && wait(&never, 0);
-                        ++mine[grp];
-                    }
-                    if (!ok) break;
-                    if (a.na > 0) umma::mma_commit(&a_empty[ra.i]);
-                    ra.next(a.sa);
-                    rb.next(a.sb);
-                }
-                if (ok) umma::mma_commit(&q_free);
-            }
+            const int clear = clear_of(g);
+            ok = wait(&q_full, n_seg & 1);
             ++n_seg;
-            ok = __all_sync(0xFFFFFFFFu, ok);
+            for (int t = g.t0; t < g.t1; ++t) {
+                if (a.na > 0) ok = ok && wait(&a_full[ra.i], ra.parity);
+                if (LATENT) {
+                    ok = ok && wait(&b_full[rb.i], rb.parity);
+                    if (partial(t, clear)) {
+                        ok = ok && wait(&fixed[n_fix % kFix], (n_fix / kFix) & 1);
+                        ++n_fix;
+                    }
+                }
+#pragma unroll
+                for (int grp = 0; grp < G; ++grp) {
+                    if (t >= tiles_end(g, grp)) continue;
+                    const int bf = mine[grp] & 1;
+                    if (mine[grp] >= 2) ok = ok && wait(&o_done[grp][bf], ((mine[grp] >> 1) - 1) & 1);  // the buffer's last weights have been used
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    umma::tc_fence_after();
+                    const uint32_t t_s = tmem + 256 + grp * 128 + bf * 64;
+                    uint32_t acc = 0;
+                    uint64_t dq = umma::desc_sw128(sm + grp * q_group), dk = umma::desc_sw128(a0 + ra.i * a_bytes);
+                    for (int c = 0; c < a.na; ++c, dq += kQChunk >> 4, dk += kChunk >> 4) {
+                        const int steps = c < plain ? 4 : min(4, (a.dr - (c - plain) * 64 + 15) / 16);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            if (s < steps) {
+                                mma_ss(t_s, dq + 2 * s, dk + 2 * s, id, acc, one);
+                                acc = 1;
+                            }
+                    }
+                    if (LATENT) {
+                        dk = umma::desc_sw128(b0 + rb.i * b_bytes);
+                        for (int c = 0; c < a.nb; ++c, dq += kQChunk >> 4, dk += kChunk >> 4)
+#pragma unroll
+                            for (int s = 0; s < 4; ++s, acc = 1) mma_ss(t_s, dq + 2 * s, dk + 2 * s, id, acc, one);
+                    }
+                    commit(&s_full[grp][bf], one);
+                    // test hook: with S in flight, wait for what never comes
+                    if (a.inject && mine[grp] == 0) ok = wait(&never, 0);
+                    ++mine[grp];
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (a.na > 0) commit(&a_empty[ra.i], one);
+                ra.next(a.sa);
+                rb.next(a.sb);
+            }
+            if (ok) commit(&q_free, one);
         }
-        if (lane == 0) {  // all products issued complete before tensor memory goes back
-            umma::mma_commit(&drain);
-            umma::mbar_wait(&drain, 0, pa::kDrainNs);
-        }
-        __syncwarp();
+        commit(&drain, one);  // all products issued complete before tensor memory goes back
+        umma::mbar_wait(&drain, 0, pa::kDrainNs);
     } else if (warp == W0 + 6) {
         // ---- PV ---------------------------------------------------------------------------------------
         const uint32_t id = umma::idesc_f16_bmn(kRows, a.dv, 1);
+        const bool one = elected();
         pa::Segment g;
         Ring rb;
         int mine[G] = {}, n_fix = 0, n_seg = 0;
         bool ok = true;
         while (ok && next_segment(g, n_seg)) {
             ++n_seg;
-            if (lane == 0) {
-                const int clear = clear_of(g);
-                for (int t = g.t0; ok && t < g.t1; ++t, rb.next(a.sb)) {
-                    ok = wait(&b_full[rb.i], rb.parity);
-                    if (partial(t, clear)) {
-                        ok = ok && wait(&fixed[n_fix % kFix], (n_fix / kFix) & 1);
-                        ++n_fix;
-                    }
-                    const uint64_t dv = umma::desc_sw128_mn(b0 + rb.i * b_bytes, kChunk);
-#pragma unroll
-                    for (int grp = 0; grp < G; ++grp) {
-                        if (t >= tiles_end(g, grp)) continue;
-                        const int bf = mine[grp] & 1;
-                        ok = ok && wait(&p_full[grp][bf], (mine[grp] >> 1) & 1);
-                        if (!ok) break;
-                        umma::tc_fence_after();
-                        const uint32_t t_p = tmem + 256 + grp * 128 + bf * 64, t_o = tmem + grp * 128;
-#pragma unroll
-                        for (int s = 0; s < kKeys / 16; ++s) umma::mma_f16_ts(t_o, t_p + 8 * s, dv + s * 128, id, !(t == g.t0 && s == 0));
-                        umma::mma_commit(&o_done[grp][bf]);
-                        ++mine[grp];
-                    }
-                    if (ok) umma::mma_commit(&b_empty[rb.i]);
+            const int clear = clear_of(g);
+            for (int t = g.t0; t < g.t1; ++t, rb.next(a.sb)) {
+                ok = wait(&b_full[rb.i], rb.parity);
+                if (partial(t, clear)) {
+                    ok = ok && wait(&fixed[n_fix % kFix], (n_fix / kFix) & 1);
+                    ++n_fix;
                 }
+                const uint64_t dv = umma::desc_sw128_mn(b0 + rb.i * b_bytes, kChunk);
+#pragma unroll
+                for (int grp = 0; grp < G; ++grp) {
+                    if (t >= tiles_end(g, grp)) continue;
+                    const int bf = mine[grp] & 1;
+                    ok = ok && wait(&p_full[grp][bf], (mine[grp] >> 1) & 1);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    umma::tc_fence_after();
+                    const uint32_t t_p = tmem + 256 + grp * 128 + bf * 64, t_o = tmem + grp * 128;
+#pragma unroll
+                    for (int s = 0; s < kKeys / 16; ++s) mma_ts(t_o, t_p + 8 * s, dv + s * 128, id, !(t == g.t0 && s == 0), one);
+                    commit(&o_done[grp][bf], one);
+                    ++mine[grp];
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                commit(&b_empty[rb.i], one);
             }
-            ok = __all_sync(0xFFFFFFFFu, ok);
         }
-        if (lane == 0) {
-            umma::mma_commit(&drain);
-            umma::mbar_wait(&drain, 0, pa::kDrainNs);
-        }
-        __syncwarp();
+        commit(&drain, one);
+        umma::mbar_wait(&drain, 0, pa::kDrainNs);
     } else if constexpr (LATENT) {
         // ---- this CTA's part of the line, unit by unit ---------------------------------------------------
         pa::Line<kRows, kKeys> line(a, reinterpret_cast<long long *>(base));  // (Q's place: no segment is out yet)
