@@ -122,19 +122,11 @@ bool rotated_map(CUtensorMap *m, const void *data, int channels, int64_t rows, i
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The rings' stages: what Q leaves of the shared memory.  Absorbed form: ring B
-// serves both products and gets all but two stages of the (small) ring A;
-// expanded form: as many of each.
+// The rings' stages: what Q leaves of the shared memory.
 void stages(la::Args &a, bool latent) {
-    const int q = latent ? (a.na + a.nb) * la::kQChunk : 2 * a.na * la::kQChunk;
-    const int room = la::kSmem - 1024 - q, A = a.na * la::kChunk, B = a.nb * la::kChunk;
-    if (latent) {
-        a.sa = a.na ? 2 : 0;
-        a.sb = std::min(la::kMostStages, (room - a.sa * A) / B);
-    } else {
-        a.sb = std::min(la::kMostStages, room / (A + B));
-        a.sa = std::min(la::kMostStages, (room - a.sb * B) / A);
-    }
+    const int room = la::kSmem - 1024 - (latent ? 1 : 2) * a.na * la::kQChunk, A = a.na * la::kChunk, B = a.nb * la::kChunk;
+    a.sb = std::min(la::kMostStages, room / (A + B));
+    a.sa = latent ? 0 : std::min(la::kMostStages, (room - a.sb * B) / A);
 }
 
 template <bool LATENT>

@@ -45,8 +45,8 @@ struct Args : pa::Args {
     const uint16_t *qr;  // (q: the part of the queries before the rotated one)
     long long q_h, qr_t, qr_h;  // (q_stride: q's token stride)
     int dk, dr, dv;      // channels of q; of the rotated part; of v
-    int na, nb;          // 64-channel chunks of ring A (read by S alone) and of ring B (V)
-    int sa, sb;          // stages of the rings
+    int na, nb;          // 64-channel chunks of a tile: read by S alone (the rotated part; expanded form: all of K), and V's
+    int sa, sb;          // stages of the rings (absorbed form: one ring, whose stages hold both)
     // expanded form
     const int32_t *cu_k;
     int total_k, max_k;
@@ -228,11 +228,12 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x;
-    const int nq_chunks = LATENT ? a.na + a.nb : a.na, q_group = nq_chunks * kQChunk;
+    const int q_group = a.na * kQChunk;  // of a group's Q in shared memory (absorbed form: the rotated part, the rest is in tensor memory)
     uint8_t *base = dyn + ((1024u - (umma::smem_u32(dyn) & 1023u)) & 1023u);
     const uint32_t sm = umma::smem_u32(base);
-    const uint32_t a0 = sm + G * q_group, b0 = a0 + a.sa * a.na * kChunk;
-    const int a_bytes = a.na * kChunk, b_bytes = a.nb * kChunk;
+    // ring A: stages of na chunks, then ring B: of nb; absorbed form: stages of both, ring B's place is within them
+    const int a_bytes = (LATENT ? a.na + a.nb : a.na) * kChunk, b_bytes = LATENT ? a_bytes : a.nb * kChunk;
+    const uint32_t a0 = sm + G * q_group, b0 = a0 + (LATENT ? a.na * kChunk : a.sa * a_bytes);
     if (tid == 0) {
         fail = 0;
         issued[0] = issued[1] = 0;
@@ -265,7 +266,8 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
     }
     __syncthreads();
     umma::tc_fence_after();
-    const uint32_t tmem = tmem_base;  // O of the groups from 0 (128 columns each; LATENT: 256), then S, two buffers a group
+    // O of the groups from 0 (128 columns each; LATENT: 256), S from 256, two buffers a group, LATENT: Q but its rotated part from 384
+    const uint32_t tmem = tmem_base;
     volatile int *vfail = &fail;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return pa::wait(bar, parity, vfail, a.wait_ns); };
     auto next_segment = [&](pa::Segment &g, int n) {
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
                             top4[i] = fmaxf(fmaxf(top4[i], __uint_as_float(v[c / 32][c % 32 + 2 * i])), __uint_as_float(v[c / 32][c % 32 + 2 * i + 1]));
                     const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
                     const bool fresh = ref == -INFINITY;
-                    const bool move = fresh ? top > -INFINITY : (top - ref) * a.scale_log2 > kRaise;
+                    const bool move = live && (fresh ? top > -INFINITY : (top - ref) * a.scale_log2 > kRaise);
                     const float f = move && !fresh ? pa::ex2((ref - top) * a.scale_log2) : 1.0f;
                     if (move) ref = top;
                     if (t != g.t0 && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
@@ -460,14 +462,31 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
                 const uint16_t *q = a.q + (g.q0 + tq) * a.q_stride + h * a.q_h + piece * 8;
                 const uint16_t *qr = a.qr + (g.q0 + tq) * a.qr_t + h * a.qr_h + piece * 8;
                 uint8_t *dst = base + (i >> 7) * q_group + row * 128 + ((piece ^ (row & 7)) << 4);
-                const int rot = LATENT ? 0 : a.dk / 64, rots = (a.dr + 63) / 64;  // chunks of the rotated part: from `rot` on
-                for (int c = 0; c < nq_chunks; ++c) {
-                    const int e = c - rot;  // chunk of the rotated part
-                    const bool is_r = e >= 0 && e < rots;
-                    const bool in = !is_r || e * 64 + piece * 8 < a.dr;
-                    const uint16_t *src = is_r ? qr + e * 64 : q + (LATENT ? c - rots : c) * 64;
-                    umma::cp_async16(dst + c * kQChunk, in ? src : a.q, in);
+                const int plain = LATENT ? 0 : a.dk / 64;  // chunks before the rotated part's
+                for (int c = 0; c < a.na; ++c) {
+                    const bool in = c < plain || (c - plain) * 64 + piece * 8 < a.dr;
+                    umma::cp_async16(dst + c * kQChunk, !in ? a.q : c < plain ? q + c * 64 : qr + (c - plain) * 64, in);
                 }
+            }
+            if constexpr (LATENT) {  // a thread's row into its lane of tensor memory
+                const uint32_t gi = static_cast<uint32_t>(g.r) * kRows + w;
+                const int tq = static_cast<int>(gi / static_cast<uint32_t>(a.grp)), h = static_cast<int>(gi) - tq * a.grp;
+                const bool live = tq < g.nq;
+                const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (g.q0 + (live ? tq : 0)) * a.q_stride + (live ? h : 0) * a.q_h);
+                const uint32_t t_q = tmem + 384 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+                if (__any_sync(0xFFFFFFFFu, live)) {
+                    for (int c = 0; c < a.nb; ++c) {
+                        uint32_t x[32];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint4 v = live ? q[c * 8 + e] : make_uint4(0, 0, 0, 0);
+                            x[4 * e] = v.x, x[4 * e + 1] = v.y, x[4 * e + 2] = v.z, x[4 * e + 3] = v.w;
+                        }
+                        umma::tmem_st32(t_q + c * 32, x);
+                    }
+                    umma::tmem_st_wait();
+                }
+                umma::tc_fence_before();
             }
             umma::cp_async_wait_all();
             umma::fence_proxy_async_smem();
@@ -535,46 +554,46 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
             int now = first_of(g.t0);
             for (int t = g.t0; t < g.t1; ++t, ++it) {
                 const int then = first_of(t + 1);
-                const int there = LATENT ? __popc(__ballot_sync(0xFFFFFFFFu, now >= 0)) : 1;
-                if (a.na > 0) {
+                const int there = LATENT ? __popc(__ballot_sync(0xFFFFFFFFu, now >= 0)) : 0;
+                if constexpr (LATENT) {
+                    if (it >= a.sb) ok = wait(&b_empty[rb.i], rb.parity ^ 1u);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    uint64_t *full = &b_full[rb.i];
+                    const uint32_t dst = b0 + rb.i * b_bytes, dst_r = a0 + rb.i * a_bytes;
+                    if (one) umma::mbar_arrive_expect_tx(full, there * (a.na + a.nb) * (pr * 128));
+                    for (int p = 0; p < pieces; ++p) {
+                        const int at = __shfl_sync(0xFFFFFFFFu, now, p);
+                        if (at < 0) continue;
+                        if (pieces == 1) {
+                            if (one) tma_load_3d(dst, &kmap, 0, at, 0, full);
+                        } else {
+                            for (int c = 0; c < a.nb; ++c)
+                                if (one) tma_load_3d(dst + c * kChunk + p * (pr * 128), &kmap, 0, at, c, full);
+                        }
+                        for (int c = 0; c < a.na; ++c)
+                            if (one) tma_load_2d(dst_r + c * kChunk + p * (pr * 128), &rmap, c * 64, at, full);
+                    }
+                } else {
                     if (it >= a.sa) ok = wait(&a_empty[ra.i], ra.parity ^ 1u);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     const uint32_t dst = a0 + ra.i * a_bytes;
-                    if (one) umma::mbar_arrive_expect_tx(&a_full[ra.i], there * a.na * (pr * 128));
-                    if constexpr (LATENT) {
-                        for (int p = 0; p < pieces; ++p) {
-                            const int at = __shfl_sync(0xFFFFFFFFu, now, p);
-                            if (at >= 0)
-                                for (int c = 0; c < a.na; ++c)
-                                    if (one) tma_load_2d(dst + c * kChunk + p * (pr * 128), &rmap, c * 64, at, &a_full[ra.i]);
-                        }
-                    } else {
-                        if (one) tma_load_4d(dst, &kmap, 0, now, 0, u.h, &a_full[ra.i]);
-                        if (a.dr > 0 && one) tma_load_2d(dst + (a.na - 1) * kChunk, &rmap, 0, now, &a_full[ra.i]);
+                    if (one) {
+                        umma::mbar_arrive_expect_tx(&a_full[ra.i], a_bytes);
+                        tma_load_4d(dst, &kmap, 0, now, 0, u.h, &a_full[ra.i]);
+                        if (a.dr > 0) tma_load_2d(dst + (a.na - 1) * kChunk, &rmap, 0, now, &a_full[ra.i]);
+                        issued[0] = it + 1;
                     }
-                    if (one) issued[0] = it + 1;
+                    __syncwarp();
                     ra.next(a.sa);
-                }
-                if (it >= a.sb) ok = wait(&b_empty[rb.i], rb.parity ^ 1u);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                const uint32_t dst = b0 + rb.i * b_bytes;
-                if (one) umma::mbar_arrive_expect_tx(&b_full[rb.i], there * a.nb * (pr * 128));
-                if constexpr (LATENT) {
-                    if (pieces == 1) {
-                        const int at = __shfl_sync(0xFFFFFFFFu, now, 0);
-                        if (at >= 0 && one) tma_load_3d(dst, &kmap, 0, at, 0, &b_full[rb.i]);
-                    } else {
-                        for (int p = 0; p < pieces; ++p) {
-                            const int at = __shfl_sync(0xFFFFFFFFu, now, p);
-                            if (at >= 0)
-                                for (int c = 0; c < a.nb; ++c)
-                                    if (one) tma_load_3d(dst + c * kChunk + p * (pr * 128), &kmap, 0, at, c, &b_full[rb.i]);
-                        }
+                    if (it >= a.sb) ok = wait(&b_empty[rb.i], rb.parity ^ 1u);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    if (one) {
+                        umma::mbar_arrive_expect_tx(&b_full[rb.i], b_bytes);
+                        tma_load_4d(b0 + rb.i * b_bytes, &vmap, 0, now, 0, u.h, &b_full[rb.i]);
                     }
-                } else {
-                    if (one) tma_load_4d(dst, &vmap, 0, now, 0, u.h, &b_full[rb.i]);
                 }
                 if (one) issued[1] = it + 1;
                 rb.next(a.sb);
@@ -583,9 +602,9 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
         }
         __syncwarp();
     } else if (warp == W0 + 5) {
-        // ---- S: the rotated part's chunks of ring A (expanded form: all of K), then the latents' ---------
+        // ---- S -----------------------------------------------------------------------------------------
         constexpr uint32_t id = umma::idesc_f16(kRows, kKeys, 1);
-        const int plain = LATENT ? 0 : a.dk / 64;  // ring A: chunks of 64 channels each, then the rotated part's
+        const int plain = LATENT ? 0 : a.dk / 64;  // chunks before the rotated part's
         const bool one = elected();
         pa::Segment g;
         Ring ra, rb;
@@ -596,7 +615,7 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
             ok = wait(&q_full, n_seg & 1);
             ++n_seg;
             for (int t = g.t0; t < g.t1; ++t) {
-                if (a.na > 0) ok = ok && wait(&a_full[ra.i], ra.parity);
+                if (!LATENT) ok = ok && wait(&a_full[ra.i], ra.parity);
                 if (LATENT) {
                     ok = ok && wait(&b_full[rb.i], rb.parity);
                     if (partial(t, clear)) {
@@ -614,7 +633,15 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
                     umma::tc_fence_after();
                     const uint32_t t_s = tmem + 256 + grp * 128 + bf * 64;
                     uint32_t acc = 0;
-                    uint64_t dq = umma::desc_sw128(sm + grp * q_group), dk = umma::desc_sw128(a0 + ra.i * a_bytes);
+                    uint64_t dk;
+                    if (LATENT) {
+                        dk = umma::desc_sw128(b0 + rb.i * b_bytes);
+                        for (int c = 0; c < a.nb; ++c, dk += kChunk >> 4)
+#pragma unroll
+                            for (int s = 0; s < 4; ++s, acc = 1) mma_ts(t_s, tmem + 384 + c * 32 + 8 * s, dk + 2 * s, id, acc, one);
+                    }
+                    uint64_t dq = umma::desc_sw128(sm + grp * q_group);
+                    dk = umma::desc_sw128(a0 + (LATENT ? rb.i : ra.i) * a_bytes);
                     for (int c = 0; c < a.na; ++c, dq += kQChunk >> 4, dk += kChunk >> 4) {
                         const int steps = c < plain ? 4 : min(4, (a.dr - (c - plain) * 64 + 15) / 16);
 #pragma unroll
@@ -624,12 +651,6 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
                                 acc = 1;
                             }
                     }
-                    if (LATENT) {
-                        dk = umma::desc_sw128(b0 + rb.i * b_bytes);
-                        for (int c = 0; c < a.nb; ++c, dq += kQChunk >> 4, dk += kChunk >> 4)
-#pragma unroll
-                            for (int s = 0; s < 4; ++s, acc = 1) mma_ss(t_s, dq + 2 * s, dk + 2 * s, id, acc, one);
-                    }
                     commit(&s_full[grp][bf], one);
                     // test hook: with S in flight, wait for what never comes
                     if (a.inject && mine[grp] == 0) ok = wait(&never, 0);
@@ -637,9 +658,12 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
                 }
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                if (a.na > 0) commit(&a_empty[ra.i], one);
-                ra.next(a.sa);
-                rb.next(a.sb);
+                if (LATENT) {
+                    rb.next(a.sb);  // (the stage is given back by PV)
+                } else {
+                    commit(&a_empty[ra.i], one);
+                    ra.next(a.sa);
+                }
             }
             if (ok) commit(&q_free, one);
         }
@@ -709,7 +733,8 @@ __global__ void __launch_bounds__(LATENT ? 384 : 512, 1)
     if (tid == 0 && *vfail) {
         raise_error(a.err, QVG_ERR_TIMEOUT);
         // the copies in flight land before the CTA ends
-        for (int j = max(0, issued[0] - a.sa); a.na > 0 && j < issued[0]; ++j) umma::mbar_wait(&a_full[j % a.sa], (j / a.sa) & 1, pa::kDrainNs);
+        for (int j = max(0, issued[0] - a.sa); j < issued[0]; ++j)  // (none in the absorbed form)
+            umma::mbar_wait(&a_full[j % a.sa], (j / a.sa) & 1, pa::kDrainNs);
         for (int j = max(0, issued[1] - a.sb); j < issued[1]; ++j) umma::mbar_wait(&b_full[j % a.sb], (j / a.sb) & 1, pa::kDrainNs);
     }
     if (warp == W0 + 7) {
