@@ -1,0 +1,305 @@
+// expanded_attention.cuh -- attention of prompts (expanded form): the kernel.
+// Launch and entry point: latent_attention.cu.
+//
+// A unit of work is 256 query rows of one head, two groups of 128 that share
+// each tile of K and V; one unit per CTA, the longest first.  S is made for 128
+// keys at once, softmax and PV take 64 at a time: the first half's product runs
+// while the second half's weights are made.  One group's products run while the other group is
+// at its softmax.
+//
+// Tensor memory: O 2 x 128 columns, S 2 x 128.
+// Roles: softmax (8 warps, thread = row), helpers (4: Q, and V in tiles that
+// some row does not see all of), loads of K, of V, and each group's products.
+#pragma once
+
+#include "bf16_attention.cuh"
+
+namespace qvg {
+namespace la {
+
+constexpr int kPromptRows = 256, kPromptKeys = 128, kPromptWarps = 16;
+constexpr int kKChunk = kPromptKeys * 128;  // 64 channels of K's tile
+
+// A CTA's unit, and how many tiles of 64 keys each group needs.
+struct Unit {
+    int b, h, r, q0, nq, k0, kv, nt[2];
+};
+__device__ __forceinline__ Unit unit_of(const Args &a, int blocks) {
+    Unit u;
+    const int bh = a.B * a.H, i = blockIdx.x / bh, j = blockIdx.x - i * bh;
+    u.r = blocks - 1 - i;  // causal: the last rows see the most keys
+    u.b = j / a.H;
+    u.h = j - u.b * a.H;
+    bool bad = false;
+    u.q0 = u.b * a.max_q;
+    u.nq = a.max_q;
+    if (a.cu_q) {
+        u.q0 = a.cu_q[u.b];
+        u.nq = a.cu_q[u.b + 1] - u.q0;
+        bad = u.nq < 0 || u.nq > a.max_q || u.q0 < 0 || u.q0 > a.total_q - u.nq;
+        if (u.q0 < 0 || u.q0 > a.total_q) u.q0 = u.nq = 0;
+        u.nq = max(0, min(min(u.nq, a.max_q), a.total_q - u.q0));
+    }
+    u.k0 = u.b * a.max_k;
+    u.kv = a.max_k;
+    if (a.cu_k) {
+        u.k0 = a.cu_k[u.b];
+        u.kv = a.cu_k[u.b + 1] - u.k0;
+        bad = bad || u.kv < 0 || u.k0 < 0 || u.k0 > a.total_k - u.kv;
+        if (u.k0 < 0 || u.k0 > a.total_k) u.k0 = u.kv = 0;
+        u.kv = max(0, min(u.kv, a.total_k - u.k0));
+    }
+    if (bad && u.r == 0 && u.h == 0 && threadIdx.x == 0) raise_error(a.err, QVG_ERR_INVALID_ARG);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int first = u.r * kPromptRows + g * kRows, last = min(u.nq, first + kRows);
+        const int end = first >= u.nq ? 0 : a.mode == QVG_MASK_CAUSAL ? min(u.kv, u.kv - u.nq + last) : u.kv;
+        u.nt[g] = end <= 0 ? 0 : (end - 1) / kKeys + 1;
+    }
+    return u;
+}
+
+// kmap: k; rmap: the rotated key parts; vmap: v.
+__global__ void __launch_bounds__(kPromptWarps * 32, 1)
+    k_expanded_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap rmap,
+                         const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a, int blocks) {
+    extern __shared__ uint8_t dyn[];
+    __shared__ uint64_t a_full[kMostStages], a_empty[kMostStages], b_full[kMostStages], b_empty[kMostStages], fixed[kFix];
+    __shared__ uint64_t s_full[2], p_full[2][2], o_done[2][2], q_full, drain, never;
+    __shared__ uint4 s_bad[kFix];  // marked keys of a tile: key 16 w + i at bit 2 i of word w
+    __shared__ uint32_t tmem_base;
+    __shared__ int fail, issued[2];  // tiles of K and of V whose copies have been issued
+
+    const Unit u = unit_of(a, blocks);
+    if (u.r * kPromptRows >= u.nq) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int q_group = a.na * kQChunk, a_bytes = a.na * kKChunk, b_bytes = a.nb * kChunk;
+    uint8_t *base = dyn + ((1024u - (umma::smem_u32(dyn) & 1023u)) & 1023u);
+    const uint32_t sm = umma::smem_u32(base);
+    const uint32_t a0 = sm + 2 * q_group, b0 = a0 + a.sa * a_bytes;
+    if (tid == 0) {
+        fail = 0;
+        issued[0] = issued[1] = 0;
+        for (int i = 0; i < kMostStages; ++i) {
+            umma::mbar_init(&a_full[i], 1);
+            umma::mbar_init(&a_empty[i], 2);
+            umma::mbar_init(&b_full[i], 1);
+            umma::mbar_init(&b_empty[i], 6);  // each group, and the helpers' warps
+        }
+        for (int i = 0; i < kFix; ++i) umma::mbar_init(&fixed[i], 4);
+        for (int g = 0; g < 2; ++g) {
+            umma::mbar_init(&s_full[g], 1);
+            for (int i = 0; i < 2; ++i) {
+                umma::mbar_init(&p_full[g][i], 4);
+                umma::mbar_init(&o_done[g][i], 1);
+            }
+        }
+        umma::mbar_init(&q_full, 4);
+        umma::mbar_init(&drain, 2);
+        umma::mbar_init(&never, 1);
+        umma::fence_barrier_init();
+    }
+    if (warp == 12) {
+        umma::tmem_alloc(&tmem_base, 512);
+        umma::tmem_relinquish();
+    }
+    __syncthreads();
+    umma::tc_fence_after();
+    const uint32_t tmem = tmem_base;  // O of the groups at 0 and 128, S at 256 and 384
+    volatile int *vfail = &fail;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return pa::wait(bar, parity, vfail, a.wait_ns); };
+    const int most = max(u.nt[0], u.nt[1]), hist = u.kv - u.nq;
+    // The first key that some row of the unit does not see; whether tile t (of 64) has such keys.
+    const int clear = a.mode == QVG_MASK_CAUSAL ? min(u.kv, hist + 1 + u.r * kPromptRows) : u.kv;
+    auto partial = [&](int t) { return (t + 1) * kKeys > clear; };
+    bool ok = true;
+
+    if (warp < 8) {
+        // ---- softmax: thread = row -----------------------------------------------------------------
+        const int grp = warp >> 2;
+        const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16, t_o = tmem + grp * 128 + t_lane, t_s = tmem + 256 + grp * 128 + t_lane;
+        const int tq = u.r * kPromptRows + tid, end = u.nt[grp];  // (thread tid of the eight warps has row tid)
+        const bool live = tq < u.nq, idle = !__any_sync(0xFFFFFFFFu, live);
+        int n_fix = 0;
+        Row m;
+        for (int t = 0; t < end; ++t) {
+            const int half = t & 1, d = t >> 1;
+            const bool part = partial(t);
+            if (half == 0) ok = wait(&s_full[grp], d & 1);
+            uint4 bad = make_uint4(0, 0, 0, 0);
+            if (part) {
+                ok = ok && wait(&fixed[n_fix % kFix], (n_fix / kFix) & 1);
+                bad = s_bad[n_fix % kFix];
+                ++n_fix;
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            umma::tc_fence_after();
+            if (!idle) {
+                uint2 see = make_uint2(0, 0);
+                if (part) see = seen_keys(a, t, u.kv, u.nq, u.q0, live ? tq : 0);
+                // (S of this tile came after all products of the tile before)
+                ok = weigh(a, m, t_s + half * 64, t_o, part, see, bad, live, t > 0, [&] { return half == 0 || wait(&o_done[grp][0], d & 1); });
+                if (!ok) break;
+            }
+            umma::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(&p_full[grp][half]);
+        }
+        if (ok && end > 0) ok = wait(&o_done[grp][(end - 1) & 1], ((end - 1) >> 1) & 1);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok) {
+            umma::tc_fence_after();
+            if (!idle) store_rows(a, m, t_o, end == 0, live, true, 0, static_cast<long long>(u.q0 + tq) * a.Hq + u.h, u.h, u.q0 + tq);
+        }
+    } else if (warp < 12) {
+        // ---- helpers: Q, and V where some row does not see all of it ---------------------------------
+        const int w = tid - 256, piece = w & 7, plain = a.dk / 64;  // chunks before the rotated part's
+        for (int i = w >> 3; i < kPromptRows; i += 16) {
+            const int tq = u.r * kPromptRows + i, row = i & (kRows - 1);
+            if (tq >= u.nq) break;  // (rows that are left out keep what is there: no other row reads them)
+            const uint16_t *q = a.q + (u.q0 + tq) * a.q_stride + u.h * a.q_h + piece * 8;
+            const uint16_t *qr = a.qr + (u.q0 + tq) * a.qr_t + u.h * a.qr_h + piece * 8;
+            uint8_t *dst = base + (i >> 7) * q_group + row * 128 + ((piece ^ (row & 7)) << 4);
+            for (int c = 0; c < a.na; ++c) {
+                const bool in = c < plain || piece * 8 < a.dr;
+                umma::cp_async16(dst + c * kQChunk, !in ? a.q : c < plain ? q + c * 64 : qr, in);
+            }
+        }
+        umma::cp_async_wait_all();
+        umma::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&q_full);
+        Ring rb;
+        int n_fix = 0;
+        for (int t = 0; t < most; ++t, rb.next(a.sb)) {
+            ok = wait(&b_full[rb.i], rb.parity);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            if (partial(t)) {
+                const uint32_t marks = clean(base + (b0 - sm) + rb.i * b_bytes, a.nb, w, u.kv - t * kKeys);
+                __syncwarp();
+                if (lane == 0) {
+                    reinterpret_cast<uint32_t *>(&s_bad[n_fix % kFix])[warp - 8] = marks;
+                    umma::mbar_arrive(&fixed[n_fix % kFix]);
+                }
+                ++n_fix;
+            }
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(&b_empty[rb.i]);
+        }
+    } else if (warp == 12) {
+        // ---- loads of K: a copy for its channels, one for the rotated part ------------------------------
+        const bool one = elected();
+        Ring ra;
+        for (int d = 0; 2 * d < most; ++d, ra.next(a.sa)) {
+            if (d >= a.sa) ok = wait(&a_empty[ra.i], ra.parity ^ 1u);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            const uint32_t dst = a0 + ra.i * a_bytes;
+            const int at = u.k0 + d * kPromptKeys;
+            if (one) {
+                umma::mbar_arrive_expect_tx(&a_full[ra.i], a_bytes);
+                tma_load_4d(dst, &kmap, 0, at, 0, u.h, &a_full[ra.i]);
+                if (a.dr > 0) tma_load_2d(dst + (a.na - 1) * kKChunk, &rmap, 0, at, &a_full[ra.i]);
+                issued[0] = d + 1;
+            }
+            __syncwarp();
+        }
+    } else if (warp == 13) {
+        // ---- loads of V -----------------------------------------------------------------------------------
+        const bool one = elected();
+        Ring rb;
+        for (int t = 0; t < most; ++t, rb.next(a.sb)) {
+            if (t >= a.sb) ok = wait(&b_empty[rb.i], rb.parity ^ 1u);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            if (one) {
+                umma::mbar_arrive_expect_tx(&b_full[rb.i], b_bytes);
+                tma_load_4d(b0 + rb.i * b_bytes, &vmap, 0, u.k0 + t * kKeys, 0, u.h, &b_full[rb.i]);
+                issued[1] = t + 1;
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---- a group's products: S of 128 keys once all weights of the tile before have been used, PV of each half ----
+        const int grp = warp - 14, mine = u.nt[grp], plain = a.dk / 64;
+        constexpr uint32_t id_s = umma::idesc_f16(kRows, kPromptKeys, 1);
+        const uint32_t id_o = umma::idesc_f16_bmn(kRows, a.dv, 1), t_s = tmem + 256 + grp * 128, t_o = tmem + grp * 128;
+        const bool one = elected();
+        const uint64_t dq = umma::desc_sw128(sm + grp * q_group);
+        const int steps_r = (a.dr + 15) / 16;
+        Ring ra, rb;
+        int n_fix = 0;
+        ok = wait(&q_full, 0);
+        // the groups out of step: group 1 begins once group 0 is at its softmax
+        if (grp == 1 && u.nt[0] > 0) ok = ok && wait(&p_full[0][0], 0);
+        for (int d = 0; 2 * d < most; ++d, ra.next(a.sa)) {
+            ok = ok && wait(&a_full[ra.i], ra.parity);
+            if (2 * d < mine) {
+                if (d > 0) ok = ok && wait(&o_done[grp][1], (d - 1) & 1);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                umma::tc_fence_after();
+                const uint64_t dk = umma::desc_sw128(a0 + ra.i * a_bytes);
+                for (int c = 0; c < plain; ++c)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        mma_ss(t_s, dq + c * (kQChunk >> 4) + 2 * s, dk + c * (kKChunk >> 4) + 2 * s, id_s, c | s, one);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    if (s < steps_r) mma_ss(t_s, dq + plain * (kQChunk >> 4) + 2 * s, dk + plain * (kKChunk >> 4) + 2 * s, id_s, 1, one);
+                commit(&s_full[grp], one);
+                commit(&a_empty[ra.i], one);
+                // test hook: with S in flight, wait for what never comes
+                if (a.inject && d == 0) ok = wait(&never, 0);
+            } else if (one && ok) {
+                umma::mbar_arrive(&a_empty[ra.i]);
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int t = 2 * d + half;
+                if (t >= most) break;
+                ok = ok && wait(&b_full[rb.i], rb.parity);
+                if (partial(t)) {
+                    ok = ok && wait(&fixed[n_fix % kFix], (n_fix / kFix) & 1);
+                    ++n_fix;
+                }
+                if (t < mine) ok = ok && wait(&p_full[grp][half], d & 1);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (t < mine) {
+                    umma::tc_fence_after();
+                    const uint64_t dv = umma::desc_sw128_mn(b0 + rb.i * b_bytes, kChunk);
+#pragma unroll
+                    for (int s = 0; s < kKeys / 16; ++s) mma_ts(t_o, t_s + half * 64 + 8 * s, dv + s * 128, id_o, t > 0 || s > 0, one);
+                    commit(&o_done[grp][half], one);
+                    commit(&b_empty[rb.i], one);
+                } else if (one) {
+                    umma::mbar_arrive(&b_empty[rb.i]);
+                }
+                __syncwarp();
+                rb.next(a.sb);
+            }
+            if (!ok) break;
+        }
+        commit(&drain, one);  // all products issued complete before tensor memory goes back
+        umma::mbar_wait(&drain, 0, pa::kDrainNs);
+    }
+    __syncwarp();
+    umma::tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *vfail) {
+        raise_error(a.err, QVG_ERR_TIMEOUT);
+        // the copies in flight land before the CTA ends
+        for (int j = max(0, issued[0] - a.sa); j < issued[0]; ++j) umma::mbar_wait(&a_full[j % a.sa], (j / a.sa) & 1, pa::kDrainNs);
+        for (int j = max(0, issued[1] - a.sb); j < issued[1]; ++j) umma::mbar_wait(&b_full[j % a.sb], (j / a.sb) & 1, pa::kDrainNs);
+    }
+    if (warp == 12) {
+        umma::tc_fence_after();
+        umma::tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace la
+}  // namespace qvg

@@ -1,79 +1,98 @@
 // latent_attention.cu -- attention over a latent cache (absorbed form) and of
 // prompts (expanded form): launch, the join of units that several CTAs shared,
-// and the entry points.  The kernel is in latent_attention.cuh.
+// and the entry points.  The kernels are in latent_attention.cuh and
+// expanded_attention.cuh.
 #include <cmath>
 
+#include "expanded_attention.cuh"
 #include "latent_attention.cuh"
 
 namespace qvg {
 namespace {
 
-// The unit that begins in CTA i and goes on to CTA `last` left one partial
-// sum per CTA: slot 1 of CTA i, slot 0 of the others.  With references m_z,
-// sums l_z and O_z: m = max m_z, l = sum l_z 2^(m_z - m), O likewise.  One
-// warp per query row; lane z weighs part z, then the lanes share the channels
-// and go through the parts in CTA order, so the result is the same each time.
+// Units that several CTAs shared: with references m_z, sums l_z and O_z of the
+// P parts, m = max m_z, l = sum l_z 2^(m_z - m), O likewise.  The unit that
+// begins in CTA i has its part in slot 1 of CTA i and in slot 0 of the CTAs after
+// it, up to `last`.  Each of them takes part in the join: block x, as the CTA of rank x - i, has rows
+// rank, rank + P, ..; blockIdx.y: a half of the channels.  Few parts: a warp
+// a row, part by part; many: the block's warps share a row's parts and add up
+// in their order, so the result is the same each time.  (One warp per row and
+// part after part, 152 parts of 16 rows took 48 us.)
+constexpr int kJoinWarps = 8, kFewParts = 8;
+
 template <int DC>
-__global__ void __launch_bounds__(256) k_latent_merge(const __grid_constant__ la::Args a) {
-    constexpr int E = DC / 32, V = E % 4 == 0 ? 4 : 2, NV = E / V;  // a lane's channels: NV runs of V, 32 V apart
-    pdl_wait();
-    const int4 u = a.desc[blockIdx.x];
-    if (u.x < 0) return;
-    const int n = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+__device__ __forceinline__ void join(const la::Args &a, const int4 u, int rank, float (*s_acc)[DC / 2], float *s_l) {
+    constexpr int E = DC / 64;  // a lane's channels: lane, lane + 32, .. of the half
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const pa::Seq s = pa::seq_of<la::kRows, la::kKeys>(a, u.x, false);
-    const long long gi = static_cast<long long>(u.z) * la::kRows + n;
-    const int tq = static_cast<int>(gi / a.grp), h = static_cast<int>(gi - static_cast<long long>(tq) * a.grp);
-    if (tq >= s.nq) return;
-    const int first = blockIdx.x, last = min(u.w, static_cast<int>(gridDim.x) - 1);
-    auto at = [&](int z) { return static_cast<size_t>(2 * z + (z == first ? 1 : 0)) * la::kRows + n; };
-    float m = -INFINITY;
-    for (int z = first + lane; z <= last; z += 32)
-        if (a.pl[at(z)] != 0.0f) m = fmaxf(m, a.pm[at(z)]);
+    const int first = u.z, last = min(u.w, static_cast<int>(gridDim.x) - 1), parts = last - first + 1;
+    const bool few = parts <= kFewParts;
+    const long long row0 = static_cast<long long>(u.y) * la::kRows;
+    const int rows = static_cast<int>(max(0ll, min(static_cast<long long>(la::kRows), static_cast<long long>(s.nq) * a.grp - row0)));
+    const int step = few ? kJoinWarps : 1;
+    for (int n0 = rank; n0 < rows; n0 += parts * step) {  // (the block's warps go through this together)
+        const int n = few ? n0 + parts * warp : n0;
+        auto at = [&](int z) { return static_cast<size_t>(2 * z + (z == first ? 1 : 0)) * la::kRows + n; };
+        float acc[E], l = 0.0f, m = -INFINITY;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    float acc[E], l = 0.0f;
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+        if (n < rows) {
+            for (int z = first + lane; z <= last; z += 32)
+                if (a.pl[at(z)] != 0.0f) m = fmaxf(m, a.pm[at(z)]);
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int z0 = first; z0 <= last; z0 += 32) {
-        const int z = z0 + lane;
-        float lz = z <= last ? a.pl[at(z)] : 0.0f;
-        const float w = lz == 0.0f ? 0.0f : exp2f(a.pm[at(z)] - m);
-        lz *= w;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) lz += __shfl_xor_sync(0xFFFFFFFFu, lz, o);
-        l += lz;
-        const int parts = min(32, last - z0 + 1);
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
 #pragma unroll 8
-        for (int k = 0; k < parts; ++k) {
-            const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
-            const float *o = a.po + at(z0 + k) * DC + lane * V;
-            if (wk != 0.0f) {
+            for (int z = first + (few ? 0 : warp); z <= last; z += few ? 1 : kJoinWarps) {
+                const float lz = a.pl[at(z)], w = lz == 0.0f ? 0.0f : exp2f(a.pm[at(z)] - m);
+                const float *o = a.po + at(z) * DC + blockIdx.y * (DC / 2) + lane;
+                l = fmaf(lz, w, l);
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int e = 0; e < V; e += 2) {
-                        const float2 x = *reinterpret_cast<const float2 *>(o + i * 32 * V + e);
-                        acc[i * V + e] = fmaf(wk, x.x, acc[i * V + e]);
-                        acc[i * V + e + 1] = fmaf(wk, x.y, acc[i * V + e + 1]);
-                    }
+                for (int e = 0; e < E; ++e) {
+                    const float x = o[32 * e];
+                    acc[e] = w == 0.0f ? acc[e] : fmaf(w, x, acc[e]);
+                }
             }
         }
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const long long row = static_cast<long long>(s.q0 + tq) * a.Hq + h;
+        if (!few) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+            for (int e = 0; e < E; ++e) s_acc[warp][lane + 32 * e] = acc[e];
+            if (lane == 0) s_l[warp] = l;
+            __syncthreads();
+            if (warp == 0) {
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-            const long long c = row * DC + i * 32 * V + lane * V + e;
-            const float x = acc[i * V + e] * inv, y = acc[i * V + e + 1] * inv;
-            if (a.out32)
-                *reinterpret_cast<float2 *>(a.out32 + c) = make_float2(x, y);
-            else
-                *reinterpret_cast<uint32_t *>(a.out16 + c) = la::bf16x2(x, y);
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    l += s_l[w];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] += s_acc[w][lane + 32 * e];
+                }
+            }
+            __syncthreads();
         }
-    if (lane == 0 && a.lse)
-        a.lse[static_cast<long long>(h) * a.total_q + s.q0 + tq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        if (n >= rows || (!few && warp > 0)) continue;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const long long gi = row0 + n;
+        const int tq = static_cast<int>(gi / a.grp), h = static_cast<int>(gi - static_cast<long long>(tq) * a.grp);
+        const long long out = (static_cast<long long>(s.q0 + tq) * a.Hq + h) * DC + blockIdx.y * (DC / 2) + lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (a.out32)
+                a.out32[out + 32 * e] = acc[e] * inv;
+            else
+                a.out16[out + 32 * e] = f32_to_bf16(acc[e] * inv);
+        }
+        if (lane == 0 && blockIdx.y == 0 && a.lse)
+            a.lse[static_cast<long long>(h) * a.total_q + s.q0 + tq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    }
+}
+
+template <int DC>
+__global__ void __launch_bounds__(kJoinWarps * 32) k_latent_merge(const __grid_constant__ la::Args a) {
+    __shared__ float s_acc[kJoinWarps][DC / 2], s_l[kJoinWarps];
+    pdl_wait();
+    const int x = blockIdx.x;
+    const int4 head = a.desc[2 * x], cut = a.desc[2 * x + 1];
+    if (head.x >= 0) join<DC>(a, head, x - head.z, s_acc, s_l);
+    if (cut.x >= 0) join<DC>(a, cut, 0, s_acc, s_l);
 }
 
 struct Workspace {
@@ -86,7 +105,7 @@ Workspace carve(int ctas, int dc) {
     w.pm = al(rows * dc * 4);
     w.pl = w.pm + al(rows * 4);
     w.desc = w.pl + al(rows * 4);
-    w.bytes = w.desc + al(static_cast<size_t>(ctas) * sizeof(int4));
+    w.bytes = w.desc + al(static_cast<size_t>(ctas) * 2 * sizeof(int4));
     return w;
 }
 
@@ -122,26 +141,33 @@ bool rotated_map(CUtensorMap *m, const void *data, int channels, int64_t rows, i
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The rings' stages: what Q leaves of the shared memory.
-void stages(la::Args &a, bool latent) {
-    const int room = la::kSmem - 1024 - (latent ? 1 : 2) * a.na * la::kQChunk, A = a.na * la::kChunk, B = a.nb * la::kChunk;
-    a.sb = std::min(la::kMostStages, room / (A + B));
-    a.sa = latent ? 0 : std::min(la::kMostStages, (room - a.sb * B) / A);
+qvg_status launch_latent(const CUtensorMap (&map)[2], la::Args &a, int ctas, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    const qvg_status s = smem_limit_once(done, reinterpret_cast<const void *>(la::k_latent_attention), la::kSmem);
+    if (s != QVG_OK) return s;
+    // the stages: what Q's rotated part leaves of the shared memory
+    a.sb = std::min(la::kMostStages, (la::kSmem - 1024 - a.na * la::kQChunk) / ((a.na + a.nb) * la::kChunk));
+    la::k_latent_attention<<<ctas, la::kLatentWarps * 32, la::kSmem, st>>>(map[0], map[1], a);
+    QVG_LAUNCH_CHECK();
+    return QVG_OK;
 }
 
-template <bool LATENT>
-qvg_status launch(const CUtensorMap (&map)[3], const la::Args &a, int grid, int blocks, cudaStream_t st) {
+qvg_status launch_expanded(const CUtensorMap (&map)[3], la::Args &a, int grid, int blocks, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    const qvg_status s = smem_limit_once(done, reinterpret_cast<const void *>(la::k_latent_attention<LATENT>), la::kSmem);
+    const qvg_status s = smem_limit_once(done, reinterpret_cast<const void *>(la::k_expanded_attention), la::kSmem);
     if (s != QVG_OK) return s;
-    la::k_latent_attention<LATENT><<<grid, LATENT ? 384 : 512, la::kSmem, st>>>(map[0], map[1], map[2], a, blocks);
+    // two tiles of K at least, then as many half tiles of V as there is room for
+    const int room = la::kSmem - 1024 - 2 * a.na * la::kQChunk, A = a.na * la::kKChunk, B = a.nb * la::kChunk;
+    a.sb = std::min(la::kMostStages, (room - 2 * A) / B);
+    a.sa = std::min(la::kMostStages, (room - a.sb * B) / A);
+    la::k_expanded_attention<<<grid, la::kPromptWarps * 32, la::kSmem, st>>>(map[0], map[1], map[2], a, blocks);
     QVG_LAUNCH_CHECK();
     return QVG_OK;
 }
 
 template <int DC>
 qvg_status launch_merge(const la::Args &a, int ctas, cudaStream_t st) {
-    const cudaError_t e = launch_pdl(k_latent_merge<DC>, dim3(ctas, la::kRows / 8), dim3(256), 0, st, a);
+    const cudaError_t e = launch_pdl(k_latent_merge<DC>, dim3(ctas, 2), dim3(kJoinWarps * 32), 0, st, a);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         note_cuda_error(e);
@@ -202,7 +228,7 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
     if (!workspace || ws_bytes < w.bytes || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return QVG_ERR_WORKSPACE;
     const int64_t slots = static_cast<int64_t>(cache->num_pages) * cache->page_size;
     const int box = std::min(cache->page_size, la::kKeys);
-    CUtensorMap map[3] = {};
+    CUtensorMap map[2] = {};
     // (a page that holds a whole tile is copied in one go, a smaller one chunk by chunk)
     if (!chunk_map(&map[0], cache->c, dc, 0, slots, 0, dc, box, box == la::kKeys ? dc / 64 : 1) ||
         (dr > 0 && !rotated_map(&map[1], cache->kr, dr, slots, dr, box)))
@@ -223,7 +249,6 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
     a.dr = dr;
     a.na = ceil_div(dr, 64);
     a.nb = dc / 64;
-    stages(a, true);
     a.B = B;
     a.max_q = max_q;
     a.cu_q = cu_q;
@@ -248,7 +273,7 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
     a.wait_ns = wait_limit_ns();
     a.inject = wait_inject();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    s = launch<true>(map, a, ctas, 0, st);
+    s = launch_latent(map, a, ctas, st);
     if (s != QVG_OK) return s;
     switch (dc) {
         case 64: return launch_merge<64>(a, ctas, st);
@@ -279,8 +304,8 @@ qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, con
     const int64_t blocks = ceil_div(max_q, 256), grid = blocks * B * H;
     if (max_q > INT32_MAX - 256 || static_cast<int64_t>(B) * H > INT32_MAX || grid > INT32_MAX) return QVG_ERR_UNSUPPORTED;
     CUtensorMap map[3] = {};
-    if (total_k > 0 && (!chunk_map(&map[0], k->data, dn, H, total_k, k->head_stride, k->token_stride, la::kKeys, dn / 64) ||
-                        (dr > 0 && !rotated_map(&map[1], k_rope->data, dr, total_k, k_rope->token_stride, la::kKeys)) ||
+    if (total_k > 0 && (!chunk_map(&map[0], k->data, dn, H, total_k, k->head_stride, k->token_stride, la::kPromptKeys, dn / 64) ||
+                        (dr > 0 && !rotated_map(&map[1], k_rope->data, dr, total_k, k_rope->token_stride, la::kPromptKeys)) ||
                         !chunk_map(&map[2], v->data, dv, H, total_k, v->head_stride, v->token_stride, la::kKeys, dv / 64)))
         return QVG_ERR_CUDA;
     la::Args a{};
@@ -301,7 +326,6 @@ qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, con
     a.dr = dr;
     a.na = dn / 64 + (dr > 0 ? 1 : 0);
     a.nb = dv / 64;
-    stages(a, false);
     a.B = B;
     a.max_q = max_q;
     a.max_k = max_k;
@@ -315,7 +339,7 @@ qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, con
     a.err = device_error_word();
     a.wait_ns = wait_limit_ns();
     a.inject = wait_inject();
-    return launch<false>(map, a, static_cast<int>(grid), static_cast<int>(blocks), static_cast<cudaStream_t>(stream));
+    return launch_expanded(map, a, static_cast<int>(grid), static_cast<int>(blocks), static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
