@@ -36,6 +36,7 @@ struct Args : pa::Args {
     int dk, dr, dv;      // channels of q; of the rotated part; of v
     int na, nb;          // 64-channel chunks of a tile: read by S alone (the rotated part; expanded form: all of K), and V's
     int sa, sb;          // stages of the rings of both (absorbed form: sb stages of both)
+    bool wide_out;       // out is 32-byte aligned
     // expanded form
     const int32_t *cu_k;
     int total_k, max_k;
@@ -227,39 +228,62 @@ __device__ __forceinline__ bool weigh(const Args &a, Row &m, uint32_t t_s, uint3
     return true;
 }
 
+// 32 bytes, 32-byte aligned.
+__device__ __forceinline__ void store32(void *p, const uint32_t (&x)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]),
+                 "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
 // A warp's rows of O: the result (whole), or a partial sum with its reference
-// and the sum of its weights.  none: no product has been made.
-__device__ __forceinline__ void store_rows(const Args &a, const Row &m, uint32_t t_o, bool none, bool live, bool whole, long long prow, long long row,
-                                           int h, int token) {
+// and the sum of its weights.  none: no product has been made.  A partial sum
+// lies as [dv / 4][128 rows][4], so that a warp's stores are whole lines
+// (as rows, 128 of them took 6 us; so 3).
+__device__ __forceinline__ void store_rows(const Args &a, const Row &m, uint32_t t_o, bool none, bool live, bool whole, long long slot, int r,
+                                           long long row, int h, int token) {
     const float l = m.sum(), ref = m.ref * a.scale_log2;
     if (live && !whole) {
-        a.pm[prow] = ref;
-        a.pl[prow] = l;
+        a.pm[slot * kRows + r] = ref;
+        a.pl[slot * kRows + r] = l;
     } else if (live && a.lse) {
         a.lse[static_cast<long long>(h) * a.total_q + token] = l == 0.0f ? -INFINITY : (log2f(l) + ref) * 0.69314718055994531f;
     }
     const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+    float *part = a.po + slot * kRows * a.dv + 4 * r;
+    const bool wide = a.wide_out;
 #pragma unroll 1
-    for (int c = 0; c < a.dv; c += 16) {
-        uint32_t o[16];
+    for (int c = 0; c < a.dv; c += 32) {
+        uint32_t o[32];
         if (none) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = 0;
+            for (int i = 0; i < 32; ++i) o[i] = 0;
         } else {
-            pa::tmem_ld16(t_o + c, o);
+            umma::tmem_ld32(t_o + c, o);
+            umma::tmem_ld_wait_regs(o);
         }
         if (!live) continue;
-        if (whole && a.out16) {
-            uint32_t y[8];
+        if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-            uint4 *dst = reinterpret_cast<uint4 *>(a.out16 + row * a.dv + c);
-            dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-            dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4 *>(part + (c / 4 + i) * (4 * kRows)) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else if (a.out16) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = bf16x2(__uint_as_float(o[16 * k + 2 * i]) * inv, __uint_as_float(o[16 * k + 2 * i + 1]) * inv);
+                uint16_t *dst = a.out16 + row * a.dv + c + 16 * k;
+                if (wide) {
+                    store32(dst, y);
+                } else {
+                    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+                }
+            }
         } else {
-            float4 *dst = reinterpret_cast<float4 *>(whole ? a.out32 + row * a.dv + c : a.po + prow * a.dv + c);
+            float4 *dst = reinterpret_cast<float4 *>(a.out32 + row * a.dv + c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i)
                 dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv, __uint_as_float(o[4 * i + 2]) * inv,
                                      __uint_as_float(o[4 * i + 3]) * inv);
         }

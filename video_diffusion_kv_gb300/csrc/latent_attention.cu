@@ -13,87 +13,140 @@ namespace {
 // Units that several CTAs shared: with references m_z, sums l_z and O_z of the
 // P parts, m = max m_z, l = sum l_z 2^(m_z - m), O likewise.  The unit that
 // begins in CTA i has its part in slot 1 of CTA i and in slot 0 of the CTAs after
-// it, up to `last`.  Each of them takes part in the join: block x, as the CTA of rank x - i, has rows
-// rank, rank + P, ..; blockIdx.y: a half of the channels.  Few parts: a warp
-// a row, part by part; many: the block's warps share a row's parts and add up
-// in their order, so the result is the same each time.  (One warp per row and
-// part after part, 152 parts of 16 rows took 48 us.)
-constexpr int kJoinWarps = 8, kFewParts = 8;
+// it.  A task is 8 rows and some channels of a unit; the unit's CTAs share its
+// tasks, as the blocks x of their numbers.  What bounds it is latency: three
+// reads that wait for one another (the unit, its parts' references and sums, its parts).
+//   few parts: a warp a task (64 channels), parts one after another;
+//   many: a block a task (16 channels), each warp every eighth part, whose sums
+//   are added in the warps' order.
+// Either way the result is the same each time.  (A warp a row, part after part: 48 us
+// for 152 parts of 16 rows.)
+constexpr int kJoinWarps = 8, kJoinY = 4, kFewParts = 8, kMostParts = 512;
+
+struct JoinRoom {
+    float w[kMostParts][8], red[2][kJoinWarps][8];
+    float4 acc[kJoinWarps][32];
+};
+
+__device__ __forceinline__ void add_weighed(float4 &a, float e, const float4 &x) {
+    if (e != 0.0f) a = make_float4(fmaf(e, x.x, a.x), fmaf(e, x.y, a.y), fmaf(e, x.z, a.z), fmaf(e, x.w, a.w));
+}
+
+// Four channels of a joined row.
+template <int DC>
+__device__ __forceinline__ void put(const la::Args &a, const la::Shared &u, int n, int c, const float4 &acc, float inv) {
+    const int gi = u.row0 + n, tq = gi / a.grp, h = gi - tq * a.grp;
+    const long long out = (static_cast<long long>(u.q0 + tq) * a.Hq + h) * DC + c;
+    const float4 x = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (a.out32)
+        *reinterpret_cast<float4 *>(a.out32 + out) = x;
+    else
+        *reinterpret_cast<uint2 *>(a.out16 + out) = make_uint2(la::bf16x2(x.x, x.y), la::bf16x2(x.z, x.w));
+}
+__device__ __forceinline__ void put_lse(const la::Args &a, const la::Shared &u, int n, float m, float l) {
+    const int gi = u.row0 + n, tq = gi / a.grp, h = gi - tq * a.grp;
+    a.lse[static_cast<long long>(h) * a.total_q + u.q0 + tq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
 
 template <int DC>
-__device__ __forceinline__ void join(const la::Args &a, const int4 u, int rank, float (*s_acc)[DC / 2], float *s_l) {
-    constexpr int E = DC / 64;  // a lane's channels: lane, lane + 32, .. of the half
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const pa::Seq s = pa::seq_of<la::kRows, la::kKeys>(a, u.x, false);
-    const int first = u.z, last = min(u.w, static_cast<int>(gridDim.x) - 1), parts = last - first + 1;
-    const bool few = parts <= kFewParts;
-    const long long row0 = static_cast<long long>(u.y) * la::kRows;
-    const int rows = static_cast<int>(max(0ll, min(static_cast<long long>(la::kRows), static_cast<long long>(s.nq) * a.grp - row0)));
-    const int step = few ? kJoinWarps : 1;
-    for (int n0 = rank; n0 < rows; n0 += parts * step) {  // (the block's warps go through this together)
-        const int n = few ? n0 + parts * warp : n0;
-        auto at = [&](int z) { return static_cast<size_t>(2 * z + (z == first ? 1 : 0)) * la::kRows + n; };
-        float acc[E], l = 0.0f, m = -INFINITY;
+__device__ __forceinline__ void join(const la::Args &a, const la::Shared &u, int rank, JoinRoom &s) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r8 = lane & 7, cg = lane >> 3;
+    const int parts = min(u.last, static_cast<int>(gridDim.x) - 1) - u.first + 1, octets = (u.rows + 7) / 8;
+    auto slot = [&](int z) { return static_cast<size_t>(2 * (u.first + z) + (z == 0 ? 1 : 0)); };
+    if (parts <= kFewParts) {
+        for (int task = rank + parts * (blockIdx.y * kJoinWarps + warp); task < octets * (DC / 64); task += parts * (kJoinY * kJoinWarps)) {
+            const int slice = task % (DC / 64), n = task / (DC / 64) * 8 + r8;
+            const float *src = a.po + (static_cast<size_t>(slice * 16 + cg) * la::kRows + n) * 4;
+            float pm[2], w[2], m = -INFINITY, l = 0.0f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-        if (n < rows) {
-            for (int z = first + lane; z <= last; z += 32)
-                if (a.pl[at(z)] != 0.0f) m = fmaxf(m, a.pm[at(z)]);
+            for (int k = 0; k < 2; ++k) {
+                const int z = 4 * k + cg;
+                pm[k] = z < parts ? a.pm[slot(z) * la::kRows + n] : -INFINITY;
+                w[k] = z < parts ? a.pl[slot(z) * la::kRows + n] : 0.0f;
+                m = fmaxf(m, pm[k]);
+            }
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            for (int k = 0; k < 2; ++k) {
+                const float e = w[k] == 0.0f ? 0.0f : exp2f(pm[k] - m);
+                l = fmaf(w[k], e, l);
+                w[k] = e;
+            }
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+            float4 acc[4] = {};
+#pragma unroll 2
+            for (int z = 0; z < parts; ++z) {
+                const float e = __shfl_sync(0xFFFFFFFFu, z < 4 ? w[0] : w[1], (z & 3) * 8 + r8);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    add_weighed(acc[i], e, *reinterpret_cast<const float4 *>(src + slot(z) * (la::kRows * DC) + i * (16 * la::kRows)));
+            }
+            if (n >= u.rows) continue;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put<DC>(a, u, n, slice * 64 + 16 * i + 4 * cg, acc[i], inv);
+            if (cg == 0 && slice == 0 && a.lse) put_lse(a, u, n, m, l);
+        }
+        return;
+    }
+    for (int task = rank + parts * blockIdx.y; task < octets * (DC / 16); task += parts * kJoinY) {
+        const int slice = task % (DC / 16), n = task / (DC / 16) * 8 + r8, z0 = tid >> 3;
+        const float *src = a.po + (static_cast<size_t>(slice * 4 + cg) * la::kRows + n) * 4;
+        float m = -INFINITY, l = 0.0f;
+        __syncthreads();  // (the last task's room has been read)
+        // thread (row r8, parts z0 + 32 k)
+        for (int z = z0; z < parts; z += 32) {
+            s.w[z][r8] = a.pm[slot(z) * la::kRows + n];
+            m = fmaxf(m, s.w[z][r8]);
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+        if (lane < 8) s.red[0][warp][r8] = m;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kJoinWarps; ++k) m = fmaxf(m, s.red[0][k][r8]);
+        for (int z = z0; z < parts; z += 32) {
+            const float lz = a.pl[slot(z) * la::kRows + n], e = lz == 0.0f ? 0.0f : exp2f(s.w[z][r8] - m);
+            l = fmaf(lz, e, l);
+            s.w[z][r8] = e;
+        }
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+        if (lane < 8) s.red[1][warp][r8] = l;
+        __syncthreads();
+        l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kJoinWarps; ++k) l += s.red[1][k][r8];
+        float4 acc = {};
 #pragma unroll 8
-            for (int z = first + (few ? 0 : warp); z <= last; z += few ? 1 : kJoinWarps) {
-                const float lz = a.pl[at(z)], w = lz == 0.0f ? 0.0f : exp2f(a.pm[at(z)] - m);
-                const float *o = a.po + at(z) * DC + blockIdx.y * (DC / 2) + lane;
-                l = fmaf(lz, w, l);
+        for (int z = warp; z < parts; z += kJoinWarps)
+            add_weighed(acc, s.w[z][r8], *reinterpret_cast<const float4 *>(src + slot(z) * (la::kRows * DC)));
+        s.acc[warp][lane] = acc;
+        __syncthreads();
+        if (warp > 0) continue;
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float x = o[32 * e];
-                    acc[e] = w == 0.0f ? acc[e] : fmaf(w, x, acc[e]);
-                }
-            }
-        }
-        if (!few) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) s_acc[warp][lane + 32 * e] = acc[e];
-            if (lane == 0) s_l[warp] = l;
-            __syncthreads();
-            if (warp == 0) {
-#pragma unroll
-                for (int w = 1; w < kJoinWarps; ++w) {
-                    l += s_l[w];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += s_acc[w][lane + 32 * e];
-                }
-            }
-            __syncthreads();
-        }
-        if (n >= rows || (!few && warp > 0)) continue;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const long long gi = row0 + n;
-        const int tq = static_cast<int>(gi / a.grp), h = static_cast<int>(gi - static_cast<long long>(tq) * a.grp);
-        const long long out = (static_cast<long long>(s.q0 + tq) * a.Hq + h) * DC + blockIdx.y * (DC / 2) + lane;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            if (a.out32)
-                a.out32[out + 32 * e] = acc[e] * inv;
-            else
-                a.out16[out + 32 * e] = f32_to_bf16(acc[e] * inv);
-        }
-        if (lane == 0 && blockIdx.y == 0 && a.lse)
-            a.lse[static_cast<long long>(h) * a.total_q + s.q0 + tq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        for (int k = 1; k < kJoinWarps; ++k) add_weighed(acc, 1.0f, s.acc[k][lane]);
+        if (n >= u.rows) continue;
+        put<DC>(a, u, n, slice * 16 + 4 * cg, acc, l == 0.0f ? 0.0f : 1.0f / l);
+        if (cg == 0 && slice == 0 && a.lse) put_lse(a, u, n, m, l);
     }
 }
 
 template <int DC>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_latent_merge(const __grid_constant__ la::Args a) {
-    __shared__ float s_acc[kJoinWarps][DC / 2], s_l[kJoinWarps];
+    __shared__ JoinRoom s;
     pdl_wait();
     const int x = blockIdx.x;
-    const int4 head = a.desc[2 * x], cut = a.desc[2 * x + 1];
-    if (head.x >= 0) join<DC>(a, head, x - head.z, s_acc, s_l);
-    if (cut.x >= 0) join<DC>(a, cut, 0, s_acc, s_l);
+    const la::Shared *d = reinterpret_cast<const la::Shared *>(a.desc) + 2 * x;
+    const la::Shared u[2] = {d[0], d[1]};
+    if (u[0].rows > 0) join<DC>(a, u[0], x - u[0].first, s);
+    if (u[1].rows > 0) join<DC>(a, u[1], 0, s);
 }
+
+// CTAs of the absorbed form: one an SM (and no unit may have more parts than the join has room for).
+int cta_count() { return std::min(sm_count_current(), kMostParts); }
 
 struct Workspace {
     size_t pm, pl, desc, bytes;  // offsets (the partial sums of O are first)
@@ -105,7 +158,7 @@ Workspace carve(int ctas, int dc) {
     w.pm = al(rows * dc * 4);
     w.pl = w.pm + al(rows * 4);
     w.desc = w.pl + al(rows * 4);
-    w.bytes = w.desc + al(static_cast<size_t>(ctas) * 2 * sizeof(int4));
+    w.bytes = w.desc + al(static_cast<size_t>(ctas) * 2 * sizeof(la::Shared));
     return w;
 }
 
@@ -167,7 +220,7 @@ qvg_status launch_expanded(const CUtensorMap (&map)[3], la::Args &a, int grid, i
 
 template <int DC>
 qvg_status launch_merge(const la::Args &a, int ctas, cudaStream_t st) {
-    const cudaError_t e = launch_pdl(k_latent_merge<DC>, dim3(ctas, 2), dim3(kJoinWarps * 32), 0, st, a);
+    const cudaError_t e = launch_pdl(k_latent_merge<DC>, dim3(ctas, kJoinY), dim3(kJoinWarps * 32), 0, st, a);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         note_cuda_error(e);
@@ -197,7 +250,7 @@ qvg_status qvg_latent_workspace_size(int32_t dc, int32_t dr, size_t *bytes) {
     const qvg_latent l{dc, dr, 16, 1, nullptr, nullptr};
     const qvg_status s = check_latent(&l, true);
     if (s != QVG_OK) return s;
-    *bytes = carve(sm_count_current(), dc).bytes;
+    *bytes = carve(cta_count(), dc).bytes;
     return QVG_OK;
 }
 
@@ -223,7 +276,7 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
     if (static_cast<int64_t>(max_q) * Hq > INT32_MAX - la::kRows ||
         static_cast<int64_t>(cache->num_pages) * cache->page_size > INT32_MAX)
         return QVG_ERR_UNSUPPORTED;
-    const int ctas = sm_count_current();
+    const int ctas = cta_count();
     const Workspace w = carve(ctas, dc);
     if (!workspace || ws_bytes < w.bytes || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return QVG_ERR_WORKSPACE;
     const int64_t slots = static_cast<int64_t>(cache->num_pages) * cache->page_size;
@@ -264,6 +317,7 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
     a.out32 = out_dtype == QVG_OUT_F32 ? static_cast<float *>(out) : nullptr;
     a.out16 = out_dtype == QVG_OUT_BF16 ? static_cast<uint16_t *>(out) : nullptr;
     a.lse = lse;
+    a.wide_out = reinterpret_cast<uintptr_t>(out) % 32 == 0;
     char *base = static_cast<char *>(workspace);
     a.po = reinterpret_cast<float *>(base);
     a.pm = reinterpret_cast<float *>(base + w.pm);
@@ -336,6 +390,7 @@ qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, con
     a.out32 = out_dtype == QVG_OUT_F32 ? static_cast<float *>(out) : nullptr;
     a.out16 = out_dtype == QVG_OUT_BF16 ? static_cast<uint16_t *>(out) : nullptr;
     a.lse = lse;
+    a.wide_out = reinterpret_cast<uintptr_t>(out) % 32 == 0;
     a.err = device_error_word();
     a.wait_ns = wait_limit_ns();
     a.inject = wait_inject();

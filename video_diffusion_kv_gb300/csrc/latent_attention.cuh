@@ -25,6 +25,12 @@ namespace la {
 
 constexpr int kLatentWarps = 13;
 
+// A unit of which a CTA has a part: the CTAs that share it, its rows (0: there
+// is none), the first of them among the sequence's rows, the sequence's first token.
+struct __align__(16) Shared {
+    int first = 0, last = 0, rows = 0, row0 = 0, q0 = 0, pad[3] = {0, 0, 0};
+};
+
 // cmap: latents; rmap: rotated key parts.
 __global__ void __launch_bounds__(kLatentWarps * 32, 1)
     k_latent_attention(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap rmap, const __grid_constant__ Args a) {
@@ -38,6 +44,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
     __shared__ uint32_t tmem_base;
     __shared__ int fail, issued[2];  // tiles whose copies each loading warp has issued
 
+    pdl_trigger();  // the join's blocks may take the places of CTAs that are done (they wait for all of them)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x;
     uint8_t *base = dyn + ((1024u - (umma::smem_u32(dyn) & 1023u)) & 1023u);
@@ -136,10 +143,8 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             umma::tc_fence_after();
-            const int slot = cta * 2 + (g.t0 > 0 ? 0 : 1);
             if (!idle)
-                store_rows(a, m, t_o, false, live, g.whole(), static_cast<long long>(slot) * kRows + tid,
-                           static_cast<long long>(g.q0 + tq) * a.Hq + h, h, g.q0 + tq);
+                store_rows(a, m, t_o, false, live, g.whole(), cta * 2 + (g.t0 > 0 ? 0 : 1), tid, static_cast<long long>(g.q0 + tq) * a.Hq + h, h, g.q0 + tq);
             umma::tc_fence_before();
         }
     } else if (warp < W0 + 4) {
@@ -242,6 +247,8 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
                 const int now = first_of(t, page);
                 page = page_of(t + 1);
                 if (it >= a.sb) ok = wait(&empty[rg.i], rg.parity ^ 1u);
+                // (the first Q would wait behind all CTAs' first stages: it is there before the third one is asked for)
+                if (it == 2) ok = ok && wait(&q_full, 0);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 uint64_t *bar = &full[rg.i];
@@ -352,14 +359,20 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
     } else {
         // ---- this CTA's part of the line, unit by unit ---------------------------------------------------
         pa::Line<kRows, kKeys> line(a, reinterpret_cast<long long *>(base));  // (Q's place: no segment is out yet)
-        int4 head = make_int4(-1, 0, 0, 0);  // the unit that this CTA goes on with: sequence, block, its first CTA and its last
+        Shared shared[2];  // the unit that this CTA goes on with, and the one that begins here and goes on
         bool ok = true;
         for (int n_seg = 0; ok; ++n_seg) {
             pa::Segment g;
             const long long at = line.pos;
             line.next(a, g);
-            if (n_seg == 0 && g.t1 > 0 && g.t0 > 0)
-                head = make_int4(g.b, g.r, static_cast<int>((at - g.t0) / line.per), static_cast<int>((at - g.t0 + g.nt - 1) / line.per));
+            if (g.t1 > 0 && !g.whole() && (g.t0 == 0 || n_seg == 0)) {
+                Shared &x = shared[g.t0 == 0 ? 1 : 0];
+                x.first = static_cast<int>((at - g.t0) / line.per);
+                x.last = static_cast<int>((at - g.t0 + g.nt - 1) / line.per);
+                x.row0 = g.r * kRows;
+                x.rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(g.nq) * a.grp - x.row0));
+                x.q0 = g.q0;
+            }
             const int i = n_seg & (pa::kRing - 1);
             if (n_seg >= pa::kRing) ok = wait(&seg_free[i], ((n_seg / pa::kRing) - 1) & 1);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -371,9 +384,10 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
             if (g.t1 == 0) break;
         }
         if (lane == 0) {
-            const int4 cut = line.cut;
-            a.desc[2 * cta] = ok ? head : make_int4(-1, 0, 0, 0);
-            a.desc[2 * cta + 1] = ok && cut.x >= 0 ? make_int4(cut.x, cut.z, cta, cut.w) : make_int4(-1, 0, 0, 0);
+            if (!ok) shared[0].rows = shared[1].rows = 0;
+            Shared *d = reinterpret_cast<Shared *>(a.desc);
+            d[2 * cta] = shared[0];
+            d[2 * cta + 1] = shared[1];
         }
     }
     __syncwarp();
