@@ -8,8 +8,8 @@
 // at its softmax.
 //
 // Tensor memory: O 2 x 128 columns, S 2 x 128.
-// Roles: softmax (8 warps, thread = row), helpers (4: Q, and V in tiles that
-// some row does not see all of), loads of K, of V, and each group's products.
+// Roles: softmax (8 warps, thread = row), helpers (4: V in tiles that some row
+// does not see all of), loads of Q and K, of V, and each group's products.
 #pragma once
 
 #include "bf16_attention.cuh"
@@ -59,13 +59,14 @@ __device__ __forceinline__ Unit unit_of(const Args &a, int blocks) {
     return u;
 }
 
-// kmap: k; rmap: the rotated key parts; vmap: v.
+// qmap, rqmap: q and its rotated part; kmap, rkmap: k and the rotated key parts; vmap: v.
 __global__ void __launch_bounds__(kPromptWarps * 32, 1)
-    k_expanded_attention(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap rmap,
+    k_expanded_attention(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap rqmap,
+                         const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap rkmap,
                          const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a, int blocks) {
     extern __shared__ uint8_t dyn[];
     __shared__ uint64_t a_full[kMostStages], a_empty[kMostStages], b_full[kMostStages], b_empty[kMostStages], fixed[kFix];
-    __shared__ uint64_t s_full[2], p_full[2][2], o_done[2][2], q_full, drain, never;
+    __shared__ uint64_t s_full[2], p_full[2][2], o_done[2][2], q_full[2], drain, never;
     __shared__ uint4 s_bad[kFix];  // marked keys of a tile: key 16 w + i at bit 2 i of word w
     __shared__ uint32_t tmem_base;
     __shared__ int fail, issued[2];  // tiles of K and of V whose copies have been issued
@@ -89,12 +90,12 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
         for (int i = 0; i < kFix; ++i) umma::mbar_init(&fixed[i], 4);
         for (int g = 0; g < 2; ++g) {
             umma::mbar_init(&s_full[g], 1);
+            umma::mbar_init(&q_full[g], 1);
             for (int i = 0; i < 2; ++i) {
                 umma::mbar_init(&p_full[g][i], 4);
                 umma::mbar_init(&o_done[g][i], 1);
             }
         }
-        umma::mbar_init(&q_full, 4);
         umma::mbar_init(&drain, 2);
         umma::mbar_init(&never, 1);
         umma::fence_barrier_init();
@@ -153,23 +154,8 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
             if (!idle) store_rows(a, m, t_o, end == 0, live, true, 0, 0, static_cast<long long>(u.q0 + tq) * a.Hq + u.h, u.h, u.q0 + tq);
         }
     } else if (warp < 12) {
-        // ---- helpers: Q, and V where some row does not see all of it ---------------------------------
-        const int w = tid - 256, piece = w & 7, plain = a.dk / 64;  // chunks before the rotated part's
-        for (int i = w >> 3; i < kPromptRows; i += 16) {
-            const int tq = u.r * kPromptRows + i, row = i & (kRows - 1);
-            if (tq >= u.nq) break;  // (rows that are left out keep what is there: no other row reads them)
-            const uint16_t *q = a.q + (u.q0 + tq) * a.q_stride + u.h * a.q_h + piece * 8;
-            const uint16_t *qr = a.qr + (u.q0 + tq) * a.qr_t + u.h * a.qr_h + piece * 8;
-            uint8_t *dst = base + (i >> 7) * q_group + row * 128 + ((piece ^ (row & 7)) << 4);
-            for (int c = 0; c < a.na; ++c) {
-                const bool in = c < plain || piece * 8 < a.dr;
-                umma::cp_async16(dst + c * kQChunk, !in ? a.q : c < plain ? q + c * 64 : qr, in);
-            }
-        }
-        umma::cp_async_wait_all();
-        umma::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) umma::mbar_arrive(&q_full);
+        // ---- helpers: V where some row does not see all of it ----------------------------------------------
+        const int w = tid - 256;
         Ring rb;
         int n_fix = 0;
         for (int t = 0; t < most; ++t, rb.next(a.sb)) {
@@ -189,8 +175,17 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
             if (lane == 0) umma::mbar_arrive(&b_empty[rb.i]);
         }
     } else if (warp == 12) {
-        // ---- loads of K: a copy for its channels, one for the rotated part ------------------------------
+        // ---- loads of Q and K: a copy for the channels, one for the rotated part -------------------------
+        // (rows of Q past the sequence's are another one's, or 0; their results go nowhere)
         const bool one = elected();
+        auto load_q = [&](int grp) {
+            const int first = u.r * kPromptRows + grp * kRows;
+            if (!one || u.nt[grp] == 0) return;
+            umma::mbar_arrive_expect_tx(&q_full[grp], q_group);
+            tma_load_4d(sm + grp * q_group, &qmap, 0, u.q0 + first, 0, u.h, &q_full[grp]);
+            if (a.dr > 0) tma_load_3d(sm + grp * q_group + (a.na - 1) * kQChunk, &rqmap, 0, u.q0 + first, u.h, &q_full[grp]);
+        };
+        load_q(0);
         Ring ra;
         for (int d = 0; 2 * d < most; ++d, ra.next(a.sa)) {
             if (d >= a.sa) ok = wait(&a_empty[ra.i], ra.parity ^ 1u);
@@ -201,9 +196,10 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
             if (one) {
                 umma::mbar_arrive_expect_tx(&a_full[ra.i], a_bytes);
                 tma_load_4d(dst, &kmap, 0, at, 0, u.h, &a_full[ra.i]);
-                if (a.dr > 0) tma_load_2d(dst + (a.na - 1) * kKChunk, &rmap, 0, at, &a_full[ra.i]);
+                if (a.dr > 0) tma_load_2d(dst + (a.na - 1) * kKChunk, &rkmap, 0, at, &a_full[ra.i]);
                 issued[0] = d + 1;
             }
+            if (d == 0) load_q(1);
             __syncwarp();
         }
     } else if (warp == 13) {
@@ -231,7 +227,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
         const int steps_r = (a.dr + 15) / 16;
         Ring ra, rb;
         int n_fix = 0;
-        ok = wait(&q_full, 0);
+        if (mine > 0) ok = wait(&q_full[grp], 0);
         // the groups out of step: group 1 begins once group 0 is at its softmax
         if (grp == 1 && u.nt[0] > 0) ok = ok && wait(&p_full[0][0], 0);
         for (int d = 0; 2 * d < most; ++d, ra.next(a.sa)) {
@@ -291,7 +287,9 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
     __syncthreads();
     if (tid == 0 && *vfail) {
         raise_error(a.err, QVG_ERR_TIMEOUT);
-        // the copies in flight land before the CTA ends
+        // the copies in flight land before the CTA ends (Q's are issued with K's first)
+        for (int g = 0; g < 2; ++g)
+            if (u.nt[g] > 0) umma::mbar_wait(&q_full[g], 0, pa::kDrainNs);
         for (int j = max(0, issued[0] - a.sa); j < issued[0]; ++j) umma::mbar_wait(&a_full[j % a.sa], (j / a.sa) & 1, pa::kDrainNs);
         for (int j = max(0, issued[1] - a.sb); j < issued[1]; ++j) umma::mbar_wait(&b_full[j % a.sb], (j / a.sb) & 1, pa::kDrainNs);
     }

@@ -180,17 +180,19 @@ bool chunk_map(CUtensorMap *m, const void *data, int channels, int heads, int64_
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The rotated part, bf16 [rows][channels]; a box is 64 channels of `box` rows,
-// channels beyond the last are filled with 0.
-bool rotated_map(CUtensorMap *m, const void *data, int channels, int64_t rows, int64_t row_stride, int box) {
+// A rotated part, bf16 [rows][channels] (heads > 0: [rows][heads][channels]); a
+// box is 64 channels of `box` rows (of one head), channels beyond the last are
+// filled with 0.
+bool rotated_map(CUtensorMap *m, const void *data, int channels, int heads, int64_t rows, int64_t head_stride, int64_t row_stride, int box) {
     const auto fn = tensor_map_encoder();
     if (!fn) return false;
     if (rows == 1) row_stride = 64;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(channels), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * row_stride)};
-    const cuuint32_t boxes[2] = {64, static_cast<cuuint32_t>(box)};
-    const cuuint32_t es[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(data), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    if (heads == 1) head_stride = 64;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(channels), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * row_stride), static_cast<cuuint64_t>(2 * head_stride)};
+    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(box), 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, heads > 0 ? 3 : 2, const_cast<void *>(data), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -205,7 +207,7 @@ qvg_status launch_latent(const CUtensorMap (&map)[2], la::Args &a, int ctas, cud
     return QVG_OK;
 }
 
-qvg_status launch_expanded(const CUtensorMap (&map)[3], la::Args &a, int grid, int blocks, cudaStream_t st) {
+qvg_status launch_expanded(const CUtensorMap (&map)[5], la::Args &a, int grid, int blocks, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const qvg_status s = smem_limit_once(done, reinterpret_cast<const void *>(la::k_expanded_attention), la::kSmem);
     if (s != QVG_OK) return s;
@@ -213,7 +215,7 @@ qvg_status launch_expanded(const CUtensorMap (&map)[3], la::Args &a, int grid, i
     const int room = la::kSmem - 1024 - 2 * a.na * la::kQChunk, A = a.na * la::kKChunk, B = a.nb * la::kChunk;
     a.sb = std::min(la::kMostStages, (room - 2 * A) / B);
     a.sa = std::min(la::kMostStages, (room - a.sb * B) / A);
-    la::k_expanded_attention<<<grid, la::kPromptWarps * 32, la::kSmem, st>>>(map[0], map[1], map[2], a, blocks);
+    la::k_expanded_attention<<<grid, la::kPromptWarps * 32, la::kSmem, st>>>(map[0], map[1], map[2], map[3], map[4], a, blocks);
     QVG_LAUNCH_CHECK();
     return QVG_OK;
 }
@@ -284,7 +286,7 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
     CUtensorMap map[2] = {};
     // (a page that holds a whole tile is copied in one go, a smaller one chunk by chunk)
     if (!chunk_map(&map[0], cache->c, dc, 0, slots, 0, dc, box, box == la::kKeys ? dc / 64 : 1) ||
-        (dr > 0 && !rotated_map(&map[1], cache->kr, dr, slots, dr, box)))
+        (dr > 0 && !rotated_map(&map[1], cache->kr, dr, 0, slots, 0, dr, box)))
         return QVG_ERR_CUDA;
     la::Args a{};
     a.q = static_cast<const uint16_t *>(q->data);
@@ -357,20 +359,14 @@ qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, con
         return QVG_ERR_INVALID_ARG;
     const int64_t blocks = ceil_div(max_q, 256), grid = blocks * B * H;
     if (max_q > INT32_MAX - 256 || static_cast<int64_t>(B) * H > INT32_MAX || grid > INT32_MAX) return QVG_ERR_UNSUPPORTED;
-    CUtensorMap map[3] = {};
-    if (total_k > 0 && (!chunk_map(&map[0], k->data, dn, H, total_k, k->head_stride, k->token_stride, la::kPromptKeys, dn / 64) ||
-                        (dr > 0 && !rotated_map(&map[1], k_rope->data, dr, total_k, k_rope->token_stride, la::kPromptKeys)) ||
-                        !chunk_map(&map[2], v->data, dv, H, total_k, v->head_stride, v->token_stride, la::kKeys, dv / 64)))
+    CUtensorMap map[5] = {};
+    if (!chunk_map(&map[0], q->data, dn, H, total_q, q->head_stride, q->token_stride, la::kRows, dn / 64) ||
+        (dr > 0 && !rotated_map(&map[1], q_rope->data, dr, H, total_q, q_rope->head_stride, q_rope->token_stride, la::kRows)) ||
+        (total_k > 0 && (!chunk_map(&map[2], k->data, dn, H, total_k, k->head_stride, k->token_stride, la::kPromptKeys, dn / 64) ||
+                         (dr > 0 && !rotated_map(&map[3], k_rope->data, dr, 0, total_k, 0, k_rope->token_stride, la::kPromptKeys)) ||
+                         !chunk_map(&map[4], v->data, dv, H, total_k, v->head_stride, v->token_stride, la::kKeys, dv / 64))))
         return QVG_ERR_CUDA;
     la::Args a{};
-    a.q = static_cast<const uint16_t *>(q->data);
-    a.q_stride = q->token_stride;
-    a.q_h = q->head_stride;
-    if (dr > 0) {
-        a.qr = static_cast<const uint16_t *>(q_rope->data);
-        a.qr_t = q_rope->token_stride;
-        a.qr_h = q_rope->head_stride;
-    }
     a.total_q = total_q;
     a.total_k = total_k;
     a.Hq = a.H = H;

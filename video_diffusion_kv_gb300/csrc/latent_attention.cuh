@@ -4,7 +4,7 @@
 // A query row is a (new token, query head) pair.  All heads read the same
 // latents, so a unit of work is 128 rows of one sequence, and a tile's 64 keys
 // are loaded once for both products: as K, and read across (MN-major) as V.  All
-// units' tiles form one line that is cut into equal parts, one per CTA (pa::Line);
+// units' tiles form one line that is cut into equal parts, one per CTA;
 // a unit cut by a border leaves fp32 partial sums that k_latent_merge joins.
 //
 // Q's latent part is the A operand in tensor memory, where it costs shared
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
         }
         umma::fence_barrier_init();
     }
-    if (warp == WARPS - 1) {
+    if (warp == W0 + 7) {
         umma::tmem_alloc(&tmem_base, 512);
         umma::tmem_relinquish();
     }
@@ -358,31 +358,79 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
         __syncwarp();
     } else {
         // ---- this CTA's part of the line, unit by unit ---------------------------------------------------
-        pa::Line<kRows, kKeys> line(a, reinterpret_cast<long long *>(base));  // (Q's place: no segment is out yet)
+        // One pass over the sequences for the line's length, then a walk from the sequence that holds the part's begin; 32
+        // sequences at a time, a lane each.  (Code that runs once costs its instructions' way from L2, in a chain: this
+        // loop in half the instructions gets the first tile going 2 us earlier.)
         Shared shared[2];  // the unit that this CTA goes on with, and the one that begins here and goes on
-        bool ok = true;
-        for (int n_seg = 0; ok; ++n_seg) {
-            pa::Segment g;
-            const long long at = line.pos;
-            line.next(a, g);
-            if (g.t1 > 0 && !g.whole() && (g.t0 == 0 || n_seg == 0)) {
-                Shared &x = shared[g.t0 == 0 ? 1 : 0];
-                x.first = static_cast<int>((at - g.t0) / line.per);
-                x.last = static_cast<int>((at - g.t0 + g.nt - 1) / line.per);
-                x.row0 = g.r * kRows;
-                x.rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(g.nq) * a.grp - x.row0));
-                x.q0 = g.q0;
-            }
+        bool ok = true, counting = true;
+        uint32_t total = 0, first = 0, per = 1, pos = 0, end = 0;
+        int n_seg = 0;
+        auto publish = [&](const pa::Segment &g) {
             const int i = n_seg & (pa::kRing - 1);
             if (n_seg >= pa::kRing) ok = wait(&seg_free[i], ((n_seg / pa::kRing) - 1) & 1);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            if (lane == 0) {
+            if (lane == 0 && ok) {
                 s_seg[i] = g;
                 umma::mbar_arrive(&seg_full[i]);
             }
-            if (g.t1 == 0) break;
+            ++n_seg;
+        };
+        for (int b0 = 0; ok && b0 < a.B;) {
+            pa::Seq q{};
+            uint32_t w = 0;
+            if (b0 + lane < a.B) {
+                q = pa::seq_of<kRows, kKeys>(a, b0 + lane, counting && cta == 0);
+                w = static_cast<uint32_t>(q.rb) * static_cast<uint32_t>(q.nt);
+            }
+            uint32_t x = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                if (lane >= o) x += y;
+            }
+            const uint32_t all = __shfl_sync(0xFFFFFFFFu, x, 31);
+            if (counting) {
+                if (total + all < total && lane == 0) raise_error(a.err, QVG_ERR_INVALID_ARG);
+                total += all;
+                b0 += 32;
+                if (b0 < a.B) continue;
+                counting = false;
+                per = max(1u, (total - 1) / gridDim.x + 1);
+                pos = static_cast<uint32_t>(min(static_cast<uint64_t>(total), static_cast<uint64_t>(cta) * per));
+                end = total - pos > per ? pos + per : total;
+                b0 = 0;
+                if (a.B > 32) continue;
+            }
+            while (ok && pos < end && pos - first < all) {
+                const int l = __ffs(__ballot_sync(0xFFFFFFFFu, pos - first < x)) - 1;  // (the first sequence that ends behind pos)
+                pa::Segment g;
+                g.b = b0 + l;
+                g.h = 0;
+                g.q0 = __shfl_sync(0xFFFFFFFFu, q.q0, l);
+                g.nq = __shfl_sync(0xFFFFFFFFu, q.nq, l);
+                g.kv = __shfl_sync(0xFFFFFFFFu, q.kv, l);
+                g.nt = __shfl_sync(0xFFFFFFFFu, q.nt, l);
+                const uint32_t rel = pos - first - (__shfl_sync(0xFFFFFFFFu, x, l) - __shfl_sync(0xFFFFFFFFu, w, l));
+                g.r = static_cast<int>(rel / static_cast<uint32_t>(g.nt));
+                g.t0 = static_cast<int>(rel) - g.r * g.nt;
+                g.t1 = static_cast<int>(min(static_cast<uint32_t>(g.nt), g.t0 + (end - pos)));
+                publish(g);
+                if (!g.whole() && (g.t0 == 0 || n_seg == 1)) {
+                    Shared &d = shared[g.t0 == 0 ? 1 : 0];
+                    d.first = static_cast<int>((pos - g.t0) / per);
+                    d.last = static_cast<int>((pos - g.t0 + g.nt - 1) / per);
+                    d.row0 = g.r * kRows;
+                    d.rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(g.nq) * a.grp - d.row0));
+                    d.q0 = g.q0;
+                }
+                pos += g.t1 - g.t0;
+            }
+            if (pos >= end) break;
+            first += all;
+            b0 += 32;
         }
+        pa::Segment none{};
+        if (ok) publish(none);
         if (lane == 0) {
             if (!ok) shared[0].rows = shared[1].rows = 0;
             Shared *d = reinterpret_cast<Shared *>(a.desc);
@@ -400,7 +448,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
         for (int j = lo; j < hi; ++j) umma::mbar_arrive(&full[j % a.sb]);
         for (int j = max(0, hi - a.sb); j < hi; ++j) umma::mbar_wait(&full[j % a.sb], (j / a.sb) & 1, pa::kDrainNs);
     }
-    if (warp == WARPS - 1) {
+    if (warp == W0 + 7) {
         umma::tc_fence_after();
         umma::tmem_dealloc(tmem, 512);
     }

@@ -329,61 +329,103 @@ __global__ void __launch_bounds__(kCopyThreads) k_pages_copy(const __grid_consta
 // ---- compact ----------------------------------------------------------------------
 
 constexpr int kMoveThreads = 256, kMoveEach = 8;
-constexpr int kSlice = 128;  // bytes of a row that one block moves
 
 struct Move {
     const int32_t *table, *first, *keep, *n_keep;
     long long table_stride, keep_stride;
+    int slice;    // bytes of a row that one block moves, at most
     int jobs[4];  // blocks up to this buffer's end, of a sequence
 };
 
-// A block moves one slice (up to 128 bytes of a head's rows) of one sequence's
-// tokens, in order, a batch at a time: the batch is read, then written.  A token
-// only moves down (keep ascends from `first` on), so what a batch writes over
-// has been read in this batch or an earlier one, and the slices do not touch one
-// another.
+// Slots of a batch's kept tokens, from and to (-1: the token stays), three batches deep.
+struct Slots {
+    long long from[3][kMoveThreads], to[3][kMoveThreads];
+};
+
+// A block moves one slice of a head's rows of one sequence's tokens, in order, a
+// batch of 256 pieces of `width` threads at a time: the batch is read, then
+// written.  A token only moves down (keep ascends from `first` on), so what a
+// batch writes over has been read in this batch or an earlier one, never is to be
+// read in a later one, and the slices do not touch one another.
+//   Reads run ahead: while a batch is written the next one's bytes and the slots
+// of the one after that are on their way (bytes after their slots, slots after their
+// tokens, one batch after the other, it was 262 us where this takes 57).
+// Bound by HBM.
 template <typename T>
-__device__ __forceinline__ void move_rows(const Buffers &a, const Move &m, int b, int i, int h, int col, int width, int n) {
+__device__ __forceinline__ void move_rows(const Buffers &a, const Move &m, Slots &s, int b, int i, int h, int col, int width, int n) {
     const int per = kMoveThreads / width;  // rows side by side
     const int r = threadIdx.x / width, w = threadIdx.x - r * width;
+    const int each = min(kMoveEach, width);  // a batch is at most 256 rows
+    const int rows = per * each;
     const int32_t *row = m.table + b * m.table_stride, *keep = m.keep + b * m.keep_stride;
-    const int first = m.first[b], mask = (1 << a.page_log2) - 1;
-    auto at = [&](int token) {
-        const long long page = row[token >> a.page_log2];
-        return a.base[i] + (((page * a.heads[i] + h) << a.page_log2) + (token & mask)) * a.row_bytes[i] + col + w * static_cast<int>(sizeof(T));
-    };
-    for (int k0 = 0; k0 < n; k0 += per * kMoveEach) {
-        T v[kMoveEach];
-        uint8_t *to[kMoveEach];
-#pragma unroll
-        for (int e = 0; e < kMoveEach; ++e) {
-            const int k = k0 + e * per + r;
-            to[e] = nullptr;
-            if (r < per && k < n && keep[k] != first + k) {
-                v[e] = *reinterpret_cast<const T *>(at(keep[k]));
-                to[e] = at(first + k);
+    const int first = m.first[b], mask = (1 << a.page_log2) - 1, rb = a.row_bytes[i];
+    const long long skip = (static_cast<long long>(a.heads[i]) - 1) << a.page_log2, lift = static_cast<long long>(h) << a.page_log2;
+    uint8_t *const base = a.base[i] + col + w * static_cast<int>(sizeof(T));
+    auto slots = [&](int batch) {  // of kept token batch * rows + threadIdx.x
+        const int k = batch * rows + threadIdx.x, e = batch % 3;
+        if (threadIdx.x >= rows) return;
+        long long from = -1, to = -1;
+        if (k < n) {
+            const int x = keep[k], y = first + k;
+            if (x != y) {
+                from = (static_cast<long long>(row[x >> a.page_log2]) << a.page_log2) + (x & mask);
+                to = (static_cast<long long>(row[y >> a.page_log2]) << a.page_log2) + (y & mask);
             }
         }
-        __syncthreads();
+        s.from[e][threadIdx.x] = from;
+        s.to[e][threadIdx.x] = to;
+    };
+    // row (page, head, offset) of a slot
+    auto at = [&](long long slot) { return base + (slot + (slot >> a.page_log2) * skip + lift) * rb; };
+    T v[2][kMoveEach];
+    auto read = [&](int batch, T(&x)[kMoveEach]) {
 #pragma unroll
         for (int e = 0; e < kMoveEach; ++e)
-            if (to[e]) *reinterpret_cast<T *>(to[e]) = v[e];
+            if (e < each && r < per) {
+                const long long f = s.from[batch % 3][e * per + r];
+                if (f >= 0) x[e] = *reinterpret_cast<const T *>(at(f));
+            }
+    };
+    auto write = [&](int batch, const T(&x)[kMoveEach]) {
+#pragma unroll
+        for (int e = 0; e < kMoveEach; ++e)
+            if (e < each && r < per) {
+                const long long t = s.to[batch % 3][e * per + r];
+                if (t >= 0) *reinterpret_cast<T *>(at(t)) = x[e];
+            }
+    };
+    const int batches = (n + rows - 1) / rows;
+    slots(0);
+    slots(1);
+    __syncthreads();
+    read(0, v[0]);
+    for (int j = 0; j < batches; j += 2) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            if (j + p >= batches) break;
+            read(j + p + 1, v[p ^ 1]);  // (past the end: its slots are -1)
+            slots(j + p + 2);
+            __syncthreads();  // the batch has been read by all; the slots are there
+            write(j + p, v[p]);
+            __syncthreads();  // (its slots' place is the next batch's but two)
+        }
     }
 }
 
 __global__ void __launch_bounds__(kMoveThreads) k_paged_compact(const __grid_constant__ Buffers a, const __grid_constant__ Move m) {
+    __shared__ Slots s;
     const int b = blockIdx.y, n = m.n_keep[b], first = m.first[b];
     bool bad = n < 0 || n > m.keep_stride || first < 0;
     if (!bad) {
         const int32_t *row = m.table + b * m.table_stride, *keep = m.keep + b * m.keep_stride;
         const long long room = m.table_stride << a.page_log2;
-        for (int k = threadIdx.x; k < n && !bad; k += kMoveThreads) {
+#pragma unroll 4
+        for (int k = threadIdx.x; k < n; k += kMoveThreads) {
             const int x = keep[k];
-            bad = x < (k ? keep[k - 1] + 1ll : static_cast<long long>(first)) || x >= room || x < first;
-            if (!bad) {  // (ascending up to here or refused elsewhere: first + k may pass x only then)
-                const int p = row[x >> a.page_log2], to = first + k <= x ? row[(first + k) >> a.page_log2] : 0;
-                bad = p < 0 || p >= a.num_pages || to < 0 || to >= a.num_pages;
-            }
+            const bool off = x < (k ? keep[k - 1] + 1ll : static_cast<long long>(first)) || x >= room || x < first;
+            // (where keep ascends, first + k does not pass x)
+            const int p = off ? -1 : row[x >> a.page_log2], to = off || first + k > x ? 0 : row[(first + k) >> a.page_log2];
+            bad = bad || p < 0 || p >= a.num_pages || to < 0 || to >= a.num_pages;
         }
     }
     if (__syncthreads_or(bad)) {
@@ -394,14 +436,14 @@ __global__ void __launch_bounds__(kMoveThreads) k_paged_compact(const __grid_con
     while (static_cast<int>(blockIdx.x) >= m.jobs[i]) ++i;
     const int job = blockIdx.x - (i ? m.jobs[i - 1] : 0), rb = a.row_bytes[i];
     if (rb >= 16) {
-        const int slices = (rb + kSlice - 1) / kSlice, h = job / slices, col = (job - h * slices) * kSlice;
-        move_rows<uint4>(a, m, b, i, h, col, min(kSlice, rb - col) / 16, n);
+        const int slices = (rb + m.slice - 1) / m.slice, h = job / slices, col = (job - h * slices) * m.slice;
+        move_rows<uint4>(a, m, s, b, i, h, col, min(m.slice, rb - col) / 16, n);
     } else if (rb == 4) {
-        move_rows<uint32_t>(a, m, b, i, job, 0, 1, n);
+        move_rows<uint32_t>(a, m, s, b, i, job, 0, 1, n);
     } else if (rb == 2) {
-        move_rows<uint16_t>(a, m, b, i, job, 0, 1, n);
+        move_rows<uint16_t>(a, m, s, b, i, job, 0, 1, n);
     } else {
-        move_rows<uint8_t>(a, m, b, i, job, 0, 1, n);
+        move_rows<uint8_t>(a, m, s, b, i, job, 0, 1, n);
     }
 }
 
@@ -598,11 +640,16 @@ qvg_status qvg_paged_compact(const qvg_page_rows *rows, const int32_t *table, in
     m.n_keep = n_keep;
     m.table_stride = table_stride;
     m.keep_stride = keep_stride;
+    // Slices of 128 bytes, or down to 32 where those are fewer blocks than two an SM.
     int64_t jobs = 0;
-    for (int i = 0; i < a.n; ++i) {
-        jobs += static_cast<int64_t>(a.heads[i]) * ceil_div(a.row_bytes[i], kSlice);
-        if (jobs > INT32_MAX) return QVG_ERR_UNSUPPORTED;
-        m.jobs[i] = static_cast<int>(jobs);
+    for (m.slice = 128;; m.slice /= 2) {
+        jobs = 0;
+        for (int i = 0; i < a.n; ++i) {
+            jobs += static_cast<int64_t>(a.heads[i]) * ceil_div(a.row_bytes[i], m.slice);
+            if (jobs > INT32_MAX) return QVG_ERR_UNSUPPORTED;
+            m.jobs[i] = static_cast<int>(jobs);
+        }
+        if (m.slice == 32 || jobs * B >= 2 * sm_count_current()) break;
     }
     k_paged_compact<<<dim3(static_cast<unsigned>(jobs), B), kMoveThreads, 0, static_cast<cudaStream_t>(stream)>>>(a, m);
     QVG_LAUNCH_CHECK();
