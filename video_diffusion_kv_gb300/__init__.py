@@ -683,6 +683,24 @@ def paged_attention(cache: PagedKV, q, block_table, kv_len, max_q, cu_q=None, ma
     return out, lse
 
 
+def _off(t, dtype, dev):
+    """Whether a tensor is not what a call wants of it (_on says what is wrong,
+    and takes longer)."""
+    return t.dtype != dtype or t.device != dev or not t.is_contiguous()
+
+
+def _call(dev, where, function, stream, *args):
+    """A library call on `stream` with `dev` as the current device."""
+    import torch
+    if dev.type == "cuda" and torch._C._cuda_getDevice() == dev.index:
+        status = function(*args, _raw_stream(stream, dev))
+    else:
+        with _Device(dev):
+            status = function(*args, _raw_stream(stream, dev))
+    if status != QVG_OK:
+        _check(status, where)
+
+
 def latent_bytes(dc, dr, page_size, num_pages):
     """(latents, key parts) bytes of a latent cache's two buffers."""
     a, b = ct.c_size_t(0), ct.c_size_t(0)
@@ -746,14 +764,12 @@ def latent_append(cache: LatentKV, c, k_rope, slots, plan=None, positions=None, 
         ks = _rows2(k_rope, cache.dr, cache.device, "latent_append", "k_rope")
     if c.shape[0] != n or (cache.dr and k_rope.shape[0] != n):
         raise ValueError("latent_append: c, k_rope and slots must be of as many tokens")
-    _on(cache.device, "latent_append", slots=(slots, torch.int64), positions=(positions, torch.int32))
+    if _off(slots, torch.int64, cache.device) or (positions is not None and _off(positions, torch.int32, cache.device)):
+        _on(cache.device, "latent_append", slots=(slots, torch.int64), positions=(positions, torch.int32))
     if plan is not None:
         _positions(plan, positions, n, "latent_append")
-    with _Device(cache.device):
-        _check(lib().qvg_latent_append(cache._ref, c.data_ptr(), k_rope.data_ptr() if cache.dr else None, n, cs, ks,
-                                       slots.data_ptr(), None if plan is None else plan._ref,
-                                       None if plan is None else positions.data_ptr(), _raw_stream(stream, cache.device)),
-               "qvg_latent_append")
+    _call(cache.device, "qvg_latent_append", lib().qvg_latent_append, stream, cache._ref, c.data_ptr(), k_rope.data_ptr() if cache.dr else None, n,
+          cs, ks, slots.data_ptr(), None if plan is None else plan._ref, None if plan is None else positions.data_ptr())
 
 
 def latent_read(cache: LatentKV, slots, c_out=None, kr_out=None, stream=None):
@@ -766,9 +782,8 @@ def latent_read(cache: LatentKV, slots, c_out=None, kr_out=None, stream=None):
     if c_out.shape != (n, cache.dc) or kr_out.shape != (n, cache.dr):
         raise ValueError("latent_read: outputs must be [n, %d] and [n, %d]" % (cache.dc, cache.dr))
     _on(cache.device, "latent_read", slots=(slots, torch.int64), c_out=(c_out, torch.bfloat16), kr_out=(kr_out, torch.bfloat16))
-    with _Device(cache.device):
-        _check(lib().qvg_latent_read(cache._ref, slots.data_ptr(), n, c_out.data_ptr(), kr_out.data_ptr() if cache.dr else None,
-                                     _raw_stream(stream, cache.device)), "qvg_latent_read")
+    _call(cache.device, "qvg_latent_read", lib().qvg_latent_read, stream, cache._ref, slots.data_ptr(), n, c_out.data_ptr(),
+          kr_out.data_ptr() if cache.dr else None)
     return c_out, kr_out
 
 
@@ -784,12 +799,20 @@ def _view(x, shape, dev, where, name):
     """A qvg_view of a bf16 [tokens, heads, channels] tensor whose channels are
     contiguous."""
     import torch
-    if x is None or x.dim() != 3 or tuple(x.shape) != shape or x.dtype != torch.bfloat16 or x.device != dev:
+    if x is None or x.shape != shape or x.dtype != torch.bfloat16 or x.device != dev:
         raise ValueError("%s: %s must be bf16 [%d, %d, %d] on %s" % (where, name, *shape, dev))
-    s = x.stride()
-    if s[2] != 1 and shape[2] > 1:
+    token, head, channel = x.stride()
+    if channel != 1 and shape[2] > 1:
         raise ValueError("%s: %s's channels must be contiguous" % (where, name))
-    return ct.byref(_View(x.data_ptr(), s[0], s[1]))
+    return ct.byref(_View(x.data_ptr(), token, head))
+
+
+def _fresh(shape, strides, dtype, dev, stream):
+    """_empty with the (contiguous) strides spelt out, which halves its time."""
+    import torch
+    if stream is None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
+    return _empty(shape, dtype, dev, stream)
 
 
 def latent_attention(cache: LatentKV, q, q_rope, block_table, kv_len, max_q, scale, cu_q=None, mask_mode=QVG_MASK_CAUSAL,
@@ -814,22 +837,24 @@ def latent_attention(cache: LatentKV, q, q_rope, block_table, kv_len, max_q, sca
     if mask_mode == QVG_MASK_TREE and (mask is None or mask.dim() != 2 or mask.shape[0] < total):
         raise ValueError("latent_attention: QVG_MASK_TREE needs mask rows [total_q, words]")
     if out is None:
-        out = _empty((total, Hq, cache.dc), dt, q.device, stream)
+        out = _fresh((total, Hq, cache.dc), (Hq * cache.dc, cache.dc, 1), dt, cache.device, stream)
     elif out.shape != (total, Hq, cache.dc):
         raise ValueError("latent_attention: out must be [total_q, Hq, %d]" % cache.dc)
-    _on(q.device, "latent_attention", block_table=(block_table, torch.int32), kv_len=(kv_len, torch.int32),
-        cu_q=(cu_q, torch.int32), mask=(mask, torch.int32), out=(out, dt), workspace=(workspace, torch.uint8))
-    lse = _empty((Hq, total), torch.float32, q.device, stream) if want_lse else None
+    dev = cache.device
+    if _off(block_table, torch.int32, dev) or _off(kv_len, torch.int32, dev) or _off(out, dt, dev) or \
+            (cu_q is not None and _off(cu_q, torch.int32, dev)) or (mask is not None and _off(mask, torch.int32, dev)) or \
+            (workspace is not None and _off(workspace, torch.uint8, dev)):
+        _on(dev, "latent_attention", block_table=(block_table, torch.int32), kv_len=(kv_len, torch.int32),
+            cu_q=(cu_q, torch.int32), mask=(mask, torch.int32), out=(out, dt), workspace=(workspace, torch.uint8))
+    lse = _fresh((Hq, total), (total, 1), torch.float32, dev, stream) if want_lse else None
     if workspace is None:
         if cache._workspace is None:
             cache._workspace = latent_workspace_size(cache)
-        workspace = _empty((cache._workspace,), torch.uint8, q.device, stream)
-    with _Device(q.device):
-        _check(lib().qvg_latent_attention(
-            cache._ref, qv, qr, total, Hq, B, max_q, None if cu_q is None else cu_q.data_ptr(), block_table.data_ptr(),
-            block_table.shape[1], kv_len.data_ptr(), mask_mode, None if mask is None else mask.data_ptr(),
-            0 if mask is None else mask.shape[1], scale, out.data_ptr(), out_dtype, None if lse is None else lse.data_ptr(),
-            workspace.data_ptr(), workspace.numel(), _raw_stream(stream, q.device)), "qvg_latent_attention")
+        workspace = _fresh((cache._workspace,), (1,), torch.uint8, dev, stream)
+    _call(dev, "qvg_latent_attention", lib().qvg_latent_attention, stream, cache._ref, qv, qr, total, Hq, B, max_q,
+          None if cu_q is None else cu_q.data_ptr(), block_table.data_ptr(), block_table.shape[1], kv_len.data_ptr(), mask_mode,
+          None if mask is None else mask.data_ptr(), 0 if mask is None else mask.shape[1], scale, out.data_ptr(), out_dtype,
+          None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
@@ -864,16 +889,15 @@ def expanded_attention(q, q_rope, k, k_rope, v, max_q, scale=0.0, cu_q=None, cu_
             (cu_k is not None and cu_k.numel() != B + 1):
         raise ValueError("expanded_attention: cu_q and cu_k must be [B + 1]; without them every sequence has max_q, max_k rows")
     if out is None:
-        out = _empty((total, H, dv), dt, dev, stream)
+        out = _fresh((total, H, dv), (H * dv, dv, 1), dt, dev, stream)
     elif out.shape != (total, H, dv):
         raise ValueError("expanded_attention: out must be [total_q, H, %d]" % dv)
-    _on(dev, "expanded_attention", cu_q=(cu_q, torch.int32), cu_k=(cu_k, torch.int32), out=(out, dt))
-    lse = _empty((H, total), torch.float32, dev, stream) if want_lse else None
-    with _Device(dev):
-        _check(lib().qvg_expanded_attention(
-            *views, total, total_k, H, dn, dr, dv, B, max_q, max_k, None if cu_q is None else cu_q.data_ptr(),
-            None if cu_k is None else cu_k.data_ptr(), mask_mode, scale, out.data_ptr(), out_dtype,
-            None if lse is None else lse.data_ptr(), _raw_stream(stream, dev)), "qvg_expanded_attention")
+    if _off(out, dt, dev) or (cu_q is not None and _off(cu_q, torch.int32, dev)) or (cu_k is not None and _off(cu_k, torch.int32, dev)):
+        _on(dev, "expanded_attention", cu_q=(cu_q, torch.int32), cu_k=(cu_k, torch.int32), out=(out, dt))
+    lse = _fresh((H, total), (total, 1), torch.float32, dev, stream) if want_lse else None
+    _call(dev, "qvg_expanded_attention", lib().qvg_expanded_attention, stream, *views, total, total_k, H, dn, dr, dv, B, max_q, max_k,
+          None if cu_q is None else cu_q.data_ptr(), None if cu_k is None else cu_k.data_ptr(), mask_mode, scale, out.data_ptr(),
+          out_dtype, None if lse is None else lse.data_ptr())
     return out, lse
 
 
@@ -893,6 +917,7 @@ class PagePool:
         self.num_pages, self.refs, self.device = num_pages, refs, refs.device
         self._c = _PagePool(num_pages, refs.data_ptr())
         self._ref = ct.byref(self._c)
+        self._workspace = {}  # pages_reserve's scratch bytes by number of sequences
 
 
 def _sequences(pool, page_size, block_table, kv_len, where):
@@ -900,7 +925,8 @@ def _sequences(pool, page_size, block_table, kv_len, where):
     B = kv_len.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("%s: block_table must be [B, pages], kv_len [B]" % where)
-    _on(pool.device, where, block_table=(block_table, torch.int32), kv_len=(kv_len, torch.int32))
+    if _off(block_table, torch.int32, pool.device) or _off(kv_len, torch.int32, pool.device):
+        _on(pool.device, where, block_table=(block_table, torch.int32), kv_len=(kv_len, torch.int32))
     return ct.byref(_Sequences(B, page_size, block_table.shape[1], block_table.data_ptr(), kv_len.data_ptr()))
 
 
@@ -911,10 +937,9 @@ def pages_fork(pool: PagePool, page_size, block_table, kv_len, parents, children
     s = _sequences(pool, page_size, block_table, kv_len, "pages_fork")
     if parents.numel() != children.numel():
         raise ValueError("pages_fork: parents and children must be as many")
-    _on(pool.device, "pages_fork", parents=(parents, torch.int32), children=(children, torch.int32))
-    with _Device(pool.device):
-        _check(lib().qvg_pages_fork(pool._ref, s, parents.data_ptr(), children.data_ptr(), parents.numel(),
-                                    _raw_stream(stream, pool.device)), "qvg_pages_fork")
+    if _off(parents, torch.int32, pool.device) or _off(children, torch.int32, pool.device):
+        _on(pool.device, "pages_fork", parents=(parents, torch.int32), children=(children, torch.int32))
+    _call(pool.device, "qvg_pages_fork", lib().qvg_pages_fork, stream, pool._ref, s, parents.data_ptr(), children.data_ptr(), parents.numel())
 
 
 def pages_release(pool: PagePool, page_size, block_table, kv_len, ids, keep=None, stream=None):
@@ -924,10 +949,10 @@ def pages_release(pool: PagePool, page_size, block_table, kv_len, ids, keep=None
     s = _sequences(pool, page_size, block_table, kv_len, "pages_release")
     if keep is not None and keep.numel() != ids.numel():
         raise ValueError("pages_release: ids and keep must be as many")
-    _on(pool.device, "pages_release", ids=(ids, torch.int32), keep=(keep, torch.int32))
-    with _Device(pool.device):
-        _check(lib().qvg_pages_release(pool._ref, s, ids.data_ptr(), None if keep is None else keep.data_ptr(), ids.numel(),
-                                       _raw_stream(stream, pool.device)), "qvg_pages_release")
+    if _off(ids, torch.int32, pool.device) or (keep is not None and _off(keep, torch.int32, pool.device)):
+        _on(pool.device, "pages_release", ids=(ids, torch.int32), keep=(keep, torch.int32))
+    _call(pool.device, "qvg_pages_release", lib().qvg_pages_release, stream, pool._ref, s, ids.data_ptr(),
+          None if keep is None else keep.data_ptr(), ids.numel())
 
 
 def pages_reserve(pool: PagePool, page_size, block_table, kv_len, n_new=1, cu_new=None, total=None, slots=None, copies=None,
@@ -946,18 +971,21 @@ def pages_reserve(pool: PagePool, page_size, block_table, kv_len, n_new=1, cu_ne
     total = B * n_new if cu_new is None else total
     if total < 0:
         raise ValueError("pages_reserve: a negative number of tokens")
-    slots = _empty((total,), torch.int64, pool.device, stream) if slots is None else slots
-    copies = _empty((B, 2), torch.int32, pool.device, stream) if copies is None else copies
+    slots = _fresh((total,), (1,), torch.int64, pool.device, stream) if slots is None else slots
+    copies = _fresh((B, 2), (2, 1), torch.int32, pool.device, stream) if copies is None else copies
     if slots.numel() != total or copies.shape != (B, 2):
         raise ValueError("pages_reserve: slots must be [%d], copies [%d, 2]" % (total, B))
-    _on(pool.device, "pages_reserve", cu_new=(cu_new, torch.int32), slots=(slots, torch.int64), copies=(copies, torch.int32))
-    need = ct.c_size_t(0)
-    _check(lib().qvg_pages_workspace_size(pool.num_pages, B, ct.byref(need)), "qvg_pages_workspace_size")
-    workspace = _empty((need.value,), torch.uint8, pool.device, stream)
-    with _Device(pool.device):
-        _check(lib().qvg_pages_reserve(pool._ref, s, None if cu_new is None else cu_new.data_ptr(), n_new, total,
-                                       slots.data_ptr(), copies.data_ptr(), workspace.data_ptr(), need.value,
-                                       _raw_stream(stream, pool.device)), "qvg_pages_reserve")
+    if _off(slots, torch.int64, pool.device) or _off(copies, torch.int32, pool.device) or \
+            (cu_new is not None and _off(cu_new, torch.int32, pool.device)):
+        _on(pool.device, "pages_reserve", cu_new=(cu_new, torch.int32), slots=(slots, torch.int64), copies=(copies, torch.int32))
+    need = pool._workspace.get(B)
+    if need is None:
+        size = ct.c_size_t(0)
+        _check(lib().qvg_pages_workspace_size(pool.num_pages, B, ct.byref(size)), "qvg_pages_workspace_size")
+        need = pool._workspace[B] = int(size.value)
+    workspace = _fresh((need,), (1,), torch.uint8, pool.device, stream)
+    _call(pool.device, "qvg_pages_reserve", lib().qvg_pages_reserve, stream, pool._ref, s, None if cu_new is None else cu_new.data_ptr(), n_new,
+          total, slots.data_ptr(), copies.data_ptr(), workspace.data_ptr(), need)
     return slots, copies
 
 
@@ -967,8 +995,8 @@ def _page_rows(cache, where):
         rows = _PageRows()
         call = lib().qvg_latent_rows if isinstance(cache, LatentKV) else lib().qvg_paged_rows
         _check(call(cache._ref, ct.byref(rows)), where)
-        cache._rows = rows
-    return ct.byref(rows)
+        cache._rows = ct.byref(rows)
+    return cache._rows
 
 
 def pages_copy(cache, copies, stream=None):
@@ -978,10 +1006,9 @@ def pages_copy(cache, copies, stream=None):
     import torch
     if copies.dim() != 2 or copies.shape[1] != 2:
         raise ValueError("pages_copy: copies must be [n, 2]")
-    _on(cache.device, "pages_copy", copies=(copies, torch.int32))
-    with _Device(cache.device):
-        _check(lib().qvg_pages_copy(_page_rows(cache, "pages_copy"), copies.data_ptr(), copies.shape[0],
-                                    _raw_stream(stream, cache.device)), "qvg_pages_copy")
+    if _off(copies, torch.int32, cache.device):
+        _on(cache.device, "pages_copy", copies=(copies, torch.int32))
+    _call(cache.device, "qvg_pages_copy", lib().qvg_pages_copy, stream, _page_rows(cache, "pages_copy"), copies.data_ptr(), copies.shape[0])
 
 
 def paged_compact(cache, block_table, first, keep, n_keep, stream=None):
@@ -994,12 +1021,12 @@ def paged_compact(cache, block_table, first, keep, n_keep, stream=None):
     B = n_keep.numel()
     if block_table.dim() != 2 or keep.dim() != 2 or block_table.shape[0] != B or keep.shape[0] != B or first.numel() != B:
         raise ValueError("paged_compact: block_table and keep must be [B, ...], first and n_keep [B]")
-    _on(cache.device, "paged_compact", block_table=(block_table, torch.int32), first=(first, torch.int32),
-        keep=(keep, torch.int32), n_keep=(n_keep, torch.int32))
-    with _Device(cache.device):
-        _check(lib().qvg_paged_compact(_page_rows(cache, "paged_compact"), block_table.data_ptr(), block_table.shape[1], B,
-                                       first.data_ptr(), keep.data_ptr(), keep.shape[1], n_keep.data_ptr(),
-                                       _raw_stream(stream, cache.device)), "qvg_paged_compact")
+    dev = cache.device
+    if _off(block_table, torch.int32, dev) or _off(first, torch.int32, dev) or _off(keep, torch.int32, dev) or _off(n_keep, torch.int32, dev):
+        _on(dev, "paged_compact", block_table=(block_table, torch.int32), first=(first, torch.int32), keep=(keep, torch.int32),
+            n_keep=(n_keep, torch.int32))
+    _call(dev, "qvg_paged_compact", lib().qvg_paged_compact, stream, _page_rows(cache, "paged_compact"), block_table.data_ptr(),
+          block_table.shape[1], B, first.data_ptr(), keep.data_ptr(), keep.shape[1], n_keep.data_ptr())
 
 
 def query_stats(q, H, M=None, w=None, count=None, accumulate=False, stream=None):

@@ -20,6 +20,7 @@ qvg_status check_latent(const qvg_latent *c, bool shape_only) {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kAppendBlocks = 6;  // blocks an SM, at most
 
 struct LatentArgs {
     uint16_t *c, *kr;
@@ -41,88 +42,94 @@ __device__ __forceinline__ bool not_finite(uint4 v) {  // any of eight bf16 numb
     return bad;
 }
 
-// One warp per token: lane i holds channels 8 i .. of the latent, and of the
-// key part.  A key part that turns goes through shared memory, from which a
-// lane takes its channels' partners; the token's cosines and sines are made by
-// the warp, one pair a lane.  A token that holds an infinity or a NaN (before
+// A warp takes tokens one after the other, the next one's slot, rows and positions
+// on their way meanwhile.  Lane i holds channels 8 i .. of the latent and, of the
+// key part, the pairs i and i + 32 (with halves two channels dims / 2 apart; a pair
+// past the rotated ones is two neighbours), so a pair turns within its lane; the lane's
+// steps and axes stay in registers.  A token that holds an infinity or a NaN (before
 // the rotation or after) becomes NaN throughout.
-// Bound by HBM: 4 (dc + dr) bytes a token.  A warp takes two tokens, whose slots,
-// rows and positions are all asked for before any is waited for (one token, its
-// slot first: 25 us for 37,440 tokens of 256 + 64 channels, 48.7 MB; so 13).
-template <bool HALF>
-__device__ __forceinline__ uint4 turned(const RopeArgs &r, uint4 v, const float2 *cs, const uint16_t *row, int lane) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int ch = lane * 8 + 2 * i;
-        if (!HALF) {
-            if (ch >= 2 * r.pairs) continue;
-            const float2 y = rope_turn(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u), cs[ch / 2].x, cs[ch / 2].y);
-            w[i] = f32_to_bf16(y.x) | static_cast<uint32_t>(f32_to_bf16(y.y)) << 16;
-        } else {
-            uint32_t got = 0;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int x = ch + e;
-                const uint16_t own = static_cast<uint16_t>(w[i] >> (16 * e));
-                uint16_t y = own;
-                if (x < r.pairs)
-                    y = f32_to_bf16(rope_turn(bf16_to_f32(own), bf16_to_f32(row[x + r.pairs]), cs[x].x, cs[x].y).x);
-                else if (x < 2 * r.pairs)
-                    y = f32_to_bf16(rope_turn(bf16_to_f32(row[x - r.pairs]), bf16_to_f32(own), cs[x - r.pairs].x, cs[x - r.pairs].y).y);
-                got |= static_cast<uint32_t>(y) << (16 * e);
-            }
-            w[i] = got;
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
+// Bound by HBM: 4 (dc + dr) bytes a token.  (One token a warp, its channels in eights and the
+// partners through shared memory: 25 us for 37,440 tokens of 256 + 64 channels, 48.7 MB.)
+struct Token {
+    long long slot;
+    uint4 c;
+    uint32_t k[2];   // the lane's pairs
+    int32_t pos[2];
+};
 
-template <int N>  // tokens of a warp
+template <bool HALF>
 __global__ void __launch_bounds__(kWarps * 32)
     k_latent_append(const __grid_constant__ RopeArgs r, LatentArgs a, const uint16_t *__restrict__ c, const uint16_t *__restrict__ kr,
                     int n, long long cs, long long ks, const int64_t *__restrict__ slots, const int32_t *__restrict__ positions) {
-    __shared__ float2 s_cs[kWarps][N][QVG_ROPE_MAX_PAIRS];
-    __shared__ __align__(16) uint16_t s_row[kWarps][N][128];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t0 = (blockIdx.x * kWarps + warp) * N;
-    const bool in_c = lane * 8 < a.dc, in_kr = lane * 8 < a.dr;
-    long long slot[N];
-    uint4 vc[N], vk[N];
-    int32_t p0[N], p1[N];  // positions of the lane's two pairs
-    const uint64_t step0 = r.step[lane], step1 = r.step[lane + 32];
+    const int lane = threadIdx.x & 31, step = gridDim.x * kWarps;
+    const bool in_c = lane * 8 < a.dc;
+    bool in[2], turns[2];
+    int lo[2], hi[2];  // channels of the pairs
+    uint64_t angle[2];
+    int axis[2];
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-        const long long t = t0 + e;
-        const bool live = t < n;
-        slot[e] = live ? slots[t] : -1;
-        vc[e] = live && in_c ? __ldcs(reinterpret_cast<const uint4 *>(c + t * cs) + lane) : make_uint4(0, 0, 0, 0);
-        vk[e] = live && in_kr ? __ldcs(reinterpret_cast<const uint4 *>(kr + t * ks) + lane) : make_uint4(0, 0, 0, 0);
-        p0[e] = live && lane < r.pairs ? positions[t * r.axes + r.axis[lane]] : 0;
-        p1[e] = live && lane + 32 < r.pairs ? positions[t * r.axes + r.axis[lane + 32]] : 0;
+    for (int i = 0; i < 2; ++i) {
+        const int p = lane + 32 * i;
+        in[i] = 2 * p < a.dr;
+        turns[i] = p < r.pairs;
+        lo[i] = HALF && turns[i] ? p : 2 * p;
+        hi[i] = HALF && turns[i] ? p + r.pairs : 2 * p + 1;
+        angle[i] = turns[i] ? r.step[p] : 0;
+        axis[i] = turns[i] ? r.axis[p] : 0;
     }
+    auto fetch = [&](int t, Token &x) {
+        x.slot = -1;
+        if (t >= n) return;
+        x.slot = slots[t];
+        if (in_c) x.c = __ldcs(reinterpret_cast<const uint4 *>(c + t * cs) + lane);
+        const uint16_t *k = kr + t * ks;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-        if (slot[e] < 0) continue;
-        if (slot[e] >= a.n_slots) {
+        for (int i = 0; i < 2; ++i) {
+            if (!in[i]) continue;
+            x.k[i] = HALF ? k[lo[i]] | static_cast<uint32_t>(k[hi[i]]) << 16 : reinterpret_cast<const uint32_t *>(k)[lane + 32 * i];
+            if (turns[i]) x.pos[i] = positions[static_cast<long long>(t) * r.axes + axis[i]];
+        }
+    };
+    Token next;
+    next.c = make_uint4(0, 0, 0, 0);
+    next.k[0] = next.k[1] = 0;
+    next.pos[0] = next.pos[1] = 0;
+    int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    fetch(t, next);
+    for (; t < n; t += step) {
+        Token x = next;
+        fetch(t + step, next);
+        if (x.slot < 0) continue;
+        if (x.slot >= a.n_slots) {
             if (lane == 0) raise_error(a.err, QVG_ERR_INVALID_ARG);
             continue;
         }
-        bool bad = not_finite(vc[e]) || not_finite(vk[e]);
-        if (r.pairs > 0) {
-            if (lane < r.pairs) s_cs[warp][e][lane] = rope_cos_sin(step0, p0[e], r.mscale, false);
-            if (lane + 32 < r.pairs) s_cs[warp][e][lane + 32] = rope_cos_sin(step1, p1[e], r.mscale, false);
-            if (in_kr) *reinterpret_cast<uint4 *>(&s_row[warp][e][lane * 8]) = vk[e];
-            __syncwarp();
-            if (in_kr && lane * 8 < 2 * r.pairs) {
-                vk[e] = r.layout == QVG_ROPE_INTERLEAVED ? turned<false>(r, vk[e], s_cs[warp][e], s_row[warp][e], lane)
-                                                         : turned<true>(r, vk[e], s_cs[warp][e], s_row[warp][e], lane);
-                bad = bad || not_finite(vk[e]);
+        bool bad = not_finite(x.c);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            bad = bad || (x.k[i] & 0x7F80u) == 0x7F80u || (x.k[i] & 0x7F800000u) == 0x7F800000u;
+            if (!turns[i]) continue;
+            const float2 cs2 = rope_cos_sin(angle[i], x.pos[i], r.mscale, false);
+            const float2 y = rope_turn(__uint_as_float(x.k[i] << 16), __uint_as_float(x.k[i] & 0xFFFF0000u), cs2.x, cs2.y);
+            x.k[i] = f32_to_bf16(y.x) | static_cast<uint32_t>(f32_to_bf16(y.y)) << 16;
+            bad = bad || (x.k[i] & 0x7F80u) == 0x7F80u || (x.k[i] & 0x7F800000u) == 0x7F800000u;
+        }
+        if (__any_sync(0xFFFFFFFFu, bad)) {
+            x.c = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+            x.k[0] = x.k[1] = 0x7FFF7FFFu;
+        }
+        if (in_c) *(reinterpret_cast<uint4 *>(a.c + x.slot * a.dc) + lane) = x.c;
+        uint16_t *k = a.kr + x.slot * a.dr;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!in[i]) continue;
+            if (HALF) {
+                k[lo[i]] = static_cast<uint16_t>(x.k[i]);
+                k[hi[i]] = static_cast<uint16_t>(x.k[i] >> 16);
+            } else {
+                reinterpret_cast<uint32_t *>(k)[lane + 32 * i] = x.k[i];
             }
         }
-        if (__any_sync(0xFFFFFFFFu, bad)) vc[e] = vk[e] = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
-        if (in_c) *(reinterpret_cast<uint4 *>(a.c + slot[e] * a.dc) + lane) = vc[e];
-        if (in_kr) *(reinterpret_cast<uint4 *>(a.kr + slot[e] * a.dr) + lane) = vk[e];
     }
 }
 
@@ -179,11 +186,11 @@ qvg_status qvg_latent_append(const qvg_latent *cache, const void *c_bf16, const 
     const RopeArgs r = plan ? rope_args(plan, false) : RopeArgs{};
     const uint16_t *c = static_cast<const uint16_t *>(c_bf16), *kr = static_cast<const uint16_t *>(k_rope_bf16);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // two tokens a warp once that still leaves every SM four blocks
-    if (n >= 8 * kWarps * sm_count_current())
-        k_latent_append<2><<<ceil_div(n, 2 * kWarps), kWarps * 32, 0, st>>>(r, latent_args(cache), c, kr, n, c_stride, kr_stride, slots, positions);
+    const int blocks = std::min(ceil_div(n, kWarps), kAppendBlocks * sm_count_current());
+    if (plan && r.layout == QVG_ROPE_HALF)
+        k_latent_append<true><<<blocks, kWarps * 32, 0, st>>>(r, latent_args(cache), c, kr, n, c_stride, kr_stride, slots, positions);
     else
-        k_latent_append<1><<<ceil_div(n, kWarps), kWarps * 32, 0, st>>>(r, latent_args(cache), c, kr, n, c_stride, kr_stride, slots, positions);
+        k_latent_append<false><<<blocks, kWarps * 32, 0, st>>>(r, latent_args(cache), c, kr, n, c_stride, kr_stride, slots, positions);
     QVG_LAUNCH_CHECK();
     return QVG_OK;
 }

@@ -347,10 +347,10 @@ struct Slots {
 // written.  A token only moves down (keep ascends from `first` on), so what a
 // batch writes over has been read in this batch or an earlier one, never is to be
 // read in a later one, and the slices do not touch one another.
-//   Reads run ahead: while a batch is written the next one's bytes and the slots
-// of the one after that are on their way (bytes after their slots, slots after their
-// tokens, one batch after the other, it was 262 us where this takes 57).
-// Bound by HBM.
+//   Reads run ahead: while a batch is written the next one's bytes are on their way, and the
+// pages and numbers of the three after that.  (Bytes after their pages, pages after their
+// numbers, a batch after the other: 262 us for 60,000 tokens of 8 heads of 128; only the
+// bytes ahead: 139.)
 template <typename T>
 __device__ __forceinline__ void move_rows(const Buffers &a, const Move &m, Slots &s, int b, int i, int h, int col, int width, int n) {
     const int per = kMoveThreads / width;  // rows side by side
@@ -361,19 +361,26 @@ __device__ __forceinline__ void move_rows(const Buffers &a, const Move &m, Slots
     const int first = m.first[b], mask = (1 << a.page_log2) - 1, rb = a.row_bytes[i];
     const long long skip = (static_cast<long long>(a.heads[i]) - 1) << a.page_log2, lift = static_cast<long long>(h) << a.page_log2;
     uint8_t *const base = a.base[i] + col + w * static_cast<int>(sizeof(T));
-    auto slots = [&](int batch) {  // of kept token batch * rows + threadIdx.x
-        const int k = batch * rows + threadIdx.x, e = batch % 3;
-        if (threadIdx.x >= rows) return;
-        long long from = -1, to = -1;
-        if (k < n) {
-            const int x = keep[k], y = first + k;
-            if (x != y) {
-                from = (static_cast<long long>(row[x >> a.page_log2]) << a.page_log2) + (x & mask);
-                to = (static_cast<long long>(row[y >> a.page_log2]) << a.page_log2) + (y & mask);
-            }
+    // Kept token batch * rows + threadIdx.x on its way to its slots: its number, its pages, then both.
+    const bool has = static_cast<int>(threadIdx.x) < rows;
+    int number = -1, page_from = -1, page_to = -1, x = -1;
+    auto ask_number = [&](int batch) {
+        const int k = batch * rows + threadIdx.x;
+        number = has && k < n ? keep[k] : -1;
+    };
+    auto ask_pages = [&](int batch) {
+        const int y = first + batch * rows + threadIdx.x;
+        x = number == y ? -1 : number;  // (it stays where it is)
+        if (x >= 0) {
+            page_from = row[x >> a.page_log2];
+            page_to = row[y >> a.page_log2];
         }
-        s.from[e][threadIdx.x] = from;
-        s.to[e][threadIdx.x] = to;
+    };
+    auto note = [&](int batch) {
+        if (!has) return;
+        const int y = first + batch * rows + threadIdx.x, e = batch % 3;
+        s.from[e][threadIdx.x] = x < 0 ? -1 : (static_cast<long long>(page_from) << a.page_log2) + (x & mask);
+        s.to[e][threadIdx.x] = x < 0 ? -1 : (static_cast<long long>(page_to) << a.page_log2) + (y & mask);
     };
     // row (page, head, offset) of a slot
     auto at = [&](long long slot) { return base + (slot + (slot >> a.page_log2) * skip + lift) * rb; };
@@ -395,8 +402,14 @@ __device__ __forceinline__ void move_rows(const Buffers &a, const Move &m, Slots
             }
     };
     const int batches = (n + rows - 1) / rows;
-    slots(0);
-    slots(1);
+    for (int k = 0; k < 2; ++k) {
+        ask_number(k);
+        ask_pages(k);
+        note(k);
+    }
+    ask_number(2);
+    ask_pages(2);
+    ask_number(3);
     __syncthreads();
     read(0, v[0]);
     for (int j = 0; j < batches; j += 2) {
@@ -404,7 +417,9 @@ __device__ __forceinline__ void move_rows(const Buffers &a, const Move &m, Slots
         for (int p = 0; p < 2; ++p) {
             if (j + p >= batches) break;
             read(j + p + 1, v[p ^ 1]);  // (past the end: its slots are -1)
-            slots(j + p + 2);
+            note(j + p + 2);
+            ask_pages(j + p + 3);
+            ask_number(j + p + 4);
             __syncthreads();  // the batch has been read by all; the slots are there
             write(j + p, v[p]);
             __syncthreads();  // (its slots' place is the next batch's but two)
@@ -419,7 +434,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_paged_compact(const __grid_con
     if (!bad) {
         const int32_t *row = m.table + b * m.table_stride, *keep = m.keep + b * m.keep_stride;
         const long long room = m.table_stride << a.page_log2;
-#pragma unroll 4
+#pragma unroll 8
         for (int k = threadIdx.x; k < n; k += kMoveThreads) {
             const int x = keep[k];
             const bool off = x < (k ? keep[k - 1] + 1ll : static_cast<long long>(first)) || x >= room || x < first;
