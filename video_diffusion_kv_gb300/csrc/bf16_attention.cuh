@@ -144,10 +144,10 @@ __device__ __forceinline__ uint2 seen_keys(const Args &a, int t, int kv, int nq,
     return make_uint2(w[0], w[1]);
 }
 
-// A warp's rows of O times their factors.
-__device__ __forceinline__ void rescale_rows(uint32_t t_o, int dv, float f) {
+// A warp's rows of O, channels c0 .. c1 - 1, times their factors.
+__device__ __forceinline__ void rescale_rows(uint32_t t_o, int c0, int c1, float f) {
 #pragma unroll 1
-    for (int c = 0; c < dv; c += 16) {
+    for (int c = c0; c < c1; c += 16) {
         uint32_t o[16];
         pa::tmem_ld16(t_o + c, o);
 #pragma unroll
@@ -170,45 +170,46 @@ struct Row {
     }
 };
 
-// 64 keys of a warp's rows: logits at t_s into weights in the same place.
-// part: some row does not see all of them (see: this row's, bad: marked keys).
-// settled(): waits until the products before this one are in O, where there
-// are some (held).
-template <typename F>
-__device__ __forceinline__ bool weigh(const Args &a, Row &m, uint32_t t_s, uint32_t t_o, bool part, uint2 see, uint4 bad, bool live,
-                                      bool held, F settled) {
-    uint32_t v[2][32];
+// 64 keys of a warp's rows, in three steps: the logits at t_s, with those that
+// the row does not see at -inf; the largest; weights in the logits' place.
+using Logits = uint32_t[2][32];
+
+// part: some row does not see all of them (see: which this row does, bad: marked keys).
+__device__ __forceinline__ void read_logits(Logits &v, uint32_t t_s, bool part, uint2 see, uint2 bad) {
     umma::tmem_ld32(t_s, v[0]);
     umma::tmem_ld32(t_s + 32, v[1]);
     umma::tmem_ld_wait_regs(v[0]);
     umma::reg_fence32(v[1]);
     if (part) {
-        const uint32_t sw[2] = {see.x, see.y}, bw[4] = {bad.x, bad.y, bad.z, bad.w};
+        const uint32_t sw[2] = {see.x, see.y}, bw[2] = {see.x & bad.x, see.y & bad.y};
 #pragma unroll
         for (int c = 0; c < kKeys; ++c)
             if (!((sw[c / 32] >> (c & 31)) & 1u)) v[c / 32][c % 32] = 0xFF800000u;
-        if (bad.x | bad.y | bad.z | bad.w) {
+        if (bw[0] | bw[1]) {
 #pragma unroll
             for (int c = 0; c < kKeys; ++c)
-                if ((sw[c / 32] >> (c & 31)) & (bw[c / 16] >> (2 * (c % 16))) & 1u) v[c / 32][c % 32] = 0x7FFFFFFFu;
+                if ((bw[c / 32] >> (c & 31)) & 1u) v[c / 32][c % 32] = 0x7FFFFFFFu;
         }
     }
-    float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+}
+__device__ __forceinline__ float largest(const Logits &v) {
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int c = 0; c < kKeys; c += 8)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            top4[i] = fmaxf(fmaxf(top4[i], __uint_as_float(v[c / 32][c % 32 + 2 * i])), __uint_as_float(v[c / 32][c % 32 + 2 * i + 1]));
-    const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+            top[i] = fmaxf(fmaxf(top[i], __uint_as_float(v[c / 32][c % 32 + 2 * i])), __uint_as_float(v[c / 32][c % 32 + 2 * i + 1]));
+    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+// Raises the reference where the largest logit asks for it; what O has to be multiplied with.
+__device__ __forceinline__ float raise_ref(const Args &a, Row &m, float top, bool live) {
     const bool fresh = m.ref == -INFINITY;
     const bool move = live && (fresh ? top > -INFINITY : (top - m.ref) * a.scale_log2 > kRaise);
     const float f = move && !fresh ? pa::ex2((m.ref - top) * a.scale_log2) : 1.0f;
     if (move) m.ref = top;
-    if (held && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
-        if (!__all_sync(0xFFFFFFFFu, settled())) return false;
-        umma::tc_fence_after();
-        rescale_rows(t_o, a.dv, f);
-    }
+    return f;
+}
+__device__ __forceinline__ void write_weights(const Args &a, Row &m, const Logits &v, uint32_t t_s, float f) {
     const float nm = m.ref == -INFINITY ? 0.0f : -m.ref * a.scale_log2;
     const uint64_t sl2 = pa::pk2(a.scale_log2, a.scale_log2), nm2 = pa::pk2(nm, nm), f2 = pa::pk2(f, f);
     m.l2[0] = pa::mul2(m.l2[0], f2);
@@ -225,7 +226,6 @@ __device__ __forceinline__ bool weigh(const Args &a, Row &m, uint32_t t_s, uint3
     }
     umma::tmem_st32(t_s, w);
     umma::tmem_st_wait();
-    return true;
 }
 
 // 32 bytes, 32-byte aligned.
@@ -239,10 +239,12 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&x)[8]) {
 // and the sum of its weights.  none: no product has been made.  A partial sum
 // lies as [dv / 4][128 rows][4], so that a warp's stores are whole lines
 // (as rows, 128 of them took 6 us; so 3).
-__device__ __forceinline__ void store_rows(const Args &a, const Row &m, uint32_t t_o, bool none, bool live, bool whole, long long slot, int r,
-                                           long long row, int h, int token) {
-    const float l = m.sum(), ref = m.ref * a.scale_log2;
-    if (live && !whole) {
+// c0, c1: the channels that the warp's threads take; first: they store the sum, too.
+__device__ __forceinline__ void store_rows(const Args &a, float ref_logit, float l, uint32_t t_o, int c0, int c1, bool first, bool none, bool live,
+                                           bool whole, long long slot, int r, long long row, int h, int token) {
+    const float ref = ref_logit * a.scale_log2;
+    if (!first) {
+    } else if (live && !whole) {
         a.pm[slot * kRows + r] = ref;
         a.pl[slot * kRows + r] = l;
     } else if (live && a.lse) {
@@ -252,7 +254,7 @@ __device__ __forceinline__ void store_rows(const Args &a, const Row &m, uint32_t
     float *part = a.po + slot * kRows * a.dv + 4 * r;
     const bool wide = a.wide_out;
 #pragma unroll 1
-    for (int c = 0; c < a.dv; c += 32) {
+    for (int c = c0; c < c1; c += 32) {
         uint32_t o[32];
         if (none) {
 #pragma unroll
@@ -290,12 +292,12 @@ __device__ __forceinline__ void store_rows(const Args &a, const Row &m, uint32_t
     }
 }
 
-// The helpers' look at 64 keys of V (nb chunks at `v`), thread w of 128: two
-// threads a key.  `left`: keys before the sequence's end.  Returns the warp's
-// marks (key i of the warp's 16 at bit 2 i).
-__device__ __forceinline__ uint32_t clean(uint8_t *v, int nb, int w, int left) {
-    const int row = w >> 1, lane = w & 31;
-    uint8_t *line = v + row * 128 + (w & 1) * 64;
+// A helper warp's look at keys [k0, k0 + 16) of 64 keys of V (nb chunks at `v`),
+// two threads a key.  `left`: keys before the sequence's end.  Returns the
+// marks, key i at bit i.
+__device__ __forceinline__ uint32_t clean16(uint8_t *v, int nb, int k0, int left) {
+    const int lane = threadIdx.x & 31, row = k0 + (lane >> 1);
+    uint8_t *line = v + row * 128 + (lane & 1) * 64;
     bool bad = false;
     for (int c = 0; c < nb; ++c)
 #pragma unroll
@@ -305,15 +307,19 @@ __device__ __forceinline__ uint32_t clean(uint8_t *v, int nb, int w, int left) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) bad = bad || (y[e] & 0x7F80u) == 0x7F80u || (y[e] & 0x7F800000u) == 0x7F800000u;
         }
-    const uint32_t any = __ballot_sync(0xFFFFFFFFu, bad);
+    bad = __shfl_xor_sync(0xFFFFFFFFu, bad, 1) || bad;
     const bool past = row >= left;
-    if (past || (any >> (lane & 30) & 3u)) {
+    if (past || bad) {
         for (int c = 0; c < nb; ++c)
 #pragma unroll
             for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(line + c * kChunk + 16 * i) = make_uint4(0, 0, 0, 0);
     }
     umma::fence_proxy_async_smem();
-    return __ballot_sync(0xFFFFFFFFu, !past && (lane & 1) == 0 && (any >> lane & 3u));
+    uint32_t b = __ballot_sync(0xFFFFFFFFu, bad && !past) & 0x55555555u;  // every other bit, moved together
+    b = (b | b >> 1) & 0x33333333u;
+    b = (b | b >> 2) & 0x0F0F0F0Fu;
+    b = (b | b >> 4) & 0x00FF00FFu;
+    return (b | b >> 8) & 0xFFFFu;
 }
 
 }  // namespace la

@@ -20,16 +20,15 @@ namespace la {
 constexpr int kPromptRows = 256, kPromptKeys = 128, kPromptWarps = 16;
 constexpr int kKChunk = kPromptKeys * 128;  // 64 channels of K's tile
 
-// A CTA's unit, and how many tiles of 64 keys each group needs.
+// A unit, and how many tiles of 64 keys each group needs.
 struct Unit {
     int b, h, r, q0, nq, k0, kv, nt[2];
 };
-__device__ __forceinline__ Unit unit_of(const Args &a, int blocks) {
+__device__ __forceinline__ Unit unit_of(const Args &a, int b, int r, int h, bool report) {
     Unit u;
-    const int bh = a.B * a.H, i = blockIdx.x / bh, j = blockIdx.x - i * bh;
-    u.r = blocks - 1 - i;  // causal: the last rows see the most keys
-    u.b = j / a.H;
-    u.h = j - u.b * a.H;
+    u.b = b;
+    u.r = r;
+    u.h = h;
     bool bad = false;
     u.q0 = u.b * a.max_q;
     u.nq = a.max_q;
@@ -49,7 +48,7 @@ __device__ __forceinline__ Unit unit_of(const Args &a, int blocks) {
         if (u.k0 < 0 || u.k0 > a.total_k) u.k0 = u.kv = 0;
         u.kv = max(0, min(u.kv, a.total_k - u.k0));
     }
-    if (bad && u.r == 0 && u.h == 0 && threadIdx.x == 0) raise_error(a.err, QVG_ERR_INVALID_ARG);
+    if (bad && report) raise_error(a.err, QVG_ERR_INVALID_ARG);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
         const int first = u.r * kPromptRows + g * kRows, last = min(u.nq, first + kRows);
@@ -57,6 +56,28 @@ __device__ __forceinline__ Unit unit_of(const Args &a, int blocks) {
         u.nt[g] = end <= 0 ? 0 : (end - 1) / kKeys + 1;
     }
     return u;
+}
+
+// The CTA's (sequence, block of rows): heads of the longest come first, so that the short
+// ones fill the GPU's end.  Up to kSorted pairs are ranked by their tiles (each CTA
+// does it for itself: they all get the same order); of more, and of one sequence, the
+// last rows come first, which with a causal mask see the most keys.
+constexpr int kSorted = 256;
+__device__ __forceinline__ int2 pick(const Args &a, int blocks, uint32_t *key, int *got) {
+    const int n = a.B * blocks, want = blockIdx.x / a.H, i = threadIdx.x;
+    if (a.B == 1 || n > kSorted) return make_int2(want % a.B, blocks - 1 - want / a.B);
+    if (i < n) {
+        const Unit u = unit_of(a, i % a.B, blocks - 1 - i / a.B, 0, false);
+        key[i] = static_cast<uint32_t>(u.r * kPromptRows < u.nq ? min(max(u.nt[0], u.nt[1]) + 1, (1 << 24) - 1) : 0) << 8 | static_cast<uint32_t>(255 - i);
+    }
+    __syncthreads();
+    if (i < n) {
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += key[j] > key[i];
+        if (rank == want) *got = i;
+    }
+    __syncthreads();
+    return make_int2(*got % a.B, blocks - 1 - *got / a.B);
 }
 
 // qmap, rqmap: q and its rotated part; kmap, rkmap: k and the rotated key parts; vmap: v.
@@ -67,11 +88,14 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
     extern __shared__ uint8_t dyn[];
     __shared__ uint64_t a_full[kMostStages], a_empty[kMostStages], b_full[kMostStages], b_empty[kMostStages], fixed[kFix];
     __shared__ uint64_t s_full[2], p_full[2][2], o_done[2][2], q_full[2], drain, never;
-    __shared__ uint4 s_bad[kFix];  // marked keys of a tile: key 16 w + i at bit 2 i of word w
+    __shared__ uint2 s_bad[kFix];  // marked keys of a tile of 64
     __shared__ uint32_t tmem_base;
     __shared__ int fail, issued[2];  // tiles of K and of V whose copies have been issued
 
-    const Unit u = unit_of(a, blocks);
+    __shared__ int picked;
+    const int2 br = pick(a, blocks, reinterpret_cast<uint32_t *>(dyn), &picked);
+    const int head = blockIdx.x % a.H;
+    const Unit u = unit_of(a, br.x, br.y, head, br.y == 0 && head == 0 && threadIdx.x == 0);
     if (u.r * kPromptRows >= u.nq) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q_group = a.na * kQChunk, a_bytes = a.na * kKChunk, b_bytes = a.nb * kChunk;
@@ -127,7 +151,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
             const int half = t & 1, d = t >> 1;
             const bool part = partial(t);
             if (half == 0) ok = wait(&s_full[grp], d & 1);
-            uint4 bad = make_uint4(0, 0, 0, 0);
+            uint2 bad = make_uint2(0, 0);
             if (part) {
                 ok = ok && wait(&fixed[n_fix % kFix], (n_fix / kFix) & 1);
                 bad = s_bad[n_fix % kFix];
@@ -139,9 +163,18 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
             if (!idle) {
                 uint2 see = make_uint2(0, 0);
                 if (part) see = seen_keys(a, t, u.kv, u.nq, u.q0, live ? tq : 0);
-                // (S of this tile came after all products of the tile before)
-                ok = weigh(a, m, t_s + half * 64, t_o, part, see, bad, live, t > 0, [&] { return half == 0 || wait(&o_done[grp][0], d & 1); });
-                if (!ok) break;
+                Logits v;
+                read_logits(v, t_s + half * 64, part, see, bad);
+                const float f = raise_ref(a, m, largest(v), live);
+                if (t > 0 && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
+                    // the products before have to be in O (S of this tile came after those of the tile before)
+                    if (half == 1) ok = wait(&o_done[grp][0], d & 1);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    umma::tc_fence_after();
+                    rescale_rows(t_o, 0, a.dv, f);
+                }
+                write_weights(a, m, v, t_s + half * 64, f);
             }
             umma::tc_fence_before();
             __syncwarp();
@@ -151,11 +184,10 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (ok) {
             umma::tc_fence_after();
-            if (!idle) store_rows(a, m, t_o, end == 0, live, true, 0, 0, static_cast<long long>(u.q0 + tq) * a.Hq + u.h, u.h, u.q0 + tq);
+            if (!idle) store_rows(a, m.ref, m.sum(), t_o, 0, a.dv, true, end == 0, live, true, 0, 0, static_cast<long long>(u.q0 + tq) * a.Hq + u.h, u.h, u.q0 + tq);
         }
     } else if (warp < 12) {
         // ---- helpers: V where some row does not see all of it ----------------------------------------------
-        const int w = tid - 256;
         Ring rb;
         int n_fix = 0;
         for (int t = 0; t < most; ++t, rb.next(a.sb)) {
@@ -163,10 +195,10 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             if (partial(t)) {
-                const uint32_t marks = clean(base + (b0 - sm) + rb.i * b_bytes, a.nb, w, u.kv - t * kKeys);
+                const uint32_t marks = clean16(base + (b0 - sm) + rb.i * b_bytes, a.nb, 16 * (warp - 8), u.kv - t * kKeys);
                 __syncwarp();
                 if (lane == 0) {
-                    reinterpret_cast<uint32_t *>(&s_bad[n_fix % kFix])[warp - 8] = marks;
+                    reinterpret_cast<uint16_t *>(&s_bad[n_fix % kFix])[warp - 8] = static_cast<uint16_t>(marks);
                     umma::mbar_arrive(&fixed[n_fix % kFix]);
                 }
                 ++n_fix;

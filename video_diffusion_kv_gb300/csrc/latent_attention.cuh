@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
     __shared__ uint64_t s_full[2], p_full[2], o_done[2], q_full, q_free, drain, never;
     __shared__ uint64_t seg_full[pa::kRing], seg_free[pa::kRing];
     __shared__ pa::Segment s_seg[pa::kRing];
-    __shared__ uint4 s_bad[kFix];  // marked keys of a tile: key 16 w + i at bit 2 i of word w
+    __shared__ uint2 s_bad[kFix];  // marked keys of a tile
     __shared__ uint32_t tmem_base;
     __shared__ int fail, issued[2];  // tiles whose copies each loading warp has issued
 
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
                 const int bf = n & 1;
                 const bool part = partial(t, clear);
                 ok = wait(&s_full[bf], (n >> 1) & 1);
-                uint4 bad = make_uint4(0, 0, 0, 0);
+                uint2 bad = make_uint2(0, 0);
                 if (part) {
                     ok = ok && wait(&fixed[n_fix % kFix], (n_fix / kFix) & 1);
                     bad = s_bad[n_fix % kFix];
@@ -130,9 +130,18 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
                 if (!idle) {
                     uint2 see = make_uint2(0, 0);
                     if (part) see = seen_keys(a, t, g.kv, g.nq, g.q0, live ? tq : 0);
-                    ok = weigh(a, m, t_s0 + bf * 64 + t_lane, t_o, part, see, bad, live, t != g.t0,
-                               [&] { return wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1); });
-                    if (!ok) break;
+                    Logits v;
+                    read_logits(v, t_s0 + bf * 64 + t_lane, part, see, bad);
+                    const float f = raise_ref(a, m, largest(v), live);
+                    if (t != g.t0 && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
+                        // the product of the tile before has to be in O
+                        ok = wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        umma::tc_fence_after();
+                        rescale_rows(t_o, 0, a.dv, f);
+                    }
+                    write_weights(a, m, v, t_s0 + bf * 64 + t_lane, f);
                 }
                 umma::tc_fence_before();
                 __syncwarp();
@@ -144,7 +153,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
             if (!ok) break;
             umma::tc_fence_after();
             if (!idle)
-                store_rows(a, m, t_o, false, live, g.whole(), cta * 2 + (g.t0 > 0 ? 0 : 1), tid, static_cast<long long>(g.q0 + tq) * a.Hq + h, h, g.q0 + tq);
+                store_rows(a, m.ref, m.sum(), t_o, 0, a.dv, true, false, live, g.whole(), cta * 2 + (g.t0 > 0 ? 0 : 1), tid, static_cast<long long>(g.q0 + tq) * a.Hq + h, h, g.q0 + tq);
             umma::tc_fence_before();
         }
     } else if (warp < W0 + 4) {
@@ -206,9 +215,11 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 if (partial(t, clear)) {
-                    const uint32_t marks = clean(base + (c0 - sm) + rg.i * stage, a.nb, w, g.kv - t * kKeys);
+                    const int k0 = 16 * (warp - W0);
+                    const uint32_t marks = clean16(base + (c0 - sm) + rg.i * stage, a.nb, k0, g.kv - t * kKeys);
+                    __syncwarp();
                     if (lane == 0) {
-                        reinterpret_cast<uint32_t *>(&s_bad[n_fix % kFix])[warp - W0] = marks;
+                        reinterpret_cast<uint16_t *>(&s_bad[n_fix % kFix])[warp - W0] = static_cast<uint16_t>(marks);
                         umma::mbar_arrive(&fixed[n_fix % kFix]);
                     }
                     ++n_fix;
