@@ -20,7 +20,7 @@ qvg_status check_latent(const qvg_latent *c, bool shape_only) {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kAppendBlocks = 6;  // blocks an SM, at most
+constexpr int kAppendBlocks = 4;  // blocks an SM, at most: what its registers hold
 
 struct LatentArgs {
     uint16_t *c, *kr;

@@ -337,7 +337,7 @@ struct Move {
     int jobs[4];  // blocks up to this buffer's end, of a sequence
 };
 
-// Slots of a batch's kept tokens, from and to (-1: the token stays), three batches deep.
+// Bytes from the buffer's start to a batch's kept tokens' rows, from and to (-1: the token stays), three batches deep.
 struct Slots {
     long long from[3][kMoveThreads], to[3][kMoveThreads];
 };
@@ -359,7 +359,7 @@ __device__ __forceinline__ void move_rows(const Buffers &a, const Move &m, Slots
     const int rows = per * each;
     const int32_t *row = m.table + b * m.table_stride, *keep = m.keep + b * m.keep_stride;
     const int first = m.first[b], mask = (1 << a.page_log2) - 1, rb = a.row_bytes[i];
-    const long long skip = (static_cast<long long>(a.heads[i]) - 1) << a.page_log2, lift = static_cast<long long>(h) << a.page_log2;
+    const long long heads = static_cast<long long>(a.heads[i]) << a.page_log2, lift = static_cast<long long>(h) << a.page_log2;
     uint8_t *const base = a.base[i] + col + w * static_cast<int>(sizeof(T));
     // Kept token batch * rows + threadIdx.x on its way to its slots: its number, its pages, then both.
     const bool has = static_cast<int>(threadIdx.x) < rows;
@@ -379,18 +379,17 @@ __device__ __forceinline__ void move_rows(const Buffers &a, const Move &m, Slots
     auto note = [&](int batch) {
         if (!has) return;
         const int y = first + batch * rows + threadIdx.x, e = batch % 3;
-        s.from[e][threadIdx.x] = x < 0 ? -1 : (static_cast<long long>(page_from) << a.page_log2) + (x & mask);
-        s.to[e][threadIdx.x] = x < 0 ? -1 : (static_cast<long long>(page_to) << a.page_log2) + (y & mask);
+        // row (page, head, offset)
+        s.from[e][threadIdx.x] = x < 0 ? -1 : (page_from * heads + lift + (x & mask)) * rb;
+        s.to[e][threadIdx.x] = x < 0 ? -1 : (page_to * heads + lift + (y & mask)) * rb;
     };
-    // row (page, head, offset) of a slot
-    auto at = [&](long long slot) { return base + (slot + (slot >> a.page_log2) * skip + lift) * rb; };
     T v[2][kMoveEach];
     auto read = [&](int batch, T(&x)[kMoveEach]) {
 #pragma unroll
         for (int e = 0; e < kMoveEach; ++e)
             if (e < each && r < per) {
                 const long long f = s.from[batch % 3][e * per + r];
-                if (f >= 0) x[e] = *reinterpret_cast<const T *>(at(f));
+                if (f >= 0) x[e] = *reinterpret_cast<const T *>(base + f);
             }
     };
     auto write = [&](int batch, const T(&x)[kMoveEach]) {
@@ -398,7 +397,7 @@ __device__ __forceinline__ void move_rows(const Buffers &a, const Move &m, Slots
         for (int e = 0; e < kMoveEach; ++e)
             if (e < each && r < per) {
                 const long long t = s.to[batch % 3][e * per + r];
-                if (t >= 0) *reinterpret_cast<T *>(at(t)) = x[e];
+                if (t >= 0) *reinterpret_cast<T *>(base + t) = x[e];
             }
     };
     const int batches = (n + rows - 1) / rows;
