@@ -15,7 +15,7 @@
 //
 // Tensor memory: O 256 columns, S 2 x 64, Q 128.
 // Roles: softmax (4 warps, thread = row), helpers (4: Q, and V in tiles that
-// some row does not see all of), loads (2), S, PV, segments.
+// some row does not see all of), loads (4), S, PV, segments.
 #pragma once
 
 #include "bf16_attention.cuh"
@@ -23,7 +23,7 @@
 namespace qvg {
 namespace la {
 
-constexpr int kLatentWarps = 13;
+constexpr int kLoads = 4, kLatentWarps = 4 + 4 + kLoads + 3;
 
 // A unit of which a CTA has a part: the CTAs that share it, its rows (0: there
 // is none), the first of them among the sequence's rows, the sequence's first token.
@@ -37,12 +37,12 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
     constexpr int W0 = 4, WARPS = kLatentWarps;
     extern __shared__ uint8_t dyn[];
     __shared__ uint64_t full[kMostStages], empty[kMostStages], fixed[kFix];
-    __shared__ uint64_t s_full[2], p_full[2], o_done[2], q_full, q_free, drain, never;
+    __shared__ uint64_t s_full[2], p_full[2], o_done[2], q_full, q_more, q_free, drain, never;
     __shared__ uint64_t seg_full[pa::kRing], seg_free[pa::kRing];
     __shared__ pa::Segment s_seg[pa::kRing];
     __shared__ uint2 s_bad[kFix];  // marked keys of a tile
     __shared__ uint32_t tmem_base;
-    __shared__ int fail, issued[2];  // tiles whose copies each loading warp has issued
+    __shared__ int fail, issued[kLoads];  // tiles whose copies each loading warp has issued
 
     pdl_trigger();  // the join's blocks may take the places of CTAs that are done (they wait for all of them)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -54,9 +54,9 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
     const uint32_t r0 = sm + a.na * kQChunk, c0 = r0 + a.na * kChunk;
     if (tid == 0) {
         fail = 0;
-        issued[0] = issued[1] = 0;
+        for (int i = 0; i < kLoads; ++i) issued[i] = 0;
         for (int i = 0; i < kMostStages; ++i) {
-            umma::mbar_init(&full[i], 2);
+            umma::mbar_init(&full[i], kLoads);
             umma::mbar_init(&empty[i], 5);  // PV, and the helpers' warps
         }
         for (int i = 0; i < kFix; ++i) umma::mbar_init(&fixed[i], 4);
@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
             umma::mbar_init(&o_done[i], 1);
         }
         umma::mbar_init(&q_full, 4);
+        umma::mbar_init(&q_more, 4);
         umma::mbar_init(&q_free, 1);
         umma::mbar_init(&drain, 2);
         umma::mbar_init(&never, 1);
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
         }
         umma::fence_barrier_init();
     }
-    if (warp == W0 + 7) {
+    if (warp == W0 + 5 + kLoads) {
         umma::tmem_alloc(&tmem_base, 512);
         umma::tmem_relinquish();
     }
@@ -99,6 +100,33 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
         if (a.mode == QVG_MASK_TREE) return min(g.kv, hist);
         return min(g.kv, hist + 1 + static_cast<int>(static_cast<long long>(g.r) * kRows / a.grp));
     };
+    // A row of Q into its lane of tensor memory, 128 channels at a time.
+    struct Fetch {
+        const uint4 *q;
+        bool live;
+        uint4 x[16];
+        __device__ __forceinline__ void ask(int c, int nb) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = live && c * 8 + e < nb * 8 ? q[c * 8 + e] : make_uint4(0, 0, 0, 0);
+        }
+        __device__ __forceinline__ void put(uint32_t t_q, int c, int nb) const {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t y[32];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[4 * e] = x[8 * k + e].x, y[4 * e + 1] = x[8 * k + e].y, y[4 * e + 2] = x[8 * k + e].z, y[4 * e + 3] = x[8 * k + e].w;
+                if (c + k < nb) umma::tmem_st32(t_q + (c + k) * 32, y);
+            }
+        }
+    };
+    auto row_of = [&](const pa::Segment &g, int w) {
+        const uint32_t gi = static_cast<uint32_t>(g.r) * kRows + w;
+        const int t = static_cast<int>(gi / static_cast<uint32_t>(a.grp)), h = static_cast<int>(gi) - t * a.grp;
+        Fetch f;
+        f.live = t < g.nq;
+        f.q = reinterpret_cast<const uint4 *>(a.q + (g.q0 + (f.live ? t : 0)) * a.q_stride + (f.live ? h : 0) * a.q_h);
+        return f;
+    };
     auto partial = [&](int t, int clear) { return (t + 1) * kKeys > clear; };
 
     if (warp < W0) {
@@ -113,6 +141,17 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
             const int tq = static_cast<int>(gi / static_cast<uint32_t>(a.grp)), h = static_cast<int>(gi) - tq * a.grp;
             const bool live = tq < g.nq, idle = !__any_sync(0xFFFFFFFFu, live);
             const int clear = clear_of(g);
+            if (n_seg == 1) {  // the first unit's channels from 128 on: all at once they arrive a read earlier
+                if (a.nb > 2) {
+                    Fetch f = row_of(g, tid);
+                    f.ask(2, a.nb);
+                    f.put(t_q0 + t_lane, 2, a.nb);
+                    umma::tmem_st_wait();
+                }
+                umma::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(&q_more);
+            }
             Row m;
             for (int t = g.t0; t < g.t1; ++t, ++n) {
                 const int bf = n & 1;
@@ -164,19 +203,11 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
         int n_fix = 0, n_seg = 0;
         bool ok = true;
         while (ok && next_segment(g, n_seg)) {
-            // A thread's row goes into its lane of tensor memory, 128 channels at a time; the first of them are on their way
-            // before the last unit's products are done with its row.
-            const uint32_t gw = static_cast<uint32_t>(g.r) * kRows + w;
-            const int tw = static_cast<int>(gw / static_cast<uint32_t>(a.grp)), hw = static_cast<int>(gw) - tw * a.grp;
-            const bool live = tw < g.nq;
-            const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (g.q0 + (live ? tw : 0)) * a.q_stride + (live ? hw : 0) * a.q_h);
+            // (on their way before the last unit's products are done with its row)
+            Fetch f = row_of(g, w);
             const uint32_t t_q = t_q0 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            uint4 x[16];
-            auto fetch = [&](int c) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = live && c * 8 + e < a.nb * 8 ? q[c * 8 + e] : make_uint4(0, 0, 0, 0);
-            };
-            fetch(0);
+            const int upto = n_seg == 0 ? min(2, a.nb) : a.nb;  // (the first unit's others: the softmax warps)
+            f.ask(0, upto);
             if (n_seg > 0) ok = wait(&q_free, (n_seg - 1) & 1);
             ++n_seg;
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -193,15 +224,9 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
                     umma::cp_async16(dst + c * kQChunk, in ? qr + c * 64 : a.q, in);
                 }
             }
-            for (int c = 0; c < a.nb; c += 2) {
-                if (c > 0) fetch(c);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t y[32];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[4 * e] = x[8 * k + e].x, y[4 * e + 1] = x[8 * k + e].y, y[4 * e + 2] = x[8 * k + e].z, y[4 * e + 3] = x[8 * k + e].w;
-                    if (c + k < a.nb) umma::tmem_st32(t_q + (c + k) * 32, y);
-                }
+            for (int c = 0; c < upto; c += 2) {
+                if (c > 0) f.ask(c, upto);
+                f.put(t_q, c, upto);
             }
             umma::tmem_st_wait();
             umma::tc_fence_before();
@@ -229,11 +254,11 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp < W0 + 6) {
+    } else if (warp < W0 + 4 + kLoads) {
         // ---- loads -------------------------------------------------------------------------------------
         // A tile's latents take one copy where a page holds the whole tile (the first warp; the second one copies the
-        // rotated parts), else one for each piece of a page and chunk, every other piece by the same warp: a copy takes its
-        // thread about 100 clocks, which with 20 copies a tile (pages of 16) bounded the loop, 3100 clocks with one warp.
+        // rotated parts), else one for each piece of a page and chunk, a warp each piece: a copy takes its thread about 100
+        // clocks, which with 20 copies a tile (pages of 16) bounded the loop, 3100 clocks a tile with one warp, 1900 with two.
         const int me = warp - (W0 + 4), pr_log2 = min(a.page_log2, 6), pr = 1 << pr_log2, pieces = kKeys >> pr_log2;
         const bool one = elected();
         pa::Segment g;
@@ -266,26 +291,23 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
                 const uint32_t dst = c0 + rg.i * stage, dst_r = r0 + rg.i * stage;
                 if (pieces == 1) {
                     const int at = __shfl_sync(0xFFFFFFFFu, now, 0);
-                    if (one) umma::mbar_arrive_expect_tx(bar, at < 0 ? 0 : (me ? a.na : a.nb) * kChunk);
+                    if (one) umma::mbar_arrive_expect_tx(bar, at < 0 || me > 1 ? 0 : (me ? a.na : a.nb) * kChunk);
                     if (at >= 0) {
                         if (me == 0) {
                             if (one) tma_load_3d(dst, &cmap, 0, at, 0, bar);
-                        } else {
+                        } else if (me == 1) {
                             for (int c = 0; c < a.na; ++c)
                                 if (one) tma_load_2d(dst_r + c * kChunk, &rmap, c * 64, at, bar);
                         }
                     }
                 } else {
-                    const uint32_t mine = me ? 0xAu : 0x5u;  // pieces 1, 3 or 0, 2
-                    const int there = __popc(__ballot_sync(0xFFFFFFFFu, now >= 0) & mine);
-                    if (one) umma::mbar_arrive_expect_tx(bar, there * (a.na + a.nb) * (pr * 128));
-                    for (int p = me; p < pieces; p += 2) {
-                        const int at = __shfl_sync(0xFFFFFFFFu, now, p);
-                        if (at < 0) continue;
+                    const int at = __shfl_sync(0xFFFFFFFFu, now, me);  // (-1 past the last piece, too)
+                    if (one) umma::mbar_arrive_expect_tx(bar, at < 0 ? 0 : (a.na + a.nb) * (pr * 128));
+                    if (at >= 0) {
                         for (int c = 0; c < a.nb; ++c)
-                            if (one) tma_load_3d(dst + c * kChunk + p * (pr * 128), &cmap, 0, at, c, bar);
+                            if (one) tma_load_3d(dst + c * kChunk + me * (pr * 128), &cmap, 0, at, c, bar);
                         for (int c = 0; c < a.na; ++c)
-                            if (one) tma_load_2d(dst_r + c * kChunk + p * (pr * 128), &rmap, c * 64, at, bar);
+                            if (one) tma_load_2d(dst_r + c * kChunk + me * (pr * 128), &rmap, c * 64, at, bar);
                     }
                 }
                 if (one) issued[me] = it + 1;
@@ -293,7 +315,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
             }
         }
         __syncwarp();
-    } else if (warp == W0 + 6) {
+    } else if (warp == W0 + 4 + kLoads) {
         // ---- S -----------------------------------------------------------------------------------------
         constexpr uint32_t id = umma::idesc_f16(kRows, kKeys, 1);
         const bool one = elected();
@@ -305,6 +327,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
         while (ok && next_segment(g, n_seg)) {
             const int clear = clear_of(g);
             ok = wait(&q_full, n_seg & 1);
+            if (n_seg == 0) ok = ok && wait(&q_more, 0);
             ++n_seg;
             for (int t = g.t0; t < g.t1; ++t, ++n, rg.next(a.sb)) {
                 const int bf = n & 1;
@@ -340,7 +363,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
         commit(&drain, one);  // all products issued complete before tensor memory goes back
         umma::mbar_wait(&drain, 0, pa::kDrainNs);
         __syncwarp();
-    } else if (warp == W0 + 7) {
+    } else if (warp == W0 + 5 + kLoads) {
         // ---- PV ---------------------------------------------------------------------------------------
         const uint32_t id = umma::idesc_f16_bmn(kRows, a.dv, 1);
         const bool one = elected();
@@ -454,12 +477,14 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
     __syncthreads();
     if (tid == 0 && *vfail) {
         raise_error(a.err, QVG_ERR_TIMEOUT);
-        // The copies in flight land before the CTA ends (where one loading warp got further, the other one's arrival is made up for).
-        const int lo = min(issued[0], issued[1]), hi = max(issued[0], issued[1]);
-        for (int j = lo; j < hi; ++j) umma::mbar_arrive(&full[j % a.sb]);
-        for (int j = max(0, hi - a.sb); j < hi; ++j) umma::mbar_wait(&full[j % a.sb], (j / a.sb) & 1, pa::kDrainNs);
+        // The copies in flight land before the CTA ends (where one loading warp got further, the others' arrivals are made up for).
+        int most = 0;
+        for (int i = 0; i < kLoads; ++i) most = max(most, issued[i]);
+        for (int i = 0; i < kLoads; ++i)
+            for (int j = issued[i]; j < most; ++j) umma::mbar_arrive(&full[j % a.sb]);
+        for (int j = max(0, most - a.sb); j < most; ++j) umma::mbar_wait(&full[j % a.sb], (j / a.sb) & 1, pa::kDrainNs);
     }
-    if (warp == W0 + 7) {
+    if (warp == W0 + 5 + kLoads) {
         umma::tc_fence_after();
         umma::tmem_dealloc(tmem, 512);
     }
