@@ -23,6 +23,10 @@
 namespace qvg {
 namespace la {
 
+// What a unit costs besides its tiles, in tiles: the line counts it, so that a CTA with
+// three short units gets fewer tiles than one inside a long sequence (48 sequences of 700 to
+// 24,000: 89 us without, 84 with).
+constexpr int kUnitCost = 3;
 constexpr int kLoads = 4, kLatentWarps = 4 + 4 + kLoads + 3;
 
 // A unit of which a CTA has a part: the CTAs that share it, its rows (0: there
@@ -414,7 +418,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
             uint32_t w = 0;
             if (b0 + lane < a.B) {
                 q = pa::seq_of<kRows, kKeys>(a, b0 + lane, counting && cta == 0);
-                w = static_cast<uint32_t>(q.rb) * static_cast<uint32_t>(q.nt);
+                w = static_cast<uint32_t>(q.rb) * static_cast<uint32_t>(q.nt + kUnitCost);
             }
             uint32_t x = w;
 #pragma unroll
@@ -444,20 +448,23 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
                 g.nq = __shfl_sync(0xFFFFFFFFu, q.nq, l);
                 g.kv = __shfl_sync(0xFFFFFFFFu, q.kv, l);
                 g.nt = __shfl_sync(0xFFFFFFFFu, q.nt, l);
-                const uint32_t rel = pos - first - (__shfl_sync(0xFFFFFFFFu, x, l) - __shfl_sync(0xFFFFFFFFu, w, l));
-                g.r = static_cast<int>(rel / static_cast<uint32_t>(g.nt));
-                g.t0 = static_cast<int>(rel) - g.r * g.nt;
-                g.t1 = static_cast<int>(min(static_cast<uint32_t>(g.nt), g.t0 + (end - pos)));
+                // `begin`: the unit's, behind which its tiles lie from kUnitCost on
+                const uint32_t rel = pos - first - (__shfl_sync(0xFFFFFFFFu, x, l) - __shfl_sync(0xFFFFFFFFu, w, l)), length = g.nt + kUnitCost;
+                g.r = static_cast<int>(rel / length);
+                const uint32_t begin = pos - (rel - g.r * length), upto = min(end, begin + length);
+                g.t0 = max(0, static_cast<int>(pos - begin) - kUnitCost);
+                g.t1 = max(0, static_cast<int>(upto - begin) - kUnitCost);
+                pos = upto;
+                if (g.t1 <= g.t0) continue;  // (the part ends before the unit's first tile)
                 publish(g);
                 if (!g.whole() && (g.t0 == 0 || n_seg == 1)) {
                     Shared &d = shared[g.t0 == 0 ? 1 : 0];
-                    d.first = static_cast<int>((pos - g.t0) / per);
-                    d.last = static_cast<int>((pos - g.t0 + g.nt - 1) / per);
+                    d.first = static_cast<int>((begin + kUnitCost) / per);
+                    d.last = static_cast<int>((begin + length - 1) / per);
                     d.row0 = g.r * kRows;
                     d.rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(g.nq) * a.grp - d.row0));
                     d.q0 = g.q0;
                 }
-                pos += g.t1 - g.t0;
             }
             if (pos >= end) break;
             first += all;
