@@ -14,17 +14,18 @@ namespace {
 // P parts, m = max m_z, l = sum l_z 2^(m_z - m), O likewise.  The unit that
 // begins in CTA i has its part in slot 1 of CTA i and in slot 0 of the CTAs after
 // it.  A task is 8 rows and some channels of a unit; the unit's CTAs share its
-// tasks, as the blocks x of their numbers.  What bounds it is latency: three
-// reads that wait for one another (the unit, its parts' references and sums, its parts).
+// tasks, as the blocks x of their numbers.  What bounds it is latency: the unit's
+// description, then everything else, the parts (those that registers hold) along with
+// their references and sums.
 //   few parts: a warp a task (64 channels), parts one after another;
 //   many: a block a task (16 channels), each warp every eighth part, whose sums
 //   are added in the warps' order.
 // Either way the result is the same each time.  (A warp a row, part after part: 48 us
 // for 152 parts of 16 rows.)
-constexpr int kJoinWarps = 8, kJoinY = 4, kFewParts = 8, kMostParts = 512;
+constexpr int kJoinWarps = 8, kJoinY = 2, kFewParts = 8, kMostParts = 512, kAhead = 10;
 
 struct JoinRoom {
-    float w[kMostParts][8], red[2][kJoinWarps][8];
+    float w[kMostParts][8], l[kMostParts][8], red[2][kJoinWarps][8];
     float4 acc[kJoinWarps][32];
 };
 
@@ -49,14 +50,20 @@ __device__ __forceinline__ void put_lse(const la::Args &a, const la::Shared &u, 
 }
 
 template <int DC>
-__device__ __forceinline__ void join(const la::Args &a, const la::Shared &u, int rank, JoinRoom &s) {
+__device__ __forceinline__ void join(const la::Args &a, const la::Shared &u, int rank, int y, JoinRoom &s) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r8 = lane & 7, cg = lane >> 3;
     const int parts = min(u.last, static_cast<int>(gridDim.x) - 1) - u.first + 1, octets = (u.rows + 7) / 8;
     auto slot = [&](int z) { return static_cast<size_t>(2 * (u.first + z) + (z == 0 ? 1 : 0)); };
     if (parts <= kFewParts) {
-        for (int task = rank + parts * (blockIdx.y * kJoinWarps + warp); task < octets * (DC / 64); task += parts * (kJoinY * kJoinWarps)) {
+        for (int task = rank + parts * (y * kJoinWarps + warp); task < octets * (DC / 64); task += parts * (kJoinY * kJoinWarps)) {
             const int slice = task % (DC / 64), n = task / (DC / 64) * 8 + r8;
             const float *src = a.po + (static_cast<size_t>(slice * 16 + cg) * la::kRows + n) * 4;
+            auto part = [&](int z, int i) { return *reinterpret_cast<const float4 *>(src + slot(z) * (la::kRows * DC) + i * (16 * la::kRows)); };
+            float4 x[2][4];
+#pragma unroll
+            for (int z = 0; z < 2; ++z)  // (a shared unit has two parts at least)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[z][i] = part(z, i);
             float pm[2], w[2], m = -INFINITY, l = 0.0f;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -76,12 +83,17 @@ __device__ __forceinline__ void join(const la::Args &a, const la::Shared &u, int
             l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
             l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
             float4 acc[4] = {};
-#pragma unroll 2
-            for (int z = 0; z < parts; ++z) {
-                const float e = __shfl_sync(0xFFFFFFFFu, z < 4 ? w[0] : w[1], (z & 3) * 8 + r8);
+            for (int z0 = 0; z0 < parts; z0 += 2) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    add_weighed(acc[i], e, *reinterpret_cast<const float4 *>(src + slot(z) * (la::kRows * DC) + i * (16 * la::kRows)));
+                for (int k = 0; k < 2; ++k) {
+                    const float e = __shfl_sync(0xFFFFFFFFu, z0 < 4 ? w[0] : w[1], ((z0 + k) & 3) * 8 + r8);  // (0 past the last part)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) add_weighed(acc[i], e, x[k][i]);
+                    if (z0 + 2 + k < parts) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[k][i] = part(z0 + 2 + k, i);
+                    }
+                }
             }
             if (n >= u.rows) continue;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -91,15 +103,22 @@ __device__ __forceinline__ void join(const la::Args &a, const la::Shared &u, int
         }
         return;
     }
-    for (int task = rank + parts * blockIdx.y; task < octets * (DC / 16); task += parts * kJoinY) {
+    for (int task = rank + parts * y; task < octets * (DC / 16); task += parts * kJoinY) {
         const int slice = task % (DC / 16), n = task / (DC / 16) * 8 + r8, z0 = tid >> 3;
         const float *src = a.po + (static_cast<size_t>(slice * 4 + cg) * la::kRows + n) * 4;
         float m = -INFINITY, l = 0.0f;
+        float4 x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (warp + k * kJoinWarps < parts) x[k] = *reinterpret_cast<const float4 *>(src + slot(warp + k * kJoinWarps) * (la::kRows * DC));
         __syncthreads();  // (the last task's room has been read)
         // thread (row r8, parts z0 + 32 k)
+#pragma unroll 5
         for (int z = z0; z < parts; z += 32) {
-            s.w[z][r8] = a.pm[slot(z) * la::kRows + n];
-            m = fmaxf(m, s.w[z][r8]);
+            const float y = a.pm[slot(z) * la::kRows + n];
+            s.w[z][r8] = y;
+            s.l[z][r8] = a.pl[slot(z) * la::kRows + n];
+            m = fmaxf(m, y);
         }
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
@@ -108,7 +127,7 @@ __device__ __forceinline__ void join(const la::Args &a, const la::Shared &u, int
 #pragma unroll
         for (int k = 0; k < kJoinWarps; ++k) m = fmaxf(m, s.red[0][k][r8]);
         for (int z = z0; z < parts; z += 32) {
-            const float lz = a.pl[slot(z) * la::kRows + n], e = lz == 0.0f ? 0.0f : exp2f(s.w[z][r8] - m);
+            const float lz = s.l[z][r8], e = lz == 0.0f ? 0.0f : exp2f(s.w[z][r8] - m);
             l = fmaf(lz, e, l);
             s.w[z][r8] = e;
         }
@@ -120,8 +139,11 @@ __device__ __forceinline__ void join(const la::Args &a, const la::Shared &u, int
 #pragma unroll
         for (int k = 0; k < kJoinWarps; ++k) l += s.red[1][k][r8];
         float4 acc = {};
-#pragma unroll 8
-        for (int z = warp; z < parts; z += kJoinWarps)
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (warp + k * kJoinWarps < parts) add_weighed(acc, s.w[warp + k * kJoinWarps][r8], x[k]);
+#pragma unroll 4
+        for (int z = warp + kAhead * kJoinWarps; z < parts; z += kJoinWarps)
             add_weighed(acc, s.w[z][r8], *reinterpret_cast<const float4 *>(src + slot(z) * (la::kRows * DC)));
         s.acc[warp][lane] = acc;
         __syncthreads();
@@ -134,15 +156,14 @@ __device__ __forceinline__ void join(const la::Args &a, const la::Shared &u, int
     }
 }
 
+// blockIdx.y: which of the CTA's two shared units, and a share of the tasks.
 template <int DC>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_latent_merge(const __grid_constant__ la::Args a) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) k_latent_merge(const __grid_constant__ la::Args a) {
     __shared__ JoinRoom s;
     pdl_wait();
-    const int x = blockIdx.x;
-    const la::Shared *d = reinterpret_cast<const la::Shared *>(a.desc) + 2 * x;
-    const la::Shared u[2] = {d[0], d[1]};
-    if (u[0].rows > 0) join<DC>(a, u[0], x - u[0].first, s);
-    if (u[1].rows > 0) join<DC>(a, u[1], 0, s);
+    const int x = blockIdx.x, which = blockIdx.y & 1;
+    const la::Shared u = reinterpret_cast<const la::Shared *>(a.desc)[2 * x + which];
+    if (u.rows > 0) join<DC>(a, u, which ? 0 : x - u.first, blockIdx.y >> 1, s);
 }
 
 // CTAs of the absorbed form: one an SM (and no unit may have more parts than the join has room for).
@@ -222,7 +243,7 @@ qvg_status launch_expanded(const CUtensorMap (&map)[5], la::Args &a, int grid, i
 
 template <int DC>
 qvg_status launch_merge(const la::Args &a, int ctas, cudaStream_t st) {
-    const cudaError_t e = launch_pdl(k_latent_merge<DC>, dim3(ctas, kJoinY), dim3(kJoinWarps * 32), 0, st, a);
+    const cudaError_t e = launch_pdl(k_latent_merge<DC>, dim3(ctas, 2 * kJoinY), dim3(kJoinWarps * 32), 0, st, a);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
         note_cuda_error(e);

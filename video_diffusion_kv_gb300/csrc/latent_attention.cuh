@@ -26,7 +26,7 @@ namespace la {
 // What a unit costs besides its tiles, in tiles: the line counts it, so that a CTA with
 // three short units gets fewer tiles than one inside a long sequence (48 sequences of 700 to
 // 24,000: 89 us without, 84 with).
-constexpr int kUnitCost = 3;
+constexpr int kUnitCost = 5;
 constexpr int kLoads = 4, kLatentWarps = 4 + 4 + kLoads + 3;
 
 // A unit of which a CTA has a part: the CTAs that share it, its rows (0: there
