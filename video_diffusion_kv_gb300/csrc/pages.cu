@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kCopyThreads) k_pages_copy(const __grid_consta
 
 // ---- compact ----------------------------------------------------------------------
 
-constexpr int kMoveThreads = 256, kMoveEach = 8;
+constexpr int kMoveThreads = 256, kMoveEach = 4;
 
 struct Move {
     const int32_t *table, *first, *keep, *n_keep;
@@ -348,9 +348,10 @@ struct Slots {
 // batch writes over has been read in this batch or an earlier one, never is to be
 // read in a later one, and the slices do not touch one another.
 //   Reads run ahead: while a batch is written the next one's bytes are on their way, and the
-// pages and numbers of the three after that.  (Bytes after their pages, pages after their
-// numbers, a batch after the other: 262 us for 60,000 tokens of 8 heads of 128; only the
-// bytes ahead: 139.)
+// pages and numbers of the three after that.  What bounds it is this chain, about 1.5 us a
+// batch, in the longest sequence.  (Bytes after their pages, pages after their numbers, a batch
+// after the other: 262 us for 60,000 tokens of 8 heads of 128, which take 72 so; a third
+// batch of bytes ahead costs the registers of a third block an SM: 83.)
 template <typename T>
 __device__ __forceinline__ void move_rows(const Buffers &a, const Move &m, Slots &s, int b, int i, int h, int col, int width, int n) {
     const int per = kMoveThreads / width;  // rows side by side
@@ -380,25 +381,23 @@ __device__ __forceinline__ void move_rows(const Buffers &a, const Move &m, Slots
         if (!has) return;
         const int y = first + batch * rows + threadIdx.x, e = batch % 3;
         // row (page, head, offset)
-        s.from[e][threadIdx.x] = x < 0 ? -1 : (page_from * heads + lift + (x & mask)) * rb;
+        s.from[e][threadIdx.x] = x < 0 ? 0 : (page_from * heads + lift + (x & mask)) * rb;
         s.to[e][threadIdx.x] = x < 0 ? -1 : (page_to * heads + lift + (y & mask)) * rb;
     };
     T v[2][kMoveEach];
+    // (Loads are made whether their token moves or not, in place of branches that would wait for them.)
+    const int mine = min(r, per - 1);
     auto read = [&](int batch, T(&x)[kMoveEach]) {
 #pragma unroll
         for (int e = 0; e < kMoveEach; ++e)
-            if (e < each && r < per) {
-                const long long f = s.from[batch % 3][e * per + r];
-                if (f >= 0) x[e] = *reinterpret_cast<const T *>(base + f);
-            }
+            x[e] = *reinterpret_cast<const T *>(base + s.from[batch % 3][min(e, each - 1) * per + mine]);
     };
     auto write = [&](int batch, const T(&x)[kMoveEach]) {
 #pragma unroll
-        for (int e = 0; e < kMoveEach; ++e)
-            if (e < each && r < per) {
-                const long long t = s.to[batch % 3][e * per + r];
-                if (t >= 0) *reinterpret_cast<T *>(base + t) = x[e];
-            }
+        for (int e = 0; e < kMoveEach; ++e) {
+            const long long t = s.to[batch % 3][min(e, each - 1) * per + mine];
+            if (t >= 0 && e < each && r < per) *reinterpret_cast<T *>(base + t) = x[e];
+        }
     };
     const int batches = (n + rows - 1) / rows;
     for (int k = 0; k < 2; ++k) {
@@ -426,7 +425,7 @@ __device__ __forceinline__ void move_rows(const Buffers &a, const Move &m, Slots
     }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) k_paged_compact(const __grid_constant__ Buffers a, const __grid_constant__ Move m) {
+__global__ void __launch_bounds__(kMoveThreads, 3) k_paged_compact(const __grid_constant__ Buffers a, const __grid_constant__ Move m) {
     __shared__ Slots s;
     const int b = blockIdx.y, n = m.n_keep[b], first = m.first[b];
     bool bad = n < 0 || n > m.keep_stride || first < 0;
