@@ -541,6 +541,18 @@ def test_long_prompt():
     p.check(out, lse, CAUSAL)
 
 
+@pytest.mark.parametrize("B", [20, 300, 1200])
+def test_many_ragged_prompts(B):
+    """Blocks of rows that are ranked by length, and more of them than that."""
+    nq = tuple((37 * i) % 90 if i % 11 else 300 for i in range(B))
+    p = Prompt(2, 64, 8, 64, nq, tuple((13 * i) % 70 for i in range(B)), seed=B)
+    out, lse = p.run()
+    p.check(out, lse, CAUSAL)
+    p.cu_k[5] = p.cu_k[4] - 1  # a length below 0
+    p.run()
+    assert qvg.get_status() == qvg.QVG_ERR_INVALID_ARG
+
+
 def test_prompts_with_more_new_tokens_than_keys():
     p = Prompt(2, 64, 16, 64, (300, 40, 7), (-200, -40, -3), seed=21)  # 100, 0 and 4 keys
     for mode in (NONE, CAUSAL):

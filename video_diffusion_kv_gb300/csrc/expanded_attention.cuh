@@ -58,26 +58,66 @@ __device__ __forceinline__ Unit unit_of(const Args &a, int b, int r, int h, bool
     return u;
 }
 
-// The CTA's (sequence, block of rows): heads of the longest come first, so that the short
-// ones fill the GPU's end.  Up to kSorted pairs are ranked by their tiles (each CTA
-// does it for itself: they all get the same order); of more, and of one sequence, the
-// last rows come first, which with a causal mask see the most keys.
+// The CTA's (sequence, block of rows); y < 0: none.  All heads of a block follow one another.
+// - One sequence: the last rows first, which with a causal mask see the most keys.
+// - Up to kSorted possible blocks: ranked by their tiles (each CTA does it for itself: they
+//   all get the same order), so that the short ones fill the GPU's end.
+// - More: the blocks that there are, sequence by sequence, found from the lengths.
+// `room`: shared memory for kSorted integers.
 constexpr int kSorted = 256;
-__device__ __forceinline__ int2 pick(const Args &a, int blocks, uint32_t *key, int *got) {
-    const int n = a.B * blocks, want = blockIdx.x / a.H, i = threadIdx.x;
-    if (a.B == 1 || n > kSorted) return make_int2(want % a.B, blocks - 1 - want / a.B);
-    if (i < n) {
-        const Unit u = unit_of(a, i % a.B, blocks - 1 - i / a.B, 0, false);
-        key[i] = static_cast<uint32_t>(u.r * kPromptRows < u.nq ? min(max(u.nt[0], u.nt[1]) + 1, (1 << 24) - 1) : 0) << 8 | static_cast<uint32_t>(255 - i);
+__host__ __device__ inline int pair_count(int B, int blocks, int total_q) {
+    const long long n = static_cast<long long>(B) * blocks, most = total_q / kPromptRows + static_cast<long long>(B);
+    return static_cast<int>(n <= kSorted || n < most ? n : most);
+}
+__device__ __forceinline__ int2 pick(const Args &a, int blocks, uint32_t *room, int *got) {
+    const long long n = static_cast<long long>(a.B) * blocks;
+    const int want = blockIdx.x / a.H, i = threadIdx.x;
+    if (a.B == 1) return make_int2(0, blocks - 1 - want);
+    if (i == 0) *got = -1;
+    if (n <= kSorted) {
+        if (i < n) {
+            const Unit u = unit_of(a, i % a.B, blocks - 1 - i / a.B, 0, false);
+            room[i] = static_cast<uint32_t>(u.r * kPromptRows < u.nq ? min(max(u.nt[0], u.nt[1]) + 1, (1 << 24) - 1) : 0) << 8 | static_cast<uint32_t>(255 - i);
+        }
+        __syncthreads();
+        if (i < n) {
+            int rank = 0;
+            for (int j = 0; j < n; ++j) rank += room[j] > room[i];
+            if (rank == want) *got = i;
+        }
+        __syncthreads();
+        return make_int2(*got % a.B, blocks - 1 - *got / a.B);
     }
-    __syncthreads();
-    if (i < n) {
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += key[j] > key[i];
-        if (rank == want) *got = i;
+    const int lane = i & 31, warp = i >> 5;
+    long long before = 0;
+    int r = -1;
+    for (int b0 = 0; b0 < a.B; b0 += kPromptWarps * 32) {
+        const int b = b0 + i;
+        int mine = 0;
+        if (b < a.B) mine = (unit_of(a, b, 0, 0, blockIdx.x == 0).nq + kPromptRows - 1) / kPromptRows;
+        int x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) room[warp] = x;
+        __syncthreads();
+        int base = 0, all = 0;
+        for (int k = 0; k < kPromptWarps; ++k) {
+            base += k < warp ? static_cast<int>(room[k]) : 0;
+            all += static_cast<int>(room[k]);
+        }
+        const long long end = before + base + x;
+        if (want < end && want >= end - mine) {
+            *got = b;
+            room[kPromptWarps] = static_cast<uint32_t>(end - 1 - want);
+        }
+        before += all;
+        __syncthreads();
     }
-    __syncthreads();
-    return make_int2(*got % a.B, blocks - 1 - *got / a.B);
+    if (*got >= 0) r = static_cast<int>(room[kPromptWarps]);
+    return make_int2(max(*got, 0), r);
 }
 
 // qmap, rqmap: q and its rotated part; kmap, rkmap: k and the rotated key parts; vmap: v.
@@ -94,9 +134,11 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
 
     __shared__ int picked;
     const int2 br = pick(a, blocks, reinterpret_cast<uint32_t *>(dyn), &picked);
+    if (br.y < 0) return;
     const int head = blockIdx.x % a.H;
     const Unit u = unit_of(a, br.x, br.y, head, br.y == 0 && head == 0 && threadIdx.x == 0);
     if (u.r * kPromptRows >= u.nq) return;
+    umma::fence_proxy_async_smem();  // (the room for the pick becomes the copies')
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q_group = a.na * kQChunk, a_bytes = a.na * kKChunk, b_bytes = a.nb * kChunk;
     uint8_t *base = dyn + ((1024u - (umma::smem_u32(dyn) & 1023u)) & 1023u);

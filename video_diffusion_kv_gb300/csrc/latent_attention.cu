@@ -378,8 +378,10 @@ qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, con
         return QVG_ERR_INVALID_ARG;
     if (misaligned(out, 16) || (cu_q && misaligned(cu_q, 4)) || (cu_k && misaligned(cu_k, 4)) || (lse && misaligned(lse, 4)))
         return QVG_ERR_INVALID_ARG;
-    const int64_t blocks = ceil_div(max_q, 256), grid = blocks * B * H;
-    if (max_q > INT32_MAX - 256 || static_cast<int64_t>(B) * H > INT32_MAX || grid > INT32_MAX) return QVG_ERR_UNSUPPORTED;
+    if (max_q > INT32_MAX - la::kPromptRows) return QVG_ERR_UNSUPPORTED;
+    const int blocks = ceil_div(max_q, la::kPromptRows);
+    const int64_t grid = static_cast<int64_t>(la::pair_count(B, blocks, total_q)) * H;
+    if (grid > INT32_MAX) return QVG_ERR_UNSUPPORTED;
     CUtensorMap map[5] = {};
     if (!chunk_map(&map[0], q->data, dn, H, total_q, q->head_stride, q->token_stride, la::kRows, dn / 64) ||
         (dr > 0 && !rotated_map(&map[1], q_rope->data, dr, H, total_q, q_rope->head_stride, q_rope->token_stride, la::kRows)) ||
@@ -411,7 +413,7 @@ qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, con
     a.err = device_error_word();
     a.wait_ns = wait_limit_ns();
     a.inject = wait_inject();
-    return launch_expanded(map, a, static_cast<int>(grid), static_cast<int>(blocks), static_cast<cudaStream_t>(stream));
+    return launch_expanded(map, a, static_cast<int>(grid), blocks, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

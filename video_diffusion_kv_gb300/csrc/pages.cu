@@ -437,7 +437,8 @@ __global__ void __launch_bounds__(kMoveThreads, 3) k_paged_compact(const __grid_
             const int x = keep[k];
             const bool off = x < (k ? keep[k - 1] + 1ll : static_cast<long long>(first)) || x >= room || x < first;
             // (where keep ascends, first + k does not pass x)
-            const int p = off ? -1 : row[x >> a.page_log2], to = off || first + k > x ? 0 : row[(first + k) >> a.page_log2];
+            const bool past = static_cast<long long>(first) + k > x;
+            const int p = off ? -1 : row[x >> a.page_log2], to = off || past ? 0 : row[(first + k) >> a.page_log2];
             bad = bad || p < 0 || p >= a.num_pages || to < 0 || to >= a.num_pages;
         }
     }
