@@ -777,6 +777,12 @@ qvg_status qvg_latent_workspace_size(int32_t dc, int32_t dr, size_t *bytes);
  * that sees a token that is NaN, gives NaN.  The results do not depend on what
  * else the GPU runs.  All sizes on the device are read when the kernels run: a
  * captured call can be replayed with other lengths, tables and masks.
+ * QVG_ERR_INVALID_ARG for sizes, modes, a scale or strides outside the above,
+ * and missing or misaligned pointers; QVG_ERR_UNSUPPORTED for another dc,
+ * max_q * Hq above 2^31 - 129, or num_pages * page_size above 2^31 - 1;
+ * QVG_ERR_WORKSPACE for a workspace missing, too small or misaligned.  A
+ * sequence of 2^32 tiles (64 keys x 128 rows) or more latches
+ * QVG_ERR_INVALID_ARG.
  */
 qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, const qvg_view *q_rope, int32_t total_q,
                                 int32_t Hq, int32_t B, int32_t max_q, const int32_t *cu_q, const int32_t *table,
@@ -808,6 +814,8 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
  *   lse        fp32 [H][total_q] or NULL, as in qvg_paged_attention.
  * Rounding, NaN and unseen keys as in qvg_latent_attention (a row that sees a
  * value with an infinity or a NaN may be NaN in all its channels).
+ * QVG_ERR_INVALID_ARG as there; QVG_ERR_UNSUPPORTED for another dn or dv, dr
+ * above 64, max_q above 2^31 - 257, or more than 2^31 - 1 blocks of 256 rows.
  */
 qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, const qvg_view *k, const qvg_view *k_rope,
                                   const qvg_view *v, int32_t total_q, int32_t total_k, int32_t H, int32_t dn, int32_t dr,
@@ -932,6 +940,7 @@ qvg_status qvg_pages_copy(const qvg_page_rows *rows, const int32_t *copies, int3
  * n_keep outside 0 .. keep_stride, a negative first, a keep that does not
  * ascend or is beyond the row, and a page outside the cache latch
  * QVG_ERR_INVALID_ARG; that sequence is left as it was.
+ * QVG_ERR_UNSUPPORTED for B above 65535.
  */
 qvg_status qvg_paged_compact(const qvg_page_rows *rows, const int32_t *table, int32_t table_stride, int32_t B,
                              const int32_t *first, const int32_t *keep, int32_t keep_stride, const int32_t *n_keep,

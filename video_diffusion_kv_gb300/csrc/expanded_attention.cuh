@@ -7,6 +7,17 @@
 // while the second half's weights are made.  One group's products run while the other group is
 // at its softmax.
 //
+// Bound: a group's chain, 4700 clocks for 128 keys of 128 + 64 channels (stamped): S 1430, the
+// first half's softmax 900, the step to the second 300, its softmax 1140, PV until the next S 920.
+//   4680 causal tokens of 16 heads
+// (1.1e11 operations): 103 us, 1.09 PFLOP/s, 56 % of a large bf16 product's rate;
+// without the mask 176 us, 1.27 PFLOP/s.  12 prompts of 1 to 1100 tokens after 0 to 1700, 8 heads, 64 + 32
+// channels: 51 us, the longest unit's 44 tiles.
+//   Tried and slower: two threads a row, a half each (157 us for the first case: they meet
+// once a tile, and V's tiles come too late with the room that is left), a part of the weights' powers by a
+// polynomial beside the special function unit (112 us and more), S of 64 keys with two
+// buffers (a product of 64 columns takes 73 clocks, one of 128 about 60).
+//
 // Tensor memory: O 2 x 128 columns, S 2 x 128.
 // Roles: softmax (8 warps, thread = row), helpers (4: V in tiles that some row
 // does not see all of), loads of Q and K, of V, and each group's products.

@@ -48,8 +48,9 @@ __device__ __forceinline__ bool not_finite(uint4 v) {  // any of eight bf16 numb
 // past the rotated ones is two neighbours), so a pair turns within its lane; the lane's
 // steps and axes stay in registers.  A token that holds an infinity or a NaN (before
 // the rotation or after) becomes NaN throughout.
-// Bound by HBM: 4 (dc + dr) bytes a token.  (One token a warp, its channels in eights and the
-// partners through shared memory: 25 us for 37,440 tokens of 256 + 64 channels, 48.7 MB.)
+// Bound by the instructions (215 a token, most of them the angles') beside HBM, 4 (dc + dr)
+// bytes a token: 37,440 tokens of 256 + 64 channels, 48.7 MB, three axes: 12 us, 4.1 TB/s.  (One token
+// a warp, its channels in eights and the partners through shared memory: 25 us.)
 struct Token {
     long long slot;
     uint4 c;
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
 }
 
-// One warp per token.  Bound by HBM.
+// One warp per token: two loads and two stores a lane.  Bound by HBM.
 __global__ void __launch_bounds__(kWarps * 32) k_latent_read(LatentArgs a, const int64_t *__restrict__ slots, int n,
                                                             uint16_t *__restrict__ c_out, uint16_t *__restrict__ kr_out) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -13,6 +13,13 @@
 // in shared memory.  S has two buffers of 64 columns, so that the next tile's S runs while
 // this tile's softmax does.
 //
+// Bound: HBM for single tokens (a tile of 40 KB comes in 0.9 us, which is the rate of a
+// plain copy), the products for many rows.  One token of 16 heads over
+// 449,280 (256 + 64 channels, 288 MB): 60 us, 4.8 TB/s; of it 5 to 7 us until a CTA's
+// first tile is there, 2 to 3 for the last tile and its sums, 8 for the join.  48 tokens of 32 heads over 700 to 24,000
+// (381 MB): 74 us, 5.1 TB/s.  16 trees of 17 to 48 tokens, 16 heads, pages of 16 (6.8e10
+// operations): 73 us, 930 TFLOP/s, 48 % of a large bf16 product's rate.
+//
 // Tensor memory: O 256 columns, S 2 x 64, Q 128.
 // Roles: softmax (4 warps, thread = row), helpers (4: Q, and V in tiles that
 // some row does not see all of), loads (4), S, PV, segments.
@@ -25,7 +32,7 @@ namespace la {
 
 // What a unit costs besides its tiles, in tiles: the line counts it, so that a CTA with
 // three short units gets fewer tiles than one inside a long sequence (48 sequences of 700 to
-// 24,000: 89 us without, 84 with).
+// 24,000: 89 us without, 85 with).
 constexpr int kUnitCost = 5;
 constexpr int kLoads = 4, kLatentWarps = 4 + 4 + kLoads + 3;
 

@@ -140,7 +140,7 @@ constexpr int kChunks = 256;
 
 // The CTA's part of the line, made by one whole warp.  (Its walks end with the
 // batch even if the lengths change meanwhile.)
-template <int NB, int TILE = kTile>
+template <int NB>
 struct Line {
     long long pos, end, first, per;  // first: where sequence b begins
     int b;
@@ -155,7 +155,7 @@ struct Line {
         long long total = 0;
         for (int k = 0, b0 = 0; b0 < a.B; ++k, b0 += span) {
             long long mine = 0;
-            for (int i = b0 + lane; i < min(a.B, b0 + span); i += 32) mine += seq_of<NB, TILE>(a, i, cta == 0).tiles(a.H);
+            for (int i = b0 + lane; i < min(a.B, b0 + span); i += 32) mine += seq_of<NB>(a, i, cta == 0).tiles(a.H);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
             if (lane == 0) chunk[k] = mine;
@@ -171,7 +171,7 @@ struct Line {
             int k = 0;
             while (pos >= first + chunk[k]) first += chunk[k++];
             for (b = k * span; b < a.B; b += 32) {
-                const long long w = b + lane < a.B ? seq_of<NB, TILE>(a, b + lane, false).tiles(a.H) : 0;
+                const long long w = b + lane < a.B ? seq_of<NB>(a, b + lane, false).tiles(a.H) : 0;
                 long long x = w;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -190,7 +190,7 @@ struct Line {
         }
         cut = make_int4(-1, 0, 0, 0);
         if (b >= a.B) pos = end;
-        s = seq_of<NB, TILE>(a, min(b, a.B - 1), false);
+        s = seq_of<NB>(a, min(b, a.B - 1), false);
     }
 
     // t1 = 0: no more.
@@ -199,7 +199,7 @@ struct Line {
         if (pos >= end) return;
         while (b < a.B && pos >= first + s.tiles(a.H)) {
             first += s.tiles(a.H);
-            s = seq_of<NB, TILE>(a, min(++b, a.B - 1), false);
+            s = seq_of<NB>(a, min(++b, a.B - 1), false);
         }
         if (b >= a.B) return;
         const uint32_t rel = static_cast<uint32_t>(pos - first), u = rel / static_cast<uint32_t>(s.nt);
