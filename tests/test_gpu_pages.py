@@ -156,6 +156,21 @@ def test_no_room():
     assert qvg.get_status() == OK
 
 
+def test_an_invalid_argument_comes_before_a_lack_of_room():
+    """Whichever sequence has which, also where one thread meets both."""
+    B = 1030
+    for bad, long in ((0, 1024), (1024, 0), (3, 4)):
+        pool, table, lens = qvg.PagePool(8), torch.zeros(B, 2, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+        lens[bad], lens[long] = -1, 32  # (a row of two pages of 16 is full)
+        before = lens.clone()
+        slots, copies = qvg.pages_reserve(pool, 16, table, lens)
+        assert qvg.get_status() == BAD
+        assert (slots == -1).all() and (copies == -1).all() and torch.equal(lens, before) and not pool.refs.any()
+        lens[bad] = 0
+        slots, copies = qvg.pages_reserve(pool, 16, table, lens)
+        assert qvg.get_status() == qvg.QVG_ERR_CAPACITY and (slots == -1).all()
+
+
 def test_bad_arguments_on_the_device():
     b = Both(30, 6, 4, 16)
     b.reserve([20, 5, 40, 0, 0, 0])

@@ -169,18 +169,18 @@ __global__ void __launch_bounds__(kReserve) k_pages_reserve(Batch a, Reserve r) 
     __shared__ int s_count[kReserveWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int mask = (1 << a.page_log2) - 1;
-    int bad = 0;  // the status the call ends with
+    bool wrong = false, full = false;  // an argument, the room
     for (int b = tid; b < a.B; b += kReserve) {
         const int n = r.start(b + 1) - r.start(b), L = a.kv_len[b];
         int2 cp = make_int2(-1, -1);
         if (n < 0 || r.start(b) < 0 || r.start(b + 1) > r.total || L < 0) {
-            bad = QVG_ERR_INVALID_ARG;
+            wrong = true;
         } else if (a.pages(static_cast<long long>(L) + n) > a.stride || static_cast<long long>(L) + n > INT32_MAX) {
-            bad = max(bad, static_cast<int>(QVG_ERR_CAPACITY));
+            full = true;
         } else if (n > 0 && (L & mask) != 0) {
             const int page = a.row(b)[L >> a.page_log2];
             if (page < 0 || page >= a.num_pages) {
-                bad = QVG_ERR_INVALID_ARG;
+                wrong = true;
             } else if (a.refs[page] > 1) {
                 cp.x = page;
                 r.list[page] = 0;
@@ -189,9 +189,9 @@ __global__ void __launch_bounds__(kReserve) k_pages_reserve(Batch a, Reserve r) 
         }
         reinterpret_cast<int2 *>(r.copies)[b] = cp;
     }
-    if (tid == 0 && a.B > 0 && (r.start(0) != 0 || r.start(a.B) != r.total)) bad = QVG_ERR_INVALID_ARG;
+    if (tid == 0 && a.B > 0 && (r.start(0) != 0 || r.start(a.B) != r.total)) wrong = true;
     // (an invalid argument is reported before a lack of room)
-    const bool invalid = __syncthreads_or(bad == QVG_ERR_INVALID_ARG), narrow = __syncthreads_or(bad == QVG_ERR_CAPACITY);
+    const bool invalid = __syncthreads_or(wrong), narrow = __syncthreads_or(full);
     long long need = 0;
     bool ok = !invalid && !narrow;
     if (ok) {
