@@ -726,7 +726,8 @@ qvg_status qvg_latent_bytes(int32_t dc, int32_t dr, int32_t page_size, int32_t n
  * A slot at or beyond the cache's end is skipped and latches
  * QVG_ERR_INVALID_ARG.  Nothing but the tokens' slots is written.
  * Errors: QVG_ERR_INVALID_ARG for a bad cache or plan, n < 0, missing or
- * misaligned pointers, bad strides; QVG_ERR_UNSUPPORTED for another dc.
+ * misaligned pointers, bad strides; QVG_ERR_UNSUPPORTED for another dc, and
+ * for n above 2^30.
  */
 qvg_status qvg_latent_append(const qvg_latent *cache, const void *c_bf16, const void *k_rope_bf16, int32_t n,
                              int64_t c_stride, int64_t kr_stride, const int64_t *slots, const qvg_rope_plan *plan,
@@ -860,7 +861,7 @@ typedef struct {
  * be a parent in the same call.  A pair that breaks this, names a sequence
  * outside the batch, or a parent with more pages than its row, is left out and
  * latches QVG_ERR_INVALID_ARG; so does a page outside the pool, whose entry is
- * copied all the same.
+ * copied all the same.  QVG_ERR_UNSUPPORTED for n above 2^20.
  */
 qvg_status qvg_pages_fork(const qvg_page_pool *pool, const qvg_sequences *seqs, const int32_t *parents,
                           const int32_t *children, int32_t n, void *stream);
@@ -871,7 +872,7 @@ qvg_status qvg_pages_fork(const qvg_page_pool *pool, const qvg_sequences *seqs, 
  * and free where nobody holds them.  A sequence outside the batch, one named
  * twice, and a keep outside 0 .. kv_len is left as it was and latches
  * QVG_ERR_INVALID_ARG; a page outside the pool or held by nobody latches it and
- * is passed over.
+ * is passed over.  QVG_ERR_UNSUPPORTED for n above 2^20.
  */
 qvg_status qvg_pages_release(const qvg_page_pool *pool, const qvg_sequences *seqs, const int32_t *ids,
                              const int32_t *keep, int32_t n, void *stream);
@@ -899,6 +900,7 @@ qvg_status qvg_pages_workspace_size(int32_t num_pages, int32_t B, size_t *bytes)
  * cu_new does not ascend from 0 to total, kv_len is negative or a
  * shared page lies outside the pool, the same with QVG_ERR_INVALID_ARG.
  *   workspace  at least qvg_pages_workspace_size(num_pages, B) bytes.
+ * QVG_ERR_UNSUPPORTED for B, total or num_pages above 2^31 - 2049.
  */
 qvg_status qvg_pages_reserve(const qvg_page_pool *pool, const qvg_sequences *seqs, const int32_t *cu_new, int32_t n_new,
                              int32_t total, int64_t *slots, int32_t *copies, void *workspace, size_t ws_bytes,
@@ -925,6 +927,7 @@ qvg_status qvg_latent_rows(const qvg_latent *cache, qvg_page_rows *rows);
  * negative page is passed over, one with a page beyond the cache latches
  * QVG_ERR_INVALID_ARG and is passed over.  The copies run at the same time: no
  * page may be written twice, or be both read and written.
+ * QVG_ERR_UNSUPPORTED for n above 2^31 - 65536.
  */
 qvg_status qvg_pages_copy(const qvg_page_rows *rows, const int32_t *copies, int32_t n, void *stream);
 

@@ -77,6 +77,8 @@ def test_append_and_read_refusals(lib):
     assert lib.qvg_latent_read(latent(), P, 1, 0x10008, P, None) == BAD
     assert lib.qvg_latent_read(latent(), P, 1, P, 0x10008, None) == BAD
     assert lib.qvg_latent_read(latent(), P, 1, None, None, None) == qvg.QVG_OK
+    assert lib.qvg_latent_read(latent(), P, 2 ** 30 + 1, P, P, None) == UNS
+    assert lib.qvg_latent_append(latent(), P, P, 2 ** 30 + 1, 128, 32, P, None, None, None) == UNS
     assert lib.qvg_latent_read(latent(), None, 0, P, P, None) == qvg.QVG_OK
 
 
@@ -156,6 +158,10 @@ def test_page_calls_refusals(lib):
     for kw in (dict(ws=None), dict(ws=0x10008), dict(size=8)):
         assert grow(**kw) == WS, kw
     assert grow(s=seqs(B=0, table=None, kv=None), total=0) == qvg.QVG_OK
+    most = 2 ** 31 - 2049  # (one less reaches the workspace's check)
+    assert fork(n=2 ** 20 + 1) == UNS and cut(n=2 ** 20 + 1) == UNS
+    assert grow(total=most + 1) == UNS and grow(p=pool(most + 1)) == UNS and grow(s=seqs(B=most + 1)) == UNS
+    assert grow(total=most, ws=None) == WS and grow(p=pool(most)) == WS
     size = ct.c_size_t()
     assert lib.qvg_pages_workspace_size(8, 3, ct.byref(size)) == qvg.QVG_OK and size.value >= 4 * (2 * 8 + 3)
     assert lib.qvg_pages_workspace_size(0, 3, ct.byref(size)) == BAD
@@ -190,7 +196,7 @@ def test_moves_refusals(lib):
     assert copy(n=-1) == BAD and copy(c=None) == BAD and copy(c=ODD) == BAD and copy(n=0, c=None) == qvg.QVG_OK
     for kw in (dict(t=None), dict(t=ODD), dict(stride=0), dict(B=-1), dict(first=None), dict(keep=None), dict(keep=ODD), dict(ks=-1), dict(n=None)):
         assert pack(**kw) == BAD, kw
-    assert pack(B=65536) == UNS
+    assert pack(B=65536) == UNS and copy(n=2 ** 31 - 65535) == UNS
     assert pack(B=0, t=None) == qvg.QVG_OK and pack(ks=0, keep=None) == qvg.QVG_OK
 
 

@@ -58,6 +58,8 @@ struct Token {
     int32_t pos[2];
 };
 
+constexpr int kMostTokens = 1 << 30;  // of a call: the warps' indices step past the last one in 32 bits
+
 template <bool HALF>
 __global__ void __launch_bounds__(kWarps * 32)
     k_latent_append(const __grid_constant__ RopeArgs r, LatentArgs a, const uint16_t *__restrict__ c, const uint16_t *__restrict__ kr,
@@ -184,6 +186,7 @@ qvg_status qvg_latent_append(const qvg_latent *cache, const void *c_bf16, const 
     if (misaligned(c_bf16, 16) || misaligned(slots, 8) || (cache->dr > 0 && misaligned(k_rope_bf16, 16)) ||
         (plan && misaligned(positions, 4)))
         return QVG_ERR_INVALID_ARG;
+    if (n > kMostTokens) return QVG_ERR_UNSUPPORTED;
     const RopeArgs r = plan ? rope_args(plan, false) : RopeArgs{};
     const uint16_t *c = static_cast<const uint16_t *>(c_bf16), *kr = static_cast<const uint16_t *>(k_rope_bf16);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -204,6 +207,7 @@ qvg_status qvg_latent_read(const qvg_latent *cache, const int64_t *slots, int32_
     if (cache->dr == 0) kr_out = nullptr;
     if (n == 0 || (!c_out && !kr_out)) return QVG_OK;
     if (misaligned(slots, 8) || (c_out && misaligned(c_out, 16)) || (kr_out && misaligned(kr_out, 16))) return QVG_ERR_INVALID_ARG;
+    if (n > kMostTokens) return QVG_ERR_UNSUPPORTED;
     k_latent_read<<<ceil_div(n, kWarps), kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
         latent_args(cache), slots, n, static_cast<uint16_t *>(c_out), static_cast<uint16_t *>(kr_out));
     QVG_LAUNCH_CHECK();

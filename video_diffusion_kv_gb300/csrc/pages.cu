@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) k_paged_compact(const __grid_
 // ---- host ---------------------------------------------------------------------------
 
 bool misaligned(const void *p, uintptr_t to) { return !p || reinterpret_cast<uintptr_t>(p) % to != 0; }
+constexpr int kMostPairs = 1 << 20;  // each block of a fork or release looks at all pairs
 bool page_size_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128 || p == 256; }
 
 qvg_status check_sequences(const qvg_page_pool *pool, const qvg_sequences *s) {
@@ -529,6 +530,7 @@ qvg_status qvg_pages_fork(const qvg_page_pool *pool, const qvg_sequences *seqs, 
     if (n < 0) return QVG_ERR_INVALID_ARG;
     if (n == 0) return QVG_OK;
     if (seqs->B == 0 || misaligned(parents, 4) || misaligned(children, 4)) return QVG_ERR_INVALID_ARG;
+    if (n > kMostPairs) return QVG_ERR_UNSUPPORTED;
     k_pages_fork<<<n, kForkThreads, 0, static_cast<cudaStream_t>(stream)>>>(batch(pool, seqs), parents, children, n);
     QVG_LAUNCH_CHECK();
     return QVG_OK;
@@ -541,6 +543,7 @@ qvg_status qvg_pages_release(const qvg_page_pool *pool, const qvg_sequences *seq
     if (n < 0) return QVG_ERR_INVALID_ARG;
     if (n == 0) return QVG_OK;
     if (seqs->B == 0 || misaligned(ids, 4) || (keep && misaligned(keep, 4))) return QVG_ERR_INVALID_ARG;
+    if (n > kMostPairs) return QVG_ERR_UNSUPPORTED;
     k_pages_release<<<n, kForkThreads, 0, static_cast<cudaStream_t>(stream)>>>(batch(pool, seqs), ids, keep, n);
     QVG_LAUNCH_CHECK();
     return QVG_OK;
@@ -561,6 +564,8 @@ qvg_status qvg_pages_reserve(const qvg_page_pool *pool, const qvg_sequences *seq
     if (!cu_new && (n_new < 0 || static_cast<int64_t>(n_new) * seqs->B != total)) return QVG_ERR_INVALID_ARG;
     if (seqs->B == 0) return total == 0 ? QVG_OK : QVG_ERR_INVALID_ARG;
     if (misaligned(copies, 8) || (total > 0 && misaligned(slots, 8))) return QVG_ERR_INVALID_ARG;
+    // (the kernels' 32-bit indices step past the last element)
+    if (std::max({seqs->B, total, pool->num_pages}) > INT32_MAX - 2 * kReserve) return QVG_ERR_UNSUPPORTED;
     if (!workspace || ws_bytes < reserve_bytes(pool->num_pages, seqs->B) || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
         return QVG_ERR_WORKSPACE;
     const Batch a = batch(pool, seqs);
@@ -627,6 +632,7 @@ qvg_status qvg_pages_copy(const qvg_page_rows *rows, const int32_t *copies, int3
     if (n < 0) return QVG_ERR_INVALID_ARG;
     if (n == 0) return QVG_OK;
     if (misaligned(copies, 4)) return QVG_ERR_INVALID_ARG;
+    if (n > INT32_MAX - 65535) return QVG_ERR_UNSUPPORTED;
     Buffers a = buffers(rows);
     int64_t blocks = 0;
     for (int i = 0; i < a.n; ++i) {
