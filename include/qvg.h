@@ -816,7 +816,8 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
  * Rounding, NaN and unseen keys as in qvg_latent_attention (a row that sees a
  * value with an infinity or a NaN may be NaN in all its channels).
  * QVG_ERR_INVALID_ARG as there; QVG_ERR_UNSUPPORTED for another dn or dv, dr
- * above 64, max_q above 2^31 - 257, or more than 2^31 - 1 blocks of 256 rows.
+ * above 64, max_q above 2^31 - 257, total_k above 2^31 - 65, or more than
+ * 2^31 - 1 blocks of 256 rows.
  */
 qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, const qvg_view *k, const qvg_view *k_rope,
                                   const qvg_view *v, int32_t total_q, int32_t total_k, int32_t H, int32_t dn, int32_t dr,

@@ -125,7 +125,7 @@ def test_expanded_attention_refusals(lib):
                dict(max_q=-1), dict(max_k=-1), dict(cu=None, tq=3), dict(ck=None, tk=7), dict(cu=ODD), dict(ck=ODD), dict(mode=2), dict(mode=-1),
                dict(scale=math.nan), dict(out=None), dict(out=0x10008), dict(dtype=5), dict(lse=ODD)):
         assert call(**kw) == BAD, kw
-    for kw in (dict(dn=96), dict(dv=256), dict(dr=72), dict(B=2 ** 20, H=2 ** 12), dict(B=2 ** 20, H=2 ** 10, max_q=2 ** 20, tq=2 ** 30), dict(max_q=2 ** 31 - 100)):
+    for kw in (dict(dn=96), dict(dv=256), dict(dr=72), dict(B=2 ** 20, H=2 ** 12), dict(B=2 ** 20, H=2 ** 10, max_q=2 ** 20, tq=2 ** 30), dict(max_q=2 ** 31 - 100), dict(tk=2 ** 31 - 64)):
         assert call(**kw) == UNS, kw
     for kw in (dict(B=0), dict(max_q=0), dict(tq=0)):
         assert call(q=None, out=None, **kw) == qvg.QVG_OK

@@ -377,7 +377,7 @@ qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, con
         return QVG_ERR_INVALID_ARG;
     if (misaligned(out, 16) || (cu_q && misaligned(cu_q, 4)) || (cu_k && misaligned(cu_k, 4)) || (lse && misaligned(lse, 4)))
         return QVG_ERR_INVALID_ARG;
-    if (max_q > INT32_MAX - la::kPromptRows) return QVG_ERR_UNSUPPORTED;
+    if (max_q > INT32_MAX - la::kPromptRows || total_k > INT32_MAX - la::kKeys) return QVG_ERR_UNSUPPORTED;
     const int blocks = ceil_div(max_q, la::kPromptRows);
     const int64_t grid = static_cast<int64_t>(la::pair_count(B, blocks, total_q)) * H;
     if (grid > INT32_MAX) return QVG_ERR_UNSUPPORTED;
