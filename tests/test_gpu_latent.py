@@ -271,6 +271,26 @@ def test_thousands_of_sequences():
     b.check(out, lse, CAUSAL)
 
 
+@pytest.mark.parametrize("short", [1, 2, 3])
+@pytest.mark.parametrize("idle", [0, 1, 40, 700])
+@pytest.mark.parametrize("dc,dr,page", [(64, 0, 64), (256, 64, 16)])
+def test_a_short_unit_before_a_long_one(short, idle, dc, dr, page):
+    """Parts of the line that begin with a unit of 1, 2 or 3 tiles before one of
+    many, the next unit found at once or behind sequences without new tokens
+    (so that its Q and its first tiles are asked for at the same time)."""
+    parts = torch.cuda.get_device_properties(0).multi_processor_count if idle < 100 else 12
+    nq = ((1,) + (0,) * idle + (1,)) * parts
+    kv = ((64 * short,) + (70,) * idle + (64 * 20 - 3,)) * parts
+    b = Batch(3, dc, dr, page, nq, kv, seed=short)
+    out, lse = b.run()
+    assert qvg.get_status() == qvg.QVG_OK
+    b.check(out, lse, CAUSAL)
+    for _ in range(5):
+        again, again_lse = b.run()
+        assert torch.equal(again, out) and torch.equal(again_lse, lse)
+    assert qvg.get_status() == qvg.QVG_OK
+
+
 @pytest.mark.parametrize("mode", [NONE, CAUSAL, TREE])
 @pytest.mark.parametrize("nq,kv", [((5, 16), (3, 1)), ((40, 7), (10, 6)), ((200, 140), (150, 0))])
 def test_more_new_tokens_than_keys(mode, nq, kv):

@@ -294,8 +294,10 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
                 const int now = first_of(t, page);
                 page = page_of(t + 1);
                 if (it >= a.sb) ok = wait(&empty[rg.i], rg.parity ^ 1u);
-                // (the first Q would wait behind all CTAs' first stages: it is there before the third one is asked for)
-                if (it == 2) ok = ok && wait(&q_full, 0);
+                // (The first Q would wait behind all CTAs' first stages: it is there before the third one is asked for. Only
+                // inside the first unit: Q of the second one needs this tile there, so the barrier is at its first or second phase.
+                // Later it can be past that, and a wait for parity 0 would be one for the third unit's Q.)
+                if (it == 2 && n_seg == 1) ok = ok && wait(&q_full, 0);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 uint64_t *bar = &full[rg.i];
