@@ -561,6 +561,24 @@ def test_long_prompt():
     p.check(out, lse, CAUSAL)
 
 
+@pytest.mark.parametrize("dn,dr,dv", [(128, 64, 128), (128, 0, 64), (64, 8, 64)])
+@pytest.mark.parametrize("mode", [NONE, CAUSAL])
+def test_groups_of_many_blocks(mode, dn, dr, dv):
+    """Blocks of two groups over many keys, several a SM one after the other,
+    with two stages of K and with more: the second group begins after the first
+    one's weights, however far that has got meanwhile."""
+    p = Prompt(150, dn, dr, dv, (256, 200, 130), (700, 0, 1300), seed=28)
+    out, lse = p.run(mode)
+    for _ in range(10):
+        again, again_lse = p.run(mode)
+        assert torch.equal(again, out) and torch.equal(again_lse, lse)
+    assert qvg.get_status() == qvg.QVG_OK
+    p.H, keep = 3, [0, 77, 149]
+    p.q, p.k, p.v = (x[:, keep] for x in (p.q, p.k, p.v))
+    p.q_rope = p.q_rope[:, keep] if dr else None
+    p.check(out[:, keep], lse[keep], mode)
+
+
 @pytest.mark.parametrize("B", [20, 300, 1200])
 def test_many_ragged_prompts(B):
     """Blocks of rows that are ranked by length, and more of them than that."""

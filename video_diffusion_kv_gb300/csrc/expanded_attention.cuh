@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
                          const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a, int blocks) {
     extern __shared__ uint8_t dyn[];
     __shared__ uint64_t a_full[kMostStages], a_empty[kMostStages], b_full[kMostStages], b_empty[kMostStages], fixed[kFix];
-    __shared__ uint64_t s_full[2], p_full[2][2], o_done[2][2], q_full[2], drain, never;
+    __shared__ uint64_t s_full[2], p_full[2][2], o_done[2][2], q_full[2], step, drain, never;
     __shared__ uint2 s_bad[kFix];  // marked keys of a tile of 64
     __shared__ uint32_t tmem_base;
     __shared__ int fail, issued[2];  // tiles of K and of V whose copies have been issued
@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
                 umma::mbar_init(&o_done[g][i], 1);
             }
         }
+        umma::mbar_init(&step, 4);  // completes once
         umma::mbar_init(&drain, 2);
         umma::mbar_init(&never, 1);
         umma::fence_barrier_init();
@@ -231,7 +232,10 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
             }
             umma::tc_fence_before();
             __syncwarp();
-            if (lane == 0) umma::mbar_arrive(&p_full[grp][half]);
+            if (lane == 0) {
+                umma::mbar_arrive(&p_full[grp][half]);
+                if (grp == 0 && t == 0) umma::mbar_arrive(&step);
+            }
         }
         if (ok && end > 0) ok = wait(&o_done[grp][(end - 1) & 1], ((end - 1) >> 1) & 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -313,8 +317,9 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
         Ring ra, rb;
         int n_fix = 0;
         if (mine > 0) ok = wait(&q_full[grp], 0);
-        // the groups out of step: group 1 begins once group 0 is at its softmax
-        if (grp == 1 && u.nt[0] > 0) ok = ok && wait(&p_full[0][0], 0);
+        // The groups out of step: group 1 begins once group 0 has its first weights.  (p_full itself completes again with
+        // group 0's next 128 keys, which do not wait for group 1: its parity may have come round by now.)
+        if (grp == 1 && u.nt[0] > 0) ok = ok && wait(&step, 0);
         for (int d = 0; 2 * d < most; ++d, ra.next(a.sa)) {
             ok = ok && wait(&a_full[ra.i], ra.parity);
             if (2 * d < mine) {
