@@ -291,6 +291,19 @@ def test_a_short_unit_before_a_long_one(short, idle, dc, dr, page):
     assert qvg.get_status() == qvg.QVG_OK
 
 
+@pytest.mark.parametrize("dc,dr", [(64, 0), (128, 64), (256, 128)])
+def test_many_units_a_part(dc, dr):
+    """Units of one or two tiles, a dozen or more after one another in each
+    part: each one's Q takes the place of the last one's."""
+    n = 1600
+    b = Batch(20, dc, dr, 32, tuple(1 + i % 7 for i in range(n)), tuple(7 + (11 * i) % 120 for i in range(n)), seed=dc)
+    out, lse = b.run()
+    b.check(out, lse, CAUSAL)
+    for _ in range(5):
+        again, again_lse = b.run()
+        assert torch.equal(again, out) and torch.equal(again_lse, lse)
+
+
 @pytest.mark.parametrize("mode", [NONE, CAUSAL, TREE])
 @pytest.mark.parametrize("nq,kv", [((5, 16), (3, 1)), ((40, 7), (10, 6)), ((200, 140), (150, 0))])
 def test_more_new_tokens_than_keys(mode, nq, kv):

@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
             ++n_seg;
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
+            umma::tc_fence_after();  // (the stores into tensor memory come behind the products that have read the last unit's row)
             const int piece = w & 7;
             for (int i = w >> 3; a.na > 0 && i < kRows; i += 16) {
                 const uint32_t gi = static_cast<uint32_t>(g.r) * kRows + i;
