@@ -604,6 +604,25 @@ def test_many_ragged_prompts(B):
     assert qvg.get_status() == qvg.QVG_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("B", [1, 2])
+@pytest.mark.parametrize("nq,bound", [(700, 65536), (700, 65537), (700, 131072), (3000, 1 << 30), (1, 100000), (70000, 100000)])
+def test_prompts_below_a_loose_bound(B, nq, bound):
+    """max_q far above the new tokens that there are (a captured call's bound):
+    every row is computed, and nothing behind them."""
+    p = Prompt(1, 64, 0, 64, (nq,) * B, (0,) * B, seed=29)
+    want, want_lse = p.run()
+    out = torch.full((B * nq, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    call = lambda: qvg.expanded_attention(p.q, None, p.k, None, p.v, bound, cu_q=p.cu_q, cu_k=p.cu_k, out=out, want_lse=True)  # noqa: E731
+    _, lse = call()
+    assert qvg.get_status() == qvg.QVG_OK
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    if nq <= 3000:
+        p.check(out, lse, CAUSAL)
+    p.cu_q[B] = B * nq + 1  # a row that is not there
+    call()
+    assert qvg.get_status() == qvg.QVG_ERR_INVALID_ARG
+
+
 def test_prompts_with_more_new_tokens_than_keys():
     p = Prompt(2, 64, 16, 64, (300, 40, 7), (-200, -40, -3), seed=21)  # 100, 0 and 4 keys
     for mode in (NONE, CAUSAL):

@@ -70,7 +70,8 @@ __device__ __forceinline__ Unit unit_of(const Args &a, int b, int r, int h, bool
 }
 
 // The CTA's (sequence, block of rows); y < 0: none.  All heads of a block follow one another.
-// - One sequence: the last rows first, which with a causal mask see the most keys.
+// - One sequence: the last rows first, which with a causal mask see the most keys.  (Counted from the
+//   blocks that were launched: max_q may be far above the rows that there are.)
 // - Up to kSorted possible blocks: ranked by their tiles (each CTA does it for itself: they
 //   all get the same order), so that the short ones fill the GPU's end.
 // - More: the blocks that there are, sequence by sequence, found from the lengths.
@@ -83,7 +84,7 @@ __host__ __device__ inline int pair_count(int B, int blocks, int total_q) {
 __device__ __forceinline__ int2 pick(const Args &a, int blocks, uint32_t *room, int *got) {
     const long long n = static_cast<long long>(a.B) * blocks;
     const int want = blockIdx.x / a.H, i = threadIdx.x;
-    if (a.B == 1) return make_int2(0, blocks - 1 - want);
+    if (a.B == 1) return make_int2(0, static_cast<int>(gridDim.x) / a.H - 1 - want);
     if (i == 0) *got = -1;
     if (n <= kSorted) {
         if (i < n) {
