@@ -774,8 +774,9 @@ qvg_status qvg_latent_workspace_size(int32_t dc, int32_t dr, size_t *bytes);
  * Products are of bf16 numbers with fp32 sums; a weight enters the second one
  * rounded to bf16, i.e. off by at most 2^-8 of itself (lse takes it in fp32).
  * Keys that a token does not see, and slots past kv_len, have no influence
- * on it, whatever they hold.  A row of q with an infinity or a NaN, and one
- * that sees a token that is NaN, gives NaN.  The results do not depend on what
+ * on it, whatever they hold.  A row of q with an infinity or a NaN, one that
+ * sees a token that is NaN, and one whose every logit falls below fp32's range
+ * gives NaN, where it sees a key.  The results do not depend on what
  * else the GPU runs.  All sizes on the device are read when the kernels run: a
  * captured call can be replayed with other lengths, tables and masks.
  * QVG_ERR_INVALID_ARG for sizes, modes, a scale or strides outside the above,

@@ -388,6 +388,51 @@ def test_non_finite_query():
                 assert torch.equal(out[t, h], want[t, h])
 
 
+@pytest.mark.parametrize("keys", [1, 64, 65, 9000])
+@pytest.mark.parametrize("T", [1, 5])
+def test_infinite_query_over_keys_of_one_sign(keys, T):
+    """Where every key that a row sees turns an infinity of its q to -inf, the
+    softmax has no value: NaN, as with one key of another sign, in whole units
+    and in joined ones; a row that sees no key stays 0."""
+    b = Batch(4, 64, 16, 64, (T, T), (keys, 20), seed=30)
+    for x in (b.cache.c, b.cache.kr):
+        x.view(-1, x.shape[-1])[torch.from_numpy(b.slots[0]).cuda(), 3] = 2.0
+    none = max(0, T - keys)  # new tokens in front of the first key
+    want, want_lse = b.run()
+    for part in ("q", "q_rope"):
+        for sign in (math.inf, -math.inf):
+            x = getattr(b, part)
+            keep = x.clone()
+            x[:T, 1, 3] = sign
+            out, lse = b.run()
+            assert out[none:T, 1].isnan().all() and lse[1, none:T].isnan().all()
+            assert (out[:none] == 0).all() and (lse[:, :none] == -math.inf).all()
+            for h in (0, 2, 3):
+                assert torch.equal(out[:T, h], want[:T, h]) and torch.equal(lse[h, :T], want_lse[h, :T])
+            assert torch.equal(out[T:], want[T:]) and torch.equal(lse[:, T:], want_lse[:, T:])
+            x.copy_(keep)
+
+
+def test_logits_beyond_fp32_in_a_part_of_the_keys():
+    """Keys whose logit falls below fp32's range weigh nothing beside others,
+    also where all keys of a part are such."""
+    b = Batch(2, 64, 0, 64, (1,), (30000,), seed=31)
+    b.q[:] = 0
+    b.q[:, :, 0] = 2.0 ** 100
+    at = torch.from_numpy(b.slots[0]).cuda()
+    b.cache.c.view(-1, 64)[at, 0] = -(2.0 ** 100)
+    last = at[29000:29100]
+    b.cache.c.view(-1, 64)[last, 0] = 0
+    out, lse = b.run(out_dtype=qvg.QVG_OUT_F32)
+    want = b.cache.c.view(-1, 64)[last].double().mean(0)
+    # equal weights of 1 (exact in bf16), fp32 sums over 30,000 keys
+    assert ((out[0].double() - want).abs() <= 30000 * 2.0 ** -23 * b.cache.c.view(-1, 64)[last].double().abs().mean(0) + 1e-30).all()
+    assert (lse - math.log(100)).abs().max() <= 2.0 ** -18
+    b.cache.c.view(-1, 64)[last, 0] = -(2.0 ** 100)
+    out, lse = b.run()
+    assert out.isnan().all() and lse.isnan().all()
+
+
 @pytest.mark.parametrize("kw", [dict(q_scale=30.0), dict(c_scale=2.0 ** -60), dict(c_scale=2.0 ** 60, q_scale=2.0 ** -62), dict(q_scale=2.0 ** -20)])
 def test_magnitudes(kw):
     b = Batch(8, 128, 32, 32, (3, 20), (300, 1500), seed=11, **kw)
@@ -666,6 +711,26 @@ def test_prompt_keys_that_are_not_seen():
     p.v[200] = math.nan  # the first key of the second sequence
     out, lse = p.run()
     assert torch.equal(out[:200], want[:200]) and out[200:].isnan().all()
+
+
+@pytest.mark.parametrize("dr", [0, 16])
+@pytest.mark.parametrize("part", ["q", "q_rope"])
+@pytest.mark.parametrize("sign", [math.inf, -math.inf])
+def test_infinite_query_of_prompts(part, sign, dr):
+    """NaN whatever the signs of the keys that a row sees (a prompt's first row
+    sees one); a row that sees none stays 0."""
+    if part == "q_rope" and dr == 0:
+        return
+    p = Prompt(2, 64, dr, 64, (300, 7, 5), (0, 70, -3), seed=32)
+    (p.k[:, :, 3] if part == "q" else p.k_rope[:, 3:4]).fill_(2.0)
+    want, want_lse = p.run()
+    getattr(p, part)[:, 1, 3] = sign
+    out, lse = p.run()
+    none = slice(307, 310)  # (5 new tokens, 2 keys)
+    assert (out[none] == 0).all() and (lse[:, none] == -math.inf).all()
+    assert torch.equal(out[:, 0], want[:, 0]) and torch.equal(lse[0], want_lse[0])
+    some = [t for t in range(312) if not 307 <= t < 310]
+    assert out[some, 1].isnan().all() and lse[1, some].isnan().all()
 
 
 def test_prompts_on_streams_in_a_graph_and_out_of_time():

@@ -158,9 +158,10 @@ __device__ __forceinline__ void rescale_rows(uint32_t t_o, int c0, int c1, float
 }
 
 // A row's softmax so far: its reference (of the logits as S has them) and the
-// sum of its weights, in four parts.
+// sum of its weights, in four parts; whether it has seen a key.
 struct Row {
     float ref = -INFINITY;
+    bool saw = false;
     uint64_t l2[2] = {0, 0};
     __device__ __forceinline__ float sum() const {
         float a, b, c, d;
@@ -168,7 +169,13 @@ struct Row {
         pa::up2(l2[1], c, d);
         return (a + b) + (c + d);
     }
+    // Keys, and every logit -inf, the value of keys that are not seen: an infinity in q (each key turns it to -inf) or
+    // sums beyond fp32.  The softmax has no value; without this the row would come out as one without keys.
+    __device__ __forceinline__ bool lost() const { return saw && ref == -INFINITY; }
 };
+// Stands for the reference of a partial sum whose row is lost: weighs nothing beside others, and tells a
+// row without weights that has keys from one without.
+constexpr float kLost = -3.402823466e38f;
 
 // 64 keys of a warp's rows, in three steps: the logits at t_s, with those that
 // the row does not see at -inf; the largest; weights in the logits' place.
@@ -240,12 +247,12 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&x)[8]) {
 // lies as [dv / 4][128 rows][4], so that a warp's stores are whole lines
 // (as rows, 128 of them took 6 us; so 3).
 // c0, c1: the channels that the warp's threads take; first: they store the sum, too.
-__device__ __forceinline__ void store_rows(const Args &a, float ref_logit, float l, uint32_t t_o, int c0, int c1, bool first, bool none, bool live,
+__device__ __forceinline__ void store_rows(const Args &a, const Row &m, uint32_t t_o, int c0, int c1, bool first, bool none, bool live,
                                            bool whole, long long slot, int r, long long row, int h, int token) {
-    const float ref = ref_logit * a.scale_log2;
+    const float ref = m.ref * a.scale_log2, l = whole && m.lost() ? __uint_as_float(0x7FFFFFFFu) : m.sum();
     if (!first) {
     } else if (live && !whole) {
-        a.pm[slot * kRows + r] = ref;
+        a.pm[slot * kRows + r] = m.lost() ? kLost : ref;
         a.pl[slot * kRows + r] = l;
     } else if (live && a.lse) {
         a.lse[static_cast<long long>(h) * a.total_q + token] = l == 0.0f ? -INFINITY : (log2f(l) + ref) * 0.69314718055994531f;

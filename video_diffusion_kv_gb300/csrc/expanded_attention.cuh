@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (ok) {
             umma::tc_fence_after();
-            if (!idle) store_rows(a, m.ref, m.sum(), t_o, 0, a.dv, true, end == 0, live, true, 0, 0, static_cast<long long>(u.q0 + tq) * a.Hq + u.h, u.h, u.q0 + tq);
+            m.saw = u.kv > 0 && (a.mode == QVG_MASK_NONE || hist + tq >= 0);
+            if (!idle) store_rows(a, m, t_o, 0, a.dv, true, end == 0, live, true, 0, 0, static_cast<long long>(u.q0 + tq) * a.Hq + u.h, u.h, u.q0 + tq);
         }
     } else if (warp < 12) {
         // ---- helpers: V where some row does not see all of it ----------------------------------------------

@@ -32,6 +32,9 @@ __device__ __forceinline__ void add_weighed(float4 &a, float e, const float4 &x)
     if (e != 0.0f) a = make_float4(fmaf(e, x.x, a.x), fmaf(e, x.y, a.y), fmaf(e, x.z, a.z), fmaf(e, x.w, a.w));
 }
 
+// What a joined row's sums are multiplied with: 0 without keys, NaN where there are keys and no weight (la::Row::lost).
+__device__ __forceinline__ float joined_inverse(float m, float l) { return l != 0.0f ? 1.0f / l : m > -INFINITY ? __uint_as_float(0x7FFFFFFFu) : 0.0f; }
+
 // Four channels of a joined row.
 template <int DC>
 __device__ __forceinline__ void put(const la::Args &a, const la::Shared &u, int n, int c, const float4 &acc, float inv) {
@@ -45,7 +48,7 @@ __device__ __forceinline__ void put(const la::Args &a, const la::Shared &u, int 
 }
 __device__ __forceinline__ void put_lse(const la::Args &a, const la::Shared &u, int n, float m, float l) {
     const int gi = u.row0 + n, tq = gi / a.grp, h = gi - tq * a.grp;
-    a.lse[static_cast<long long>(h) * a.total_q + u.q0 + tq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    a.lse[static_cast<long long>(h) * a.total_q + u.q0 + tq] = l != 0.0f ? (m + log2f(l)) * 0.69314718055994531f : joined_inverse(m, l) == 0.0f ? -INFINITY : __uint_as_float(0x7FFFFFFFu);
 }
 
 template <int DC>
@@ -95,7 +98,7 @@ __device__ __forceinline__ void join(const la::Args &a, const la::Shared &u, int
                 }
             }
             if (n >= u.rows) continue;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float inv = joined_inverse(m, l);
 #pragma unroll
             for (int i = 0; i < 4; ++i) put<DC>(a, u, n, slice * 64 + 16 * i + 4 * cg, acc[i], inv);
             if (cg == 0 && slice == 0 && a.lse) put_lse(a, u, n, m, l);
@@ -150,7 +153,7 @@ __device__ __forceinline__ void join(const la::Args &a, const la::Shared &u, int
 #pragma unroll
         for (int k = 1; k < kJoinWarps; ++k) add_weighed(acc, 1.0f, s.acc[k][lane]);
         if (n >= u.rows) continue;
-        put<DC>(a, u, n, slice * 16 + 4 * cg, acc, l == 0.0f ? 0.0f : 1.0f / l);
+        put<DC>(a, u, n, slice * 16 + 4 * cg, acc, joined_inverse(m, l));
         if (cg == 0 && slice == 0 && a.lse) put_lse(a, u, n, m, l);
     }
 }

@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
                 if (!idle) {
                     uint2 see = make_uint2(0, 0);
                     if (part) see = seen_keys(a, t, g.kv, g.nq, g.q0, live ? tq : 0);
+                    m.saw = m.saw || !part || (see.x | see.y) != 0u;
                     Logits v;
                     read_logits(v, t_s0 + bf * 64 + t_lane, part, see, bad);
                     const float f = raise_ref(a, m, largest(v), live);
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
             if (!ok) break;
             umma::tc_fence_after();
             if (!idle)
-                store_rows(a, m.ref, m.sum(), t_o, 0, a.dv, true, false, live, g.whole(), cta * 2 + (g.t0 > 0 ? 0 : 1), tid, static_cast<long long>(g.q0 + tq) * a.Hq + h, h, g.q0 + tq);
+                store_rows(a, m, t_o, 0, a.dv, true, false, live, g.whole(), cta * 2 + (g.t0 > 0 ? 0 : 1), tid, static_cast<long long>(g.q0 + tq) * a.Hq + h, h, g.q0 + tq);
             umma::tc_fence_before();
         }
     } else if (warp < W0 + 4) {
