@@ -783,7 +783,8 @@ qvg_status qvg_latent_workspace_size(int32_t dc, int32_t dr, size_t *bytes);
  * and missing or misaligned pointers; QVG_ERR_UNSUPPORTED for another dc,
  * max_q * Hq above 2^31 - 129, or num_pages * page_size above 2^31 - 1;
  * QVG_ERR_WORKSPACE for a workspace missing, too small or misaligned.  A
- * sequence of 2^32 tiles (64 keys x 128 rows) or more latches
+ * batch whose blocks of 128 rows, each counted as its sequence's tiles of 64
+ * keys and 5 more, make 2^32 - 1 or more is left out altogether and latches
  * QVG_ERR_INVALID_ARG.
  */
 qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, const qvg_view *q_rope, int32_t total_q,

@@ -514,6 +514,27 @@ def test_same_bits_each_time_on_any_stream_and_in_a_graph():
             assert torch.equal(o, w) and torch.equal(got_lse, l)
 
 
+@pytest.mark.parametrize("B,rows,keys", [(1, 128 * 256, 1 << 30), (2, 128 * 128, 1 << 30), (32, 128 * 8, 1 << 30), (33, 128 * 8, 1 << 30),
+                                         (40, 128 * 512, 1 << 24), (1000, 128 * 17, 1 << 24)])
+def test_a_batch_beyond_the_line_is_refused(B, rows, keys):
+    """Batches of 2^32 tiles and more (the fixed cost of a block of rows counted
+    in), one sequence or many, are reported and left out: nothing is written, and it takes no time."""
+    cost = keys // 64 + 5
+    assert B * (rows // 128) * cost >= 2 ** 32 - 1
+    cache = qvg.LatentKV(64, 0, 256, 1)
+    q = torch.zeros(B * rows, 1, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(1, keys // 256, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()  # every page the same one
+    kv_len = torch.full((B,), keys, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 7.0)
+    _, lse = qvg.latent_attention(cache, q, None, table, kv_len, rows, 0.1, out=out, want_lse=True)
+    assert qvg.get_status() == qvg.QVG_ERR_INVALID_ARG
+    assert (out == 7).all()
+    kv_len.fill_(100)
+    _, lse = qvg.latent_attention(cache, q, None, table, kv_len, rows, 0.1, out=out, want_lse=True)
+    assert qvg.get_status() == qvg.QVG_OK
+    assert (out == 0).all() and (lse[:, -1] - math.log(100)).abs().max() < 1e-5
+
+
 def test_bad_device_arguments_are_reported():
     def status(**kw):
         b = Batch(4, 64, 16, 16, (2, 1), (40, 30), seed=17)

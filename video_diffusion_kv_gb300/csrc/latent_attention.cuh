@@ -42,6 +42,9 @@ struct __align__(16) Shared {
     int first = 0, last = 0, rows = 0, row0 = 0, q0 = 0, pad[3] = {0, 0, 0};
 };
 
+// The sum, or 2^32 - 1 where it does not fit.
+__device__ __forceinline__ uint32_t add_up_to(uint32_t x, uint32_t y) { return x + y < x ? UINT32_MAX : x + y; }
+
 // cmap: latents; rmap: rotated key parts.
 __global__ void __launch_bounds__(kLatentWarps * 32, 1)
     k_latent_attention(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap rmap, const __grid_constant__ Args a) {
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
     } else {
         // ---- this CTA's part of the line, unit by unit ---------------------------------------------------
         // One pass over the sequences for the line's length, then a walk from the sequence that holds the part's begin; 32
-        // sequences at a time, a lane each.  (Code that runs once costs its instructions' way from L2, in a chain: this
+        // sequences at a time, a lane each.  The sums stop at 2^32 - 1: a line that gets there is refused.  (Code that runs once costs its instructions' way from L2, in a chain: this
         // loop in half the instructions gets the first tile going 2 us earlier.)
         Shared shared[2];  // the unit that this CTA goes on with, and the one that begins here and goes on
         bool ok = true, counting = true;
@@ -429,21 +432,25 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
             uint32_t w = 0;
             if (b0 + lane < a.B) {
                 q = pa::seq_of<kRows, kKeys>(a, b0 + lane, counting && cta == 0);
-                w = static_cast<uint32_t>(q.rb) * static_cast<uint32_t>(q.nt + kUnitCost);
+                const uint64_t units = static_cast<uint64_t>(q.rb) * static_cast<uint32_t>(q.nt + kUnitCost);
+                w = static_cast<uint32_t>(min(units, static_cast<uint64_t>(UINT32_MAX)));
             }
             uint32_t x = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-                if (lane >= o) x += y;
+                if (lane >= o) x = add_up_to(x, y);
             }
             const uint32_t all = __shfl_sync(0xFFFFFFFFu, x, 31);
             if (counting) {
-                if (total + all < total && lane == 0) raise_error(a.err, QVG_ERR_INVALID_ARG);
-                total += all;
+                total = add_up_to(total, all);
                 b0 += 32;
                 if (b0 < a.B) continue;
                 counting = false;
+                if (total == UINT32_MAX) {
+                    if (cta == 0 && lane == 0) raise_error(a.err, QVG_ERR_INVALID_ARG);
+                    break;
+                }
                 per = max(1u, (total - 1) / gridDim.x + 1);
                 pos = static_cast<uint32_t>(min(static_cast<uint64_t>(total), static_cast<uint64_t>(cta) * per));
                 end = total - pos > per ? pos + per : total;
