@@ -171,6 +171,24 @@ def test_an_invalid_argument_comes_before_a_lack_of_room():
         assert qvg.get_status() == qvg.QVG_ERR_CAPACITY and (slots == -1).all()
 
 
+def test_more_than_a_billion_sequences():
+    """Twice a sequence's number, and the sum of two, pass 31 bits: the last
+    one's copy on write, and a batch without room."""
+    B = 2 ** 30 + 5
+    pool = qvg.PagePool(8)
+    table, lens = torch.zeros(B, 1, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    lens[[0, B - 1]], cu[B], pool.refs[0] = 5, 1, 2
+    slots, copies = qvg.pages_reserve(pool, 16, table, lens, cu_new=cu, total=1)
+    assert qvg.get_status() == OK
+    assert slots.tolist() == [16 + 5] and copies[B - 1].tolist() == [0, 1] and (copies[:B - 1] == -1).all()
+    assert lens[[0, B - 2, B - 1]].tolist() == [5, 0, 6] and table[B - 1].tolist() == [1] and pool.refs.tolist() == [1, 1] + [0] * 6
+    del cu, slots, copies
+    slots, copies = qvg.pages_reserve(pool, 16, table, lens)
+    assert qvg.get_status() == FULL
+    assert (slots == -1).all() and (copies == -1).all() and lens[B - 1].item() == 6
+
+
 def test_bad_arguments_on_the_device():
     b = Both(30, 6, 4, 16)
     b.reserve([20, 5, 40, 0, 0, 0])

@@ -97,7 +97,7 @@ struct Reserve {
     const int32_t *cu_new;
     int n_new, total;
     int64_t *slots;
-    int32_t *copies;  // [B][2]
+    int2 *copies;     // [B]
     int32_t *status;  // workspace: what the slots' kernel has to know
     int32_t *first;   // [B]: number of the sequence's first new page
     int32_t *list;    // [num_pages]: the free pages; before that, writers of a shared page
@@ -110,7 +110,7 @@ template <typename F>
 __device__ __forceinline__ int holder(int n, int k, F at) {
     int lo = 0, hi = n;
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
+        const int mid = lo + ((hi - lo) >> 1);
         if (at(mid) <= k)
             lo = mid;
         else
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kReserve) k_pages_reserve(Batch a, Reserve r) 
                 r.last[page] = -1;
             }
         }
-        reinterpret_cast<int2 *>(r.copies)[b] = cp;
+        r.copies[b] = cp;
     }
     if (tid == 0 && a.B > 0 && (r.start(0) != 0 || r.start(a.B) != r.total)) wrong = true;
     // (an invalid argument is reported before a lack of room)
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kReserve) k_pages_reserve(Batch a, Reserve r) 
     bool ok = !invalid && !narrow;
     if (ok) {
         for (int b = tid; b < a.B; b += kReserve) {
-            const int page = r.copies[2 * b];
+            const int page = r.copies[b].x;
             if (page >= 0) {
                 atomicAdd(r.list + page, 1);
                 atomicMax(r.last + page, b);
@@ -207,11 +207,11 @@ __global__ void __launch_bounds__(kReserve) k_pages_reserve(Batch a, Reserve r) 
             const int b = b0 + tid;
             int mine = 0;
             if (b < a.B) {
-                const int n = r.start(b + 1) - r.start(b), L = a.kv_len[b], page = r.copies[2 * b];
+                const int n = r.start(b + 1) - r.start(b), L = a.kv_len[b], page = r.copies[b].x;
                 mine = static_cast<int>(a.pages(static_cast<long long>(L) + n) - a.pages(L));
                 if (page >= 0) {
                     if (r.list[page] >= a.refs[page] && r.last[page] == b)
-                        r.copies[2 * b] = -1;  // the last holder keeps it
+                        r.copies[b].x = -1;  // the last holder keeps it
                     else
                         ++mine;
                 }
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kReserve) k_pages_reserve(Batch a, Reserve r) 
     }
     __syncthreads();
     if (!ok) {
-        for (int i = tid; i < 2 * a.B; i += kReserve) r.copies[i] = -1;
+        for (int b = tid; b < a.B; b += kReserve) r.copies[b] = make_int2(-1, -1);
         if (r.total <= kSlotsHere)
             for (int i = tid; i < r.total; i += kReserve) r.slots[i] = -1;
         if (tid == 0) {
@@ -262,13 +262,13 @@ __global__ void __launch_bounds__(kReserve) k_pages_reserve(Batch a, Reserve r) 
         return;
     }
     for (int k = tid; k < need; k += kReserve) {
-        const int b = holder(a.B, k, [&](int m) { return r.first[m]; }), page = r.list[k], old = r.copies[2 * b];
+        const int b = holder(a.B, k, [&](int m) { return r.first[m]; }), page = r.list[k], old = r.copies[b].x;
         const int have = static_cast<int>(a.pages(a.kv_len[b])), j = k - r.first[b] - (old >= 0 ? 1 : 0);
         a.row(b)[have + j] = page;  // j = -1: in the place of the shared one
         a.refs[page] = 1;
         if (j < 0) {
             atomicSub(a.refs + old, 1);
-            r.copies[2 * b + 1] = page;
+            r.copies[b].y = page;
         }
     }
     __syncthreads();
@@ -574,7 +574,7 @@ qvg_status qvg_pages_reserve(const qvg_page_pool *pool, const qvg_sequences *seq
     r.n_new = n_new;
     r.total = total;
     r.slots = slots;
-    r.copies = copies;
+    r.copies = reinterpret_cast<int2 *>(copies);
     r.status = static_cast<int32_t *>(workspace);
     r.first = r.status + 4;
     r.list = r.first + (static_cast<size_t>(seqs->B) + 3) / 4 * 4;
