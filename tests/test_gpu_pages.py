@@ -298,6 +298,18 @@ def test_copy_of_many_pairs():
     assert torch.equal(c.c[70005:140005], c.c[:70000]) and (c.c[140005:] == (torch.arange(140005, 140010, device="cuda") % 251)[:, None, None]).all()
 
 
+def test_copy_of_more_than_a_billion_pairs():
+    """Twice a pair's number passes 31 bits."""
+    n = 2 ** 30 + 3
+    c = qvg.LatentKV(64, 0, 16, 8)
+    c.c.copy_(torch.arange(8, device="cuda")[:, None, None])
+    pairs = torch.full((n, 2), -1, dtype=torch.int32, device="cuda")
+    pairs[1], pairs[2 ** 30], pairs[n - 1] = ints([0, 4]), ints([1, 5]), ints([2, 6])
+    qvg.pages_copy(c, pairs)
+    assert qvg.get_status() == OK
+    assert c.c[:, 0, 0].tolist() == [0, 1, 2, 3, 0, 1, 2, 7]
+
+
 @pytest.mark.parametrize("page", [16, 64, 256])
 @pytest.mark.parametrize("lens,share", [((1, 40, 700), 0.5), ((2000, 3), 0.9), ((513, 512, 511, 0), 0.1), ((900,), 1.0)])
 def test_compact(page, lens, share):

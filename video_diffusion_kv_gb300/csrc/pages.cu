@@ -311,7 +311,8 @@ __global__ void __launch_bounds__(kCopyThreads) k_pages_copy(const __grid_consta
     const long long bytes = a.page_bytes(i);
     const long long at = static_cast<long long>(blockIdx.x - (i ? a.blocks[i - 1] : 0)) * kCopyBlock + threadIdx.x * 16;
     for (int k = blockIdx.y; k < n; k += gridDim.y) {
-        const int from = copies[2 * k], to = copies[2 * k + 1];
+        const int32_t *pair = copies + 2ll * k;
+        const int from = pair[0], to = pair[1];
         if (from < 0 || to < 0) continue;
         if (from >= a.num_pages || to >= a.num_pages) {
             if (threadIdx.x == 0) raise_error(a.err, QVG_ERR_INVALID_ARG);
