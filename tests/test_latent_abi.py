@@ -200,6 +200,13 @@ def test_moves_refusals(lib):
     assert pack(B=0, t=None) == qvg.QVG_OK and pack(ks=0, keep=None) == qvg.QVG_OK
 
 
+def test_compaction_refuses_more_kept_tokens_than_its_indices_hold(lib):
+    pack = lambda ks, B=2, first=P: lib.qvg_paged_compact(rows(), P, 4, B, first, P, ks, P, None)  # noqa: E731
+    for ks in (2 ** 31 - 2048, 2 ** 31 - 1):
+        assert pack(ks) == UNS and pack(ks, B=1) == UNS
+    assert pack(2 ** 31 - 2049, first=None) == BAD  # (no limit: the next check's answer)
+
+
 def test_python_refusals(lib):
     """Shapes, types and devices are checked before the library is called."""
     c = qvg.LatentKV(64, 8, 16, 2, device="cpu")

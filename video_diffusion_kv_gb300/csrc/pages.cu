@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(kCopyThreads) k_pages_copy(const __grid_consta
 // ---- compact ----------------------------------------------------------------------
 
 constexpr int kMoveThreads = 256, kMoveEach = 4;
+constexpr int kMostKept = INT32_MAX - 8 * kMoveThreads;  // of a sequence
 
 struct Move {
     const int32_t *table, *first, *keep, *n_keep;
@@ -653,7 +654,8 @@ qvg_status qvg_paged_compact(const qvg_page_rows *rows, const int32_t *table, in
     const qvg_status s = check_rows(rows);
     if (s != QVG_OK) return s;
     if (B < 0 || table_stride < 1 || keep_stride < 0) return QVG_ERR_INVALID_ARG;
-    if (B > 65535) return QVG_ERR_UNSUPPORTED;
+    // (the kernel's 32-bit numbers of kept tokens step up to five batches past the last one)
+    if (B > 65535 || keep_stride > kMostKept) return QVG_ERR_UNSUPPORTED;
     if (B == 0 || keep_stride == 0) return QVG_OK;
     if (misaligned(table, 4) || misaligned(first, 4) || misaligned(keep, 4) || misaligned(n_keep, 4)) return QVG_ERR_INVALID_ARG;
     const Buffers a = buffers(rows);
