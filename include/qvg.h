@@ -911,7 +911,7 @@ qvg_status qvg_pages_reserve(const qvg_page_pool *pool, const qvg_sequences *seq
 
 /*
  * What the next two calls move: the buffers of a cache as rows.  Buffer i is
- * [num_pages][heads[i]][page_size][row_bytes[i]] bytes at base[i].
+ * [num_pages][heads[i]][page_size][row_bytes[i]] bytes at base[i], below 2^63.
  */
 typedef struct {
     int32_t page_size;

@@ -207,6 +207,14 @@ def test_compaction_refuses_more_kept_tokens_than_its_indices_hold(lib):
     assert pack(2 ** 31 - 2049, first=None) == BAD  # (no limit: the next check's answer)
 
 
+def test_rows_of_more_bytes_than_63_bits(lib):
+    big = 2 ** 31 - 16
+    for kw in (dict(heads=(big, 1), row_bytes=(big, 64)), dict(heads=(1, big), row_bytes=(256, big), pages=2 ** 20),
+               dict(heads=(2 ** 20, 1), row_bytes=(2 ** 24, 64), pages=2 ** 30, page=256)):
+        assert lib.qvg_pages_copy(rows(**kw), P, 1, None) == BAD
+        assert lib.qvg_paged_compact(rows(**kw), P, 4, 2, P, P, 3, P, None) == BAD
+
+
 def test_python_refusals(lib):
     """Shapes, types and devices are checked before the library is called."""
     c = qvg.LatentKV(64, 8, 16, 2, device="cpu")

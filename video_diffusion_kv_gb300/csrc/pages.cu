@@ -498,6 +498,8 @@ qvg_status check_rows(const qvg_page_rows *r) {
         const int rb = r->row_bytes[i];
         if (misaligned(r->base[i], 16) || r->heads[i] < 1) return QVG_ERR_INVALID_ARG;
         if (rb != 1 && rb != 2 && rb != 4 && (rb < 16 || rb % 16 != 0)) return QVG_ERR_INVALID_ARG;
+        // (its bytes are worked out in 64 bits)
+        if (static_cast<int64_t>(r->heads[i]) * rb > INT64_MAX / (static_cast<int64_t>(r->page_size) * r->num_pages)) return QVG_ERR_INVALID_ARG;
     }
     return QVG_OK;
 }
