@@ -781,7 +781,8 @@ qvg_status qvg_latent_workspace_size(int32_t dc, int32_t dr, size_t *bytes);
  * captured call can be replayed with other lengths, tables and masks.
  * QVG_ERR_INVALID_ARG for sizes, modes, a scale or strides outside the above,
  * and missing or misaligned pointers; QVG_ERR_UNSUPPORTED for another dc,
- * max_q * Hq above 2^31 - 129, or num_pages * page_size above 2^31 - 1;
+ * B above 2^20, max_q * Hq above 2^31 - 129, or num_pages * page_size above
+ * 2^31 - 1;
  * QVG_ERR_WORKSPACE for a workspace missing, too small or misaligned.  A
  * batch whose blocks of 128 rows, each counted as its sequence's tiles of 64
  * keys and 5 more, make 2^32 - 1 or more is left out altogether and latches
@@ -818,8 +819,8 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
  * Rounding, NaN and unseen keys as in qvg_latent_attention (a row that sees a
  * value with an infinity or a NaN may be NaN in all its channels).
  * QVG_ERR_INVALID_ARG as there; QVG_ERR_UNSUPPORTED for another dn or dv, dr
- * above 64, max_q above 2^31 - 257, total_k above 2^31 - 65, or more than
- * 2^31 - 1 blocks of 256 rows.
+ * above 64, B above 2^20, max_q above 2^31 - 257, total_k above 2^31 - 65, or
+ * more than 2^31 - 1 blocks of 256 rows.
  */
 qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, const qvg_view *k, const qvg_view *k_rope,
                                   const qvg_view *v, int32_t total_q, int32_t total_k, int32_t H, int32_t dn, int32_t dr,

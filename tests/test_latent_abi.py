@@ -215,6 +215,18 @@ def test_rows_of_more_bytes_than_63_bits(lib):
         assert lib.qvg_paged_compact(rows(**kw), P, 4, 2, P, P, 3, P, None) == BAD
 
 
+def test_attention_refuses_more_sequences_than_its_walks_hold(lib):
+    def latent_call(B, ws=None):
+        return lib.qvg_latent_attention(latent(), view(), view(), 4, 16, B, 2, P, P, 4, P, 1, None, 0, 0.1, P, 1, P, ws, 0, None)
+
+    def prompt_call(B, max_q=2, total=4, H=1):
+        return lib.qvg_expanded_attention(view(), view(), view(), view(), view(), total, 9, H, 128, 32, 64, B, max_q, 4, P, P, 1, 0.0, P, 1, P, None)
+    for B in (2 ** 20 + 1, 2 ** 30 + 1, 2 ** 31 - 20, 2 ** 31 - 1):
+        assert latent_call(B) == UNS and prompt_call(B) == UNS
+        assert prompt_call(B, max_q=300, total=2 ** 31 - 1) == UNS  # (the blocks pass 31 bits)
+    assert latent_call(2 ** 20) == WS  # (no limit: the next check's answer)
+
+
 def test_python_refusals(lib):
     """Shapes, types and devices are checked before the library is called."""
     c = qvg.LatentKV(64, 8, 16, 2, device="cpu")

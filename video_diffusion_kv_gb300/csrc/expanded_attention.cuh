@@ -77,9 +77,9 @@ __device__ __forceinline__ Unit unit_of(const Args &a, int b, int r, int h, bool
 // - More: the blocks that there are, sequence by sequence, found from the lengths.
 // `room`: shared memory for kSorted integers.
 constexpr int kSorted = 256;
-__host__ __device__ inline int pair_count(int B, int blocks, int total_q) {
+__host__ __device__ inline long long pair_count(int B, int blocks, int total_q) {
     const long long n = static_cast<long long>(B) * blocks, most = total_q / kPromptRows + static_cast<long long>(B);
-    return static_cast<int>(n <= kSorted || n < most ? n : most);
+    return n <= kSorted || n < most ? n : most;
 }
 __device__ __forceinline__ int2 pick(const Args &a, int blocks, uint32_t *room, int *got) {
     const long long n = static_cast<long long>(a.B) * blocks;

@@ -168,6 +168,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) k_latent_merge(const __gri
     if (u.rows > 0) join<DC>(a, u, which ? 0 : x - u.first, blockIdx.y >> 1, s);
 }
 
+// Sequences of a call: every CTA walks over all of them, 32 (prompts: 512) at a time, with 32-bit numbers that step
+// past the last one, while the other roles' waits run.
+constexpr int kMostSequences = 1 << 20;
+
 // CTAs of the absorbed form: one an SM (and no unit may have more parts than the join has room for).
 int cta_count() { return std::min(sm_count_current(), kMostParts); }
 
@@ -298,7 +302,7 @@ qvg_status qvg_latent_attention(const qvg_latent *cache, const qvg_view *q, cons
         (lse && misaligned(lse, 4)))
         return QVG_ERR_INVALID_ARG;
     if (mask_mode == QVG_MASK_TREE && (misaligned(mask, 4) || mask_words < ceil_div(max_q, 32))) return QVG_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(max_q) * Hq > INT32_MAX - la::kRows ||
+    if (B > kMostSequences || static_cast<int64_t>(max_q) * Hq > INT32_MAX - la::kRows ||
         static_cast<int64_t>(cache->num_pages) * cache->page_size > INT32_MAX)
         return QVG_ERR_UNSUPPORTED;
     const int ctas = cta_count();
@@ -380,9 +384,9 @@ qvg_status qvg_expanded_attention(const qvg_view *q, const qvg_view *q_rope, con
         return QVG_ERR_INVALID_ARG;
     if (misaligned(out, 16) || (cu_q && misaligned(cu_q, 4)) || (cu_k && misaligned(cu_k, 4)) || (lse && misaligned(lse, 4)))
         return QVG_ERR_INVALID_ARG;
-    if (max_q > INT32_MAX - la::kPromptRows || total_k > INT32_MAX - la::kKeys) return QVG_ERR_UNSUPPORTED;
+    if (B > kMostSequences || max_q > INT32_MAX - la::kPromptRows || total_k > INT32_MAX - la::kKeys) return QVG_ERR_UNSUPPORTED;
     const int blocks = ceil_div(max_q, la::kPromptRows);
-    const int64_t grid = static_cast<int64_t>(la::pair_count(B, blocks, total_q)) * H;
+    const int64_t grid = la::pair_count(B, blocks, total_q) * H;
     if (grid > INT32_MAX) return QVG_ERR_UNSUPPORTED;
     CUtensorMap map[5] = {};
     if (!chunk_map(&map[0], q->data, dn, H, total_q, q->head_stride, q->token_stride, la::kRows, dn / 64) ||
