@@ -227,6 +227,32 @@ def test_attention_refuses_more_sequences_than_its_walks_hold(lib):
     assert latent_call(2 ** 20) == WS  # (no limit: the next check's answer)
 
 
+def test_no_gradient_is_lost_without_a_word(lib):
+    """There is no backward pass: inputs that require a gradient are refused
+    where gradients are recorded, and not otherwise (the next check, for a
+    CUDA device, answers then)."""
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    cache = qvg.LatentKV(64, 8, 16, 2, device="cpu")
+    calls = (
+        (lambda **a: qvg.latent_append(cache, slots=torch.zeros(3, dtype=torch.int64), **a), dict(c=bf(3, 64), k_rope=bf(3, 8))),
+        (lambda **a: qvg.latent_attention(cache, block_table=i32(2, 3), kv_len=i32(2), max_q=2, scale=0.1, cu_q=i32(3), **a),
+         dict(q=bf(4, 2, 64), q_rope=bf(4, 2, 8))),
+        (lambda **a: qvg.expanded_attention(max_q=2, cu_q=i32(3), cu_k=i32(3), **a),
+         dict(q=bf(4, 2, 64), q_rope=bf(4, 2, 8), k=bf(6, 2, 64), k_rope=bf(6, 8), v=bf(6, 2, 64))))
+    for call, inputs in calls:
+        for name in inputs:
+            some = {**inputs, name: inputs[name].clone().requires_grad_()}
+            with pytest.raises(ValueError, match="no gradient"):
+                call(**some)
+            with torch.no_grad(), pytest.raises(ValueError) as e:
+                call(**some)
+            assert "gradient" not in str(e.value)
+        with pytest.raises(ValueError) as e:
+            call(**inputs)
+        assert "gradient" not in str(e.value)
+
+
 def test_python_refusals(lib):
     """Shapes, types and devices are checked before the library is called."""
     c = qvg.LatentKV(64, 8, 16, 2, device="cpu")

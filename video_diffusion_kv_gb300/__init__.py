@@ -689,6 +689,16 @@ def _off(t, dtype, dev):
     return t.dtype != dtype or t.device != dev or not t.is_contiguous()
 
 
+def _without_gradient(where, *inputs):
+    """These calls have no backward pass: an input that wants one is refused,
+    so that its gradient is not lost without a word."""
+    import torch
+    if torch.is_grad_enabled():
+        for t in inputs:
+            if t is not None and t.requires_grad:
+                raise ValueError("%s: no gradient through it; detach its inputs, or call under torch.no_grad()" % where)
+
+
 def _call(dev, where, function, stream, *args):
     """A library call on `stream` with `dev` as the current device."""
     import torch
@@ -754,8 +764,9 @@ def latent_append(cache: LatentKV, c, k_rope, slots, plan=None, positions=None, 
     [n, dr]; None where dr is 0) into the slots (int64 [n]; negative: skip);
     both may be strided by token.  With a RopePlan, k_rope is rotated at
     `positions` on the way.  A slot beyond the cache is reported by
-    get_status()."""
+    get_status().  No gradient: inputs that require one are refused."""
     import torch
+    _without_gradient("latent_append", c, k_rope)
     n = slots.numel()
     cs, ks = _rows2(c, cache.dc, cache.device, "latent_append", "c"), 0
     if cache.dr:
@@ -824,8 +835,9 @@ def latent_attention(cache: LatentKV, q, q_rope, block_table, kv_len, max_q, sca
     ([total_q, Hq, dc]).  scale has no default: it follows from the channels
     before the absorption.  The rest as in paged_attention.  Returns (out, lse
     or None).  Two calls that run at once need a workspace each (None: one per
-    call)."""
+    call).  No gradient: inputs that require one are refused."""
     import torch
+    _without_gradient("latent_attention", q, q_rope)
     if q.dim() != 3:
         raise ValueError("latent_attention: q must be [total_q, Hq, %d]" % cache.dc)
     total, Hq, B = q.shape[0], q.shape[1], kv_len.numel()
@@ -866,8 +878,10 @@ def expanded_attention(q, q_rope, k, k_rope, v, max_q, scale=0.0, cu_q=None, cu_
     [tokens, H, dr] and k_rope [tokens, dr], which all heads share (both None:
     no such part).  A sequence's new tokens (cu_q: int32 [B + 1]; None: max_q
     each) are the last of its keys (cu_k; None: max_k each).  Returns (out
-    [total_q, H, dv], lse or None)."""
+    [total_q, H, dv], lse or None).  No gradient: inputs that require one are
+    refused."""
     import torch
+    _without_gradient("expanded_attention", q, q_rope, k, k_rope, v)
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("expanded_attention: q, k and v must be [tokens, heads, channels]")
     (total, H, dn), total_k, dv = q.shape, k.shape[0], v.shape[2]
