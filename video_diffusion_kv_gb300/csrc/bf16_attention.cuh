@@ -144,10 +144,10 @@ __device__ __forceinline__ uint2 seen_keys(const Args &a, int t, int kv, int nq,
     return make_uint2(w[0], w[1]);
 }
 
-// A warp's rows of O, channels c0 .. c1 - 1, times their factors.
-__device__ __forceinline__ void rescale_rows(uint32_t t_o, int c0, int c1, float f) {
+// A warp's rows of O, dv channels, times their factors.
+__device__ __forceinline__ void rescale_rows(uint32_t t_o, int dv, float f) {
 #pragma unroll 1
-    for (int c = c0; c < c1; c += 16) {
+    for (int c = 0; c < dv; c += 16) {
         uint32_t o[16];
         pa::tmem_ld16(t_o + c, o);
 #pragma unroll
@@ -246,12 +246,10 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&x)[8]) {
 // and the sum of its weights.  none: no product has been made.  A partial sum
 // lies as [dv / 4][128 rows][4], so that a warp's stores are whole lines
 // (as rows, 128 of them took 6 us; so 3).
-// c0, c1: the channels that the warp's threads take; first: they store the sum, too.
-__device__ __forceinline__ void store_rows(const Args &a, const Row &m, uint32_t t_o, int c0, int c1, bool first, bool none, bool live,
-                                           bool whole, long long slot, int r, long long row, int h, int token) {
+__device__ __forceinline__ void store_rows(const Args &a, const Row &m, uint32_t t_o, bool none, bool live, bool whole, long long slot, int r,
+                                           long long row, int h, int token) {
     const float ref = m.ref * a.scale_log2, l = whole && m.lost() ? __uint_as_float(0x7FFFFFFFu) : m.sum();
-    if (!first) {
-    } else if (live && !whole) {
+    if (live && !whole) {
         a.pm[slot * kRows + r] = m.lost() ? kLost : ref;
         a.pl[slot * kRows + r] = l;
     } else if (live && a.lse) {
@@ -261,7 +259,7 @@ __device__ __forceinline__ void store_rows(const Args &a, const Row &m, uint32_t
     float *part = a.po + slot * kRows * a.dv + 4 * r;
     const bool wide = a.wide_out;
 #pragma unroll 1
-    for (int c = c0; c < c1; c += 32) {
+    for (int c = 0; c < a.dv; c += 32) {
         uint32_t o[32];
         if (none) {
 #pragma unroll

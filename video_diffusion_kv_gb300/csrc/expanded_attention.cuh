@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     umma::tc_fence_after();
-                    rescale_rows(t_o, 0, a.dv, f);
+                    rescale_rows(t_o, a.dv, f);
                 }
                 write_weights(a, m, v, t_s + half * 64, f);
             }
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
         if (ok) {
             umma::tc_fence_after();
             m.saw = u.kv > 0 && (a.mode == QVG_MASK_NONE || hist + tq >= 0);
-            if (!idle) store_rows(a, m, t_o, 0, a.dv, true, end == 0, live, true, 0, 0, static_cast<long long>(u.q0 + tq) * a.Hq + u.h, u.h, u.q0 + tq);
+            if (!idle) store_rows(a, m, t_o, end == 0, live, true, 0, 0, static_cast<long long>(u.q0 + tq) * a.Hq + u.h, u.h, u.q0 + tq);
         }
     } else if (warp < 12) {
         // ---- helpers: V where some row does not see all of it ----------------------------------------------

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
                         umma::tc_fence_after();
-                        rescale_rows(t_o, 0, a.dv, f);
+                        rescale_rows(t_o, a.dv, f);
                     }
                     write_weights(a, m, v, t_s0 + bf * 64 + t_lane, f);
                 }
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kLatentWarps * 32, 1)
             if (!ok) break;
             umma::tc_fence_after();
             if (!idle)
-                store_rows(a, m, t_o, 0, a.dv, true, false, live, g.whole(), cta * 2 + (g.t0 > 0 ? 0 : 1), tid, static_cast<long long>(g.q0 + tq) * a.Hq + h, h, g.q0 + tq);
+                store_rows(a, m, t_o, false, live, g.whole(), cta * 2 + (g.t0 > 0 ? 0 : 1), tid, static_cast<long long>(g.q0 + tq) * a.Hq + h, h, g.q0 + tq);
             umma::tc_fence_before();
         }
     } else if (warp < W0 + 4) {
