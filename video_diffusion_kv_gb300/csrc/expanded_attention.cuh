@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
                 umma::mbar_init(&o_done[g][i], 1);
             }
         }
-        umma::mbar_init(&step, 4);  // completes once
+        umma::mbar_init(&step, 1);  // completes once
         umma::mbar_init(&drain, 2);
         umma::mbar_init(&never, 1);
         umma::fence_barrier_init();
@@ -233,10 +233,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
             }
             umma::tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                umma::mbar_arrive(&p_full[grp][half]);
-                if (grp == 0 && t == 0) umma::mbar_arrive(&step);
-            }
+            if (lane == 0) umma::mbar_arrive(&p_full[grp][half]);
         }
         if (ok && end > 0) ok = wait(&o_done[grp][(end - 1) & 1], ((end - 1) >> 1) & 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -319,10 +316,14 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
         Ring ra, rb;
         int n_fix = 0;
         if (mine > 0) ok = wait(&q_full[grp], 0);
-        // The groups out of step: group 1 begins once group 0 has its first weights.  (p_full itself completes again with
-        // group 0's next 128 keys, which do not wait for group 1: its parity may have come round by now.)
-        if (grp == 1 && u.nt[0] > 0) ok = ok && wait(&step, 0);
+        // The groups out of step: group 1 begins once group 0 has its first weights.  (That barrier completes again with group
+        // 0's next 128 keys, which wait until group 1 has seen it: else its parity might have come round.  With a barrier
+        // of its own that the softmax warps arrive at, 104.6 us for the first case where this takes 103.8.)
+        if (grp == 1 && u.nt[0] > 0) ok = ok && wait(&p_full[0][0], 0);
+        __syncwarp();
+        if (grp == 1 && one && ok) umma::mbar_arrive(&step);
         for (int d = 0; 2 * d < most; ++d, ra.next(a.sa)) {
+            if (grp == 0 && d == 1) ok = ok && wait(&step, 0);
             ok = ok && wait(&a_full[ra.i], ra.parity);
             if (2 * d < mine) {
                 if (d > 0) ok = ok && wait(&o_done[grp][1], (d - 1) & 1);
