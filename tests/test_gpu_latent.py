@@ -658,6 +658,22 @@ def test_groups_of_many_blocks(mode, dn, dr, dv):
     p.check(out[:, keep], lse[keep], mode)
 
 
+@pytest.mark.parametrize("rows", [1, 129, 140])
+def test_a_group_with_far_fewer_keys(rows):
+    """Blocks whose second group has no row, or a few, beside a first one over
+    many keys, and one whose first group sees far less: the group that is done
+    gives back the stages that it has no use for."""
+    p = Prompt(160, 128, 64, 128, (rows, 256), (2500, -100), seed=33)
+    out, lse = p.run()
+    for _ in range(5):
+        again, again_lse = p.run()
+        assert torch.equal(again, out) and torch.equal(again_lse, lse)
+    assert qvg.get_status() == qvg.QVG_OK
+    p.H, keep = 2, [0, 159]
+    p.q, p.k, p.v, p.q_rope = (x[:, keep] for x in (p.q, p.k, p.v, p.q_rope))
+    p.check(out[:, keep], lse[keep], CAUSAL)
+
+
 @pytest.mark.parametrize("B", [20, 300, 1200])
 def test_many_ragged_prompts(B):
     """Blocks of rows that are ranked by length, and more of them than that."""

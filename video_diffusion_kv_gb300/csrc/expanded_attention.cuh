@@ -342,8 +342,9 @@ __global__ void __launch_bounds__(kPromptWarps * 32, 1)
                 commit(&a_empty[ra.i], one);
                 // test hook: with S in flight, wait for what never comes
                 if (a.inject && d == 0) ok = wait(&never, 0);
-            } else if (one && ok) {
-                umma::mbar_arrive(&a_empty[ra.i]);
+            } else {
+                __syncwarp();  // (all lanes have seen the stage)
+                if (one && ok) umma::mbar_arrive(&a_empty[ra.i]);
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
