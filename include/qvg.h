@@ -946,8 +946,8 @@ qvg_status qvg_pages_copy(const qvg_page_rows *rows, const int32_t *copies, int3
  *   table, table_stride, B  as in qvg_paged_attention.
  * n_keep outside 0 .. keep_stride, a negative first, a keep that does not
  * ascend or is beyond the row, and a page outside the cache latch
- * QVG_ERR_INVALID_ARG; that sequence is left as it was.
- * QVG_ERR_UNSUPPORTED for B above 65535 or keep_stride above 2^31 - 2049.
+ * QVG_ERR_INVALID_ARG; that sequence is left as it was.  (Where keep_stride is
+ * 0 nothing is looked at.)  QVG_ERR_UNSUPPORTED for B above 65535 or keep_stride above 2^31 - 2049.
  */
 qvg_status qvg_paged_compact(const qvg_page_rows *rows, const int32_t *table, int32_t table_stride, int32_t B,
                              const int32_t *first, const int32_t *keep, int32_t keep_stride, const int32_t *n_keep,

@@ -75,8 +75,8 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *map, int c
 }
 
 // The issuing warps stay whole and name the thread that issues by a predicate, so that
-// addresses and counts are the same for the warp as the compiler sees it: 20 products take
-// 1200 clocks to issue, under `if (lane == 0)` 1800.
+// addresses and counts are the same for the warp as the compiler sees it (4680 causal tokens of
+// 16 heads: 149 us where `if (lane == 0)` took 213, when this was changed).
 __device__ __forceinline__ bool elected() {
     uint32_t r;
     asm volatile(

@@ -7,13 +7,13 @@
 // while the second half's weights are made.  One group's products run while the other group is
 // at its softmax.
 //
-// Bound: a group's chain, 4700 clocks for 128 keys of 128 + 64 channels (stamped): S 1430, the
-// first half's softmax 900, the step to the second 300, its softmax 1140, PV until the next S 920.
+// Bound: a group's chain, 4780 clocks for 128 keys of 128 + 64 channels (stamped): S 1440, the
+// first half's softmax 930, the step to the second 340, its softmax 1110, PV until the next S 960.
 //   4680 causal tokens of 16 heads
-// (1.1e11 operations): 103 us, 1.09 PFLOP/s, 56 % of a large bf16 product's rate;
-// without the mask 176 us, 1.27 PFLOP/s.  12 prompts of 1 to 1100 tokens after 0 to 1700, 8 heads, 64 + 32
-// channels: 51 us, the longest unit's 44 tiles.
-//   Tried and slower: two threads a row, a half each (157 us for the first case: they meet
+// (1.1e11 operations): 105 us, 1.07 PFLOP/s, 55 % of a large bf16 product's rate;
+// without the mask 184 us, 1.22 PFLOP/s.  12 prompts of 1 to 1100 tokens after 0 to 1700, 8 heads, 64 + 32
+// channels: 52 us, the longest unit's 44 tiles.
+//   Tried and slower: two threads a row, a half each (157 us where one took 117 then: they meet
 // once a tile, and V's tiles come too late with the room that is left), a part of the weights' powers by a
 // polynomial beside the special function unit (112 us and more), S of 64 keys with two
 // buffers (a product of 64 columns takes 73 clocks, one of 128 about 60).
@@ -73,7 +73,9 @@ __device__ __forceinline__ Unit unit_of(const Args &a, int b, int r, int h, bool
 // - One sequence: the last rows first, which with a causal mask see the most keys.  (Counted from the
 //   blocks that were launched: max_q may be far above the rows that there are.)
 // - Up to kSorted possible blocks: ranked by their tiles (each CTA does it for itself: they
-//   all get the same order), so that the short ones fill the GPU's end.
+//   all get the same order), so that the short ones fill the GPU's end.  (The ragged prompts above, 60 blocks a
+//   head: 52 us, 59 in the sequences' order.  The ranking takes a CTA the longer the more blocks there
+//   are: 64 prompts of 10 to 1000 tokens, 256 blocks, 142 us, in the sequences' order 124.)
 // - More: the blocks that there are, sequence by sequence, found from the lengths.
 // `room`: shared memory for kSorted integers.
 constexpr int kSorted = 256;

@@ -21,6 +21,9 @@ namespace {
 //   many: a block a task (16 channels), each warp every eighth part, whose sums
 //   are added in the warps' order.
 // Either way the result is the same each time.  152 parts of 16 rows add 8 us to the call.
+// Few: eight, what a warp's lanes hold of references and sums (all joins the other way: 74 -> 91 us for the
+// decode batch, 73 -> 154 for the trees).  kAhead: parts asked for along with the weights; four or ten, 59 us for
+// one long token either way.
 constexpr int kJoinWarps = 8, kJoinY = 2, kFewParts = 8, kMostParts = 512, kAhead = 10;
 
 struct JoinRoom {

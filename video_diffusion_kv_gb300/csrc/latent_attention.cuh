@@ -18,7 +18,7 @@
 // 449,280 (256 + 64 channels, 288 MB): 60 us, 4.8 TB/s; of it 5 to 7 us until a CTA's
 // first tile is there, 2 to 3 for the last tile and its sums, 8 for the join.  48 tokens of 32 heads over 700 to 24,000
 // (381 MB): 74 us, 5.1 TB/s.  16 trees of 17 to 48 tokens, 16 heads, pages of 16 (6.8e10
-// operations): 73 us, 930 TFLOP/s, 48 % of a large bf16 product's rate.
+// operations): 74 us, 920 TFLOP/s, 48 % of a large bf16 product's rate.
 //
 // Tensor memory: O 256 columns, S 2 x 64, Q 128.
 // Roles: softmax (4 warps, thread = row), helpers (4: Q, and V in tiles that
