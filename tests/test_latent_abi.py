@@ -253,6 +253,25 @@ def test_no_gradient_is_lost_without_a_word(lib):
         assert "gradient" not in str(e.value)
 
 
+def test_counts_beyond_32_bits_are_not_cut_off(lib):
+    """(Shapes of expanded tensors: nothing of that size is allocated.)"""
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    many = torch.zeros(1, dtype=torch.int32).expand(2 ** 32 + 1)
+    cache, pool_ = qvg.LatentKV(64, 8, 16, 2, device="cpu"), qvg.PagePool(4, device="cpu")
+    t, n = i32(2, 3), i32(2)
+    for call in (lambda: qvg.latent_attention(cache, bf(4, 2, 64), bf(4, 2, 8), t, n, 2 ** 32, 0.1, cu_q=i32(3)),
+                 lambda: qvg.expanded_attention(bf(4, 2, 64), None, bf(6, 2, 64), None, bf(6, 2, 64), 2 ** 32 + 1, cu_q=i32(3), cu_k=i32(3)),
+                 lambda: qvg.expanded_attention(bf(4, 2, 64), None, bf(6, 2, 64), None, bf(6, 2, 64), 2, cu_q=i32(3), cu_k=i32(3), max_k=2 ** 33),
+                 lambda: qvg.pages_fork(pool_, 16, t, n, many, many), lambda: qvg.pages_release(pool_, 16, t, n, many),
+                 lambda: qvg.pages_release(pool_, 16, many[:, None].expand(-1, 3), many, i32(1)),
+                 lambda: qvg.pages_reserve(pool_, 16, t, n, n_new=2 ** 32), lambda: qvg.pages_reserve(pool_, 16, t, n, cu_new=i32(3), total=2 ** 32),
+                 lambda: qvg.pages_copy(cache, many[:, None].expand(-1, 2)),
+                 lambda: qvg.paged_compact(cache, t, n, i32(1).expand(2, 2 ** 32), n)):
+        with pytest.raises(ValueError, match="32-bit counts"):
+            call()
+
+
 def test_python_refusals(lib):
     """Shapes, types and devices are checked before the library is called."""
     c = qvg.LatentKV(64, 8, 16, 2, device="cpu")

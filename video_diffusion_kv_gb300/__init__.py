@@ -689,6 +689,14 @@ def _off(t, dtype, dev):
     return t.dtype != dtype or t.device != dev or not t.is_contiguous()
 
 
+def _counts(where, *counts):
+    """Numbers that the library takes in 32 bits: ctypes would cut off a larger
+    one's upper bits, and a bound of 2^32 would be one of 0."""
+    for n in counts:
+        if n > 0x7FFFFFFF:
+            raise ValueError("%s: %d is more than the library's 32-bit counts hold" % (where, n))
+
+
 def _without_gradient(where, *inputs):
     """These calls have no backward pass: an input that wants one is refused,
     so that its gradient is not lost without a word."""
@@ -838,6 +846,7 @@ def latent_attention(cache: LatentKV, q, q_rope, block_table, kv_len, max_q, sca
     call).  No gradient: inputs that require one are refused."""
     import torch
     _without_gradient("latent_attention", q, q_rope)
+    _counts("latent_attention", max_q)
     if q.dim() != 3:
         raise ValueError("latent_attention: q must be [total_q, Hq, %d]" % cache.dc)
     total, Hq, B = q.shape[0], q.shape[1], kv_len.numel()
@@ -882,6 +891,7 @@ def expanded_attention(q, q_rope, k, k_rope, v, max_q, scale=0.0, cu_q=None, cu_
     refused."""
     import torch
     _without_gradient("expanded_attention", q, q_rope, k, k_rope, v)
+    _counts("expanded_attention", max_q, max_k)
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("expanded_attention: q, k and v must be [tokens, heads, channels]")
     (total, H, dn), total_k, dv = q.shape, k.shape[0], v.shape[2]
@@ -939,6 +949,7 @@ def _sequences(pool, page_size, block_table, kv_len, where):
     B = kv_len.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("%s: block_table must be [B, pages], kv_len [B]" % where)
+    _counts(where, B, block_table.shape[1])
     if _off(block_table, torch.int32, pool.device) or _off(kv_len, torch.int32, pool.device):
         _on(pool.device, where, block_table=(block_table, torch.int32), kv_len=(kv_len, torch.int32))
     return ct.byref(_Sequences(B, page_size, block_table.shape[1], block_table.data_ptr(), kv_len.data_ptr()))
@@ -951,6 +962,7 @@ def pages_fork(pool: PagePool, page_size, block_table, kv_len, parents, children
     s = _sequences(pool, page_size, block_table, kv_len, "pages_fork")
     if parents.numel() != children.numel():
         raise ValueError("pages_fork: parents and children must be as many")
+    _counts("pages_fork", parents.numel())
     if _off(parents, torch.int32, pool.device) or _off(children, torch.int32, pool.device):
         _on(pool.device, "pages_fork", parents=(parents, torch.int32), children=(children, torch.int32))
     _call(pool.device, "qvg_pages_fork", lib().qvg_pages_fork, stream, pool._ref, s, parents.data_ptr(), children.data_ptr(), parents.numel())
@@ -963,6 +975,7 @@ def pages_release(pool: PagePool, page_size, block_table, kv_len, ids, keep=None
     s = _sequences(pool, page_size, block_table, kv_len, "pages_release")
     if keep is not None and keep.numel() != ids.numel():
         raise ValueError("pages_release: ids and keep must be as many")
+    _counts("pages_release", ids.numel())
     if _off(ids, torch.int32, pool.device) or (keep is not None and _off(keep, torch.int32, pool.device)):
         _on(pool.device, "pages_release", ids=(ids, torch.int32), keep=(keep, torch.int32))
     _call(pool.device, "qvg_pages_release", lib().qvg_pages_release, stream, pool._ref, s, ids.data_ptr(),
@@ -985,6 +998,7 @@ def pages_reserve(pool: PagePool, page_size, block_table, kv_len, n_new=1, cu_ne
     total = B * n_new if cu_new is None else total
     if total < 0:
         raise ValueError("pages_reserve: a negative number of tokens")
+    _counts("pages_reserve", n_new, total)
     slots = _fresh((total,), (1,), torch.int64, pool.device, stream) if slots is None else slots
     copies = _fresh((B, 2), (2, 1), torch.int32, pool.device, stream) if copies is None else copies
     if slots.numel() != total or copies.shape != (B, 2):
@@ -1020,6 +1034,7 @@ def pages_copy(cache, copies, stream=None):
     import torch
     if copies.dim() != 2 or copies.shape[1] != 2:
         raise ValueError("pages_copy: copies must be [n, 2]")
+    _counts("pages_copy", copies.shape[0])
     if _off(copies, torch.int32, cache.device):
         _on(cache.device, "pages_copy", copies=(copies, torch.int32))
     _call(cache.device, "qvg_pages_copy", lib().qvg_pages_copy, stream, _page_rows(cache, "pages_copy"), copies.data_ptr(), copies.shape[0])
@@ -1035,6 +1050,7 @@ def paged_compact(cache, block_table, first, keep, n_keep, stream=None):
     B = n_keep.numel()
     if block_table.dim() != 2 or keep.dim() != 2 or block_table.shape[0] != B or keep.shape[0] != B or first.numel() != B:
         raise ValueError("paged_compact: block_table and keep must be [B, ...], first and n_keep [B]")
+    _counts("paged_compact", B, block_table.shape[1], keep.shape[1])
     dev = cache.device
     if _off(block_table, torch.int32, dev) or _off(first, torch.int32, dev) or _off(keep, torch.int32, dev) or _off(n_keep, torch.int32, dev):
         _on(dev, "paged_compact", block_table=(block_table, torch.int32), first=(first, torch.int32), keep=(keep, torch.int32),
